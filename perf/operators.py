@@ -251,7 +251,7 @@ def _exponent(amax):
     """The smallest e >= -126 with amax <= 127 * 2^e, as 2^e (1 where amax is 0)."""
     m, x = torch.frexp(amax)
     e = torch.where(m <= 127.0 / 128.0, x - 7, x - 6).clamp(min=-126)
-    return torch.where(amax > 0, torch.exp2(e.double()).float(), torch.ones_like(amax))
+    return torch.where(amax > 0, torch.exp2(e.double()), 1.0).float()
 
 
 def _bounds(k):
@@ -295,7 +295,10 @@ def _plain_write(s):
 def _plain_summarize(s):
     ids = s["ids"][s["live"]].long()
     k = s["k_pool"][ids]
-    k = k.view(torch.float8_e4m3fn).float() * s["k_scale"][ids][:, None, :, None] if "k_scale" in s else k.float()
+    if "k_scale" in s:  # products in 64 bits: a bound is rounded outwards, and 32 bits can land on a step
+        k = k.view(torch.float8_e4m3fn).double() * s["k_scale"][ids].double()[:, None, :, None]
+    else:
+        k = k.float()
     codes, sc = _bounds(k)
     s["summary"].index_copy_(0, ids, codes)
     s["summary_scale"].index_copy_(0, ids, sc)
