@@ -71,6 +71,8 @@ typedef enum pkv_dtype { PKV_F32 = 0, PKV_F16 = 1, PKV_BF16 = 2 } pkv_dtype;
 #define PKV_DEV_ERR_LENGTH 8u   /* decode: context length < 0 or > the table / max_context_len */
 #define PKV_DEV_ERR_TIMEOUT 16u /* decode: a wait for a tile copy exceeded its time limit */
 #define PKV_DEV_ERR_SMEM 32u    /* decode: shared memory not 1024-byte aligned; kernel did nothing */
+#define PKV_DEV_ERR_POSITION 64u /* norm_rope_write: position outside the angle table (and not -1) */
+#define PKV_DEV_ERR_SELECT 128u  /* decode_sparse: bad list length, or an entry not ascending or past the sequence */
 
 /*
  * pkv_write_cache -- the write path [P1 "The write path: slot mapping and
@@ -434,6 +436,164 @@ pkv_status pkv_decode_step_partitions_fp8(void* out, const void* q, const void* 
                                           float scale, int partition_size, int max_context_len, void* workspace,
                                           size_t workspace_bytes, pkv_dtype q_dtype,
                                           pkv_dtype out_dtype, int32_t* dev_status, void* stream);
+
+/*
+ * ------------------------------------------------------------ layer operators
+ *
+ * What runs around paged decode in a layer: norms and position rotation of
+ * new rows on their way into the pools, and decode over a chosen part of a
+ * long history.  The pages have no counterpart of these entry points.
+ */
+
+/*
+ * pkv_norm_rope_write -- for every token t, in float32 from 16-bit rows:
+ *   query and key heads   y = x * rsqrt(mean(x^2) + eps) * w   (with a weight),
+ *                         then the first rot_dim channels rotated by the
+ *                         token's position in pairs (a, b):
+ *                         (a cos - b sin, b cos + a sin);
+ *   queries go to q_out, keys to their slot of the K pool (and to k_out when
+ *   it is not NULL), values bit for bit to their slot of the V pool.
+ * Each result is rounded once, to kv_dtype.
+ *   q_out, k_out : [num_tokens][num_q_heads | num_kv_heads][head_dim] of
+ *                  kv_dtype; may be q and k themselves (same stride).  Any
+ *                  other overlap of inputs and outputs is not allowed.
+ *   q, k, v      : new rows, kv_dtype.
+ *   *_stride     : elements between consecutive tokens (0 = dense, else a
+ *                  multiple of 8 and at least a row); new_row_stride is k's
+ *                  and v's.  Rows of a fused projection pass as they are.
+ *   q_weight, k_weight : head_dim values of kv_dtype shared by the heads, or
+ *                  NULL: no norm.  eps > 0 when one is given.
+ *   rot_dim      : rotated channels, a multiple of 16, 0 (none) to head_dim.
+ *   interleaved  : 0: channel i pairs with i + rot_dim / 2; 1: 2i with 2i + 1.
+ *   cos_sin      : float32 [max_positions][rot_dim]: the rot_dim / 2 cosines
+ *                  of a position, then its sines (NULL when rot_dim is 0).
+ *   positions    : int32[num_tokens] (NULL when rot_dim is 0).  -1: a
+ *                  padding token, for which nothing is read or written
+ *                  anywhere.  Any other position outside the table sets
+ *                  PKV_DEV_ERR_POSITION and is treated alike.
+ *   slot_mapping : as pkv_write_cache; -1: the pools are not written (q_out
+ *                  and k_out are).
+ * All pointers 16-byte aligned but the int32 ones.  head_dim 64 or 128, block
+ * sizes 8 to 64.  num_tokens == 0 is a no-op.
+ */
+pkv_status pkv_norm_rope_write(void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                               const void* q, int64_t q_stride, const void* k, const void* v,
+                               int64_t new_row_stride, const void* q_weight, const void* k_weight, float eps,
+                               const float* cos_sin, const int32_t* positions, int max_positions, int rot_dim,
+                               int interleaved, void* k_pool, void* v_pool, int64_t block_stride,
+                               const int32_t* slot_mapping, int num_tokens, int num_q_heads, int num_kv_heads,
+                               int head_dim, int block_size, int num_blocks, pkv_dtype kv_dtype,
+                               int32_t* dev_status, void* stream);
+
+/*
+ * pkv_norm_rope_write_fp8 -- the same into FP8 pools: the float32 key (after
+ * norm and rotation, not rounded to 16 bits before) and value are quantised
+ * with the scales of their block as in pkv_write_cache_fp8.  Blocks of 16.
+ */
+pkv_status pkv_norm_rope_write_fp8(void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                   const void* q, int64_t q_stride, const void* k, const void* v,
+                                   int64_t new_row_stride, const void* q_weight, const void* k_weight, float eps,
+                                   const float* cos_sin, const int32_t* positions, int max_positions, int rot_dim,
+                                   int interleaved, void* k_pool, void* v_pool, const float* k_scale,
+                                   const float* v_scale, const int32_t* slot_mapping, int num_tokens,
+                                   int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                   int num_layers, pkv_dtype new_dtype, int32_t* dev_status, void* stream);
+
+/*
+ * pkv_summarize_blocks -- bounds of a block's keys, for pkv_select_blocks.
+ * For each listed block and KV head, over the block's block_size keys k_t:
+ *     lo[d] = min_t k_t[d],  hi[d] = max_t k_t[d],
+ *     summary_scale = 2^e, the smallest (e >= -126) with every |lo|, |hi| <= 127 * 2^e
+ *                     (1 when all are 0),
+ *     summary[block][g][0][d] = floor(lo[d] / 2^e),  summary[block][g][1][d] = ceil(hi[d] / 2^e).
+ * NaN keys are passed over (a channel without a number counts as 0) and
+ * infinities count as the type's largest value.
+ *   summary      : int8 [num_blocks][num_kv_heads][2][head_dim], 16-byte aligned.
+ *   summary_scale: float32 [num_blocks][num_kv_heads].
+ *   block_ids    : int32[num_ids] physical blocks; -1 entries are passed
+ *                  over, others outside the pool set PKV_DEV_ERR_BLOCK.
+ * Call it for blocks whose rows are all written: after a prompt for its full
+ * blocks, in decode for the block a step has filled (-1 for sequences whose
+ * last block has room left).  The last block of a sequence is always
+ * selected, so it needs no summary before the next one is begun.  A summary
+ * belongs to the physical block: call it again for the destinations of
+ * pkv_copy_blocks and pkv_swap_blocks whose blocks are full.
+ * head_dim 64 or 128; block sizes 16, 32 and 64.
+ */
+pkv_status pkv_summarize_blocks(void* summary, float* summary_scale, const void* k_pool, int64_t block_stride,
+                                const int32_t* block_ids, int num_ids, int num_kv_heads, int head_dim,
+                                int block_size, int num_blocks, pkv_dtype kv_dtype, int32_t* dev_status,
+                                void* stream);
+
+/*
+ * pkv_summarize_blocks_fp8 -- the same over an FP8 pool: keys are
+ * decode(code) * k_scale of their (block, KV head), bounds rounded outwards
+ * from the exact product.  A scale that is not positive and finite gives a
+ * summary of zeros.
+ */
+pkv_status pkv_summarize_blocks_fp8(void* summary, float* summary_scale, const void* k_pool, const float* k_scale,
+                                    const int32_t* block_ids, int num_ids, int num_kv_heads, int head_dim,
+                                    int block_size, int num_blocks, int num_layers, int32_t* dev_status,
+                                    void* stream);
+
+/*
+ * pkv_select_blocks -- which blocks of its history each (sequence, KV head)
+ * attends to this step.  With n = ceil(L / block_size) blocks:
+ *   n <= keep: all of them.  Otherwise the first first_blocks, the last
+ *   last_blocks, and of those between the best-scored, `keep` in all.
+ *   score(b) = max over the group's query heads of
+ *       (sum_d max(c_d lo_d, c_d hi_d)) * q_scale * summary_scale
+ *   with the block's summary codes lo, hi and c = q in int8 steps of q_scale
+ *   (the power of two that summaries use; nearest, ties to even): an upper
+ *   bound of the scores of the block's keys for the rounded q.  The sum is
+ *   an integer, so equal inputs give equal choices everywhere; equal scores
+ *   go to the lowest block.
+ *   selected     : int32 [num_seqs][num_kv_heads][keep] logical blocks, ascending, then -1.
+ *   counts       : int32 [num_seqs][num_kv_heads] = min(n, keep).
+ *   q            : [num_seqs][num_q_heads][head_dim] of q_dtype, 16-byte aligned.
+ *   first_blocks >= 0, last_blocks >= 1, their sum <= keep <= 2^20.
+ * Lengths are clamped and flagged as in pkv_decode_attention; a table entry
+ * outside the pool sets PKV_DEV_ERR_BLOCK and is taken last.  head_dim 64 or
+ * 128, 1 <= group <= 8, block sizes 16, 32 and 64, at most 49152 blocks a
+ * sequence (min of max_context_len's and max_blocks_per_seq).
+ */
+pkv_status pkv_select_blocks(int32_t* selected, int32_t* counts, const void* q, const void* summary,
+                             const float* summary_scale, const int32_t* block_tables, int max_blocks_per_seq,
+                             const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+                             int head_dim, int block_size, int num_blocks, int keep, int first_blocks,
+                             int last_blocks, int max_context_len, pkv_dtype q_dtype, int32_t* dev_status,
+                             void* stream);
+
+/*
+ * pkv_decode_sparse -- pkv_decode_attention over the tokens of the selected
+ * blocks alone:
+ *     out[s][h] = sum_t softmax_t(scale * q[s][h] . k_t) v_t,
+ *                 t in {b * block_size + o : b in selected[s][g][0 .. counts[s][g]), t < L}.
+ *   selected, counts, keep : as pkv_select_blocks writes them, or a list of
+ *                  the caller's own: logical blocks of the sequence, strictly
+ *                  ascending.  An entry that is not larger than the one
+ *                  before it or lies outside the sequence sets
+ *                  PKV_DEV_ERR_SELECT and is passed over; so does a count
+ *                  outside [0, keep], which is clamped.
+ * A row without tokens is zero.  One kernel, no workspace.  q 16-byte
+ * aligned; head_dim 64 or 128, 1 <= group <= 8, block sizes 16, 32 and 64;
+ * other arguments and flags as in pkv_decode_attention.
+ */
+pkv_status pkv_decode_sparse(void* out, const void* q, const void* k_pool, const void* v_pool, int64_t block_stride,
+                             const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                             const int32_t* selected, const int32_t* counts, int keep, int num_seqs,
+                             int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                             float scale, int max_context_len, pkv_dtype kv_dtype, pkv_dtype out_dtype,
+                             int32_t* dev_status, void* stream);
+
+/* pkv_decode_sparse_fp8 -- the same over FP8 pools (head_dim 128, blocks of 16), as pkv_decode_attention_fp8. */
+pkv_status pkv_decode_sparse_fp8(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                 const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                 int max_blocks_per_seq, const int32_t* context_lens, const int32_t* selected,
+                                 const int32_t* counts, int keep, int num_seqs, int num_q_heads, int num_kv_heads,
+                                 int head_dim, int block_size, int num_blocks, int num_layers, float scale,
+                                 int max_context_len, pkv_dtype q_dtype, pkv_dtype out_dtype, int32_t* dev_status,
+                                 void* stream);
 
 /*
  * ------------------------------------------------------------ block manager

@@ -17,9 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpkv.so")
 SOURCES = ["pkv_api.cu", "pkv_cache_ops.cu", "pkv_decode.cu", "pkv_decode_hg.cu", "pkv_decode_balanced.cu",
-           "pkv_decode_fp8.cu",
+           "pkv_decode_fp8.cu", "pkv_norm_rope.cu", "pkv_sparse_select.cu", "pkv_sparse_decode.cu", "pkv_api_layer.cu",
            "pkv_static_ws.cu", "pkv_checks.cu", "pkv_block_manager.cpp"]
-HEADERS = ["pkv_internal.h", "pkv_device.cuh", "pkv_balanced.cuh", "pkv_fp8.cuh", os.path.join("..", "..", "include", "pkv.h")]
+HEADERS = ["pkv_internal.h", "pkv_device.cuh", "pkv_balanced.cuh", "pkv_fp8.cuh", "pkv_fp8_attention.cuh", os.path.join("..", "..", "include", "pkv.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -88,7 +88,7 @@ cudaError_t ensure_dynamic_smem(const void* kernel, size_t bytes) {
     int dev;
     size_t bytes;
   };
-  static Entry table[64];
+  static Entry table[128];
   static int used = 0;
   static std::mutex mu;
   int dev = 0;
@@ -104,7 +104,7 @@ cudaError_t ensure_dynamic_smem(const void* kernel, size_t bytes) {
       table[i].bytes = bytes;
       return cudaSuccess;
     }
-  if (used < 64) table[used++] = Entry{kernel, dev, bytes};
+  if (used < 128) table[used++] = Entry{kernel, dev, bytes};
   return cudaSuccess;
 }
 
@@ -131,10 +131,6 @@ WorkspaceLayout balanced_workspace_layout(int num_seqs, int num_q_heads, int hea
 }
 
 namespace {
-
-constexpr long long kWaitTimeoutNs = 2000000000LL;  // 2 s per bounded wait
-
-bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 bool kv_dtype_ok(pkv_dtype d) { return d == PKV_F16 || d == PKV_BF16; }
 
@@ -222,12 +218,14 @@ bool encode_pool_map_uncached(CUtensorMap* map, const void* pool, int num_blocks
   return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
 // Descriptors depend only on the pool address and geometry, so recent ones
 // are kept (a small round-robin cache) instead of re-encoded every call.
 // heads_per_box > 1 (blocks of >= 16 tokens): one box holds that many
 // adjacent KV heads' tiles of a block, one after the other.
 bool encode_pool_map(CUtensorMap* map, const void* pool, int num_blocks, int block_size, int num_kv_heads,
-                     int head_dim, int eb, int64_t block_stride, int heads_per_box = 1) {
+                     int head_dim, int eb, int64_t block_stride, int heads_per_box) {
   struct Entry {
     const void* pool;
     int num_blocks, block_size, num_kv_heads, head_dim, eb, heads_per_box;
@@ -276,6 +274,8 @@ int64_t resolve_block_stride(int64_t block_stride, int block_size, int num_kv_he
   if (block_stride < dense || block_stride % 8 != 0) return -1;
   return block_stride;
 }
+
+namespace {
 
 int parts_for(int max_context_len, int partition_size, int* ps_out) {
   int ps = partition_size;

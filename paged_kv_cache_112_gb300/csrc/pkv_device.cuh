@@ -502,12 +502,14 @@ struct SoftmaxState {
 //   S^T[16 tok x 8 heads] = K[16 x D] Q^T[D x 8]     (tokens on M)
 //   O^T[D x 8 heads]     += V^T[D x 16] P^T[16 x 8]  (head_dim on M)
 // V^T comes from ldmatrix.trans; P^T is S^T's C fragment transposed in
-// registers with movmatrix.  P is rounded to the KV type for the MMA; for
-// bf16 it is split into hi + lo parts (two MMAs), keeping the rounding error
-// near 2^-17 relative (fp16 alone is 2^-11).  Lane (gr = lane/4, tq = lane%4)
+// registers with movmatrix.  P is rounded to the KV type for the MMA; with
+// SPLIT (bf16 always) it is split into hi + lo parts (two MMAs), keeping the
+// rounding error near 2^-17 relative for bf16 and 2^-22 for fp16 (fp16 alone
+// is 2^-11).  Lane (gr = lane/4, tq = lane%4)
 // owns heads 2tq and 2tq+1 (a, b) and the output rows d = 16mt + gr (+8).
-template <int D, bool BF16>
+template <int D, bool BF16, bool SPLIT = BF16>
 struct WarpAttention : SoftmaxState<D / 16> {
+  static_assert(SPLIT || !BF16, "bf16 weights alone (2^-9) are too coarse");
   static constexpr int KT = D / 16;
   using Base = SoftmaxState<KT>;
   using Base::acc;
@@ -575,8 +577,15 @@ struct WarpAttention : SoftmaxState<D / 16> {
       pl0 = movmatrix_trans(pack_bf16(p0 - f0.x, p1 - f0.y));
       pl1 = movmatrix_trans(pack_bf16(p2 - f1.x, p3 - f1.y));
     } else {
-      pb0 = movmatrix_trans(pack_f16(p0, p1));
-      pb1 = movmatrix_trans(pack_f16(p2, p3));
+      const uint32_t h0 = pack_f16(p0, p1), h1 = pack_f16(p2, p3);
+      pb0 = movmatrix_trans(h0);
+      pb1 = movmatrix_trans(h1);
+      if constexpr (SPLIT) {
+        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+        pl0 = movmatrix_trans(pack_f16(p0 - f0.x, p1 - f0.y));
+        pl1 = movmatrix_trans(pack_f16(p2 - f1.x, p3 - f1.y));
+      }
     }
 
     // V rows past the valid tokens may hold anything (even NaN): zero them in
@@ -596,7 +605,7 @@ struct WarpAttention : SoftmaxState<D / 16> {
       va[2] &= m23;
       va[3] &= m23;
       mma_16816<BF16>(acc[mt], va, pb0, pb1);
-      if constexpr (BF16) mma_16816<BF16>(acc[mt], va, pl0, pl1);
+      if constexpr (SPLIT) mma_16816<BF16>(acc[mt], va, pl0, pl1);
     }
   }
 

@@ -125,6 +125,69 @@ struct DecodeArgs {
   int64_t scale_stride;
 };
 
+// Norms of queries and keys per head, position rotation and the scatter of K
+// and V (pkv_norm_rope.cu).  Row strides in elements; pool strides in pool
+// elements (FP8: bytes).
+struct NormRopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* q_out;
+  uint16_t* k_out;  // null: K goes to the pool only
+  const uint16_t* q_weight;  // null: no norm
+  const uint16_t* k_weight;
+  const float* cos_sin;      // [max_positions][rot_dim]: cosines, then sines
+  const int32_t* positions;  // null when rot_dim is 0
+  const int32_t* slot_mapping;
+  void* k_pool;
+  void* v_pool;
+  const float* k_scale;  // FP8 pools only
+  const float* v_scale;
+  int32_t* dev_status;
+  int64_t q_stride, kv_stride, q_out_stride, k_out_stride;
+  int64_t block_stride, scale_stride;
+  int64_t num_slots;
+  float eps;
+  int num_tokens, num_q_heads, num_kv_heads;
+  int rot_dim, interleaved, max_positions;
+  int block_shift;
+};
+
+// Bounds of a block's keys (pkv_sparse_select.cu).
+struct SummarizeArgs {
+  const uint8_t* k_pool;
+  const float* k_scale;  // FP8 pools only
+  const int32_t* block_ids;
+  int8_t* summary;       // [num_blocks][num_kv_heads][2][head_dim]
+  float* summary_scale;  // [num_blocks][num_kv_heads]
+  int32_t* dev_status;
+  int64_t block_bytes;   // bytes between consecutive blocks
+  int64_t scale_stride;
+  int num_ids, num_kv_heads, num_blocks, block_size;
+};
+
+// Block selection (pkv_sparse_select.cu).
+struct SelectArgs {
+  int32_t* selected;  // [num_seqs][num_kv_heads][keep]
+  int32_t* counts;    // [num_seqs][num_kv_heads]
+  const uint16_t* q;
+  const int8_t* summary;
+  const float* summary_scale;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  int32_t* dev_status;
+  int num_seqs, num_q_heads, num_kv_heads, group;
+  int max_blocks_per_seq, num_blocks, block_shift, max_context_len;
+  int keep, first_blocks, last_blocks;
+};
+
+// The selected blocks of a sparse decode call, beside its DecodeArgs.
+struct SparseArgs {
+  const int32_t* selected;
+  const int32_t* counts;
+  int keep;
+};
+
 // Split-K workspace layout (regions 256-byte aligned).  Fixed partitions:
 // records [S][H_q][max_parts].  Balanced split: per-pair metadata [S][<=H_q]
 // then records [W warps][2 slots][<= 8 heads].
@@ -218,5 +281,30 @@ cudaError_t launch_swap_blocks(const SwapBlocksArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_balanced(const DecodeArgs& a, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                                    int head_dim, int kv_bf16, cudaStream_t stream);
 cudaError_t launch_decode_reduce_balanced(const DecodeArgs& a, int head_dim, cudaStream_t stream);
+
+
+// head_dim 64 or 128; bf16: 0 = f16 values, 1 = bf16; fp8: e4m3 pools.
+cudaError_t launch_norm_rope_write(const NormRopeArgs& a, int head_dim, bool bf16, bool fp8, cudaStream_t stream);
+cudaError_t launch_summarize_blocks(const SummarizeArgs& a, int head_dim, bool bf16, bool fp8, cudaStream_t stream);
+// Largest number of blocks a sequence may have for launch_select_blocks.
+constexpr int kSelectMaxBlocks = 49152;
+// Bounds of one call of the sparse operators: list length, sequences x KV heads.
+constexpr int kMaxKeep = 1 << 20;
+constexpr int64_t kMaxUnits = 1 << 24;
+cudaError_t launch_select_blocks(const SelectArgs& a, int head_dim, bool bf16, cudaStream_t stream);
+// `a` as for launch_decode_partitions(_fp8) with one head a box; blocks of 16 tokens or more.
+cudaError_t launch_decode_sparse(const DecodeArgs& a, const SparseArgs& sp, const CUtensorMap& tmap_k,
+                                 const CUtensorMap& tmap_v, int head_dim, bool bf16, bool fp8, cudaStream_t stream);
+
+// Argument helpers shared by the entry points (pkv_api.cu).
+constexpr long long kWaitTimeoutNs = 2000000000LL;  // 2 s per bounded wait
+inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+// log2 of a supported block size (8, 16, 32 or 64 tokens), else -1.
+int block_shift_of(int block_size);
+// Block stride of a pool in elements: 0 means dense; -1 when invalid.
+int64_t resolve_block_stride(int64_t block_stride, int block_size, int num_kv_heads, int head_dim);
+// Tensor map of a pool for TMA tile loads; false (and the thread's CUDA error set) on failure.
+bool encode_pool_map(CUtensorMap* map, const void* pool, int num_blocks, int block_size, int num_kv_heads,
+                     int head_dim, int eb, int64_t block_stride, int heads_per_box = 1);
 
 }  // namespace pkv

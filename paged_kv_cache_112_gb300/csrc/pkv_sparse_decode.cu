@@ -1,0 +1,269 @@
+// Single-token attention over selected blocks.
+//
+// For each sequence s and KV head g a list of logical blocks is given
+// (pkv_select_blocks, or the caller's own choice), and every query head h of
+// the group attends to those blocks' tokens alone:
+//     out[s][h] = sum_t softmax_t(scale * q[s][h] . k_t) v_t,
+//                 t in {b * B + o : b selected, o < B, t < L}.
+//
+// Bound: HBM bytes of the selected K and V rows (each read once; all query
+// heads of the group share them); with few units the latency of length ->
+// list -> table entry -> tile.
+//
+// One CTA of NW warps per (s, g).  The list's 16-token tiles are dealt to the
+// warps in turn; each warp streams its tiles through a private ring of TMA
+// copies and keeps its own online-softmax state on the tensor cores
+// (WarpAttention, WarpAttentionFp8).  The states meet in shared memory, so one
+// launch writes final rows and no workspace is needed.
+#include <type_traits>
+
+#include "pkv_fp8_attention.cuh"
+
+namespace pkv {
+namespace {
+
+using namespace dev;
+
+constexpr int kSparseWarps = 4;
+
+// A tile's place: physical block, or -1 for a tile to be skipped, first row
+// and valid rows.
+struct TilePlace {
+  int phys, row0, nv;
+};
+
+template <int D, bool BF16, bool FP8, int NW, int NST>
+__global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs a, const SparseArgs sp,
+                                                                const __grid_constant__ CUtensorMap tmap_k,
+                                                                const __grid_constant__ CUtensorMap tmap_v) {
+  constexpr int EB = FP8 ? 1 : 2;
+  using Geom = TileGeom<D, EB>;
+  using Att = std::conditional_t<FP8, WarpAttentionFp8<128>, WarpAttention<D, BF16, true>>;
+  constexpr int kRow = D + 4;                    // floats between a saved state's head rows
+  constexpr int kState = 8 * kRow + 16;          // 8 rows, then running max and sum of each head
+  static_assert(kState * 4 <= NST * Geom::kStageBytes, "a saved state must fit its warp's ring");
+  extern __shared__ __align__(1024) uint8_t smem[];
+  griddep_wait();
+  griddep_launch_dependents();
+  if (smem_misaligned(smem, a.dev_status)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t unit = blockIdx.x;
+  const int s = static_cast<int>(unit / a.num_kv_heads), g = static_cast<int>(unit % a.num_kv_heads);
+  const int G = a.group, B = 1 << a.block_shift;
+  const int L = clamped_len(a, s, g == 0 && threadIdx.x == 0);
+  const int nblk = (L >> a.block_shift) + ((L & (B - 1)) ? 1 : 0);
+  int count = sp.counts[unit];
+  if (count < 0 || count > sp.keep) {
+    if (threadIdx.x == 0) flag(a.dev_status, 128u);  // PKV_DEV_ERR_SELECT
+    count = count < 0 ? 0 : sp.keep;
+  }
+  const int32_t* list = sp.selected + unit * sp.keep;
+  const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
+  const int tshift = a.block_shift - 4;  // log2 of tiles per block
+  const int tiles = L > 0 ? count << tshift : 0;
+  const int cnt = tiles > warp ? (tiles - warp + NW - 1) / NW : 0;
+
+  // Place of this warp's tile i.  A list entry counts when it is larger than
+  // its predecessor and inside the sequence, so no token counts twice.
+  auto place = [&](int i) {
+    TilePlace p{-1, 0, 0};
+    if (i >= cnt) return p;
+    const int t = i * NW + warp, e = t >> tshift;
+    const int b = __ldg(list + e), prev = e > 0 ? __ldg(list + e - 1) : -1;
+    if (b <= prev || b < 0 || b >= nblk) {
+      flag(a.dev_status, 128u);  // PKV_DEV_ERR_SELECT
+      return p;
+    }
+    const int phys = __ldg(tbl + b);
+    if (phys < 0 || phys >= a.num_blocks) {
+      flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK
+      return p;
+    }
+    p.phys = phys;
+    p.row0 = (t & ((1 << tshift) - 1)) * kTile;
+    p.nv = max(0, min(kTile, L - b * B - p.row0));
+    return p;
+  };
+
+  WarpRing<D, NST, EB> ring{smem_u32(smem + static_cast<size_t>(warp) * NST * Geom::kStageBytes),
+                            smem_u32(smem + static_cast<size_t>(NW) * NST * Geom::kStageBytes) + 8 * NST * warp};
+  ring.init(lane);
+  // FP8: K and V scale of the tile in each stage (behind the barriers).
+  float2* stage_scale =
+      reinterpret_cast<float2*>(smem + static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 8)) + warp * NST;
+
+  // Lane j holds the place (and scales) of the warp's tile j of a chunk of 32.
+  TilePlace cur = place(lane), nxt = place(32 + lane);
+  auto scale_of = [&](const float* sc, int phys) {
+    return phys >= 0 ? __ldg(sc + static_cast<int64_t>(phys) * a.scale_stride + g) : 0.f;
+  };
+  float ks = 0.f, vs = 0.f;
+  if constexpr (FP8) {
+    ks = scale_of(a.k_scale, cur.phys);
+    vs = scale_of(a.v_scale, cur.phys);
+  }
+  uint32_t stage_nv = 0;  // 8 bits per stage: valid rows of its tile
+  static_assert(NST <= 4, "stage_nv");
+  auto issue = [&](int j) {
+    if ((j & 31) == 0 && j > 0) {
+      cur = nxt;
+      nxt = place(j + 32 + lane);
+      if constexpr (FP8) {
+        ks = scale_of(a.k_scale, cur.phys);
+        vs = scale_of(a.v_scale, cur.phys);
+      }
+    }
+    const int st = j % NST, from = j & 31;
+    const int phys = __shfl_sync(kFull, cur.phys, from);
+    const int row0 = __shfl_sync(kFull, cur.row0, from);
+    const int nv = __shfl_sync(kFull, cur.nv, from);
+    stage_nv = (stage_nv & ~(0xffu << (8 * st))) | (static_cast<uint32_t>(nv) << (8 * st));
+    if constexpr (FP8) {
+      const float k = __shfl_sync(kFull, ks, from), v = __shfl_sync(kFull, vs, from);
+      if (lane == 0) stage_scale[st] = make_float2(k, v);
+    }
+    ring.issue(j, max(phys, 0), -1, row0, g, &tmap_k, &tmap_v, lane);
+  };
+  auto nv_of = [&](int j) { return static_cast<int>((stage_nv >> (8 * (j % NST))) & 0xffu); };
+
+  Att at;
+  at.reset();
+  for (int j = 0; j < min(cnt, NST); ++j) issue(j);
+  const uint16_t* q0 = a.q + (static_cast<int64_t>(s) * a.num_q_heads + g * G) * D;
+  if constexpr (!FP8) {
+    at.load_q(q0, G, lane);
+    for (int i = 0; i < cnt; ++i) {
+      if (!__all_sync(kFull, ring.wait(i, a.timeout_ns))) {
+        ring.drain(i, min(cnt, i + NST), a.timeout_ns);
+        if (lane == 0) flag(a.dev_status, 16u);  // PKV_DEV_ERR_TIMEOUT; the output is undefined
+        break;
+      }
+      const uint32_t sK = ring.k_tile(i);
+      const int nv = nv_of(i);
+      if (nv > 0) at.tile(sK, sK + Geom::kTileBytes, nv, a.scale_log2, lane);
+      __syncwarp();
+      if (i + NST < cnt) issue(i + NST);
+    }
+  } else {
+    // Two tiles a step; the accumulator's unit is a power of two at least
+    // the largest V scale seen (it only grows).
+    const float sl2q = a.scale_log2 * at.template load_q<BF16>(q0, G, lane);
+    int vexp = -126;
+    float inv_unit = exp2i(126);
+    __syncwarp();
+    for (int i = 0; i < cnt; i += 2) {
+      const bool two = i + 1 < cnt;
+      const bool ok = ring.wait(i, a.timeout_ns) && (!two || ring.wait(i + 1, a.timeout_ns));
+      if (!__all_sync(kFull, ok)) {
+        ring.drain(i, min(cnt, i + NST), a.timeout_ns);
+        if (lane == 0) flag(a.dev_status, 16u);
+        break;
+      }
+      uint32_t sK[2];
+      int nv[2];
+      float sl2k[2], vsc[2], pv[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int j = two ? i + u : i;  // a missing second tile reuses the first one's stage, no valid token
+        const float2 sc = stage_scale[j % NST];
+        nv[u] = u == 1 && !two ? 0 : nv_of(j);
+        sK[u] = ring.k_tile(j);
+        sl2k[u] = sl2q * sc.x;
+        vsc[u] = nv[u] > 0 ? sc.y : 0.f;
+      }
+      const float vmax = fmaxf(vsc[0], vsc[1]);
+      const int e = min(max(static_cast<int>((__float_as_uint(vmax) >> 23) & 0xff) - 127, -126), 126);
+      if (e > vexp) {
+        at.scale_acc(unit_change(vexp, e));
+        vexp = e;
+        inv_unit = exp2i(-e);
+      }
+      pv[0] = vsc[0] * inv_unit;
+      pv[1] = vsc[1] * inv_unit;
+      at.template tiles<2>(sK, nv, sl2k, pv, lane);
+      __syncwarp();
+      if (i + NST < cnt) issue(i + NST);
+      if (i + 1 + NST < cnt) issue(i + 1 + NST);
+      __syncwarp();  // the stage scales written by lane 0
+    }
+    at.scale_acc(exp2i(vexp));
+  }
+  at.finish_sums();
+
+  // Save this warp's state: rows [8][kRow], running max [8], running sum [8].
+  {
+    float* st = reinterpret_cast<float*>(smem + static_cast<size_t>(warp) * NST * Geom::kStageBytes);
+    const int gr = lane >> 2, tq = lane & 3;
+    float* ra = st + (2 * tq) * kRow;
+    float* rb = ra + kRow;
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt) {
+      const int d0 = FP8 ? 16 * gr + 2 * mt : 16 * mt + gr, d1 = FP8 ? d0 + 1 : d0 + 8;
+      ra[d0] = at.acc[mt][0];
+      rb[d0] = at.acc[mt][1];
+      ra[d1] = at.acc[mt][2];
+      rb[d1] = at.acc[mt][3];
+    }
+    if (gr == 0) {
+      st[8 * kRow + 2 * tq] = at.m_a;
+      st[8 * kRow + 2 * tq + 1] = at.m_b;
+      st[8 * kRow + 8 + 2 * tq] = at.l_a;
+      st[8 * kRow + 8 + 2 * tq + 1] = at.l_b;
+    }
+  }
+  __syncthreads();
+  // Merge over the warps: M = max m_w, out = sum 2^(m_w - M) acc_w / sum 2^(m_w - M) l_w.
+  for (int e = threadIdx.x; e < G * D; e += NW * 32) {
+    const int h = e / D, d = e % D;
+    float M = kNegInf, o = 0.f, l = 0.f;
+    float m[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      m[w] = reinterpret_cast<const float*>(smem + static_cast<size_t>(w) * NST * Geom::kStageBytes)[8 * kRow + h];
+      M = fmaxf(M, m[w]);
+    }
+    const float mu = M == kNegInf ? 0.f : M;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float* st = reinterpret_cast<const float*>(smem + static_cast<size_t>(w) * NST * Geom::kStageBytes);
+      const float c = exp2f(m[w] - mu);
+      o += st[h * kRow + d] * c;
+      l += st[8 * kRow + 8 + h] * c;
+    }
+    store_out(a.out, (static_cast<int64_t>(s) * a.num_q_heads + g * G) * D + e, l > 0.f ? o / l : 0.f, a.out_dtype);
+  }
+}
+
+template <int D, bool BF16, bool FP8>
+cudaError_t launch_sparse_t(const DecodeArgs& a, const SparseArgs& sp, const CUtensorMap& tk, const CUtensorMap& tv,
+                            cudaStream_t stream) {
+  using Geom = TileGeom<D, FP8 ? 1 : 2>;
+  constexpr int NW = kSparseWarps, NST = FP8 ? 4 : 3;
+  const size_t smem = static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 8 + (FP8 ? 8 : 0));
+  auto kern = decode_sparse_kernel<D, BF16, FP8, NW, NST>;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(a.num_seqs) * a.num_kv_heads), dim3(NW * 32), smem, stream, a, sp,
+                    tk, tv);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_sparse(const DecodeArgs& a, const SparseArgs& sp, const CUtensorMap& tmap_k,
+                                 const CUtensorMap& tmap_v, int head_dim, bool bf16, bool fp8, cudaStream_t stream) {
+  if (a.num_seqs == 0) return cudaSuccess;
+  if (fp8) {
+    if (head_dim != 128) return cudaErrorInvalidValue;
+    return bf16 ? launch_sparse_t<128, true, true>(a, sp, tmap_k, tmap_v, stream)
+                : launch_sparse_t<128, false, true>(a, sp, tmap_k, tmap_v, stream);
+  }
+  if (head_dim == 128)
+    return bf16 ? launch_sparse_t<128, true, false>(a, sp, tmap_k, tmap_v, stream)
+                : launch_sparse_t<128, false, false>(a, sp, tmap_k, tmap_v, stream);
+  if (head_dim == 64)
+    return bf16 ? launch_sparse_t<64, true, false>(a, sp, tmap_k, tmap_v, stream)
+                : launch_sparse_t<64, false, false>(a, sp, tmap_k, tmap_v, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pkv
