@@ -237,6 +237,26 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// launch_pdl with clusters of `cluster` CTAs along x (the grid is a multiple of it).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
+                               cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 cudaError_t launch_write_cache(const WriteCacheArgs& a, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, cudaStream_t stream);
 // kv_bf16: 0 = f16, 1 = bf16.  Tensor maps describe the K and V pools.
@@ -287,7 +307,7 @@ cudaError_t launch_decode_reduce_balanced(const DecodeArgs& a, int head_dim, cud
 cudaError_t launch_norm_rope_write(const NormRopeArgs& a, int head_dim, bool bf16, bool fp8, cudaStream_t stream);
 cudaError_t launch_summarize_blocks(const SummarizeArgs& a, int head_dim, bool bf16, bool fp8, cudaStream_t stream);
 // Largest number of blocks a sequence may have for launch_select_blocks.
-constexpr int kSelectMaxBlocks = 49152;
+constexpr int kSelectMaxBlocks = 1 << 18;
 // Bounds of one call of the sparse operators: list length, sequences x KV heads.
 constexpr int kMaxKeep = 1 << 20;
 constexpr int64_t kMaxUnits = 1 << 24;

@@ -10,11 +10,12 @@
 // heads of the group share them); with few units the latency of length ->
 // list -> table entry -> tile.
 //
-// One CTA of NW warps per (s, g).  The list's 16-token tiles are dealt to the
-// warps in turn; each warp streams its tiles through a private ring of TMA
-// copies and keeps its own online-softmax state on the tensor cores
-// (WarpAttention, WarpAttentionFp8).  The states meet in shared memory, so one
-// launch writes final rows and no workspace is needed.
+// One cluster of C CTAs of NW warps per (s, g).  The list's 16-token tiles are
+// dealt to the cluster's warps in turn; each warp streams its tiles through a
+// private ring of TMA copies and keeps its own online-softmax state on the
+// tensor cores (WarpAttention, WarpAttentionFp8).  The states meet in shared
+// memory, first a CTA's, then through distributed shared memory the
+// cluster's, so one launch writes final rows and no workspace is needed.
 #include <type_traits>
 
 #include "pkv_fp8_attention.cuh"
@@ -41,34 +42,39 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
   using Att = std::conditional_t<FP8, WarpAttentionFp8<128>, WarpAttention<D, BF16, true>>;
   constexpr int kRow = D + 4;                    // floats between a saved state's head rows
   constexpr int kState = 8 * kRow + 16;          // 8 rows, then running max and sum of each head
+  // Shared memory: rings, barriers, stage scales, the CTA's merged state.
+  constexpr size_t kScalesAt = static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 8);
+  constexpr size_t kStateAt = kScalesAt + static_cast<size_t>(NW) * NST * 8;
   static_assert(kState * 4 <= NST * Geom::kStageBytes, "a saved state must fit its warp's ring");
   extern __shared__ __align__(1024) uint8_t smem[];
   griddep_wait();
   griddep_launch_dependents();
   if (smem_misaligned(smem, a.dev_status)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t unit = blockIdx.x;
+  const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int64_t unit = blockIdx.x / C;
   const int s = static_cast<int>(unit / a.num_kv_heads), g = static_cast<int>(unit % a.num_kv_heads);
   const int G = a.group, B = 1 << a.block_shift;
-  const int L = clamped_len(a, s, g == 0 && threadIdx.x == 0);
+  const int L = clamped_len(a, s, g == 0 && rank == 0 && threadIdx.x == 0);
   const int nblk = (L >> a.block_shift) + ((L & (B - 1)) ? 1 : 0);
   int count = sp.counts[unit];
   if (count < 0 || count > sp.keep) {
-    if (threadIdx.x == 0) flag(a.dev_status, 128u);  // PKV_DEV_ERR_SELECT
+    if (rank == 0 && threadIdx.x == 0) flag(a.dev_status, 128u);  // PKV_DEV_ERR_SELECT
     count = count < 0 ? 0 : sp.keep;
   }
   const int32_t* list = sp.selected + unit * sp.keep;
   const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
   const int tshift = a.block_shift - 4;  // log2 of tiles per block
   const int tiles = L > 0 ? count << tshift : 0;
-  const int cnt = tiles > warp ? (tiles - warp + NW - 1) / NW : 0;
+  const int W = C * NW, w0 = rank * NW + warp;  // this warp's tiles: w0, w0 + W, ...
+  const int cnt = tiles > w0 ? (tiles - w0 + W - 1) / W : 0;
 
   // Place of this warp's tile i.  A list entry counts when it is larger than
   // its predecessor and inside the sequence, so no token counts twice.
   auto place = [&](int i) {
     TilePlace p{-1, 0, 0};
     if (i >= cnt) return p;
-    const int t = i * NW + warp, e = t >> tshift;
+    const int t = i * W + w0, e = t >> tshift;
     const int b = __ldg(list + e), prev = e > 0 ? __ldg(list + e - 1) : -1;
     if (b <= prev || b < 0 || b >= nblk) {
       flag(a.dev_status, 128u);  // PKV_DEV_ERR_SELECT
@@ -88,9 +94,8 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
   WarpRing<D, NST, EB> ring{smem_u32(smem + static_cast<size_t>(warp) * NST * Geom::kStageBytes),
                             smem_u32(smem + static_cast<size_t>(NW) * NST * Geom::kStageBytes) + 8 * NST * warp};
   ring.init(lane);
-  // FP8: K and V scale of the tile in each stage (behind the barriers).
-  float2* stage_scale =
-      reinterpret_cast<float2*>(smem + static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 8)) + warp * NST;
+  // FP8: K and V scale of the tile in each stage.
+  float2* stage_scale = reinterpret_cast<float2*>(smem + kScalesAt) + warp * NST;
 
   // Lane j holds the place (and scales) of the warp's tile j of a chunk of 32.
   TilePlace cur = place(lane), nxt = place(32 + lane);
@@ -212,39 +217,73 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
     }
   }
   __syncthreads();
-  // Merge over the warps: M = max m_w, out = sum 2^(m_w - M) acc_w / sum 2^(m_w - M) l_w.
+  // Merge over the warps: M = max m_w, acc = sum 2^(m_w - M) acc_w, l likewise.
+  auto merged = [&](int n, int h, int d, auto load, float& M, float& o, float& l) {
+    M = kNegInf;
+    for (int w = 0; w < n; ++w) M = fmaxf(M, load(w, 8 * kRow + h));
+    const float mu = M == kNegInf ? 0.f : M;
+    o = l = 0.f;
+    for (int w = 0; w < n; ++w) {
+      const float c = exp2f(load(w, 8 * kRow + h) - mu);
+      o += load(w, h * kRow + d) * c;
+      l += load(w, 8 * kRow + 8 + h) * c;
+    }
+  };
+  auto of_warp = [&](int w, int i) {
+    return reinterpret_cast<const float*>(smem + static_cast<size_t>(w) * NST * Geom::kStageBytes)[i];
+  };
+  const int64_t row0 = (static_cast<int64_t>(s) * a.num_q_heads + g * G) * D;
+  if (C == 1) {
+    for (int e = threadIdx.x; e < G * D; e += NW * 32) {
+      float M, o, l;
+      merged(NW, e / D, e % D, of_warp, M, o, l);
+      store_out(a.out, row0 + e, l > 0.f ? o / l : 0.f, a.out_dtype);
+    }
+    return;
+  }
+  float* mine = reinterpret_cast<float*>(smem + kStateAt);
   for (int e = threadIdx.x; e < G * D; e += NW * 32) {
     const int h = e / D, d = e % D;
-    float M = kNegInf, o = 0.f, l = 0.f;
-    float m[NW];
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      m[w] = reinterpret_cast<const float*>(smem + static_cast<size_t>(w) * NST * Geom::kStageBytes)[8 * kRow + h];
-      M = fmaxf(M, m[w]);
+    float M, o, l;
+    merged(NW, h, d, of_warp, M, o, l);
+    mine[h * kRow + d] = o;
+    if (d == 0) {
+      mine[8 * kRow + h] = M;
+      mine[8 * kRow + 8 + h] = l;
     }
-    const float mu = M == kNegInf ? 0.f : M;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float* st = reinterpret_cast<const float*>(smem + static_cast<size_t>(w) * NST * Geom::kStageBytes);
-      const float c = exp2f(m[w] - mu);
-      o += st[h * kRow + d] * c;
-      l += st[8 * kRow + 8 + h] * c;
-    }
-    store_out(a.out, (static_cast<int64_t>(s) * a.num_q_heads + g * G) * D + e, l > 0.f ? o / l : 0.f, a.out_dtype);
   }
+  cluster_sync();
+  const uint32_t at_mine = smem_u32(mine);
+  auto of_cta = [&](int r, int i) { return cluster_load_float(cluster_map(at_mine + 4 * i, r)); };
+  for (int e = rank * NW * 32 + threadIdx.x; e < G * D; e += C * NW * 32) {
+    float M, o, l;
+    merged(C, e / D, e % D, of_cta, M, o, l);
+    store_out(a.out, row0 + e, l > 0.f ? o / l : 0.f, a.out_dtype);
+  }
+  cluster_sync();  // no CTA leaves while another reads its shared memory
 }
+
+// CTAs per unit: doubled while the batch fills at most half of the resident
+// CTAs (kSparsePerSm a SM) and a warp keeps at least kSparseLeast tiles.
+constexpr int kSparsePerSm = 2, kSparseLeast = 2, kSparseMaxCluster = 8;
 
 template <int D, bool BF16, bool FP8>
 cudaError_t launch_sparse_t(const DecodeArgs& a, const SparseArgs& sp, const CUtensorMap& tk, const CUtensorMap& tv,
                             cudaStream_t stream) {
   using Geom = TileGeom<D, FP8 ? 1 : 2>;
   constexpr int NW = kSparseWarps, NST = FP8 ? 4 : 3;
-  const size_t smem = static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 8 + (FP8 ? 8 : 0));
+  const size_t smem = static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 16) + (8 * (D + 4) + 16) * sizeof(float);
   auto kern = decode_sparse_kernel<D, BF16, FP8, NW, NST>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(a.num_seqs) * a.num_kv_heads), dim3(NW * 32), smem, stream, a, sp,
-                    tk, tv);
+  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+  const int64_t tiles = min((static_cast<int64_t>(a.max_context_len) + kTile - 1) / kTile,
+                            static_cast<int64_t>(sp.keep) << (a.block_shift - 4));
+  int C = 1;
+  while (C < kSparseMaxCluster && units * C * 2 <= kSparsePerSm * current_sm_count(152) &&
+         tiles >= 2 * C * NW * kSparseLeast)
+    C *= 2;
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(units * C)), dim3(NW * 32), smem, C, stream, a, sp, tk, tv);
 }
 
 }  // namespace

@@ -254,39 +254,46 @@ __device__ __forceinline__ int2 block_scan(int2 v, int2* warp_sums) {
   return before;
 }
 
-// One CTA per (sequence, KV head): scores of the blocks into shared memory
-// (order keys), the keep-th largest key by histograms over ever narrower
-// ranges (2048 bins each), then the chosen block numbers in order.
+// One cluster of C CTAs per (sequence, KV head), each CTA with a contiguous
+// share of the blocks: scores into its shared memory (order keys), the
+// keep-th largest key by histograms over ever narrower ranges (2048 bins
+// each; every CTA adds up all CTAs' counts through distributed shared memory
+// and comes to the same bin), then the chosen block numbers in order.
 template <int D, bool BF16, int GP>
 __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectArgs a) {
   constexpr int LPB = D / 16;    // lanes per block: 16 channels each
   constexpr int BPW = 32 / LPB;  // blocks per warp step
   constexpr int LEFT = GP > LPB ? GP / LPB : 1;
   extern __shared__ uint32_t keys[];
-  __shared__ int hist[kBins];
+  __shared__ __align__(16) int hist[2][kBins];  // the histogram of even and odd rounds
   __shared__ int2 warp_sums[kSelThreads / 32];
   __shared__ uint32_t warp_range[2][kSelThreads / 32];
-  __shared__ int found[2];  // the bin, and how many keys lie above it
+  __shared__ int2 shared_pair[2];  // what the other CTAs read: the range of keys; the counts of chosen ones
+  __shared__ int found[3];  // the bin, how many keys lie above it and in it
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t unit = blockIdx.x;
+  const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int64_t unit = blockIdx.x / C;
   const int s = static_cast<int>(unit / a.num_kv_heads), g = static_cast<int>(unit % a.num_kv_heads);
   const int cap = min(a.max_context_len, static_cast<int>(min(static_cast<int64_t>(a.max_blocks_per_seq) << a.block_shift,
                                                               static_cast<int64_t>(0x7fffffff))));
   int L = a.context_lens[s];
   if (L < 0 || L > cap) {
-    if (g == 0 && tid == 0) flag(a.dev_status, 8u);  // PKV_DEV_ERR_LENGTH
+    if (g == 0 && rank == 0 && tid == 0) flag(a.dev_status, 8u);  // PKV_DEV_ERR_LENGTH
     L = L < 0 ? 0 : cap;
   }
   const int n = (L >> a.block_shift) + ((L & ((1 << a.block_shift) - 1)) ? 1 : 0);
   const int count = min(n, a.keep);
   int32_t* out = a.selected + unit * a.keep;
-  if (tid == 0) a.counts[unit] = count;
-  if (n <= a.keep) {
-    for (int i = tid; i < a.keep; i += kSelThreads) out[i] = i < n ? i : -1;
+  if (rank == 0 && tid == 0) a.counts[unit] = count;
+  if (n <= a.keep) {  // the same for every CTA of the cluster
+    for (int i = rank * kSelThreads + tid; i < a.keep; i += C * kSelThreads) out[i] = i < n ? i : -1;
     return;
   }
+  // This CTA's blocks are [lo_b, hi_b), whole steps of 32; keys[] holds theirs.
+  const int share = ((n + C - 1) / C + 31) & ~31;
+  const int lo_b = min(n, rank * share), hi_b = min(n, lo_b + share);
 
   // Query codes of this lane's 16 channels: negative and positive parts, and the scale per head.
   const int ch = (lane % LPB) * 16;
@@ -334,10 +341,10 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
   const int first = a.first_blocks, last = n - a.last_blocks;  // blocks outside [first, last) are always taken
   const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
   uint32_t kmin = 0xffffffffu, kmax = 0u;
-  for (int b0 = warp * 32; b0 < n; b0 += kSelThreads) {
-    int phys = b0 + lane < n ? __ldg(tbl + b0 + lane) : -1;
+  for (int b0 = lo_b + warp * 32; b0 < hi_b; b0 += kSelThreads) {
+    int phys = b0 + lane < hi_b ? __ldg(tbl + b0 + lane) : -1;
     if (phys < 0 || phys >= a.num_blocks) {
-      if (b0 + lane < n) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK: the block is scored last
+      if (b0 + lane < hi_b) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK: the block is scored last
       phys = -1;
     }
     const float sc = phys >= 0 ? __ldg(a.summary_scale + static_cast<int64_t>(phys) * a.num_kv_heads + g) : 0.f;
@@ -377,9 +384,9 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
 #pragma unroll
       for (int o = 1; o < LPB; o <<= 1) best = fmaxf(best, __shfl_xor_sync(kFull, best, o));
       const int b = b0 + mine;
-      if (lane % LPB == 0 && b < n) {
+      if (lane % LPB == 0 && b < hi_b) {
         const uint32_t key = p >= 0 ? order_key(best) : 0u;
-        keys[b] = key;
+        keys[b - lo_b] = key;
         if (b >= first && b < last) {
           kmin = min(kmin, key);
           kmax = max(kmax, key);
@@ -399,6 +406,16 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     kmin = min(kmin, warp_range[0][w]);
     kmax = max(kmax, warp_range[1][w]);
   }
+  if (tid == 0) shared_pair[0] = make_int2(static_cast<int>(kmin), static_cast<int>(kmax));
+  for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
+  cluster_sync();
+  for (int r = 0; r < C; ++r) {
+    const int2 p = cluster_load_int2(cluster_map(smem_u32(&shared_pair[0]), r));
+    kmin = min(kmin, static_cast<uint32_t>(p.x));
+    kmax = max(kmax, static_cast<uint32_t>(p.y));
+  }
+  // This CTA's middle blocks, as indices of keys[].
+  const int mid0 = max(first, lo_b) - lo_b, mid1 = min(last, hi_b) - lo_b;
 
   // The threshold: `need` of the middle keys are taken.  Keys above `lo` are
   // taken whole, `ties` of those equal to it (lowest block first).
@@ -409,39 +426,49 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     const int bits = 32 - __clz(kmax - kmin);
     int shift = max(0, bits - 11);
     uint32_t width = 0xffffffffu;  // keys in [lo, lo + width] are still candidates
-    for (;;) {
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int b = first + tid; b < last; b += kSelThreads) {
+    for (int round = 0;; ++round) {
+      int* mine = hist[round & 1];  // zeroed one cluster barrier ago
+      for (int b = mid0 + tid; b < mid1; b += kSelThreads) {
         const uint32_t d = keys[b] - lo;
-        if (keys[b] >= lo && d <= width) atomicAdd(&hist[d >> shift], 1);
+        if (keys[b] >= lo && d <= width) atomicAdd(&mine[d >> shift], 1);
       }
-      __syncthreads();
-      // Thread t owns bins of descending value: 8t .. 8t + 7 counted from the top.
-      int own[8], sum = 0;
+      cluster_sync();
+      // The other buffer was last read before this barrier.
+      for (int i = tid; i < kBins; i += kSelThreads) hist[(round + 1) & 1][i] = 0;
+      // Thread t owns bins 8 (255 - t) .. + 7: descending with t.
+      int own[8] = {}, sum = 0;
+      const uint32_t at = smem_u32(mine + 8 * (kSelThreads - 1 - tid));
+      for (int r = 0; r < C; ++r) {
+        const uint32_t p = cluster_map(at, r);
+        const int4 x = cluster_load_int4(p), y = cluster_load_int4(p + 16);
+        own[0] += y.w;
+        own[1] += y.z;
+        own[2] += y.y;
+        own[3] += y.x;
+        own[4] += x.w;
+        own[5] += x.z;
+        own[6] += x.y;
+        own[7] += x.x;
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        own[i] = hist[kBins - 1 - (tid * 8 + i)];
-        sum += own[i];
-      }
+      for (int i = 0; i < 8; ++i) sum += own[i];
       int above = block_scan(make_int2(sum, 0), warp_sums).x;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (above < need && above + own[i] >= need) {
           found[0] = kBins - 1 - (tid * 8 + i);
           found[1] = above;
+          found[2] = own[i];
         }
         above += own[i];
       }
       __syncthreads();
-      const int bin = found[0];
-      const int in_bin = hist[bin];
+      const int bin = found[0], in_bin = found[2];
       need -= found[1];
       lo += static_cast<uint32_t>(bin) << shift;
       if (in_bin == need || shift == 0) break;
       width = (1u << shift) - 1;
       shift = max(0, shift - 11);
-      __syncthreads();
     }
     // Either every key of the last bin is taken, or the bin is a single key and `need` of them are.
     ties = need;
@@ -450,36 +477,54 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     lo = 0xffffffffu;  // no middle block: no key is above it, none of those equal is taken
   }
 
-  // Ordered output: thread t owns a run of consecutive blocks.
-  const int run = (n + kSelThreads - 1) / kSelThreads;
-  const int b1 = min(n, (tid + 1) * run);
+  // Ordered output: thread t owns a run of this CTA's consecutive blocks.
+  const int run = (hi_b - lo_b + kSelThreads - 1) / kSelThreads;
+  const int i1 = min(hi_b - lo_b, (tid + 1) * run);
   int2 mine = make_int2(0, 0);  // (taken for sure, equal to the threshold)
-  for (int b = tid * run; b < b1; ++b) {
-    if (b < first || b >= last || keys[b] > lo)
+  for (int i = tid * run; i < i1; ++i) {
+    if (i < mid0 || i >= mid1 || keys[i] > lo)
       ++mine.x;
-    else if (keys[b] == lo)
+    else if (keys[i] == lo)
       ++mine.y;
   }
   __syncthreads();  // warp_sums is reused
   int2 before = block_scan(mine, warp_sums);
-  for (int b = tid * run; b < b1; ++b) {
-    const bool sure = b < first || b >= last || keys[b] > lo;
-    const bool tie = !sure && keys[b] == lo;
-    if (sure || (tie && before.y < ties)) out[before.x + min(before.y, ties)] = b;
+  if (tid == kSelThreads - 1) shared_pair[1] = make_int2(before.x + mine.x, before.y + mine.y);
+  cluster_sync();
+  for (int r = 0; r < rank; ++r) {
+    const int2 p = cluster_load_int2(cluster_map(smem_u32(&shared_pair[1]), r));
+    before.x += p.x;
+    before.y += p.y;
+  }
+  for (int i = tid * run; i < i1; ++i) {
+    const bool sure = i < mid0 || i >= mid1 || keys[i] > lo;
+    const bool tie = !sure && keys[i] == lo;
+    if (sure || (tie && before.y < ties)) out[before.x + min(before.y, ties)] = lo_b + i;
     before.x += sure;
     before.y += tie;
   }
+  cluster_sync();  // no CTA leaves while another reads its shared memory
 }
+
+// CTAs per (sequence, KV head): doubled while the batch has fewer than
+// kSelTarget CTAs a SM and a CTA keeps at least kSelLeast blocks, and until
+// its keys fit kSelKeys.
+constexpr int kSelTarget = 3, kSelLeast = 128, kSelKeys = 1 << 15, kSelMaxCluster = 8;
 
 template <int D, bool BF16, int GP>
 cudaError_t launch_select_t(const SelectArgs& a, cudaStream_t stream) {
   auto kern = select_blocks_kernel<D, BF16, GP>;
   const int64_t cap = min(static_cast<int64_t>(a.max_blocks_per_seq),
                           (static_cast<int64_t>(a.max_context_len) + (1 << a.block_shift) - 1) >> a.block_shift);
-  const size_t smem = static_cast<size_t>(max(cap, static_cast<int64_t>(1))) * sizeof(uint32_t);
+  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+  int C = 1;
+  while (C < kSelMaxCluster &&
+         ((units * C < kSelTarget * current_sm_count(152) && cap >= 2 * C * kSelLeast) || cap > C * static_cast<int64_t>(kSelKeys)))
+    C *= 2;
+  const size_t smem = (static_cast<size_t>((cap + C - 1) / C) + 32) * sizeof(uint32_t);
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(a.num_seqs) * a.num_kv_heads), dim3(kSelThreads), smem, stream, a);
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(units * C)), dim3(kSelThreads), smem, C, stream, a);
 }
 
 template <int D, bool BF16>
