@@ -554,7 +554,7 @@ pkv_status pkv_summarize_blocks_fp8(void* summary, float* summary_scale, const v
  *   first_blocks >= 0, last_blocks >= 1, their sum <= keep <= 2^20.
  * Lengths are clamped and flagged as in pkv_decode_attention; a table entry
  * outside the pool sets PKV_DEV_ERR_BLOCK and is taken last.  head_dim 64 or
- * 128, 1 <= group <= 8, block sizes 16, 32 and 64, at most 2^18 blocks a
+ * 128, 1 <= group <= 8, block sizes 16, 32 and 64, at most 49152 blocks a
  * sequence (min of max_context_len's and max_blocks_per_seq).
  */
 pkv_status pkv_select_blocks(int32_t* selected, int32_t* counts, const void* q, const void* summary,

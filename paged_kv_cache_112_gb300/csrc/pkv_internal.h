@@ -307,7 +307,7 @@ cudaError_t launch_decode_reduce_balanced(const DecodeArgs& a, int head_dim, cud
 cudaError_t launch_norm_rope_write(const NormRopeArgs& a, int head_dim, bool bf16, bool fp8, cudaStream_t stream);
 cudaError_t launch_summarize_blocks(const SummarizeArgs& a, int head_dim, bool bf16, bool fp8, cudaStream_t stream);
 // Largest number of blocks a sequence may have for launch_select_blocks.
-constexpr int kSelectMaxBlocks = 1 << 18;
+constexpr int kSelectMaxBlocks = 49152;
 // Bounds of one call of the sparse operators: list length, sequences x KV heads.
 constexpr int kMaxKeep = 1 << 20;
 constexpr int64_t kMaxUnits = 1 << 24;

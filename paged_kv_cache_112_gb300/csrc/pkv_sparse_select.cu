@@ -227,10 +227,10 @@ __device__ __forceinline__ void reduce_heads(int (&acc)[GP], int lane, int& firs
   }
 }
 
-constexpr int kSelThreads = 256;
 constexpr int kBins = 2048;
 
 // Exclusive prefix sums of a pair of counts over the CTA's threads.
+template <int NT>
 __device__ __forceinline__ int2 block_scan(int2 v, int2* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int2 s = v;
@@ -246,7 +246,7 @@ __device__ __forceinline__ int2 block_scan(int2 v, int2* warp_sums) {
   __syncthreads();
   int2 before = make_int2(s.x - v.x, s.y - v.y);
 #pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w)
+  for (int w = 0; w < NT / 32; ++w)
     if (w < warp) {
       before.x += warp_sums[w].x;
       before.y += warp_sums[w].y;
@@ -254,21 +254,27 @@ __device__ __forceinline__ int2 block_scan(int2 v, int2* warp_sums) {
   return before;
 }
 
-// One cluster of C CTAs per (sequence, KV head), each CTA with a contiguous
-// share of the blocks: scores into its shared memory (order keys), the
-// keep-th largest key by histograms over ever narrower ranges (2048 bins
-// each; every CTA adds up all CTAs' counts through distributed shared memory
-// and comes to the same bin), then the chosen block numbers in order.
-template <int D, bool BF16, int GP>
-__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectArgs a) {
+// One cluster of C CTAs per (sequence, KV head).  Every CTA scores a contiguous
+// share of the blocks and stores the order keys into the first CTA's shared
+// memory; then the first CTA alone finds the keep-th largest key by
+// histograms over ever narrower ranges (2048 bins each) and writes the chosen
+// block numbers in order.  (Histograms kept by every CTA and added up through
+// distributed shared memory took 25 us of the 79 us that 8 sequences of up to
+// 8192 blocks needed: 64 KB of remote loads a CTA and round.)
+template <int D, bool BF16, int GP, int NT>
+__global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a) {
   constexpr int LPB = D / 16;    // lanes per block: 16 channels each
   constexpr int BPW = 32 / LPB;  // blocks per warp step
-  constexpr int LEFT = GP > LPB ? GP / LPB : 1;
+  constexpr int LEFT = GP > LPB ? GP / LPB : 1;  // heads whose sums a lane ends up with
+  constexpr int NWARP = NT / 32;
+  constexpr int BATCH = GP > 4 ? 4 : LPB;  // warp steps whose summaries are loaded together
+  constexpr int BPT = kBins / NT;  // bins per thread
   extern __shared__ uint32_t keys[];
-  __shared__ __align__(16) int hist[2][kBins];  // the histogram of even and odd rounds
-  __shared__ int2 warp_sums[kSelThreads / 32];
-  __shared__ uint32_t warp_range[2][kSelThreads / 32];
-  __shared__ int2 shared_pair[2];  // what the other CTAs read: the range of keys; the counts of chosen ones
+  __shared__ __align__(16) int hist[kBins];
+  __shared__ __align__(16) uint32_t q_codes[2][GP][D / 4];  // negative and positive parts
+  __shared__ int q_exp[GP];
+  __shared__ int2 warp_sums[NWARP];
+  __shared__ uint32_t warp_range[2][NWARP];
   __shared__ int found[3];  // the bin, how many keys lie above it and in it
   griddep_wait();
   griddep_launch_dependents();
@@ -276,9 +282,38 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int64_t unit = blockIdx.x / C;
   const int s = static_cast<int>(unit / a.num_kv_heads), g = static_cast<int>(unit % a.num_kv_heads);
-  const int cap = min(a.max_context_len, static_cast<int>(min(static_cast<int64_t>(a.max_blocks_per_seq) << a.block_shift,
-                                                              static_cast<int64_t>(0x7fffffff))));
   int L = a.context_lens[s];
+
+  // Query codes, a head per warp: 4 channels a lane (D = 64: the lower half-warp).
+  for (int h = warp; h < GP; h += NWARP) {
+    const bool live = h < a.group && lane < D / 4;
+    const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(
+                               a.q + (static_cast<int64_t>(s) * a.num_q_heads + g * a.group + h) * D) + lane)
+                         : make_uint2(0u, 0u);
+    const float2 f0 = widen2<BF16>(w.x), f1 = widen2<BF16>(w.y);
+    const float most = BF16 ? __uint_as_float(0x7f7f0000u) : 65504.f;
+    float x[4] = {finite_bound(f0.x, most), finite_bound(f0.y, most), finite_bound(f1.x, most),
+                  finite_bound(f1.y, most)};
+    float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    // Positive floats order as their bits.
+    top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
+    const int e = top > 0.f ? bound_exponent(top, 0.f) : -126;
+    const float inv = exp2_int(-e);
+    uint32_t neg = 0, pos = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = __float2int_rn(x[j] * inv);
+      neg |= (static_cast<uint32_t>(min(c, 0)) & 0xffu) << (8 * j);
+      pos |= static_cast<uint32_t>(max(c, 0)) << (8 * j);
+    }
+    if (lane < D / 4) {
+      q_codes[0][h][lane] = neg;
+      q_codes[1][h][lane] = pos;
+    }
+    if (lane == 0) q_exp[h] = e;
+  }
+
+  const int cap = min(a.max_context_len, a.max_blocks_per_seq << a.block_shift);
   if (L < 0 || L > cap) {
     if (g == 0 && rank == 0 && tid == 0) flag(a.dev_status, 8u);  // PKV_DEV_ERR_LENGTH
     L = L < 0 ? 0 : cap;
@@ -288,111 +323,105 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
   int32_t* out = a.selected + unit * a.keep;
   if (rank == 0 && tid == 0) a.counts[unit] = count;
   if (n <= a.keep) {  // the same for every CTA of the cluster
-    for (int i = rank * kSelThreads + tid; i < a.keep; i += C * kSelThreads) out[i] = i < n ? i : -1;
+    for (int i = rank * NT + tid; i < a.keep; i += C * NT) out[i] = i < n ? i : -1;
     return;
   }
-  // This CTA's blocks are [lo_b, hi_b), whole steps of 32; keys[] holds theirs.
+  // This CTA scores blocks [lo_b, hi_b), whole steps of 32; the first CTA's keys[] receives all keys.
   const int share = ((n + C - 1) / C + 31) & ~31;
   const int lo_b = min(n, rank * share), hi_b = min(n, lo_b + share);
+  const int first = a.first_blocks, last = n - a.last_blocks;  // blocks outside [first, last) are always taken
 
-  // Query codes of this lane's 16 channels: negative and positive parts, and the scale per head.
-  const int ch = (lane % LPB) * 16;
-  int qn[GP][4], qp[GP][4], qe[GP], emax = -126;
+  // A warp takes 32 consecutive blocks at a time; lane j holds block j's
+  // table entry, fetched one chunk ahead, and its scale.
+  const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
+  auto entry = [&](int b0) { return b0 + lane < hi_b ? __ldg(tbl + b0 + lane) : -1; };
+  int b0 = lo_b + warp * 32;
+  int phys = entry(b0);
+  __syncthreads();  // q_codes
+
+  // This lane's 16 channels of every head.  All heads' scales times 2^-(22 +
+  // the largest exponent): the order stays, and integer * scale * summary
+  // scale neither overflows nor, for the head with that exponent, loses a bit
+  // (2^-22 * 2^-126 is a subnormal float32).
+  int qn[GP][4], qp[GP][4], emax = -126;
 #pragma unroll
   for (int h = 0; h < GP; ++h) {
-    float x[16], top = 0.f;
-    const bool live = h < a.group;
-    const uint16_t* row = a.q + (static_cast<int64_t>(s) * a.num_q_heads + g * a.group + (live ? h : 0)) * D + ch;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = widen2<BF16>(live ? __ldg(reinterpret_cast<const uint32_t*>(row) + i) : 0u);
-      const float most = BF16 ? __uint_as_float(0x7f7f0000u) : 65504.f;
-      x[2 * i] = finite_bound(f.x, most);
-      x[2 * i + 1] = finite_bound(f.y, most);
-      top = fmaxf(top, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
-    }
-#pragma unroll
-    for (int o = 1; o < LPB; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    qe[h] = top > 0.f ? bound_exponent(top, 0.f) : -126;
-    emax = max(emax, qe[h]);
-    const float inv = exp2_int(-qe[h]);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      qn[h][w] = qp[h][w] = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = __float2int_rn(x[4 * w + j] * inv);
-        if (c < 0)
-          qn[h][w] |= (c & 0xff) << (8 * j);
-        else
-          qp[h][w] |= c << (8 * j);
-      }
-    }
+    const int4 x = *reinterpret_cast<const int4*>(&q_codes[0][h][(lane % LPB) * 4]);
+    const int4 y = *reinterpret_cast<const int4*>(&q_codes[1][h][(lane % LPB) * 4]);
+    qn[h][0] = x.x; qn[h][1] = x.y; qn[h][2] = x.z; qn[h][3] = x.w;
+    qp[h][0] = y.x; qp[h][1] = y.y; qp[h][2] = y.z; qp[h][3] = y.w;
+    emax = max(emax, q_exp[h]);
   }
-
-  // All heads' scales times 2^-(22 + the largest exponent): the order stays,
-  // and integer * scale * summary scale neither overflows nor, for the head
-  // with that exponent, loses a bit (2^-22 * 2^-126 is a subnormal float32).
-  float qs[GP];
+  // The heads whose sums this lane gets from reduce_heads, and their scales (-1: padding).
+  int h0;
+  {
+    int none[GP] = {};
+    reduce_heads<GP, LPB>(none, lane, h0);
+  }
+  float my_scale[LEFT];
 #pragma unroll
-  for (int h = 0; h < GP; ++h) qs[h] = exp2_int(max(qe[h] - emax - 22, -126));
+  for (int i = 0; i < LEFT; ++i)
+    my_scale[i] = h0 + i < a.group ? exp2_int(max(q_exp[h0 + i] - emax - 22, -126)) : -1.f;
 
-  // Scores.  A warp takes 32 consecutive blocks at a time (lane j: block j's table entry and scale).
-  const int first = a.first_blocks, last = n - a.last_blocks;  // blocks outside [first, last) are always taken
-  const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
-  uint32_t kmin = 0xffffffffu, kmax = 0u;
-  for (int b0 = lo_b + warp * 32; b0 < hi_b; b0 += kSelThreads) {
-    int phys = b0 + lane < hi_b ? __ldg(tbl + b0 + lane) : -1;
+  const uint32_t keys_at = cluster_map(smem_u32(keys), 0);
+  for (; b0 < hi_b; b0 += NT) {
+    const int next = entry(b0 + NT);
     if (phys < 0 || phys >= a.num_blocks) {
       if (b0 + lane < hi_b) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK: the block is scored last
       phys = -1;
     }
-    const float sc = phys >= 0 ? __ldg(a.summary_scale + static_cast<int64_t>(phys) * a.num_kv_heads + g) : 0.f;
-#pragma unroll 4
-    for (int j = 0; j < LPB; ++j) {
-      const int mine = j * BPW + lane / LPB;  // which of the 32 blocks
-      const int p = __shfl_sync(kFull, phys, mine);
-      const float psc = __shfl_sync(kFull, sc, mine);
-      const int8_t* sum = a.summary + ((static_cast<int64_t>(max(p, 0)) * a.num_kv_heads + g) * 2) * D + ch;
-      const uint4 lo = *reinterpret_cast<const uint4*>(sum), hi = *reinterpret_cast<const uint4*>(sum + D);
-      const int lw[4] = {static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z),
-                         static_cast<int>(lo.w)};
-      const int hw[4] = {static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z),
-                         static_cast<int>(hi.w)};
-      int acc[GP];
+    const float sc = phys >= 0 ? __ldg(a.summary_scale + static_cast<int64_t>(phys) * a.num_kv_heads + g) : -1.f;
 #pragma unroll
-      for (int h = 0; h < GP; ++h) {
-        acc[h] = 0;
+    for (int j0 = 0; j0 < LPB; j0 += BATCH) {
+      if (b0 + j0 * BPW >= hi_b) break;
+      uint4 lo[BATCH], hi[BATCH];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) acc[h] = __dp4a(hw[w], qp[h][w], __dp4a(lw[w], qn[h][w], acc[h]));
-      }
-      int h0;
-      reduce_heads<GP, LPB>(acc, lane, h0);
-      float best = kNegInf;
-#pragma unroll
-      for (int i = 0; i < LEFT; ++i) {
-        float f = 0.f;
-        bool live = false;
-#pragma unroll
-        for (int h = 0; h < GP; ++h)
-          if (h == h0 + i && h < a.group) {
-            f = qs[h];
-            live = true;
-          }
-        if (live) best = fmaxf(best, static_cast<float>(acc[i]) * f * psc);
+      for (int j = 0; j < BATCH; ++j) {
+        const int p = max(__shfl_sync(kFull, phys, (j0 + j) * BPW + lane / LPB), 0);
+        const uint4* sum = reinterpret_cast<const uint4*>(
+            a.summary + (static_cast<int64_t>(p) * a.num_kv_heads + g) * (2 * D) + (lane % LPB) * 16);
+        lo[j] = __ldg(sum);
+        hi[j] = __ldg(sum + D / 16);
       }
 #pragma unroll
-      for (int o = 1; o < LPB; o <<= 1) best = fmaxf(best, __shfl_xor_sync(kFull, best, o));
-      const int b = b0 + mine;
-      if (lane % LPB == 0 && b < hi_b) {
-        const uint32_t key = p >= 0 ? order_key(best) : 0u;
-        keys[b - lo_b] = key;
-        if (b >= first && b < last) {
-          kmin = min(kmin, key);
-          kmax = max(kmax, key);
+      for (int j = 0; j < BATCH; ++j) {
+        const int lw[4] = {static_cast<int>(lo[j].x), static_cast<int>(lo[j].y), static_cast<int>(lo[j].z),
+                           static_cast<int>(lo[j].w)};
+        const int hw[4] = {static_cast<int>(hi[j].x), static_cast<int>(hi[j].y), static_cast<int>(hi[j].z),
+                           static_cast<int>(hi[j].w)};
+        int acc[GP];
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          acc[h] = 0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) acc[h] = __dp4a(hw[w], qp[h][w], __dp4a(lw[w], qn[h][w], acc[h]));
         }
+        int from;
+        reduce_heads<GP, LPB>(acc, lane, from);
+        const int mine = (j0 + j) * BPW + lane / LPB;  // which of the 32 blocks
+        const float psc = __shfl_sync(kFull, sc, mine);
+        float best = kNegInf;
+#pragma unroll
+        for (int i = 0; i < LEFT; ++i)
+          if (my_scale[i] >= 0.f) best = fmaxf(best, static_cast<float>(acc[i]) * my_scale[i] * psc);
+        // Lanes with the same heads differ in the low bits of the lane, so only the others exchange.
+#pragma unroll
+        for (int o = LPB / 2; o >= 1 && o * GP >= LPB; o >>= 1)
+          best = fmaxf(best, __shfl_xor_sync(kFull, best, o));
+        const int b = b0 + mine;
+        if (lane % LPB == 0 && b < hi_b) cluster_store_u32(keys_at + 4 * b, psc >= 0.f ? order_key(best) : 0u);
       }
     }
+    phys = next;
+  }
+  cluster_sync();  // every key has arrived
+  if (rank != 0) return;
+
+  // The range of the middle keys.
+  uint32_t kmin = 0xffffffffu, kmax = 0u;
+  for (int b = first + tid; b < last; b += NT) {
+    kmin = min(kmin, keys[b]);
+    kmax = max(kmax, keys[b]);
   }
   kmin = __reduce_min_sync(kFull, kmin);
   kmax = __reduce_max_sync(kFull, kmax);
@@ -400,22 +429,13 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     warp_range[0][warp] = kmin;
     warp_range[1][warp] = kmax;
   }
+  for (int i = tid; i < kBins; i += NT) hist[i] = 0;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) {
+  for (int w = 0; w < NWARP; ++w) {
     kmin = min(kmin, warp_range[0][w]);
     kmax = max(kmax, warp_range[1][w]);
   }
-  if (tid == 0) shared_pair[0] = make_int2(static_cast<int>(kmin), static_cast<int>(kmax));
-  for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
-  cluster_sync();
-  for (int r = 0; r < C; ++r) {
-    const int2 p = cluster_load_int2(cluster_map(smem_u32(&shared_pair[0]), r));
-    kmin = min(kmin, static_cast<uint32_t>(p.x));
-    kmax = max(kmax, static_cast<uint32_t>(p.y));
-  }
-  // This CTA's middle blocks, as indices of keys[].
-  const int mid0 = max(first, lo_b) - lo_b, mid1 = min(last, hi_b) - lo_b;
 
   // The threshold: `need` of the middle keys are taken.  Keys above `lo` are
   // taken whole, `ties` of those equal to it (lowest block first).
@@ -426,37 +446,31 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     const int bits = 32 - __clz(kmax - kmin);
     int shift = max(0, bits - 11);
     uint32_t width = 0xffffffffu;  // keys in [lo, lo + width] are still candidates
-    for (int round = 0;; ++round) {
-      int* mine = hist[round & 1];  // zeroed one cluster barrier ago
-      for (int b = mid0 + tid; b < mid1; b += kSelThreads) {
-        const uint32_t d = keys[b] - lo;
-        if (keys[b] >= lo && d <= width) atomicAdd(&mine[d >> shift], 1);
+    for (;;) {
+      for (int b = first + tid; b < last; b += NT) {
+        const uint32_t k = keys[b], d = k - lo;
+        if (k >= lo && d <= width) atomicAdd(&hist[d >> shift], 1);
       }
-      cluster_sync();
-      // The other buffer was last read before this barrier.
-      for (int i = tid; i < kBins; i += kSelThreads) hist[(round + 1) & 1][i] = 0;
-      // Thread t owns bins 8 (255 - t) .. + 7: descending with t.
-      int own[8] = {}, sum = 0;
-      const uint32_t at = smem_u32(mine + 8 * (kSelThreads - 1 - tid));
-      for (int r = 0; r < C; ++r) {
-        const uint32_t p = cluster_map(at, r);
-        const int4 x = cluster_load_int4(p), y = cluster_load_int4(p + 16);
-        own[0] += y.w;
-        own[1] += y.z;
-        own[2] += y.y;
-        own[3] += y.x;
-        own[4] += x.w;
-        own[5] += x.z;
-        own[6] += x.y;
-        own[7] += x.x;
+      __syncthreads();
+      // Thread t owns BPT bins, descending with t.
+      int own[BPT], sum = 0;
+      int* at = hist + BPT * (NT - 1 - tid);
+#pragma unroll
+      for (int i = 0; i < BPT; i += 4) {
+        const int4 x = *reinterpret_cast<const int4*>(at + i);
+        own[BPT - 1 - i] = x.x;
+        own[BPT - 2 - i] = x.y;
+        own[BPT - 3 - i] = x.z;
+        own[BPT - 4 - i] = x.w;
+        *reinterpret_cast<int4*>(at + i) = make_int4(0, 0, 0, 0);  // for the next round
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += own[i];
-      int above = block_scan(make_int2(sum, 0), warp_sums).x;
+      for (int i = 0; i < BPT; ++i) sum += own[i];
+      int above = block_scan<NT>(make_int2(sum, 0), warp_sums).x;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < BPT; ++i) {
         if (above < need && above + own[i] >= need) {
-          found[0] = kBins - 1 - (tid * 8 + i);
+          found[0] = kBins - 1 - (tid * BPT + i);
           found[1] = above;
           found[2] = own[i];
         }
@@ -477,51 +491,42 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     lo = 0xffffffffu;  // no middle block: no key is above it, none of those equal is taken
   }
 
-  // Ordered output: thread t owns a run of this CTA's consecutive blocks.
-  const int run = (hi_b - lo_b + kSelThreads - 1) / kSelThreads;
-  const int i1 = min(hi_b - lo_b, (tid + 1) * run);
+  // Ordered output: thread t owns a run of consecutive blocks (odd, so that the lanes' keys lie in different banks).
+  const int run = ((n + NT - 1) / NT) | 1;
+  const int b1 = min(n, (tid + 1) * run);
   int2 mine = make_int2(0, 0);  // (taken for sure, equal to the threshold)
-  for (int i = tid * run; i < i1; ++i) {
-    if (i < mid0 || i >= mid1 || keys[i] > lo)
+  for (int b = tid * run; b < b1; ++b) {
+    if (b < first || b >= last || keys[b] > lo)
       ++mine.x;
-    else if (keys[i] == lo)
+    else if (keys[b] == lo)
       ++mine.y;
   }
   __syncthreads();  // warp_sums is reused
-  int2 before = block_scan(mine, warp_sums);
-  if (tid == kSelThreads - 1) shared_pair[1] = make_int2(before.x + mine.x, before.y + mine.y);
-  cluster_sync();
-  for (int r = 0; r < rank; ++r) {
-    const int2 p = cluster_load_int2(cluster_map(smem_u32(&shared_pair[1]), r));
-    before.x += p.x;
-    before.y += p.y;
-  }
-  for (int i = tid * run; i < i1; ++i) {
-    const bool sure = i < mid0 || i >= mid1 || keys[i] > lo;
-    const bool tie = !sure && keys[i] == lo;
-    if (sure || (tie && before.y < ties)) out[before.x + min(before.y, ties)] = lo_b + i;
+  int2 before = block_scan<NT>(mine, warp_sums);
+  for (int b = tid * run; b < b1; ++b) {
+    const bool sure = b < first || b >= last || keys[b] > lo;
+    const bool tie = !sure && keys[b] == lo;
+    if (sure || (tie && before.y < ties)) out[before.x + min(before.y, ties)] = b;
     before.x += sure;
     before.y += tie;
   }
-  cluster_sync();  // no CTA leaves while another reads its shared memory
 }
 
 // CTAs per (sequence, KV head): doubled while the batch has fewer than
-// kSelTarget CTAs a SM and a CTA keeps at least kSelLeast blocks, and until
-// its keys fit kSelKeys.
-constexpr int kSelTarget = 3, kSelLeast = 128, kSelKeys = 1 << 15, kSelMaxCluster = 8;
+// kSelTarget CTAs a SM and a CTA keeps at least kSelLeast blocks.
+constexpr int kSelTarget = 4, kSelLeast = 128, kSelMaxCluster = 8;
+
+constexpr int kSelThreads = 128;
 
 template <int D, bool BF16, int GP>
 cudaError_t launch_select_t(const SelectArgs& a, cudaStream_t stream) {
-  auto kern = select_blocks_kernel<D, BF16, GP>;
+  auto kern = select_blocks_kernel<D, BF16, GP, kSelThreads>;
   const int64_t cap = min(static_cast<int64_t>(a.max_blocks_per_seq),
                           (static_cast<int64_t>(a.max_context_len) + (1 << a.block_shift) - 1) >> a.block_shift);
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   int C = 1;
-  while (C < kSelMaxCluster &&
-         ((units * C < kSelTarget * current_sm_count(152) && cap >= 2 * C * kSelLeast) || cap > C * static_cast<int64_t>(kSelKeys)))
-    C *= 2;
-  const size_t smem = (static_cast<size_t>((cap + C - 1) / C) + 32) * sizeof(uint32_t);
+  while (C < kSelMaxCluster && units * C < kSelTarget * current_sm_count(152) && cap >= 2 * C * kSelLeast) C *= 2;
+  const size_t smem = static_cast<size_t>(max(cap, static_cast<int64_t>(1))) * sizeof(uint32_t);
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(units * C)), dim3(kSelThreads), smem, C, stream, a);
