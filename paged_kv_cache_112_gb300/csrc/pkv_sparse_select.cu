@@ -9,7 +9,7 @@
 //     score_h(b) = sum_d max(q_d lo_d, q_d hi_d)
 // for query head h; q is rounded to int8 steps of a power of two of its own,
 // so the sum is an integer, sum_d q_d^- lo_d + q_d^+ hi_d with q^- = min(q, 0)
-// and q^+ = max(q, 0): two dp4a dot products, below 2^22 in magnitude and
+// and q^+ = max(q, 0): two integer dot products, below 2^22 in magnitude and
 // free of any summation order.  A block's score is the largest over the
 // group's heads; the best ones are taken, equal scores by the lowest block.
 #include "pkv_device.cuh"
@@ -199,32 +199,17 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// The integer dot products of GP heads, acc[h], summed over the LPB lanes of
-// a block: halves of the heads are exchanged while more than one is left, so
-// GP + log2 shuffles do instead of GP * log2.  Afterwards this lane holds the
-// sums of heads first .. first + left - 1.
-template <int GP, int LPB>
-__device__ __forceinline__ void reduce_heads(int (&acc)[GP], int lane, int& first) {
-  first = 0;
-  int left = GP;
-#pragma unroll
-  for (int o = LPB / 2; o >= 1; o >>= 1) {
-    if (left > 1) {
-      const int half = left / 2;
-      const bool high = lane & o;
-#pragma unroll
-      for (int i = 0; i < GP / 2; ++i)
-        if (i < half) {
-          const int send = high ? acc[i] : acc[i + half];
-          const int keep = high ? acc[i + half] : acc[i];
-          acc[i] = keep + __shfl_xor_sync(kFull, send, o);
-        }
-      first += high ? half : 0;
-      left = half;
-    } else {
-      acc[0] += __shfl_xor_sync(kFull, acc[0], o);
-    }
-  }
+// 16 x 8 integer products over 32 channels: c += a b.  (The integer tensor
+// path of this GPU is slow -- 115 of these a microsecond and SM, measured --
+// but eight of them still score 16 blocks for 8 heads in less time than their
+// 4 KB take from memory, and leave the issue slots free; with dp4a the same
+// loop was issue-bound at 20 instructions a block.)
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 constexpr int kBins = 2048;
@@ -261,18 +246,22 @@ __device__ __forceinline__ int2 block_scan(int2 v, int2* warp_sums) {
 // block numbers in order.  (Histograms kept by every CTA and added up through
 // distributed shared memory took 25 us of the 79 us that 8 sequences of up to
 // 8192 blocks needed: 64 KB of remote loads a CTA and round.)
-template <int D, bool BF16, int GP, int NT>
+//
+// Scoring: a warp takes 16 blocks at a time as the rows of an m16n8k32 product
+// whose columns are the group's heads.  Lane (gr = lane / 4, tq = lane % 4)
+// needs rows gr and gr + 8; since any order of the channels will do as long as
+// q has the same, it reads 16-byte chunks 4x + tq of a bound straight from
+// global memory and uses words 2i, 2i + 1 of chunk x in k-step 2x + i.  The
+// next 16 blocks' summaries are loaded before the current ones are used.
+template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a) {
-  constexpr int LPB = D / 16;    // lanes per block: 16 channels each
-  constexpr int BPW = 32 / LPB;  // blocks per warp step
-  constexpr int LEFT = GP > LPB ? GP / LPB : 1;  // heads whose sums a lane ends up with
+  constexpr int X = D / 64;      // 16-byte chunks of one bound per lane and row
   constexpr int NWARP = NT / 32;
-  constexpr int BATCH = GP > 4 ? 4 : LPB;  // warp steps whose summaries are loaded together
   constexpr int BPT = kBins / NT;  // bins per thread
   extern __shared__ uint32_t keys[];
   __shared__ __align__(16) int hist[kBins];
-  __shared__ __align__(16) uint32_t q_codes[2][GP][D / 4];  // negative and positive parts
-  __shared__ int q_exp[GP];
+  __shared__ __align__(16) uint32_t q_codes[2][8][D / 4];  // negative and positive parts; heads past the group are 0
+  __shared__ int q_exp[8];
   __shared__ int2 warp_sums[NWARP];
   __shared__ uint32_t warp_range[2][NWARP];
   __shared__ int found[3];  // the bin, how many keys lie above it and in it
@@ -285,7 +274,7 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a) {
   int L = a.context_lens[s];
 
   // Query codes, a head per warp: 4 channels a lane (D = 64: the lower half-warp).
-  for (int h = warp; h < GP; h += NWARP) {
+  for (int h = warp; h < 8; h += NWARP) {
     const bool live = h < a.group && lane < D / 4;
     const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(
                                a.q + (static_cast<int64_t>(s) * a.num_q_heads + g * a.group + h) * D) + lane)
@@ -332,87 +321,106 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a) {
   const int first = a.first_blocks, last = n - a.last_blocks;  // blocks outside [first, last) are always taken
 
   // A warp takes 32 consecutive blocks at a time; lane j holds block j's
-  // table entry, fetched one chunk ahead, and its scale.
+  // table entry, fetched two chunks ahead, and its scale, one chunk ahead.
   const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
-  auto entry = [&](int b0) { return b0 + lane < hi_b ? __ldg(tbl + b0 + lane) : -1; };
+  auto entry = [&](int b) {
+    if (b + lane >= hi_b) return -1;
+    const int p = __ldg(tbl + b + lane);
+    return p;
+  };
+  auto checked = [&](int p, int b) {  // PKV_DEV_ERR_BLOCK: the block is scored last
+    if (p >= 0 && p < a.num_blocks) return p;
+    if (b + lane < hi_b) flag(a.dev_status, 4u);
+    return -1;
+  };
+  auto scale_of = [&](int p) {
+    return p >= 0 ? __ldg(a.summary_scale + static_cast<int64_t>(p) * a.num_kv_heads + g) : -1.f;
+  };
+  const int gr = lane >> 2, tq = lane & 3;
+  struct Group {
+    uint4 lo[2][X], hi[2][X];  // [row gr, gr + 8]
+  };
+  auto load = [&](Group& u, int p, int half) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int block = max(__shfl_sync(kFull, p, 16 * half + gr + 8 * r), 0);
+      const uint4* src = reinterpret_cast<const uint4*>(
+                             a.summary + (static_cast<int64_t>(block) * a.num_kv_heads + g) * (2 * D)) + tq;
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        u.lo[r][x] = __ldg(src + 4 * x);
+        u.hi[r][x] = __ldg(src + D / 16 + 4 * x);
+      }
+    }
+  };
   int b0 = lo_b + warp * 32;
-  int phys = entry(b0);
+  int phys = entry(b0), ahead = entry(b0 + NT);
+  phys = checked(phys, b0);
+  float sc = scale_of(phys);
+  Group even, odd;
+  load(even, phys, 0);
   __syncthreads();  // q_codes
 
-  // This lane's 16 channels of every head.  All heads' scales times 2^-(22 +
-  // the largest exponent): the order stays, and integer * scale * summary
-  // scale neither overflows nor, for the head with that exponent, loses a bit
-  // (2^-22 * 2^-126 is a subnormal float32).
-  int qn[GP][4], qp[GP][4], emax = -126;
+  // Query fragments: this lane's words of head gr.  All heads' scales times
+  // 2^-(22 + the largest exponent): the order stays, and integer * scale *
+  // summary scale neither overflows nor, for the head with that exponent,
+  // loses a bit (2^-22 * 2^-126 is a subnormal float32).
+  uint32_t qf[2][X][4];
 #pragma unroll
-  for (int h = 0; h < GP; ++h) {
-    const int4 x = *reinterpret_cast<const int4*>(&q_codes[0][h][(lane % LPB) * 4]);
-    const int4 y = *reinterpret_cast<const int4*>(&q_codes[1][h][(lane % LPB) * 4]);
-    qn[h][0] = x.x; qn[h][1] = x.y; qn[h][2] = x.z; qn[h][3] = x.w;
-    qp[h][0] = y.x; qp[h][1] = y.y; qp[h][2] = y.z; qp[h][3] = y.w;
-    emax = max(emax, q_exp[h]);
-  }
-  // The heads whose sums this lane gets from reduce_heads, and their scales (-1: padding).
-  int h0;
-  {
-    int none[GP] = {};
-    reduce_heads<GP, LPB>(none, lane, h0);
-  }
-  float my_scale[LEFT];
+  for (int sign = 0; sign < 2; ++sign)
 #pragma unroll
-  for (int i = 0; i < LEFT; ++i)
-    my_scale[i] = h0 + i < a.group ? exp2_int(max(q_exp[h0 + i] - emax - 22, -126)) : -1.f;
+    for (int x = 0; x < X; ++x) {
+      const uint4 w = *reinterpret_cast<const uint4*>(&q_codes[sign][gr][16 * x + 4 * tq]);
+      qf[sign][x][0] = w.x;
+      qf[sign][x][1] = w.y;
+      qf[sign][x][2] = w.z;
+      qf[sign][x][3] = w.w;
+    }
+  int emax = -126;
+#pragma unroll
+  for (int h = 0; h < 8; ++h) emax = max(emax, q_exp[h]);
+  // The scales of heads 2 tq and 2 tq + 1 (columns of this lane's sums).
+  const bool live_a = 2 * tq < a.group, live_b = 2 * tq + 1 < a.group;
+  const float scale_a = exp2_int(max(q_exp[2 * tq] - emax - 22, -126));
+  const float scale_b = exp2_int(max(q_exp[2 * tq + 1] - emax - 22, -126));
 
   const uint32_t keys_at = cluster_map(smem_u32(keys), 0);
-  for (; b0 < hi_b; b0 += NT) {
-    const int next = entry(b0 + NT);
-    if (phys < 0 || phys >= a.num_blocks) {
-      if (b0 + lane < hi_b) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK: the block is scored last
-      phys = -1;
+  auto score = [&](const Group& u, int half, int base, float scales) {
+    int c[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      const uint4 l0 = u.lo[0][x], l1 = u.lo[1][x], h0 = u.hi[0][x], h1 = u.hi[1][x];
+      mma_s8(c, l0.x, l1.x, l0.y, l1.y, qf[0][x][0], qf[0][x][1]);
+      mma_s8(c, l0.z, l1.z, l0.w, l1.w, qf[0][x][2], qf[0][x][3]);
+      mma_s8(c, h0.x, h1.x, h0.y, h1.y, qf[1][x][0], qf[1][x][1]);
+      mma_s8(c, h0.z, h1.z, h0.w, h1.w, qf[1][x][2], qf[1][x][3]);
     }
-    const float sc = phys >= 0 ? __ldg(a.summary_scale + static_cast<int64_t>(phys) * a.num_kv_heads + g) : -1.f;
+    float best[2];
 #pragma unroll
-    for (int j0 = 0; j0 < LPB; j0 += BATCH) {
-      if (b0 + j0 * BPW >= hi_b) break;
-      uint4 lo[BATCH], hi[BATCH];
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        const int p = max(__shfl_sync(kFull, phys, (j0 + j) * BPW + lane / LPB), 0);
-        const uint4* sum = reinterpret_cast<const uint4*>(
-            a.summary + (static_cast<int64_t>(p) * a.num_kv_heads + g) * (2 * D) + (lane % LPB) * 16);
-        lo[j] = __ldg(sum);
-        hi[j] = __ldg(sum + D / 16);
-      }
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        const int lw[4] = {static_cast<int>(lo[j].x), static_cast<int>(lo[j].y), static_cast<int>(lo[j].z),
-                           static_cast<int>(lo[j].w)};
-        const int hw[4] = {static_cast<int>(hi[j].x), static_cast<int>(hi[j].y), static_cast<int>(hi[j].z),
-                           static_cast<int>(hi[j].w)};
-        int acc[GP];
-#pragma unroll
-        for (int h = 0; h < GP; ++h) {
-          acc[h] = 0;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) acc[h] = __dp4a(hw[w], qp[h][w], __dp4a(lw[w], qn[h][w], acc[h]));
-        }
-        int from;
-        reduce_heads<GP, LPB>(acc, lane, from);
-        const int mine = (j0 + j) * BPW + lane / LPB;  // which of the 32 blocks
-        const float psc = __shfl_sync(kFull, sc, mine);
-        float best = kNegInf;
-#pragma unroll
-        for (int i = 0; i < LEFT; ++i)
-          if (my_scale[i] >= 0.f) best = fmaxf(best, static_cast<float>(acc[i]) * my_scale[i] * psc);
-        // Lanes with the same heads differ in the low bits of the lane, so only the others exchange.
-#pragma unroll
-        for (int o = LPB / 2; o >= 1 && o * GP >= LPB; o >>= 1)
-          best = fmaxf(best, __shfl_xor_sync(kFull, best, o));
-        const int b = b0 + mine;
-        if (lane % LPB == 0 && b < hi_b) cluster_store_u32(keys_at + 4 * b, psc >= 0.f ? order_key(best) : 0u);
-      }
+    for (int r = 0; r < 2; ++r) {
+      best[r] = fmaxf(live_a ? static_cast<float>(c[2 * r]) * scale_a : kNegInf,
+                      live_b ? static_cast<float>(c[2 * r + 1]) * scale_b : kNegInf);
+      best[r] = fmaxf(best[r], __shfl_xor_sync(kFull, best[r], 1));
+      best[r] = fmaxf(best[r], __shfl_xor_sync(kFull, best[r], 2));
     }
+    // Lanes tq = 0 and 1 store rows gr and gr + 8 (a power of two after the maximum: the same as before it).
+    const int row = 16 * half + gr + 8 * (tq & 1);
+    const float psc = __shfl_sync(kFull, scales, row);
+    const int b = base + row;
+    if (tq < 2 && b < hi_b)
+      cluster_store_u32(keys_at + 4 * b, psc >= 0.f ? order_key((tq ? best[1] : best[0]) * psc) : 0u);
+  };
+  while (b0 < hi_b) {
+    load(odd, phys, 1);
+    const int next = checked(ahead, b0 + NT);
+    ahead = entry(b0 + 2 * NT);
+    const float next_sc = scale_of(next);
+    score(even, 0, b0, sc);
+    load(even, next, 0);
+    score(odd, 1, b0, sc);
     phys = next;
+    sc = next_sc;
+    b0 += NT;
   }
   cluster_sync();  // every key has arrived
   if (rank != 0) return;
@@ -513,31 +521,28 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a) {
 }
 
 // CTAs per (sequence, KV head): doubled while the batch has fewer than
-// kSelTarget CTAs a SM and a CTA keeps at least kSelLeast blocks.
-constexpr int kSelTarget = 4, kSelLeast = 128, kSelMaxCluster = 8;
+// kSelWarps warps a SM and a CTA keeps at least 4 chunks a warp.
+constexpr int kSelWarps = 12, kSelMaxCluster = 8;
 
-constexpr int kSelThreads = 128;
-
-template <int D, bool BF16, int GP>
-cudaError_t launch_select_t(const SelectArgs& a, cudaStream_t stream) {
-  auto kern = select_blocks_kernel<D, BF16, GP, kSelThreads>;
-  const int64_t cap = min(static_cast<int64_t>(a.max_blocks_per_seq),
-                          (static_cast<int64_t>(a.max_context_len) + (1 << a.block_shift) - 1) >> a.block_shift);
+template <int D, bool BF16, int NT>
+cudaError_t launch_select_t(const SelectArgs& a, int64_t cap, cudaStream_t stream) {
+  auto kern = select_blocks_kernel<D, BF16, NT>;
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   int C = 1;
-  while (C < kSelMaxCluster && units * C < kSelTarget * current_sm_count(152) && cap >= 2 * C * kSelLeast) C *= 2;
+  while (C < kSelMaxCluster && units * C * (NT / 32) < kSelWarps * current_sm_count(152) && cap >= 2 * C * NT) C *= 2;
   const size_t smem = static_cast<size_t>(max(cap, static_cast<int64_t>(1))) * sizeof(uint32_t);
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(units * C)), dim3(kSelThreads), smem, C, stream, a);
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(units * C)), dim3(NT), smem, C, stream, a);
 }
 
+// 256 threads where a sequence may have more blocks than 128 threads score in
+// four chunks each: the first CTA's search of the keys takes half the time.
 template <int D, bool BF16>
-cudaError_t launch_select_g(const SelectArgs& a, cudaStream_t stream) {
-  if (a.group == 1) return launch_select_t<D, BF16, 1>(a, stream);
-  if (a.group == 2) return launch_select_t<D, BF16, 2>(a, stream);
-  if (a.group <= 4) return launch_select_t<D, BF16, 4>(a, stream);
-  return launch_select_t<D, BF16, 8>(a, stream);
+cudaError_t launch_select_n(const SelectArgs& a, cudaStream_t stream) {
+  const int64_t cap = min(static_cast<int64_t>(a.max_blocks_per_seq),
+                          (static_cast<int64_t>(a.max_context_len) + (1 << a.block_shift) - 1) >> a.block_shift);
+  return cap <= 512 ? launch_select_t<D, BF16, 128>(a, cap, stream) : launch_select_t<D, BF16, 256>(a, cap, stream);
 }
 
 template <int D, int KIND>
@@ -562,8 +567,8 @@ cudaError_t launch_summarize_blocks(const SummarizeArgs& a, int head_dim, bool b
 
 cudaError_t launch_select_blocks(const SelectArgs& a, int head_dim, bool bf16, cudaStream_t stream) {
   if (a.num_seqs == 0) return cudaSuccess;
-  if (head_dim == 128) return bf16 ? launch_select_g<128, true>(a, stream) : launch_select_g<128, false>(a, stream);
-  if (head_dim == 64) return bf16 ? launch_select_g<64, true>(a, stream) : launch_select_g<64, false>(a, stream);
+  if (head_dim == 128) return bf16 ? launch_select_n<128, true>(a, stream) : launch_select_n<128, false>(a, stream);
+  if (head_dim == 64) return bf16 ? launch_select_n<64, true>(a, stream) : launch_select_n<64, false>(a, stream);
   return cudaErrorInvalidValue;
 }
 
