@@ -213,6 +213,9 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
 }
 
 constexpr int kBins = 2048;
+constexpr int kListed = 512;      // candidates that are listed once no more are left
+constexpr int kAhead = 8;         // keys a thread reads ahead of using them
+constexpr int kRankBlocks = 256;  // up to here every key is ranked directly
 
 // Exclusive prefix sums of a pair of counts over the CTA's threads.
 template <int NT>
@@ -254,7 +257,7 @@ __device__ __forceinline__ int2 block_scan(int2 v, int2* warp_sums) {
 // global memory and uses words 2i, 2i + 1 of chunk x in k-step 2x + i.  The
 // next 16 blocks' summaries are loaded before the current ones are used.
 template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, int a_keys, int words_max) {
   constexpr int X = D / 64;      // 16-byte chunks of one bound per lane and row
   constexpr int NWARP = NT / 32;
   constexpr int BPT = kBins / NT;  // bins per thread
@@ -265,6 +268,8 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a) {
   __shared__ int2 warp_sums[NWARP];
   __shared__ uint32_t warp_range[2][NWARP];
   __shared__ int found[3];  // the bin, how many keys lie above it and in it
+  __shared__ uint2 list[kListed];  // candidates left: key and block
+  __shared__ int listed;
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -425,39 +430,78 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a) {
   cluster_sync();  // every key has arrived
   if (rank != 0) return;
 
-  // The range of the middle keys.
-  uint32_t kmin = 0xffffffffu, kmax = 0u;
-  for (int b = first + tid; b < last; b += NT) {
-    kmin = min(kmin, keys[b]);
-    kmax = max(kmax, keys[b]);
-  }
-  kmin = __reduce_min_sync(kFull, kmin);
-  kmax = __reduce_max_sync(kFull, kmax);
-  if (lane == 0) {
-    warp_range[0][warp] = kmin;
-    warp_range[1][warp] = kmax;
-  }
-  for (int i = tid; i < kBins; i += NT) hist[i] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < NWARP; ++w) {
-    kmin = min(kmin, warp_range[0][w]);
-    kmax = max(kmax, warp_range[1][w]);
-  }
-
-  // The threshold: `need` of the middle keys are taken.  Keys above `lo` are
-  // taken whole, `ties` of those equal to it (lowest block first).
-  int need = a.keep - a.first_blocks - a.last_blocks;
-  uint32_t lo = kmin;
+  // What is taken goes into two bitmaps: blocks taken for sure, and blocks
+  // whose key equals the threshold, of which the first `ties` are taken.
+  const int words = (n + 31) / 32;
+  uint32_t* sure_bits = keys + a_keys;
+  uint32_t* tie_bits = sure_bits + words_max;
+  int need = a.keep - first - a.last_blocks;  // middle blocks to take
   int ties = 0;
-  if (need > 0) {
-    const int bits = 32 - __clz(kmax - kmin);
-    int shift = max(0, bits - 11);
-    uint32_t width = 0xffffffffu;  // keys in [lo, lo + width] are still candidates
-    for (;;) {
-      for (int b = first + tid; b < last; b += NT) {
-        const uint32_t k = keys[b], d = k - lo;
-        if (k >= lo && d <= width) atomicAdd(&hist[d >> shift], 1);
+  auto forced = [&](int b) { return b < first || b >= last; };
+  if (n <= kRankBlocks) {
+    // Few blocks: each thread counts the middle keys that come before its own.
+    for (int b = tid; b < words * 32; b += NT) {
+      bool take = b < n && forced(b);
+      if (b < n && !take) {
+        const uint32_t k = keys[b];
+        int before = 0;
+        for (int j = first; j < last; ++j) before += keys[j] > k || (keys[j] == k && j < b);
+        take = before < need;
+      }
+      const uint32_t w = __ballot_sync(kFull, take);
+      if (lane == 0) sure_bits[b / 32] = w;
+    }
+    __syncthreads();
+    for (int b = tid; b < words * 32; b += NT) {
+      const uint32_t w = sure_bits[b / 32];
+      int at = __popc(w & ((1u << lane) - 1));
+      for (int i = 0; i < b / 32; ++i) at += __popc(sure_bits[i]);
+      if ((w >> lane) & 1) out[at] = b;
+    }
+    return;
+  }
+  {
+    // The range of the middle keys.
+    uint32_t kmin = 0xffffffffu, kmax = 0u;
+#pragma unroll 8
+    for (int b = first + tid; b < last; b += NT) {
+      const uint32_t k = keys[b];
+      kmin = min(kmin, k);
+      kmax = max(kmax, k);
+    }
+    kmin = __reduce_min_sync(kFull, kmin);
+    kmax = __reduce_max_sync(kFull, kmax);
+    if (lane == 0) {
+      warp_range[0][warp] = kmin;
+      warp_range[1][warp] = kmax;
+    }
+    for (int i = tid; i < kBins; i += NT) hist[i] = 0;
+    if (tid == 0) listed = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NWARP; ++w) {
+      kmin = min(kmin, warp_range[0][w]);
+      kmax = max(kmax, warp_range[1][w]);
+    }
+    // Rounds: the candidates, keys in [lo, lo + width], are counted in 2048
+    // bins; the bin of the need-th largest is the next round's range.  Once
+    // it holds few enough they are listed, and the rest is settled.
+    uint32_t lo = kmin, width = kmax - kmin;
+    bool in_list = false;
+    int shift = max(0, 32 - __clz(width) - 11);
+    if (need == 0) lo = 0xffffffffu, shift = -1;  // no middle block: none lies above
+    while (shift >= 0) {
+      const int items = in_list ? listed : last - first;
+      for (int i0 = tid; i0 < items; i0 += kAhead * NT) {
+        uint32_t k[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int i = min(i0 + u * NT, items - 1);
+          k[u] = in_list ? list[i].x : keys[first + i];
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (i0 + u * NT < items && k[u] >= lo && k[u] - lo <= width) atomicAdd(&hist[(k[u] - lo) >> shift], 1);
       }
       __syncthreads();
       // Thread t owns BPT bins, descending with t.
@@ -485,38 +529,90 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a) {
         above += own[i];
       }
       __syncthreads();
-      const int bin = found[0], in_bin = found[2];
+      const int in_bin = found[2];
       need -= found[1];
-      lo += static_cast<uint32_t>(bin) << shift;
-      if (in_bin == need || shift == 0) break;
+      lo += static_cast<uint32_t>(found[0]) << shift;
       width = (1u << shift) - 1;
+      // Settled: every key of the bin is taken, or the bin is a single key.
+      ties = in_bin == need ? 0x7fffffff : need;
+      if (in_bin == need || shift == 0) break;
       shift = max(0, shift - 11);
+      if (!in_list && in_bin <= kListed) {
+        for (int i0 = tid; i0 < words * 32; i0 += kAhead * NT) {
+          uint32_t k[kAhead];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) k[u] = keys[min(i0 + u * NT, n - 1)];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const int b = i0 + u * NT;
+            if (b >= words * 32) break;  // the same for a whole warp
+            const bool mid = b < n && !forced(b);
+            const uint32_t w = __ballot_sync(kFull, (b < n && !mid) || (mid && k[u] > lo && k[u] - lo > width));
+            const uint32_t open = __ballot_sync(kFull, mid && k[u] >= lo && k[u] - lo <= width);
+            if (lane == 0) {
+              sure_bits[b / 32] = w;
+              tie_bits[b / 32] = open;
+            }
+          }
+        }
+        __syncthreads();
+        for (int w0 = 0; w0 < words; w0 += NT) {
+          const int w = w0 + tid;
+          uint32_t open = w < words ? tie_bits[w] : 0u;
+          int at = listed + block_scan<NT>(make_int2(__popc(open), 0), warp_sums).x;
+          const int end = at + __popc(open);
+          for (; open; open &= open - 1, ++at) {
+            const int b = w * 32 + __ffs(open) - 1;
+            list[at] = make_uint2(keys[b], static_cast<uint32_t>(b));
+          }
+          if (w < words) tie_bits[w] = 0;
+          __syncthreads();
+          if (tid == NT - 1) listed = end;
+          __syncthreads();
+        }
+        in_list = true;
+      }
     }
-    // Either every key of the last bin is taken, or the bin is a single key and `need` of them are.
-    ties = need;
-    if (shift > 0) ties = 0x7fffffff;
-  } else {
-    lo = 0xffffffffu;  // no middle block: no key is above it, none of those equal is taken
+    if (in_list) {
+      for (int i = tid; i < listed; i += NT)
+        if (list[i].x >= lo)
+          atomicOr((list[i].x > lo ? sure_bits : tie_bits) + list[i].y / 32, 1u << (list[i].y % 32));
+    } else {
+      for (int b = tid; b < words * 32; b += NT) {
+        const uint32_t k = b < n ? keys[b] : 0u;
+        const bool mid = b < n && !forced(b);
+        const uint32_t w = __ballot_sync(kFull, (b < n && !mid) || (mid && k > lo));
+        const uint32_t v = __ballot_sync(kFull, mid && k == lo && need > 0);
+        if (lane == 0) {
+          sure_bits[b / 32] = w;
+          tie_bits[b / 32] = v;
+        }
+      }
+    }
   }
+  __syncthreads();
 
-  // Ordered output: thread t owns a run of consecutive blocks (odd, so that the lanes' keys lie in different banks).
-  const int run = ((n + NT - 1) / NT) | 1;
-  const int b1 = min(n, (tid + 1) * run);
-  int2 mine = make_int2(0, 0);  // (taken for sure, equal to the threshold)
-  for (int b = tid * run; b < b1; ++b) {
-    if (b < first || b >= last || keys[b] > lo)
-      ++mine.x;
-    else if (keys[b] == lo)
-      ++mine.y;
-  }
-  __syncthreads();  // warp_sums is reused
-  int2 before = block_scan<NT>(mine, warp_sums);
-  for (int b = tid * run; b < b1; ++b) {
-    const bool sure = b < first || b >= last || keys[b] > lo;
-    const bool tie = !sure && keys[b] == lo;
-    if (sure || (tie && before.y < ties)) out[before.x + min(before.y, ties)] = b;
-    before.x += sure;
-    before.y += tie;
+  // Ordered output from the bitmaps, a word of 32 blocks a thread.
+  int2 done = make_int2(0, 0);
+  for (int w0 = 0; w0 < words; w0 += NT) {
+    const int w = w0 + tid;
+    const uint32_t su = w < words ? sure_bits[w] : 0u, ti = w < words ? tie_bits[w] : 0u;
+    const int2 mine = make_int2(__popc(su), __popc(ti));
+    int2 before = block_scan<NT>(mine, warp_sums);
+    before.x += done.x;
+    before.y += done.y;
+    if (tid == NT - 1) {
+      found[0] = before.x + mine.x;
+      found[1] = before.y + mine.y;
+    }
+    for (uint32_t m = su | ti; m; m &= m - 1) {
+      const uint32_t bit = m & (0u - m);
+      if ((su & bit) || before.y < ties) out[before.x + min(before.y, ties)] = w * 32 + __ffs(m) - 1;
+      before.x += (su & bit) != 0;
+      before.y += (ti & bit) != 0;
+    }
+    __syncthreads();
+    done = make_int2(found[0], found[1]);
   }
 }
 
@@ -530,10 +626,13 @@ cudaError_t launch_select_t(const SelectArgs& a, int64_t cap, cudaStream_t strea
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   int C = 1;
   while (C < kSelMaxCluster && units * C * (NT / 32) < kSelWarps * current_sm_count(152) && cap >= 2 * C * NT) C *= 2;
-  const size_t smem = static_cast<size_t>(max(cap, static_cast<int64_t>(1))) * sizeof(uint32_t);
+  // Keys of the longest sequence, then the two bitmaps.
+  const int words = static_cast<int>((cap + 31) / 32);
+  const size_t smem = static_cast<size_t>(34) * words * sizeof(uint32_t);
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(units * C)), dim3(NT), smem, C, stream, a);
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(units * C)), dim3(NT), smem, C, stream, a,
+                            32 * words, words);
 }
 
 // 256 threads where a sequence may have more blocks than 128 threads score in
