@@ -1,4 +1,5 @@
-"""ctypes binding of libpkv (include/pkv.h): argument marshalling only.
+"""ctypes binding of libpkv (include/pkv.h): argument marshalling only.  (The
+layer operators' tensors go through a small extension, csrc/pkv_torch.cpp.)
 
 Every function takes torch tensors that already live on the GPU, checks
 their dtype, shape, strides and that they are CUDA tensors, and forwards raw
@@ -11,6 +12,8 @@ and the library must be built (see build.py) or calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -460,67 +463,26 @@ def decode_step_partitions_fp8(out, q, k_new, v_new, k_pool, v_pool, k_scale, v_
 # ------------------------------------------------------------------ layer operators
 
 
-def _one_device(*ts):
-    """All tensors given live on the current CUDA device, where the library launches."""
-    here = torch.cuda.current_device()
-    for t in ts:
-        if t is not None and t.get_device() != here:  # -1 for a CPU tensor
-            raise PkvError("tensors must be CUDA tensors on the current device")
+# Their tensors are checked and passed on by the extension csrc/pkv_torch.cpp.
+
+_EXT = None
 
 
-def _need_dense(*ts):
-    for t in ts:
-        if t is not None and not t.is_contiguous():
-            raise PkvError("outputs, tables and lists must be contiguous")
-
-
-def _need_i32(**ts):
-    for name, t in ts.items():
-        if t is not None and t.dtype != torch.int32:
-            raise PkvError(f"{name} must be int32")
-
-
-def _rows(t, heads, D, dtype, what):
-    """Row stride of [T, heads, D] rows (each row dense, rows may be strided)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.dtype != dtype or \
-            (t.numel() and (t.stride(2) != 1 or t.stride(1) != D)):
-        raise PkvError(f"{what} must be [T, heads, D] with dense rows of one dtype")
-    if t.shape[0] <= 1:
-        return 0
-    if t.stride(0) < heads * D:
-        raise PkvError(f"{what}: rows of consecutive tokens overlap")
-    return int(t.stride(0))
-
-
-def _norm_rope_args(q, k, v, slot_mapping, q_out, k_out, q_weight, k_weight, eps, cos_sin, positions, interleaved,
-                    Hkv, D, status):
-    _one_device(q, k, v, slot_mapping, q_out, k_out, q_weight, k_weight, cos_sin, positions, status)
-    _need_dense(slot_mapping, q_weight, k_weight, cos_sin, positions)
-    _need_i32(slot_mapping=slot_mapping, positions=positions, status=status)
-    dt = _kv_dtype(q)
-    T, Hq = int(q.shape[0]), int(q.shape[1]) if q.dim() == 3 else 0
-    q_s = _rows(q, Hq, D, q.dtype, "q")
-    k_s, v_s = _rows(k, Hkv, D, q.dtype, "k"), _rows(v, Hkv, D, q.dtype, "v")
-    qo_s = _rows(q_out, Hq, D, q.dtype, "q_out")
-    ko_s = _rows(k_out, Hkv, D, q.dtype, "k_out") if k_out is not None else 0
-    if k_s != v_s:
-        raise PkvError("k and v must share a row stride")
-    for name, t in (("k", k), ("v", v), ("q_out", q_out), ("k_out", k_out), ("slot_mapping", slot_mapping),
-                    ("positions", positions)):
-        if t is not None and t.shape[0] != T:
-            raise PkvError(f"{name} must have one row a token")
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != q.dtype or tuple(w.shape) != (D,)):
-            raise PkvError("norm weights must be [D] of the rows' dtype")
-    rot = top = 0
-    if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or positions is None or positions.dim() != 1:
-            raise PkvError("cos_sin must be float32 [max_positions, rot_dim], with int32 positions [T]")
-        top, rot = int(cos_sin.shape[0]), int(cos_sin.shape[1])
-    if slot_mapping.dim() != 1:
-        raise PkvError("slot_mapping must be int32 [T]")
-    return dt, T, Hq, (_ptr(q_out), qo_s, _ptr(k_out), ko_s, _ptr(q), q_s, _ptr(k), _ptr(v), k_s, _ptr(q_weight),
-                       _ptr(k_weight), float(eps), _ptr(cos_sin), _ptr(positions), top, rot, int(bool(interleaved)))
+def _ext():
+    """The marshalling extension, loaded with the library it calls."""
+    global _EXT
+    if _EXT is None:
+        load()
+        if not os.path.exists(_build.EXT):
+            raise PkvError(f"the torch extension is not built ({_build.EXT} missing); run "
+                           "`python -c 'import __graft_entry__ as g; g.build()'`")
+        spec = importlib.util.spec_from_loader("_pkv_torch", importlib.machinery.ExtensionFileLoader(
+            "_pkv_torch", _build.EXT))
+        ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ext)
+        ext.set_error_type(PkvError)
+        _EXT = ext
+    return _EXT
 
 
 def norm_rope_write(q, k, v, k_pool, v_pool, slot_mapping, *, q_out, k_out=None, q_weight=None, k_weight=None,
@@ -531,128 +493,50 @@ def norm_rope_write(q, k, v, k_pool, v_pool, slot_mapping, *, q_out, k_out=None,
     q [T, H_q, D], k and v [T, H_kv, D] f16/bf16 (rows may be slices of a fused projection);
     q_out (and k_out, optional) receive the rotated rows and may be q and k themselves; pools as
     write_cache.  Tokens with position -1 are padding and are left alone; slot -1 writes no pool row."""
-    bstride = _pool_stride(k_pool, v_pool)
-    NB, B, Hkv, D = k_pool.shape
-    if k_pool.dtype != q.dtype or v_pool.dtype != q.dtype:
-        raise PkvError("rows and pools must share a dtype")
-    _one_device(k_pool, v_pool)
-    dt, T, Hq, head = _norm_rope_args(q, k, v, slot_mapping, q_out, k_out, q_weight, k_weight, eps, cos_sin,
-                                      positions, interleaved, Hkv, D, status)
-    _check(load().pkv_norm_rope_write(*head, _ptr(k_pool), _ptr(v_pool), bstride, _ptr(slot_mapping), T, Hq, Hkv, D,
-                                      B, NB, dt, _ptr(status), _stream(stream)), "pkv_norm_rope_write")
+    (_EXT or _ext()).norm_rope_write(q, k, v, k_pool, v_pool, None, None, slot_mapping, q_out, k_out, q_weight,
+                                     k_weight, eps, cos_sin, positions, interleaved, status, stream, False)
 
 
 def norm_rope_write_fp8(q, k, v, k_pool, v_pool, k_scale, v_scale, slot_mapping, *, q_out, k_out=None, q_weight=None,
                         k_weight=None, eps=1e-6, cos_sin=None, positions=None, interleaved=False, status=None,
                         stream=None):
     """pkv_norm_rope_write_fp8: norm_rope_write into FP8 pools (uint8 codes, scales as write_cache_fp8)."""
-    NB, B, Hkv, D, layers = _fp8_pools(k_pool, v_pool, k_scale, v_scale)
-    _one_device(k_pool, v_pool, k_scale, v_scale)
-    dt, T, Hq, head = _norm_rope_args(q, k, v, slot_mapping, q_out, k_out, q_weight, k_weight, eps, cos_sin,
-                                      positions, interleaved, Hkv, D, status)
-    _check(load().pkv_norm_rope_write_fp8(*head, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
-                                          _ptr(slot_mapping), T, Hq, Hkv, D, B, NB, layers, dt, _ptr(status),
-                                          _stream(stream)), "pkv_norm_rope_write_fp8")
-
-
-def _summary_of(summary, summary_scale):
-    """(blocks, KV heads, head dim) of a summary and its scales."""
-    if summary.dtype != torch.int8 or summary.dim() != 4 or summary.shape[2] != 2 or \
-            summary_scale.dtype != torch.float32 or tuple(summary_scale.shape) != tuple(summary.shape[:2]):
-        raise PkvError("summary must be int8 [NB, H_kv, 2, D] and summary_scale float32 [NB, H_kv]")
-    _need_dense(summary, summary_scale)
-    return int(summary.shape[0]), int(summary.shape[1]), int(summary.shape[3])
+    (_EXT or _ext()).norm_rope_write(q, k, v, k_pool, v_pool, k_scale, v_scale, slot_mapping, q_out, k_out, q_weight,
+                                     k_weight, eps, cos_sin, positions, interleaved, status, stream, True)
 
 
 def summarize_blocks(summary, summary_scale, k_pool, block_ids, *, status=None, stream=None):
     """pkv_summarize_blocks: per-channel bounds of the keys of the listed full blocks (int32 [n], -1:
     none) into summary int8 [NB, H_kv, 2, D] and summary_scale float32 [NB, H_kv]."""
-    bstride = _pool_stride(k_pool, k_pool)
-    NB, B, Hkv, D = k_pool.shape
-    _one_device(summary, summary_scale, k_pool, block_ids, status)
-    _need_dense(block_ids)
-    _need_i32(block_ids=block_ids, status=status)
-    if _summary_of(summary, summary_scale) != (NB, Hkv, D) or block_ids.dim() != 1:
-        raise PkvError("summary must have the pool's blocks, KV heads and head dim; block_ids must be [n]")
-    _check(load().pkv_summarize_blocks(_ptr(summary), _ptr(summary_scale), _ptr(k_pool), bstride, _ptr(block_ids),
-                                       int(block_ids.shape[0]), Hkv, D, B, NB, _kv_dtype(k_pool), _ptr(status),
-                                       _stream(stream)), "pkv_summarize_blocks")
+    (_EXT or _ext()).summarize_blocks(summary, summary_scale, k_pool, None, block_ids, status, stream, False)
 
 
 def summarize_blocks_fp8(summary, summary_scale, k_pool, k_scale, block_ids, *, status=None, stream=None):
     """pkv_summarize_blocks_fp8: summarize_blocks over an FP8 pool (uint8 codes, k_scale [NB, H_kv])."""
-    NB, B, Hkv, D, layers = _fp8_pools(k_pool, k_pool, k_scale, k_scale)
-    _one_device(summary, summary_scale, k_pool, k_scale, block_ids, status)
-    _need_dense(block_ids)
-    _need_i32(block_ids=block_ids, status=status)
-    if _summary_of(summary, summary_scale) != (NB, Hkv, D) or block_ids.dim() != 1:
-        raise PkvError("summary must have the pool's blocks, KV heads and head dim; block_ids must be [n]")
-    _check(load().pkv_summarize_blocks_fp8(_ptr(summary), _ptr(summary_scale), _ptr(k_pool), _ptr(k_scale),
-                                           _ptr(block_ids), int(block_ids.shape[0]), Hkv, D, B, NB, layers,
-                                           _ptr(status), _stream(stream)), "pkv_summarize_blocks_fp8")
+    (_EXT or _ext()).summarize_blocks(summary, summary_scale, k_pool, k_scale, block_ids, status, stream, True)
 
 
 def select_blocks(selected, counts, q, summary, summary_scale, block_tables, context_lens, *, block_size,
                   first_blocks=1, last_blocks=1, max_context_len, status=None, stream=None):
     """pkv_select_blocks: the logical blocks each (sequence, KV head) attends to, by the summaries' bounds.
     selected int32 [S, H_kv, keep] (ascending, then -1), counts int32 [S, H_kv]; q f16/bf16 [S, H_q, D]."""
-    _one_device(selected, counts, q, summary, summary_scale, block_tables, context_lens, status)
-    _need_dense(selected, counts, q, block_tables, context_lens)
-    _need_i32(selected=selected, counts=counts, block_tables=block_tables, context_lens=context_lens, status=status)
-    NB, Hkv, D = _summary_of(summary, summary_scale)
-    if q.dim() != 3 or q.shape[2] != D:
-        raise PkvError("q must be [S, H_q, D] with the summary's D")
-    S, Hq = int(q.shape[0]), int(q.shape[1])
-    if selected.dim() != 3 or selected.shape[:2] != (S, Hkv) or counts.shape != (S, Hkv) or \
-            block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
-        raise PkvError("selected [S, H_kv, keep], counts [S, H_kv], block_tables [S, blocks], context_lens [S]")
-    _check(load().pkv_select_blocks(_ptr(selected), _ptr(counts), _ptr(q), _ptr(summary), _ptr(summary_scale),
-                                    _ptr(block_tables), int(block_tables.shape[1]), _ptr(context_lens), S, Hq, Hkv, D,
-                                    int(block_size), NB, int(selected.shape[2]), int(first_blocks), int(last_blocks),
-                                    int(max_context_len), _kv_dtype(q), _ptr(status), _stream(stream)),
-           "pkv_select_blocks")
-
-
-def _sparse_shapes(out, q, block_tables, context_lens, selected, counts, Hkv, D, status):
-    _need_dense(out, q, block_tables, context_lens, selected, counts)
-    _need_i32(selected=selected, counts=counts, block_tables=block_tables, context_lens=context_lens, status=status)
-    if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape or out.dtype not in _DTYPES:
-        raise PkvError("q and out must be [S, H_q, D] with the pools' D")
-    S = int(q.shape[0])
-    if selected.dim() != 3 or selected.shape[:2] != (S, Hkv) or counts.shape != (S, Hkv) or \
-            block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
-        raise PkvError("selected [S, H_kv, keep], counts [S, H_kv], block_tables [S, blocks], context_lens [S]")
-    return S, int(q.shape[1])
+    (_EXT or _ext()).select_blocks(selected, counts, q, summary, summary_scale, block_tables, context_lens,
+                                   block_size, first_blocks, last_blocks, max_context_len, status, stream)
 
 
 def decode_sparse(out, q, k_pool, v_pool, block_tables, context_lens, selected, counts, scale, *, max_context_len,
                   status=None, stream=None):
     """pkv_decode_sparse: decode_attention over the selected blocks' tokens alone (select_blocks' output,
     or strictly ascending logical blocks of the caller's own); one kernel, no workspace."""
-    bstride = _pool_stride(k_pool, v_pool)
-    NB, B, Hkv, D = k_pool.shape
-    _one_device(out, q, k_pool, v_pool, block_tables, context_lens, selected, counts, status)
-    if q.dtype != k_pool.dtype or v_pool.dtype != k_pool.dtype:
-        raise PkvError("q, k_pool and v_pool must share a dtype")
-    S, Hq = _sparse_shapes(out, q, block_tables, context_lens, selected, counts, Hkv, D, status)
-    _check(load().pkv_decode_sparse(_ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), bstride, _ptr(block_tables),
-                                    int(block_tables.shape[1]), _ptr(context_lens), _ptr(selected), _ptr(counts),
-                                    int(selected.shape[2]), S, Hq, Hkv, D, B, NB, float(scale), int(max_context_len),
-                                    _kv_dtype(k_pool), _DTYPES[out.dtype], _ptr(status), _stream(stream)),
-           "pkv_decode_sparse")
+    (_EXT or _ext()).decode_sparse(out, q, k_pool, v_pool, None, None, block_tables, context_lens, selected, counts,
+                                   scale, max_context_len, status, stream, False)
 
 
 def decode_sparse_fp8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, selected, counts, scale,
                       *, max_context_len, status=None, stream=None):
     """pkv_decode_sparse_fp8: decode_sparse over FP8 pools (q f16/bf16)."""
-    NB, B, Hkv, D, layers = _fp8_pools(k_pool, v_pool, k_scale, v_scale)
-    _one_device(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, selected, counts, status)
-    S, Hq = _sparse_shapes(out, q, block_tables, context_lens, selected, counts, Hkv, D, status)
-    _check(load().pkv_decode_sparse_fp8(_ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
-                                        _ptr(block_tables), int(block_tables.shape[1]), _ptr(context_lens),
-                                        _ptr(selected), _ptr(counts), int(selected.shape[2]), S, Hq, Hkv, D, B, NB,
-                                        layers, float(scale), int(max_context_len), _kv_dtype(q), _DTYPES[out.dtype],
-                                        _ptr(status), _stream(stream)), "pkv_decode_sparse_fp8")
+    (_EXT or _ext()).decode_sparse(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, selected,
+                                   counts, scale, max_context_len, status, stream, True)
 
 
 # ------------------------------------------------------------------ swap

@@ -1,4 +1,5 @@
-"""Builds libpkv.so in-tree with nvcc for sm_103a (GB300).
+"""Builds libpkv.so in-tree with nvcc for sm_103a (GB300), and beside it the
+extension that passes torch tensors to its layer operators (g++).
 
 Each translation unit compiles in parallel; the result links the CUDA runtime
 statically, so the library needs only the NVIDIA driver at run time.
@@ -9,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpkv.so")
+EXT = os.path.join(OUT_DIR, "_pkv_torch.so")  # CPython extension over libpkv and torch
+EXT_SOURCE = "pkv_torch.cpp"
 SOURCES = ["pkv_api.cu", "pkv_cache_ops.cu", "pkv_decode.cu", "pkv_decode_hg.cu", "pkv_decode_balanced.cu",
            "pkv_decode_fp8.cu", "pkv_norm_rope.cu", "pkv_sparse_select.cu", "pkv_sparse_decode.cu", "pkv_api_layer.cu",
            "pkv_static_ws.cu", "pkv_checks.cu", "pkv_block_manager.cpp"]
@@ -34,10 +38,10 @@ def _nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.abspath(__file__)]
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [EXT_SOURCE]] + [os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
 
 
@@ -58,14 +62,49 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ext_obj = ex.submit(_compile_ext)
         objs = list(ex.map(compile_one, SOURCES))
+        ext_obj = ext_obj.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_ext(ext_obj)
     return LIB
+
+
+def _torch_dirs() -> tuple:
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    return os.path.join(root, "include"), os.path.join(root, "lib")
+
+
+def _compile_ext() -> str:
+    inc, _ = _torch_dirs()
+    obj = os.path.join(OUT_DIR, "pkv_torch.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(ROOT, "include"), "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-isystem",
+           sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {EXT_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_ext(obj: str) -> None:
+    """Links against libpkv.so beside it and the installed torch."""
+    _, lib = _torch_dirs()
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-l:libpkv.so", "-L", lib, "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
 
 
 if __name__ == "__main__":
