@@ -57,7 +57,7 @@ int resident_warp_slots(const void* kernel, int threads, size_t smem) {
     size_t smem;
     int slots;
   };
-  static Entry table[32];
+  static Entry table[256];
   static int used = 0;
   static std::mutex mu;
   int dev = 0;
@@ -78,7 +78,7 @@ int resident_warp_slots(const void* kernel, int threads, size_t smem) {
   }
   const int slots = current_sm_count(1) * per_sm * (threads / 32);
   std::lock_guard<std::mutex> lock(mu);
-  if (used < 32) table[used++] = Entry{kernel, dev, threads, smem, slots};
+  if (used < 256) table[used++] = Entry{kernel, dev, threads, smem, slots};
   return slots;
 }
 

@@ -34,8 +34,8 @@ pkv_status prepare_norm_rope(NormRopeArgs* a, void* q_out, int64_t q_out_stride,
   if ((q_weight || k_weight) && !(std::isfinite(eps) && eps > 0.f)) return PKV_ERR_INVALID_ARG;
   if ((head_dim != 64 && head_dim != 128) || rot_dim % 16 != 0 || block_shift_of(block_size) < 0)
     return PKV_ERR_UNSUPPORTED;
-  // Task and slot counts stay inside the grid's and an int32's range.
-  if (static_cast<int64_t>(num_tokens) * (num_q_heads + 2LL * num_kv_heads) > (1LL << 32)) return PKV_ERR_UNSUPPORTED;
+  // Tasks (at most one a token and head) are numbered in 32 bits.
+  if (num_tokens * (num_q_heads + 2LL * num_kv_heads) > 0xfffffff0LL) return PKV_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_q_heads) * head_dim > 0x7fffffff ||
       static_cast<int64_t>(num_kv_heads) * head_dim > 0x7fffffff)
     return PKV_ERR_UNSUPPORTED;
@@ -62,6 +62,7 @@ pkv_status prepare_norm_rope(NormRopeArgs* a, void* q_out, int64_t q_out_stride,
   a->q_weight = static_cast<const uint16_t*>(q_weight);
   a->k_weight = static_cast<const uint16_t*>(k_weight);
   a->eps = eps;
+  a->timeout_ns = kWaitTimeoutNs;
   a->cos_sin = cos_sin;
   a->positions = positions;
   a->slot_mapping = slot_mapping;

@@ -147,6 +147,7 @@ struct NormRopeArgs {
   int64_t q_stride, kv_stride, q_out_stride, k_out_stride;
   int64_t block_stride, scale_stride;
   int64_t num_slots;
+  long long timeout_ns;
   float eps;
   int num_tokens, num_q_heads, num_kv_heads;
   int rot_dim, interleaved, max_positions;

@@ -14,178 +14,389 @@
 // Layout: D/16 lanes share a head, each holding two 16-byte chunks chosen so
 // that both members of every rotated pair (i, i + rot_dim/2) sit in one lane:
 // the rotation needs no exchange and the norm log2(D/16) shuffles.  A warp
-// serves 32 / (D/16) adjacent heads of one token and reads the token's angle
-// row once for all of them.
+// serves groups of 32 / (D/16) adjacent heads of one token and reads the
+// token's angle row once for all of them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "pkv_device.cuh"
 #include "pkv_fp8.cuh"
-#include "pkv_internal.h"
 
 namespace pkv {
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
+using namespace dev;
 
-__device__ __forceinline__ void flag(int32_t* status, unsigned bit) {
-  if (status) atomicOr(reinterpret_cast<unsigned*>(status), bit);
+// Pairs of floats, two operations an instruction (the kernel is as near the
+// issue limit as the memory's).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 pair(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 halves(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
 
-// Eight 16-bit values of a 16-byte chunk, widened.
 template <bool BF16>
-__device__ __forceinline__ void widen8(const uint4& u, float (&x)[8]) {
+__device__ __forceinline__ void widen8(const uint4& u, F2 (&x)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = fp8::widen16(w[i] & 0xffffu, BF16);
-    x[2 * i + 1] = fp8::widen16(w[i] >> 16, BF16);
+    if constexpr (BF16) {
+      x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[i] = pair(f.x, f.y);
+    }
   }
 }
 
 template <bool BF16>
-__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+__device__ __forceinline__ uint32_t narrow2(F2 a) {
+  const float2 f = halves(a);
   if constexpr (BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
     return *reinterpret_cast<const uint32_t*>(&h);
   } else {
-    const __half2 h = __floats2half2_rn(lo, hi);
+    const __half2 h = __floats2half2_rn(f.x, f.y);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
 
 template <bool BF16>
-__device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
-  return make_uint4(narrow2<BF16>(x[0], x[1]), narrow2<BF16>(x[2], x[3]), narrow2<BF16>(x[4], x[5]),
-                    narrow2<BF16>(x[6], x[7]));
+__device__ __forceinline__ uint4 narrow8(const F2 (&x)[4]) {
+  return make_uint4(narrow2<BF16>(x[0]), narrow2<BF16>(x[1]), narrow2<BF16>(x[2]), narrow2<BF16>(x[3]));
 }
 
-// Eight e4m3 codes of x / scale (IEEE division).
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
-  uint32_t c[4];
+// Eight e4m3 codes of x / scale, the division in IEEE float32.  x * (1 / scale)
+// is within 2^-22 of it (three roundings, of 2^-24 each); where the codes of
+// that product moved by 2^-21 either way agree, the quotient's code lies
+// between them and is the same, and only elsewhere (one element in some
+// 10^5, next to a rounding border) is the division carried out.  Scales whose
+// reciprocal is not a normal number always divide.
+__device__ __forceinline__ uint2 codes8(const F2 (&x)[4], float scale) {
+  const float inv = __frcp_rn(scale);
+  const F2 ii = pair(inv, inv), down = pair(1.f - 4.76837158203125e-7f, 1.f - 4.76837158203125e-7f);
+  const F2 up = pair(1.f + 4.76837158203125e-7f, 1.f + 4.76837158203125e-7f);
+  uint32_t c[4], differ = fabsf(inv) < 1.17549435e-38f || fabsf(inv) > 3.4028234e38f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = fp8::e4m3x2_satfinite(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
+  for (int i = 0; i < 4; ++i) {
+    const F2 y = mul2(x[i], ii);
+    const float2 lo = halves(mul2(y, down)), hi = halves(mul2(y, up));
+    c[i] = fp8::e4m3x2_satfinite(lo.x, lo.y);
+    differ |= c[i] ^ fp8::e4m3x2_satfinite(hi.x, hi.y);
+  }
+  if (differ) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = halves(x[i]);
+      c[i] = fp8::e4m3x2_satfinite(__fdiv_rn(f.x, scale), __fdiv_rn(f.y, scale));
+    }
+  }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// One lane's work on a head: the norm, the rotation and the stores of its two
+// chunks of the head's D values, with the token's angles and the norm weights
+// kept from head to head.  All lanes of a warp call together.
 template <int D, bool BF16, bool FP8>
-__global__ void __launch_bounds__(128) norm_rope_write_kernel(const NormRopeArgs a) {
-  constexpr int LPH = D / 16;    // lanes per head
-  constexpr int HPW = 32 / LPH;  // heads per warp
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int heads = a.num_q_heads + 2 * a.num_kv_heads;
-  const int groups = (heads + HPW - 1) / HPW;
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * 4 + warp;
-  if (task >= static_cast<int64_t>(a.num_tokens) * groups) return;
-  const int64_t t = task / groups;
-  const int h = static_cast<int>(task % groups) * HPW + lane / LPH;
-  const int l = lane % LPH;
-  const bool live = h < heads;
-  const bool is_q = h < a.num_q_heads;
-  const bool is_v = h >= a.num_q_heads + a.num_kv_heads;
-  const int g = is_q ? 0 : (h - a.num_q_heads) % a.num_kv_heads;
+struct LaneWork {
+  static constexpr int LPH = D / 16;    // lanes per head
+  static constexpr int HPW = 32 / LPH;  // heads per warp
+  const NormRopeArgs& a;
+  int l, rc, c0, c1;  // lane of the head; rotated chunks / 2; this lane's chunks
+  int first_k, first_v, heads;
+  int64_t t, at, block;  // token; its row in the pools and its block
+  bool writes;
+  F2 cs[4], sn[4], ns[4];
+  const uint16_t* w_now = nullptr;  // whose weights w0 and w1 hold
+  F2 w0[4], w1[4];
 
-  // Chunks c0 and c1 of the head: (l, l + rot/16) while l < rot/16, then the unrotated rest in pairs.
-  const int rc = a.rot_dim / 16;
-  const int c0 = l < rc ? l : 2 * rc + 2 * (l - rc);
-  const int c1 = l < rc ? l + rc : c0 + 1;
+  __device__ __forceinline__ LaneWork(const NormRopeArgs& args, int lane) : a(args) {
+    l = lane % LPH;
+    // Chunks (l, l + rot/16) while l < rot/16, then the unrotated rest in pairs.
+    rc = a.rot_dim / 16;
+    c0 = l < rc ? l : 2 * rc + 2 * (l - rc);
+    c1 = l < rc ? l + rc : c0 + 1;
+    first_k = a.num_q_heads;
+    first_v = first_k + a.num_kv_heads;
+    heads = first_v + a.num_kv_heads;
+  }
 
-  const uint16_t* src = is_q   ? a.q + t * a.q_stride + h * D
-                        : is_v ? a.v + t * a.kv_stride + g * D
-                               : a.k + t * a.kv_stride + g * D;
+  // Whether token t with this position is worked on: -1 marks a padding
+  // token, for which nothing is written; any other position outside the
+  // table is treated alike and reported.
+  __device__ __forceinline__ bool in_table(int pos) const {
+    return a.rot_dim == 0 || (pos >= 0 && pos < a.max_positions);
+  }
+  __device__ __forceinline__ void report(int pos, int slot) const {
+    if (!in_table(pos)) {
+      if (pos != -1) flag(a.dev_status, 64u);  // PKV_DEV_ERR_POSITION
+    } else if (slot != -1 && (slot < 0 || slot >= a.num_slots)) {
+      flag(a.dev_status, 1u);  // PKV_DEV_ERR_SLOT
+    }
+  }
+
+  // `row`: the position's cosines, then sines.  This lane's are those of
+  // channels 8 c0 .. 8 c0 + 7 (paired with c1's), or, interleaved, of pairs
+  // 4 c0 .. + 3 and 4 c1 .. + 3.
+  __device__ __forceinline__ void begin(int64_t token, int slot, const float* row) {
+    t = token;
+    writes = slot >= 0 && slot < a.num_slots;  // -1: the token has no slot
+    block = writes ? slot >> a.block_shift : 0;
+    at = block * a.block_stride +
+         static_cast<int64_t>(writes ? slot & ((1 << a.block_shift) - 1) : 0) * a.num_kv_heads * D;
+    if (l >= rc) return;
+    const int i0 = a.interleaved ? 4 * c0 : 8 * c0, i1 = a.interleaved ? 4 * c1 : 8 * c0 + 4;
+    const float4 x = *reinterpret_cast<const float4*>(row + i0), y = *reinterpret_cast<const float4*>(row + i1);
+    row += a.rot_dim / 2;
+    const float4 z = *reinterpret_cast<const float4*>(row + i0), w = *reinterpret_cast<const float4*>(row + i1);
+    cs[0] = pair(x.x, x.y), cs[1] = pair(x.z, x.w), cs[2] = pair(y.x, y.y), cs[3] = pair(y.z, y.w);
+    sn[0] = pair(z.x, z.y), sn[1] = pair(z.z, z.w), sn[2] = pair(w.x, w.y), sn[3] = pair(w.z, w.w);
+    ns[0] = pair(-z.x, -z.y), ns[1] = pair(-z.z, -z.w), ns[2] = pair(-w.x, -w.y), ns[3] = pair(-w.z, -w.w);
+  }
+
+  __device__ __forceinline__ void head(int h, const uint4& u0, const uint4& u1) {
+    const bool is_q = h < first_k, is_v = h >= first_v;
+    const int g = is_q ? h : is_v ? h - first_v : h - first_k;
+    F2 x0[4], x1[4];
+    widen8<BF16>(u0, x0);
+    widen8<BF16>(u1, x1);
+    const uint16_t* w = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
+    if (__any_sync(kFull, w != nullptr)) {
+      F2 ss = mul2(x0[0], x0[0]), st = mul2(x1[0], x1[0]);
+#pragma unroll
+      for (int j = 1; j < 4; ++j) {
+        ss = fma2(x0[j], x0[j], ss);
+        st = fma2(x1[j], x1[j], st);
+      }
+      const float2 s0 = halves(ss), s1 = halves(st);
+      float sum = (s0.x + s0.y) + (s1.x + s1.y);
+#pragma unroll
+      for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      if (w) {
+        if (w != w_now) {
+          widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(w) + c0), w0);
+          widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(w) + c1), w1);
+          w_now = w;
+        }
+        const float r = rsqrtf(sum * (1.f / D) + a.eps);
+        const F2 rr = pair(r, r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x0[j] = mul2(mul2(x0[j], rr), w0[j]);
+          x1[j] = mul2(mul2(x1[j], rr), w1[j]);
+        }
+      }
+    }
+    if (l < rc && !is_v) {
+      if (a.interleaved) {  // pairs (2i, 2i + 1): chunk c holds pairs 4c .. 4c + 3
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 c = halves(cs[j / 2]), s = halves(sn[j / 2]), d = halves(cs[2 + j / 2]), e = halves(sn[2 + j / 2]);
+          const float ca = j & 1 ? c.y : c.x, sa = j & 1 ? s.y : s.x, cb = j & 1 ? d.y : d.x, sb = j & 1 ? e.y : e.x;
+          const float2 p = halves(x0[j]), q = halves(x1[j]);
+          x0[j] = pair(p.x * ca - p.y * sa, p.y * ca + p.x * sa);
+          x1[j] = pair(q.x * cb - q.y * sb, q.y * cb + q.x * sb);
+        }
+      } else {  // pairs (i, i + rot/2): element j of chunk c0 with element j of c1
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const F2 p = x0[j], q = x1[j];
+          x0[j] = fma2(q, ns[j], mul2(p, cs[j]));
+          x1[j] = fma2(p, sn[j], mul2(q, cs[j]));
+        }
+      }
+    }
+    if (h >= heads) return;
+    if (is_q || (a.k_out && !is_v) || (!FP8 && !is_v && writes)) {
+      const uint4 y0 = narrow8<BF16>(x0), y1 = narrow8<BF16>(x1);
+      if (is_q || a.k_out) {
+        uint16_t* dst = is_q ? a.q_out + t * a.q_out_stride + g * D : a.k_out + t * a.k_out_stride + g * D;
+        reinterpret_cast<uint4*>(dst)[c0] = y0;
+        reinterpret_cast<uint4*>(dst)[c1] = y1;
+      }
+      if (!FP8 && !is_q && writes) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_pool) + at + g * D);
+        dst[c0] = y0;
+        dst[c1] = y1;
+      }
+    }
+    if (is_q || !writes) return;
+    if constexpr (FP8) {
+      const float sc = __ldg((is_v ? a.v_scale : a.k_scale) + block * a.scale_stride + g);
+      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) + at + g * D);
+      dst[c0] = codes8(x0, sc);
+      dst[c1] = codes8(x1, sc);
+    } else if (is_v) {  // moves bit by bit
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v_pool) + at + g * D);
+      dst[c0] = u0;
+      dst[c1] = u1;
+    }
+  }
+};
+
+// Few tokens: a warp per (token, HPW heads), everything straight from global memory.
+template <int D, bool BF16, bool FP8>
+__global__ void __launch_bounds__(128) norm_rope_write_kernel(const NormRopeArgs a, uint32_t parts) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const uint32_t task = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const uint32_t token = task / parts;
+  if (token >= static_cast<uint32_t>(a.num_tokens)) return;
+  LaneWork<D, BF16, FP8> work(a, lane);
+  const int part = static_cast<int>(task - token * parts);
+  const int h = part * work.HPW + lane / work.LPH;
+  const int64_t t = token;
+  const uint16_t* src = h < work.first_k   ? a.q + t * a.q_stride + h * D
+                        : h < work.first_v ? a.k + t * a.kv_stride + (h - work.first_k) * D
+                                           : a.v + t * a.kv_stride + (h - work.first_v) * D;
   uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-  if (live) {
-    u0 = *(reinterpret_cast<const uint4*>(src) + c0);
-    u1 = *(reinterpret_cast<const uint4*>(src) + c1);
+  if (h < work.heads) {
+    u0 = *(reinterpret_cast<const uint4*>(src) + work.c0);
+    u1 = *(reinterpret_cast<const uint4*>(src) + work.c1);
   }
-  const int slot = a.slot_mapping[t];
-  const int pos = a.rot_dim ? a.positions[t] : 0;
-  if (a.rot_dim && (pos < 0 || pos >= a.max_positions)) {
-    // -1 marks a padding token; any other position outside the table is an error.  Nothing is written.
-    if (pos != -1 && task % groups == 0 && lane == 0) flag(a.dev_status, 64u);  // PKV_DEV_ERR_POSITION
-    return;
-  }
-  float x0[8], x1[8];
-  widen8<BF16>(u0, x0);
-  widen8<BF16>(u1, x1);
+  const int slot = __ldg(a.slot_mapping + t);
+  const int pos = a.rot_dim ? __ldg(a.positions + t) : 0;
+  if (part == 0 && lane == 0) work.report(pos, slot);
+  if (!work.in_table(pos)) return;
+  work.begin(t, slot, a.cos_sin + static_cast<int64_t>(pos) * a.rot_dim);
+  work.head(h, u0, u1);
+}
 
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss += x0[i] * x0[i] + x1[i] * x1[i];
-#pragma unroll
-  for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
-  const uint16_t* w = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
-  if (w) {
-    const float r = rsqrtf(ss * (1.f / D) + a.eps);
-    float w0[8], w1[8];
-    widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(w) + c0), w0);
-    widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(w) + c1), w1);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x0[i] *= r * w0[i];
-      x1[i] *= r * w1[i];
-    }
-  }
-  if (l < rc && !is_v) {
-    const float* cs = a.cos_sin + static_cast<int64_t>(pos) * a.rot_dim;
-    const int half = a.rot_dim / 2;
-    if (a.interleaved) {  // pairs (2i, 2i + 1): chunk c holds pairs 4c .. 4c + 3
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float ca = __ldg(cs + 4 * c0 + i), sa = __ldg(cs + half + 4 * c0 + i);
-        const float cb = __ldg(cs + 4 * c1 + i), sb = __ldg(cs + half + 4 * c1 + i);
-        const float p = x0[2 * i], q = x0[2 * i + 1], y = x1[2 * i], z = x1[2 * i + 1];
-        x0[2 * i] = p * ca - q * sa;
-        x0[2 * i + 1] = q * ca + p * sa;
-        x1[2 * i] = y * cb - z * sb;
-        x1[2 * i + 1] = z * cb + y * sb;
-      }
-    } else {  // pairs (i, i + rot/2): element i of chunk c0 with element i of c1
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float c = __ldg(cs + 8 * c0 + i), s = __ldg(cs + half + 8 * c0 + i);
-        const float p = x0[i], q = x1[i];
-        x0[i] = p * c - q * s;
-        x1[i] = q * c + p * s;
-      }
-    }
-  }
-  if (!live) return;
+// Many tokens: persistent CTAs, each streaming its tokens' rows and angle rows
+// through a ring of bulk copies into shared memory, so that what is in flight
+// does not depend on registers and the chain position -> angles is off the
+// path (loaded ahead by registers instead, the kernel stayed at 5.0 TB/s
+// whatever the heads per warp, 80 to 90 us for 16384 tokens of 32 + 16 heads).
+// A stage: the token's query heads, key heads, value heads, angle row.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
 
-  if (is_q || (a.k_out && !is_v)) {
-    uint16_t* dst = is_q ? a.q_out + t * a.q_out_stride + h * D : a.k_out + t * a.k_out_stride + g * D;
-    reinterpret_cast<uint4*>(dst)[c0] = narrow8<BF16>(x0);
-    reinterpret_cast<uint4*>(dst)[c1] = narrow8<BF16>(x1);
+constexpr int kStages = 4;
+
+template <int D, bool BF16, bool FP8>
+__global__ void __launch_bounds__(256) norm_rope_stream_kernel(const NormRopeArgs a, uint32_t stage_bytes) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[kStages];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  LaneWork<D, BF16, FP8> work(a, lane);
+  const uint32_t ring = smem_u32(smem), bar0 = smem_u32(bars);
+  const uint32_t q_bytes = a.num_q_heads * D * 2, kv_bytes = a.num_kv_heads * D * 2, angle_bytes = a.rot_dim * 4;
+  if (threadIdx.x == 0) {
+    for (int st = 0; st < kStages; ++st) mbar_init(bar0 + 8 * st, 1);
+    fence_barrier_init();
+    fence_proxy_async_smem();
   }
-  if (is_q) return;
-  if (slot < 0 || slot >= a.num_slots) {  // -1: the token has no slot
-    if (slot != -1 && !is_v && g == 0 && l == 0) flag(a.dev_status, 1u);  // PKV_DEV_ERR_SLOT
-    return;
+  __syncthreads();
+
+  const int64_t step = gridDim.x;
+  auto position = [&](int64_t t) { return a.rot_dim && t < a.num_tokens ? __ldg(a.positions + t) : 0; };
+  auto slot_of = [&](int64_t t) { return t < a.num_tokens ? __ldg(a.slot_mapping + t) : -1; };
+  auto issue = [&](int64_t t, int st, int pos) {  // one thread
+    if (t >= a.num_tokens) return;
+    const uint32_t bar = bar0 + 8 * st, dst = ring + st * stage_bytes;
+    if (!work.in_table(pos)) {
+      mbar_arrive_expect_tx(bar, 0);
+      return;
+    }
+    mbar_arrive_expect_tx(bar, q_bytes + 2 * kv_bytes + angle_bytes);
+    bulk_load(dst, a.q + t * a.q_stride, q_bytes, bar);
+    bulk_load(dst + q_bytes, a.k + t * a.kv_stride, kv_bytes, bar);
+    bulk_load(dst + q_bytes + kv_bytes, a.v + t * a.kv_stride, kv_bytes, bar);
+    if (angle_bytes)
+      bulk_load(dst + q_bytes + 2 * kv_bytes, a.cos_sin + static_cast<int64_t>(pos) * a.rot_dim, angle_bytes, bar);
+  };
+  int64_t t = blockIdx.x;
+  int ahead = 0;  // thread 0: the position of the token whose copies go out next
+  if (threadIdx.x == 0) {
+    int first[kStages];
+    for (int st = 0; st < kStages; ++st) first[st] = position(t + st * step);
+    ahead = position(t + kStages * step);
+    for (int st = 0; st < kStages; ++st) issue(t + st * step, st, first[st]);
   }
-  const int64_t block = slot >> a.block_shift;
-  const int64_t at = block * a.block_stride +
-                     (static_cast<int64_t>(slot & ((1 << a.block_shift) - 1)) * a.num_kv_heads + g) * D;
-  if constexpr (FP8) {
-    const float sc = (is_v ? a.v_scale : a.k_scale)[block * a.scale_stride + g];
-    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) + at);
-    dst[c0] = codes8(x0, sc);
-    dst[c1] = codes8(x1, sc);
-  } else {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? a.v_pool : a.k_pool) + at);
-    dst[c0] = is_v ? u0 : narrow8<BF16>(x0);  // V rows move bit by bit
-    dst[c1] = is_v ? u1 : narrow8<BF16>(x1);
+  int pos = position(t), slot = slot_of(t);
+  for (int i = 0; t < a.num_tokens; ++i, t += step) {
+    const int next_pos = position(t + step), next_slot = slot_of(t + step);
+    const int st = i % kStages;
+    const bool ok = __all_sync(kFull, mbar_wait_bounded(bar0 + 8 * st, (i / kStages) & 1, a.timeout_ns));
+    if (ok) {
+      if (threadIdx.x == 0) work.report(pos, slot);
+      if (work.in_table(pos)) {
+        const uint8_t* stage = smem + st * stage_bytes;
+        work.begin(t, slot, reinterpret_cast<const float*>(stage + q_bytes + 2 * kv_bytes));
+        for (int h0 = warp * work.HPW; h0 < work.heads; h0 += warps * work.HPW) {
+          const int h = h0 + lane / work.LPH;
+          const uint4* row = reinterpret_cast<const uint4*>(stage + min(h, work.heads - 1) * (D * 2));
+          work.head(h, row[work.c0], row[work.c1]);
+        }
+      }
+    }
+    // Every warp is done with the stage; a timed-out wait anywhere ends the CTA.
+    if (__syncthreads_or(!ok)) {
+      if (warp == 0)  // copies in flight land before the CTA exits
+        for (int j = i; j < i + kStages && t + (j - i) * step < a.num_tokens; ++j)
+          mbar_wait_bounded(bar0 + 8 * (j % kStages), (j / kStages) & 1, a.timeout_ns);
+      if (threadIdx.x == 0) flag(a.dev_status, 16u);  // PKV_DEV_ERR_TIMEOUT; the output is undefined
+      return;
+    }
+    if (threadIdx.x == 0) {
+      issue(t + kStages * step, st, ahead);
+      ahead = position(t + (kStages + 1) * step);
+    }
+    pos = next_pos;
+    slot = next_slot;
   }
 }
+
+// The streaming kernel from kManyWarps head groups a SM on, unless a token's
+// rows are too long for its ring.
+constexpr int kManyWarps = 64;
+constexpr uint32_t kMaxRing = 200 * 1024;
 
 template <int D, bool BF16, bool FP8>
 cudaError_t launch_t(const NormRopeArgs& a, cudaStream_t stream) {
   constexpr int HPW = 32 / (D / 16);
-  const int64_t groups = (a.num_q_heads + 2 * a.num_kv_heads + HPW - 1) / HPW;
-  const int64_t tasks = a.num_tokens * groups;
-  return launch_pdl(norm_rope_write_kernel<D, BF16, FP8>, dim3(static_cast<unsigned>((tasks + 3) / 4)), dim3(128), 0,
-                    stream, a);
+  const int64_t heads = a.num_q_heads + 2LL * a.num_kv_heads, groups = (heads + HPW - 1) / HPW;
+  const int64_t stage = heads * D * 2 + a.rot_dim * 4;
+  if (a.num_tokens * groups < static_cast<int64_t>(kManyWarps) * current_sm_count(152) || stage * kStages > kMaxRing)
+    return launch_pdl(norm_rope_write_kernel<D, BF16, FP8>,
+                      dim3(static_cast<unsigned>((a.num_tokens * groups + 3) / 4)), dim3(128), 0, stream, a,
+                      static_cast<uint32_t>(groups));
+  // 4 to 8 warps, the number that leaves fewest idle in a token's last round.
+  int warps = 4;
+  for (int w = 5; w <= 8; ++w)
+    if ((groups + w - 1) / w * w <= (groups + warps - 1) / warps * warps) warps = w;
+  auto kern = norm_rope_stream_kernel<D, BF16, FP8>;
+  const uint32_t stage_bytes = static_cast<uint32_t>((stage + 127) & ~127LL);
+  const size_t smem = static_cast<size_t>(stage_bytes) * kStages;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  const int64_t slots = resident_warp_slots(reinterpret_cast<const void*>(kern), warps * 32, smem) / warps;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(a.num_tokens < slots ? a.num_tokens : slots)), dim3(warps * 32),
+                    smem, stream, a, stage_bytes);
 }
 
 }  // namespace

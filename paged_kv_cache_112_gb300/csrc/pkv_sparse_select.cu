@@ -31,14 +31,14 @@ __device__ __forceinline__ int bound_exponent(float p, float r) {
   return max(e, -126);
 }
 
-// floor (ceil) of (p + r) * 2^-e in int8 steps; r as above.  A power of two
-// scales p exactly, so p + r crosses an integer only where p sits on it; a
-// result that underflowed still has its sign.
+// floor of (p + r) * 2^-e, r as above (inv = 2^-e).  A power of two scales p
+// exactly, so p + r crosses an integer only where p sits on it; a product
+// that underflowed to zero keeps p's sign.
 __device__ __forceinline__ int step_down(float p, float r, float inv) {
   const float y = p * inv;
-  int c = static_cast<int>(floorf(y));
+  int c = __float2int_rd(y);
   if (static_cast<float>(c) == y && (r < 0.f || (c == 0 && p < 0.f))) --c;
-  return max(c, -127);
+  return c;
 }
 __device__ __forceinline__ int step_up(float p, float r, float inv) { return -step_down(-p, -r, inv); }
 
@@ -76,10 +76,12 @@ __device__ __forceinline__ float finite_bound(float x, float most) {
   return x == x ? fminf(fmaxf(x, -most), most) : 0.f;
 }
 
-// One warp per (listed block, KV head).  Rows of D * EB bytes are read as
-// 16-byte vectors, 32 / LPR rows at a time; each lane keeps the packed min
-// and max of its channels, the row groups are merged by shuffles, and group 0
-// writes the lower bounds, group 1 the upper ones.  KIND: 0 = f16, 1 = bf16,
+// A warp takes (listed block, KV head) pairs in turn.  Rows of D * EB bytes
+// are read as 16-byte vectors, 32 / LPR rows at a time and 16 rows a step,
+// the next step's rows on their way while the current ones are compared.
+// Each lane keeps the packed min and max of its channels; the row groups then
+// halve their channels with every exchange, so each lane ends up with CF of
+// them, rounds their bounds and stores the codes.  KIND: 0 = f16, 1 = bf16,
 // 2 = FP8 (codes compared as f16, which holds every e4m3 value).
 template <int D, int KIND>
 __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeArgs a) {
@@ -87,107 +89,149 @@ __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeAr
   constexpr bool BF16 = KIND == 1;
   constexpr int LPR = D * EB / 16;  // lanes per row
   constexpr int RPL = 32 / LPR;     // rows per load
+  constexpr int NL = 16 / RPL;      // loads per step
   constexpr int NW = KIND == 2 ? 8 : 4;  // packed pairs of channels per lane
-  constexpr int CH = 2 * NW;             // channels per lane
+  constexpr int CF = 2 * NW / RPL;       // channels per lane in the end
+  constexpr uint32_t kNone = BF16 ? 0x7fc07fc0u : 0x7e007e00u;  // NaN: no number yet
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (task >= static_cast<int64_t>(a.num_ids) * a.num_kv_heads) return;
-  const int g = static_cast<int>(task % a.num_kv_heads);
-  const int id = a.block_ids[task / a.num_kv_heads];
-  if (id < 0 || id >= a.num_blocks) {  // -1: no block
-    if (id != -1 && g == 0 && lane == 0) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK
-    return;
-  }
+  const int64_t tasks = static_cast<int64_t>(a.num_ids) * a.num_kv_heads;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
+  int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int64_t row_bytes = static_cast<int64_t>(a.num_kv_heads) * D * EB;
-  const uint8_t* src = a.k_pool + id * a.block_bytes + (lane / LPR) * row_bytes + g * (D * EB) + (lane % LPR) * 16;
+  const int64_t lane_at = (lane / LPR) * row_bytes + (lane % LPR) * 16;
+
+  auto id_of = [&](int64_t k) { return k < tasks ? a.block_ids[k / a.num_kv_heads] : -1; };
+  // The step's rows; none for a task that is not there (-1 or out of range).
+  auto load = [&](uint4 (&u)[NL], int64_t k, int id, int r0) {
+    if (id < 0 || id >= a.num_blocks) return;
+    const uint8_t* src = a.k_pool + id * a.block_bytes + static_cast<int>(k % a.num_kv_heads) * (D * EB) +
+                         r0 * row_bytes + lane_at;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(src + i * RPL * row_bytes));
+  };
+
+  int id = id_of(task), next_id = id_of(task + stride), r0 = 0;
+  uint4 cur[NL], nxt[NL];
+  load(cur, task, id, 0);
   uint32_t lo[NW], hi[NW];
 #pragma unroll
-  for (int i = 0; i < NW; ++i) lo[i] = hi[i] = KIND == 1 ? 0x7fc07fc0u : 0x7e007e00u;  // NaN: no number yet
-  for (int r0 = 0; r0 < a.block_size; r0 += 16) {
-    uint4 u[16 / RPL];
+  for (int i = 0; i < NW; ++i) lo[i] = hi[i] = kNone;
+  while (task < tasks) {
+    const bool last = r0 + 16 >= a.block_size;
+    const int id_after = last ? id_of(task + 2 * stride) : 0;
+    if (last)
+      load(nxt, task + stride, next_id, 0);
+    else
+      load(nxt, task, id, r0 + 16);
+    const bool there = id >= 0 && id < a.num_blocks;
+    if (there) {
 #pragma unroll
-    for (int i = 0; i < 16 / RPL; ++i)
-      u[i] = *reinterpret_cast<const uint4*>(src + (r0 + i * RPL) * row_bytes);
+      for (int i = 0; i < NL; ++i) {
+        const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
 #pragma unroll
-    for (int i = 0; i < 16 / RPL; ++i) {
-      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (KIND == 2) {
-          uint32_t p, q;
-          asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-              "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-              : "=r"(p), "=r"(q)
-              : "r"(w[j]));
-          min_max2<false>(lo[2 * j], hi[2 * j], p);
-          min_max2<false>(lo[2 * j + 1], hi[2 * j + 1], q);
-        } else {
-          min_max2<BF16>(lo[j], hi[j], w[j]);
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (KIND == 2) {
+            uint32_t p, q;
+            asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+                "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+                : "=r"(p), "=r"(q)
+                : "r"(w[j]));
+            min_max2<false>(lo[2 * j], hi[2 * j], p);
+            min_max2<false>(lo[2 * j + 1], hi[2 * j + 1], q);
+          } else {
+            min_max2<BF16>(lo[j], hi[j], w[j]);
+          }
         }
       }
+    } else if (id != -1 && r0 == 0 && task % a.num_kv_heads == 0 && lane == 0) {
+      flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK
     }
-  }
+    if (last && there) {
+      // Row groups: each exchange keeps half of the pairs, picked by the lane's bit.
+      int kept = 0, left = NW;
 #pragma unroll
-  for (int o = LPR; o < 32; o <<= 1)
+      for (int o = 16; o >= LPR; o >>= 1) {
+        left /= 2;
+        const bool upper = lane & o;
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      uint32_t dump = lo[i];
-      min_max2<BF16>(lo[i], dump, __shfl_xor_sync(kFull, lo[i], o));
-      dump = hi[i];
-      min_max2<BF16>(dump, hi[i], __shfl_xor_sync(kFull, hi[i], o));
-    }
-
-  // Values p + r, exactly: the keys themselves (r = 0), or code * scale as
-  // its float32 product and the remainder.
-  const float most = KIND == 0 ? 65504.f : KIND == 1 ? __uint_as_float(0x7f7f0000u) : 448.f;
-  float sc = 1.f;
-  if constexpr (KIND == 2) {
-    sc = a.k_scale[id * a.scale_stride + g];
-    if (!(sc > 0.f) || sc > 3.4028234e38f) sc = 0.f;  // no such scale: the block counts as zeros
-  }
-  const bool upper = (lane / LPR) & 1;
-  float v[CH], top = 0.f;
-#pragma unroll
-  for (int i = 0; i < NW; ++i) {
-    const float2 l = widen2<BF16>(lo[i]), h = widen2<BF16>(hi[i]);
-    const float lx = finite_bound(l.x, most), ly = finite_bound(l.y, most);
-    const float hx = finite_bound(h.x, most), hy = finite_bound(h.y, most);
-    top = fmaxf(top, fmaxf(fmaxf(-lx, hx), fmaxf(-ly, hy)));
-    v[2 * i] = upper ? hx : lx;
-    v[2 * i + 1] = upper ? hy : ly;
-  }
-#pragma unroll
-  for (int o = 1; o < LPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  const float ptop = fminf(top * sc, 3.4028234e38f);
-  const int e = bound_exponent(ptop, KIND == 2 ? fmaf(top, sc, -ptop) : 0.f);
-  const float inv = exp2_int(-e);
-  uint32_t code[CH / 4];
-#pragma unroll
-  for (int i = 0; i < CH / 4; ++i) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float x = v[4 * i + j];
-      float p = x, r = 0.f;
-      if constexpr (KIND == 2) {
-        p = fminf(fmaxf(x * sc, -3.4028234e38f), 3.4028234e38f);
-        r = fmaf(x, sc, -p);
+        for (int i = 0; i < NW / 2; ++i)
+          if (i < left) {
+            uint32_t dump;
+            const uint32_t l = __shfl_xor_sync(kFull, upper ? lo[i] : lo[i + left], o);
+            const uint32_t h = __shfl_xor_sync(kFull, upper ? hi[i] : hi[i + left], o);
+            lo[i] = upper ? lo[i + left] : lo[i];
+            hi[i] = upper ? hi[i + left] : hi[i];
+            dump = lo[i];
+            min_max2<BF16>(lo[i], dump, l);
+            dump = hi[i];
+            min_max2<BF16>(dump, hi[i], h);
+          }
+        kept += upper ? left : 0;
       }
-      const int c = upper ? step_up(p, r, inv) : step_down(p, r, inv);
-      w |= (static_cast<uint32_t>(c) & 0xffu) << (8 * j);
+      // Values p + r, exactly: the keys themselves (r = 0), or code * scale
+      // as its float32 product and the remainder.
+      const int g = static_cast<int>(task % a.num_kv_heads);
+      const int64_t head = static_cast<int64_t>(id) * a.num_kv_heads + g;
+      const float most = KIND == 0 ? 65504.f : KIND == 1 ? __uint_as_float(0x7f7f0000u) : 448.f;
+      float sc = 1.f;
+      if constexpr (KIND == 2) {
+        sc = __ldg(a.k_scale + id * a.scale_stride + g);
+        if (!(sc > 0.f) || sc > 3.4028234e38f) sc = 0.f;  // no such scale: the block counts as zeros
+      }
+      float vl[CF], vh[CF], top = 0.f;
+#pragma unroll
+      for (int i = 0; i < CF / 2; ++i) {
+        const float2 l = widen2<BF16>(lo[i]), h = widen2<BF16>(hi[i]);
+        vl[2 * i] = finite_bound(l.x, most);
+        vl[2 * i + 1] = finite_bound(l.y, most);
+        vh[2 * i] = finite_bound(h.x, most);
+        vh[2 * i + 1] = finite_bound(h.y, most);
+        top = fmaxf(top, fmaxf(fmaxf(-vl[2 * i], vh[2 * i]), fmaxf(-vl[2 * i + 1], vh[2 * i + 1])));
+      }
+      top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));  // top >= 0: its bits order as it does
+      const float ptop = fminf(top * sc, 3.4028234e38f);
+      const int e = bound_exponent(ptop, KIND == 2 ? fmaf(top, sc, -ptop) : 0.f);
+      const float inv = exp2_int(-e);
+      uint32_t cl = 0, ch = 0;
+#pragma unroll
+      for (int j = 0; j < CF; ++j) {
+        float pl = vl[j], ph = vh[j], rl = 0.f, rh = 0.f;
+        if constexpr (KIND == 2) {
+          pl = fmaxf(vl[j] * sc, -3.4028234e38f);
+          ph = fminf(vh[j] * sc, 3.4028234e38f);
+          pl = fminf(pl, 3.4028234e38f);
+          ph = fmaxf(ph, -3.4028234e38f);
+          rl = fmaf(vl[j], sc, -pl);
+          rh = fmaf(vh[j], sc, -ph);
+        }
+        cl |= (static_cast<uint32_t>(step_down(pl, rl, inv)) & 0xffu) << (8 * j);
+        ch |= (static_cast<uint32_t>(step_up(ph, rh, inv)) & 0xffu) << (8 * j);
+      }
+      int8_t* dst = a.summary + head * (2 * D) + (lane % LPR) * (2 * NW) + 2 * kept;
+      if constexpr (CF == 4) {
+        *reinterpret_cast<uint32_t*>(dst) = cl;
+        *reinterpret_cast<uint32_t*>(dst + D) = ch;
+      } else {
+        static_assert(CF == 2, "two or four channels a lane");
+        *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(cl);
+        *reinterpret_cast<uint16_t*>(dst + D) = static_cast<uint16_t>(ch);
+      }
+      if (lane == 0) a.summary_scale[head] = exp2_int(e);
     }
-    code[i] = w;
-  }
-  if (lane / LPR < 2) {
-    const int64_t head = static_cast<int64_t>(id) * a.num_kv_heads + g;
-    int8_t* dst = a.summary + (head * 2 + (upper ? 1 : 0)) * D + (lane % LPR) * CH;
-    if constexpr (CH == 16)
-      *reinterpret_cast<uint4*>(dst) = make_uint4(code[0], code[1], code[2], code[3]);
-    else
-      *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
-    if (lane == 0) a.summary_scale[head] = exp2_int(e);
+    if (last) {
+      task += stride;
+      id = next_id;
+      next_id = id_after;
+      r0 = 0;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) lo[i] = hi[i] = kNone;
+    } else {
+      r0 += 16;
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) cur[i] = nxt[i];
   }
 }
 
@@ -646,9 +690,10 @@ cudaError_t launch_select_n(const SelectArgs& a, cudaStream_t stream) {
 
 template <int D, int KIND>
 cudaError_t launch_summarize_t(const SummarizeArgs& a, cudaStream_t stream) {
-  const int64_t tasks = static_cast<int64_t>(a.num_ids) * a.num_kv_heads;
-  return launch_pdl(summarize_blocks_kernel<D, KIND>, dim3(static_cast<unsigned>((tasks + 7) / 8)), dim3(256), 0,
-                    stream, a);
+  auto kern = summarize_blocks_kernel<D, KIND>;
+  const int64_t ctas = (static_cast<int64_t>(a.num_ids) * a.num_kv_heads + 7) / 8;
+  const int64_t most = resident_warp_slots(reinterpret_cast<const void*>(kern), 256, 0) / 8;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(min(ctas, most))), dim3(256), 0, stream, a);
 }
 
 }  // namespace

@@ -244,3 +244,31 @@ def test_refusals():
                dict(cs=s.cs[:, :100].contiguous()), dict(slots=s.slots[:2])):
         with pytest.raises(pkv.PkvError):
             f(**kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_fp8_codes_are_those_of_the_division(dtype):
+    """Values and scales whose quotients lie on, next to and far from rounding borders, beyond the largest
+    code, among the subnormals, and scales of every size (subnormal, zero, infinite and NaN among them):
+    bit for bit write_cache_fp8's codes."""
+    g = torch.Generator().manual_seed(3)
+    T, Hkv = 512, 8
+    s = Step(T=T, Hq=8, Hkv=Hkv, rot=0, qw=False, kw=False, fp8=True, dtype=dtype)
+    scales = torch.exp2(torch.randint(-20, 20, s.ks.shape, generator=g).float()) * (
+        1 + torch.randint(0, 64, s.ks.shape, generator=g) / 64)
+    odd = torch.tensor([1e-39, 2e38, 0.0, float("inf"), float("nan"), 1.0, 3e-38, 2.0 ** 127])
+    scales[::3] = odd
+    s.ks.copy_(scales)
+    s.vs.copy_(scales.flip(0))
+    # multiples of half a code step times the block's scale, as near as the type holds them
+    b = (s.slots.long() // 16).cpu()
+    border = (torch.randint(-127, 128, (T, Hkv, 128), generator=g) / 16) * torch.exp2(
+        torch.randint(-8, 8, (T, Hkv, 128), generator=g).float())
+    for x, sc in ((s.k, s.ks), (s.v, s.vs)):
+        y = border * sc.cpu()[b][..., None]
+        x.copy_(torch.nan_to_num(y, nan=1.5, posinf=3.0, neginf=-3.0).clamp(-60000, 60000).to(x.dtype))
+    kp, vp = s.kp.clone(), s.vp.clone()
+    s.call()
+    pkv.write_cache_fp8(s.k, s.v, kp, vp, s.ks, s.vs, s.slots)
+    torch.cuda.synchronize()
+    assert torch.equal(s.kp, kp) and torch.equal(s.vp, vp)
