@@ -281,122 +281,142 @@ __global__ void __launch_bounds__(128) norm_rope_write_kernel(const NormRopeArgs
   work.head(h, u0, u1);
 }
 
-// Many tokens: persistent CTAs, each streaming its tokens' rows and angle rows
-// through a ring of bulk copies into shared memory, so that what is in flight
-// does not depend on registers and the chain position -> angles is off the
-// path (loaded ahead by registers instead, the kernel stayed at 5.0 TB/s
-// whatever the heads per warp, 80 to 90 us for 16384 tokens of 32 + 16 heads).
-// A stage: the token's query heads, key heads, value heads, angle row.
+// Many tokens: persistent warps, each streaming its share of the (token, part)
+// tasks -- a part is kGroups * HPW adjacent heads -- through a private ring of
+// bulk copies into shared memory, a stage the part's rows and the token's
+// angle row.  What is in flight does not depend on registers then, the chain
+// position -> angles is off the path, and no warp waits for another.  (Loaded
+// by registers the kernel stayed at 5.0 TB/s whatever the heads per warp, 80
+// to 90 us for 16384 tokens of 32 + 16 heads; with a CTA per token and a
+// barrier a token it took 73 us.)
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
 
-constexpr int kStages = 4;
+constexpr int kGroups = 4, kStages = 2, kStreamWarps = 4;
+
+// Shared memory of one warp's ring: rows and angles, then position and slot, then the barrier of each stage.
+template <int D>
+constexpr int kStageBytes = kGroups * (32 / (D / 16)) * D * 2 + D * 4;
+template <int D>
+constexpr int kRingBytes = (kStages * (kStageBytes<D> + 16) + 127) / 128 * 128;
 
 template <int D, bool BF16, bool FP8>
-__global__ void __launch_bounds__(256) norm_rope_stream_kernel(const NormRopeArgs a, uint32_t stage_bytes) {
+__global__ void __launch_bounds__(kStreamWarps * 32) norm_rope_stream_kernel(const NormRopeArgs a, uint32_t parts) {
+  using Work = LaneWork<D, BF16, FP8>;
+  constexpr int kHeads = kGroups * Work::HPW, kRowBytes = D * 2, kAngles = kHeads * kRowBytes;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[kStages];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  LaneWork<D, BF16, FP8> work(a, lane);
-  const uint32_t ring = smem_u32(smem), bar0 = smem_u32(bars);
-  const uint32_t q_bytes = a.num_q_heads * D * 2, kv_bytes = a.num_kv_heads * D * 2, angle_bytes = a.rot_dim * 4;
-  if (threadIdx.x == 0) {
-    for (int st = 0; st < kStages; ++st) mbar_init(bar0 + 8 * st, 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Work work(a, lane);
+  uint8_t* ring = smem + warp * kRingBytes<D>;
+  int2* info = reinterpret_cast<int2*>(ring + kStages * kStageBytes<D>);  // position and slot of each stage
+  const uint32_t bars = smem_u32(info + kStages);
+  if (lane == 0) {
+    for (int st = 0; st < kStages; ++st) mbar_init(bars + 8 * st, 1);
     fence_barrier_init();
     fence_proxy_async_smem();
   }
-  __syncthreads();
+  __syncwarp();
 
-  const int64_t step = gridDim.x;
-  auto position = [&](int64_t t) { return a.rot_dim && t < a.num_tokens ? __ldg(a.positions + t) : 0; };
-  auto slot_of = [&](int64_t t) { return t < a.num_tokens ? __ldg(a.slot_mapping + t) : -1; };
-  auto issue = [&](int64_t t, int st, int pos) {  // one thread
-    if (t >= a.num_tokens) return;
-    const uint32_t bar = bar0 + 8 * st, dst = ring + st * stage_bytes;
-    if (!work.in_table(pos)) {
+  const uint32_t total = static_cast<uint32_t>(a.num_tokens) * parts;
+  const uint32_t step = gridDim.x * kStreamWarps, first = blockIdx.x * kStreamWarps + warp;
+  const uint32_t count = first < total ? (total - first + step - 1) / step : 0;  // this warp's tasks
+  auto token_of = [&](uint32_t j) { return static_cast<int64_t>((first + j * step) / parts); };
+  auto fetch = [&](uint32_t j) {  // task j's position and slot
+    if (j >= count) return make_int2(-1, -1);
+    const int64_t t = token_of(j);
+    return make_int2(a.rot_dim ? __ldg(a.positions + t) : 0, __ldg(a.slot_mapping + t));
+  };
+  auto issue = [&](uint32_t j, int2 at) {  // lane 0
+    if (j >= count) return;
+    const int st = j % kStages;
+    const uint32_t bar = bars + 8 * st, dst = smem_u32(ring) + st * kStageBytes<D>;
+    info[st] = at;
+    if (!work.in_table(at.x)) {
       mbar_arrive_expect_tx(bar, 0);
       return;
     }
-    mbar_arrive_expect_tx(bar, q_bytes + 2 * kv_bytes + angle_bytes);
-    bulk_load(dst, a.q + t * a.q_stride, q_bytes, bar);
-    bulk_load(dst + q_bytes, a.k + t * a.kv_stride, kv_bytes, bar);
-    bulk_load(dst + q_bytes + kv_bytes, a.v + t * a.kv_stride, kv_bytes, bar);
-    if (angle_bytes)
-      bulk_load(dst + q_bytes + 2 * kv_bytes, a.cos_sin + static_cast<int64_t>(pos) * a.rot_dim, angle_bytes, bar);
+    const int64_t t = token_of(j);
+    const int h0 = static_cast<int>((first + j * step) % parts) * kHeads, h1 = min(h0 + kHeads, work.heads);
+    mbar_arrive_expect_tx(bar, (h1 - h0) * kRowBytes + a.rot_dim * 4);
+    auto copy = [&](const uint16_t* rows, int lo, int hi) {  // heads [lo, hi) of a kind whose first head `rows` is
+      const int from = max(h0, lo), to = min(h1, hi);
+      if (from < to) bulk_load(dst + (from - h0) * kRowBytes, rows + (from - lo) * D, (to - from) * kRowBytes, bar);
+    };
+    copy(a.q + t * a.q_stride, 0, work.first_k);
+    copy(a.k + t * a.kv_stride, work.first_k, work.first_v);
+    copy(a.v + t * a.kv_stride, work.first_v, work.heads);
+    if (a.rot_dim) bulk_load(dst + kAngles, a.cos_sin + static_cast<int64_t>(at.x) * a.rot_dim, a.rot_dim * 4, bar);
   };
-  int64_t t = blockIdx.x;
-  int ahead = 0;  // thread 0: the position of the token whose copies go out next
-  if (threadIdx.x == 0) {
-    int first[kStages];
-    for (int st = 0; st < kStages; ++st) first[st] = position(t + st * step);
-    ahead = position(t + kStages * step);
-    for (int st = 0; st < kStages; ++st) issue(t + st * step, st, first[st]);
+
+  int2 ahead = make_int2(0, 0);
+  if (lane == 0) {
+    int2 at[kStages];
+    for (int j = 0; j < kStages; ++j) at[j] = fetch(j);
+    ahead = fetch(kStages);
+    for (int j = 0; j < kStages; ++j) issue(j, at[j]);
   }
-  int pos = position(t), slot = slot_of(t);
-  for (int i = 0; t < a.num_tokens; ++i, t += step) {
-    const int next_pos = position(t + step), next_slot = slot_of(t + step);
+  __syncwarp();
+  for (uint32_t i = 0; i < count; ++i) {
     const int st = i % kStages;
-    const bool ok = __all_sync(kFull, mbar_wait_bounded(bar0 + 8 * st, (i / kStages) & 1, a.timeout_ns));
-    if (ok) {
-      if (threadIdx.x == 0) work.report(pos, slot);
-      if (work.in_table(pos)) {
-        const uint8_t* stage = smem + st * stage_bytes;
-        work.begin(t, slot, reinterpret_cast<const float*>(stage + q_bytes + 2 * kv_bytes));
-        for (int h0 = warp * work.HPW; h0 < work.heads; h0 += warps * work.HPW) {
-          const int h = h0 + lane / work.LPH;
-          const uint4* row = reinterpret_cast<const uint4*>(stage + min(h, work.heads - 1) * (D * 2));
-          work.head(h, row[work.c0], row[work.c1]);
-        }
-      }
-    }
-    // Every warp is done with the stage; a timed-out wait anywhere ends the CTA.
-    if (__syncthreads_or(!ok)) {
-      if (warp == 0)  // copies in flight land before the CTA exits
-        for (int j = i; j < i + kStages && t + (j - i) * step < a.num_tokens; ++j)
-          mbar_wait_bounded(bar0 + 8 * (j % kStages), (j / kStages) & 1, a.timeout_ns);
-      if (threadIdx.x == 0) flag(a.dev_status, 16u);  // PKV_DEV_ERR_TIMEOUT; the output is undefined
+    if (!__all_sync(kFull, mbar_wait_bounded(bars + 8 * st, (i / kStages) & 1, a.timeout_ns))) {
+      for (uint32_t j = i; j < min(count, i + kStages); ++j)  // copies in flight land before the warp leaves
+        mbar_wait_bounded(bars + 8 * (j % kStages), (j / kStages) & 1, a.timeout_ns);
+      if (lane == 0) flag(a.dev_status, 16u);  // PKV_DEV_ERR_TIMEOUT; the output is undefined
       return;
     }
-    if (threadIdx.x == 0) {
-      issue(t + kStages * step, st, ahead);
-      ahead = position(t + (kStages + 1) * step);
+    const uint8_t* stage = ring + st * kStageBytes<D>;
+    const int2 at = info[st];
+    const int h0 = static_cast<int>((first + i * step) % parts) * kHeads;
+    if (h0 == 0 && lane == 0) work.report(at.x, at.y);
+    if (work.in_table(at.x)) {
+      work.begin(token_of(i), at.y, reinterpret_cast<const float*>(stage + kAngles));
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        const int hh = k * Work::HPW + lane / Work::LPH;  // past the last head: the stage's old contents, not stored
+        if (h0 + k * Work::HPW >= work.heads) break;
+        const uint4* row = reinterpret_cast<const uint4*>(stage + hh * kRowBytes);
+        work.head(h0 + hh, row[work.c0], row[work.c1]);
+      }
     }
-    pos = next_pos;
-    slot = next_slot;
+    __syncwarp();  // every lane is done with the stage
+    if (lane == 0) {
+      issue(i + kStages, ahead);
+      ahead = fetch(i + kStages + 1);
+    }
+    __syncwarp();
   }
 }
 
-// The streaming kernel from kManyWarps head groups a SM on, unless a token's
-// rows are too long for its ring.
-constexpr int kManyWarps = 64;
-constexpr uint32_t kMaxRing = 200 * 1024;
+// The streaming kernel from this many head groups a SM on; below, the direct
+// kernel's shorter start counts for more.  Microseconds direct / streaming at
+// 81, 162, 323 and 647 groups a SM (32 + 16 heads, 16 bits): 5.8 / 7.1,
+// 13.0 / 13.1, 24.0 / 20.2, 45.3 / 34.8; FP8 pools (32 + 8 heads) at 135,
+// 270 and 539: 11.0 / 13.1, 20.2 / 21.1, 37.2 / 35.5.
+template <bool FP8>
+constexpr int kManyTasks = FP8 ? 320 : 160;
 
 template <int D, bool BF16, bool FP8>
 cudaError_t launch_t(const NormRopeArgs& a, cudaStream_t stream) {
   constexpr int HPW = 32 / (D / 16);
   const int64_t heads = a.num_q_heads + 2LL * a.num_kv_heads, groups = (heads + HPW - 1) / HPW;
-  const int64_t stage = heads * D * 2 + a.rot_dim * 4;
-  if (a.num_tokens * groups < static_cast<int64_t>(kManyWarps) * current_sm_count(152) || stage * kStages > kMaxRing)
+  if (a.num_tokens * groups < static_cast<int64_t>(kManyTasks<FP8>) * current_sm_count(152))
     return launch_pdl(norm_rope_write_kernel<D, BF16, FP8>,
                       dim3(static_cast<unsigned>((a.num_tokens * groups + 3) / 4)), dim3(128), 0, stream, a,
                       static_cast<uint32_t>(groups));
-  // 4 to 8 warps, the number that leaves fewest idle in a token's last round.
-  int warps = 4;
-  for (int w = 5; w <= 8; ++w)
-    if ((groups + w - 1) / w * w <= (groups + warps - 1) / warps * warps) warps = w;
+  const int64_t parts = (groups + kGroups - 1) / kGroups;
   auto kern = norm_rope_stream_kernel<D, BF16, FP8>;
-  const uint32_t stage_bytes = static_cast<uint32_t>((stage + 127) & ~127LL);
-  const size_t smem = static_cast<size_t>(stage_bytes) * kStages;
+  constexpr size_t smem = static_cast<size_t>(kStreamWarps) * kRingBytes<D>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int64_t slots = resident_warp_slots(reinterpret_cast<const void*>(kern), warps * 32, smem) / warps;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(a.num_tokens < slots ? a.num_tokens : slots)), dim3(warps * 32),
-                    smem, stream, a, stage_bytes);
+  const int64_t ctas = (a.num_tokens * parts + kStreamWarps - 1) / kStreamWarps;
+  const int64_t slots = resident_warp_slots(reinterpret_cast<const void*>(kern), kStreamWarps * 32, smem) / kStreamWarps;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas < slots ? ctas : slots)), dim3(kStreamWarps * 32), smem,
+                    stream, a, static_cast<uint32_t>(parts));
 }
 
 }  // namespace
