@@ -201,10 +201,17 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return n;
 }
 
-// Barrier over all threads of the cluster; shared-memory writes before it
-// are seen by the cluster's CTAs after it.
+// Barrier over all threads of the cluster, whole or as its two halves;
+// shared-memory writes before it are seen by the cluster's CTAs after it.  A
+// CTA's shared memory may be written from another only once it has begun to
+// run: kernels arrive first thing and wait before their first remote store.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 
 // The address of this CTA's shared-memory object `addr` in CTA `rank` of the cluster.
@@ -218,10 +225,13 @@ __device__ __forceinline__ void cluster_store_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-__device__ __forceinline__ float cluster_load_float(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void cluster_store_float4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
+__device__ __forceinline__ void cluster_store_float(uint32_t addr, float v) {
+  cluster_store_u32(addr, __float_as_uint(v));
 }
 
 // ------------------------------------------------------------- tile geometry

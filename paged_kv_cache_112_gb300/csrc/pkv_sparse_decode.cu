@@ -25,7 +25,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kSparseWarps = 4;
+constexpr int kSparseMaxCluster = 8;
 
 // A tile's place: physical block, or -1 for a tile to be skipped, first row
 // and valid rows.
@@ -42,67 +42,83 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
   using Att = std::conditional_t<FP8, WarpAttentionFp8<128>, WarpAttention<D, BF16, true>>;
   constexpr int kRow = D + 4;                    // floats between a saved state's head rows
   constexpr int kState = 8 * kRow + 16;          // 8 rows, then running max and sum of each head
-  // Shared memory: rings, barriers, stage scales, the CTA's merged state.
-  constexpr size_t kScalesAt = static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 8);
-  constexpr size_t kStateAt = kScalesAt + static_cast<size_t>(NW) * NST * 8;
+  // Shared memory: rings, barriers, then what the cluster's CTAs send: per
+  // CTA its share of the rows, and running max and sum of each head.
+  constexpr size_t kInboxAt = static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 8);
   static_assert(kState * 4 <= NST * Geom::kStageBytes, "a saved state must fit its warp's ring");
   extern __shared__ __align__(1024) uint8_t smem[];
+  cluster_arrive();  // see the wait before the merge
   griddep_wait();
   griddep_launch_dependents();
-  if (smem_misaligned(smem, a.dev_status)) return;
+  if (smem_misaligned(smem, a.dev_status)) return;  // the same for every CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int64_t unit = blockIdx.x / C;
   const int s = static_cast<int>(unit / a.num_kv_heads), g = static_cast<int>(unit % a.num_kv_heads);
   const int G = a.group, B = 1 << a.block_shift;
-  const int L = clamped_len(a, s, g == 0 && rank == 0 && threadIdx.x == 0);
-  const int nblk = (L >> a.block_shift) + ((L & (B - 1)) ? 1 : 0);
+  const int32_t* list = sp.selected + unit * sp.keep;
+  const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
+  const int tshift = a.block_shift - 4;     // log2 of tiles per block
+  const int W = C * NW, w0 = rank * NW + warp;  // this warp's tiles of the list: w0, w0 + W, ...
+
+  // The list entry of the warp's tile i, the one before it, and its table
+  // entry: read before the length and the count are known (inside the list
+  // and the table whatever they are), so the chain is list -> table -> tile.
+  struct Entry {
+    int block, prev, phys;
+  };
+  auto fetch = [&](int i) {
+    Entry r{-1, -1, -1};
+    const int64_t e = (static_cast<int64_t>(i) * W + w0) >> tshift;
+    if (e >= sp.keep) return r;
+    r.block = __ldg(list + e);
+    r.prev = e > 0 ? __ldg(list + e - 1) : -1;
+    if (r.block >= 0 && r.block < a.max_blocks_per_seq) r.phys = __ldg(tbl + r.block);
+    return r;
+  };
+  const int raw_len = a.context_lens[s];
   int count = sp.counts[unit];
+  const Entry first = fetch(lane);
+  const int L = clamp_len(a, raw_len, g == 0 && rank == 0 && threadIdx.x == 0);
+  const int nblk = (L >> a.block_shift) + ((L & (B - 1)) ? 1 : 0);
   if (count < 0 || count > sp.keep) {
     if (rank == 0 && threadIdx.x == 0) flag(a.dev_status, 128u);  // PKV_DEV_ERR_SELECT
     count = count < 0 ? 0 : sp.keep;
   }
-  const int32_t* list = sp.selected + unit * sp.keep;
-  const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
-  const int tshift = a.block_shift - 4;  // log2 of tiles per block
   const int tiles = L > 0 ? count << tshift : 0;
-  const int W = C * NW, w0 = rank * NW + warp;  // this warp's tiles: w0, w0 + W, ...
   const int cnt = tiles > w0 ? (tiles - w0 + W - 1) / W : 0;
 
   // Place of this warp's tile i.  A list entry counts when it is larger than
   // its predecessor and inside the sequence, so no token counts twice.
-  auto place = [&](int i) {
+  auto place = [&](int i, const Entry& r) {
     TilePlace p{-1, 0, 0};
     if (i >= cnt) return p;
-    const int t = i * W + w0, e = t >> tshift;
-    const int b = __ldg(list + e), prev = e > 0 ? __ldg(list + e - 1) : -1;
-    if (b <= prev || b < 0 || b >= nblk) {
+    if (r.block <= r.prev || r.block < 0 || r.block >= nblk) {
       flag(a.dev_status, 128u);  // PKV_DEV_ERR_SELECT
       return p;
     }
-    const int phys = __ldg(tbl + b);
-    if (phys < 0 || phys >= a.num_blocks) {
+    if (r.phys < 0 || r.phys >= a.num_blocks) {
       flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK
       return p;
     }
-    p.phys = phys;
-    p.row0 = (t & ((1 << tshift) - 1)) * kTile;
-    p.nv = max(0, min(kTile, L - b * B - p.row0));
+    p.phys = r.phys;
+    p.row0 = ((i * W + w0) & ((1 << tshift) - 1)) * kTile;
+    p.nv = max(0, min(kTile, L - r.block * B - p.row0));
     return p;
   };
 
   WarpRing<D, NST, EB> ring{smem_u32(smem + static_cast<size_t>(warp) * NST * Geom::kStageBytes),
                             smem_u32(smem + static_cast<size_t>(NW) * NST * Geom::kStageBytes) + 8 * NST * warp};
   ring.init(lane);
-  // FP8: K and V scale of the tile in each stage.
-  float2* stage_scale = reinterpret_cast<float2*>(smem + kScalesAt) + warp * NST;
-
-  // Lane j holds the place (and scales) of the warp's tile j of a chunk of 32.
-  TilePlace cur = place(lane), nxt = place(32 + lane);
+  // Lane j holds the place (and scales) of the warp's tile j of a chunk of
+  // 32; the previous chunk's scales stay until its last tile is done.
+  TilePlace cur = place(lane, first);
+  Entry ahead = fetch(32 + lane);
   auto scale_of = [&](const float* sc, int phys) {
     return phys >= 0 ? __ldg(sc + static_cast<int64_t>(phys) * a.scale_stride + g) : 0.f;
   };
-  float ks = 0.f, vs = 0.f;
+  float ks = 0.f, vs = 0.f, ks_prev = 0.f, vs_prev = 0.f;
+  int chunk = 0;
   if constexpr (FP8) {
     ks = scale_of(a.k_scale, cur.phys);
     vs = scale_of(a.v_scale, cur.phys);
@@ -111,11 +127,14 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
   static_assert(NST <= 4, "stage_nv");
   auto issue = [&](int j) {
     if ((j & 31) == 0 && j > 0) {
-      cur = nxt;
-      nxt = place(j + 32 + lane);
+      cur = place(j + lane, ahead);
+      ahead = fetch(j + 32 + lane);
       if constexpr (FP8) {
+        ks_prev = ks;
+        vs_prev = vs;
         ks = scale_of(a.k_scale, cur.phys);
         vs = scale_of(a.v_scale, cur.phys);
+        chunk = j >> 5;
       }
     }
     const int st = j % NST, from = j & 31;
@@ -123,10 +142,6 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
     const int row0 = __shfl_sync(kFull, cur.row0, from);
     const int nv = __shfl_sync(kFull, cur.nv, from);
     stage_nv = (stage_nv & ~(0xffu << (8 * st))) | (static_cast<uint32_t>(nv) << (8 * st));
-    if constexpr (FP8) {
-      const float k = __shfl_sync(kFull, ks, from), v = __shfl_sync(kFull, vs, from);
-      if (lane == 0) stage_scale[st] = make_float2(k, v);
-    }
     ring.issue(j, max(phys, 0), -1, row0, g, &tmap_k, &tmap_v, lane);
   };
   auto nv_of = [&](int j) { return static_cast<int>((stage_nv >> (8 * (j % NST))) & 0xffu); };
@@ -155,7 +170,6 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
     const float sl2q = a.scale_log2 * at.template load_q<BF16>(q0, G, lane);
     int vexp = -126;
     float inv_unit = exp2i(126);
-    __syncwarp();
     for (int i = 0; i < cnt; i += 2) {
       const bool two = i + 1 < cnt;
       const bool ok = ring.wait(i, a.timeout_ns) && (!two || ring.wait(i + 1, a.timeout_ns));
@@ -164,17 +178,19 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
         if (lane == 0) flag(a.dev_status, 16u);
         break;
       }
+      const bool now = (i >> 5) == chunk;  // both tiles of a pair lie in one chunk
+      const float ksel = now ? ks : ks_prev, vsel = now ? vs : vs_prev;
       uint32_t sK[2];
       int nv[2];
       float sl2k[2], vsc[2], pv[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int j = two ? i + u : i;  // a missing second tile reuses the first one's stage, no valid token
-        const float2 sc = stage_scale[j % NST];
+        const float kj = __shfl_sync(kFull, ksel, j & 31), vj = __shfl_sync(kFull, vsel, j & 31);
         nv[u] = u == 1 && !two ? 0 : nv_of(j);
         sK[u] = ring.k_tile(j);
-        sl2k[u] = sl2q * sc.x;
-        vsc[u] = nv[u] > 0 ? sc.y : 0.f;
+        sl2k[u] = sl2q * kj;
+        vsc[u] = nv[u] > 0 ? vj : 0.f;
       }
       const float vmax = fmaxf(vsc[0], vsc[1]);
       const int e = min(max(static_cast<int>((__float_as_uint(vmax) >> 23) & 0xff) - 127, -126), 126);
@@ -189,7 +205,6 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
       __syncwarp();
       if (i + NST < cnt) issue(i + NST);
       if (i + 1 + NST < cnt) issue(i + 1 + NST);
-      __syncwarp();  // the stage scales written by lane 0
     }
     at.scale_acc(exp2i(vexp));
   }
@@ -217,73 +232,125 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
     }
   }
   __syncthreads();
-  // Merge over the warps: M = max m_w, acc = sum 2^(m_w - M) acc_w, l likewise.
-  auto merged = [&](int n, int h, int d, auto load, float& M, float& o, float& l) {
+  // Merge over the warps, four channels a thread:
+  //     M = max m_w, acc = sum 2^(m_w - M) acc_w, l = sum 2^(m_w - M) l_w.
+  auto merged = [&](int h, int d, float& M, float4& o, float& l) {
+    const float* st[NW];
+    float m[NW];
     M = kNegInf;
-    for (int w = 0; w < n; ++w) M = fmaxf(M, load(w, 8 * kRow + h));
-    const float mu = M == kNegInf ? 0.f : M;
-    o = l = 0.f;
-    for (int w = 0; w < n; ++w) {
-      const float c = exp2f(load(w, 8 * kRow + h) - mu);
-      o += load(w, h * kRow + d) * c;
-      l += load(w, 8 * kRow + 8 + h) * c;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      st[w] = reinterpret_cast<const float*>(smem + static_cast<size_t>(w) * NST * Geom::kStageBytes);
+      m[w] = st[w][8 * kRow + h];
+      M = fmaxf(M, m[w]);
     }
-  };
-  auto of_warp = [&](int w, int i) {
-    return reinterpret_cast<const float*>(smem + static_cast<size_t>(w) * NST * Geom::kStageBytes)[i];
+    const float mu = M == kNegInf ? 0.f : M;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float c = exp2f(m[w] - mu);
+      const float4 v = *reinterpret_cast<const float4*>(st[w] + h * kRow + d);
+      o.x += v.x * c;
+      o.y += v.y * c;
+      o.z += v.z * c;
+      o.w += v.w * c;
+      l += st[w][8 * kRow + 8 + h] * c;
+    }
   };
   const int64_t row0 = (static_cast<int64_t>(s) * a.num_q_heads + g * G) * D;
+  auto store4 = [&](int e, float4 o, float l) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    store_out(a.out, row0 + e, o.x * inv, a.out_dtype);
+    store_out(a.out, row0 + e + 1, o.y * inv, a.out_dtype);
+    store_out(a.out, row0 + e + 2, o.z * inv, a.out_dtype);
+    store_out(a.out, row0 + e + 3, o.w * inv, a.out_dtype);
+  };
   if (C == 1) {
-    for (int e = threadIdx.x; e < G * D; e += NW * 32) {
-      float M, o, l;
-      merged(NW, e / D, e % D, of_warp, M, o, l);
-      store_out(a.out, row0 + e, l > 0.f ? o / l : 0.f, a.out_dtype);
+    for (int e = 4 * threadIdx.x; e < G * D; e += 4 * NW * 32) {
+      float M, l;
+      float4 o;
+      merged(e / D, e % D, M, o, l);
+      store4(e, o, l);
     }
+    cluster_wait();
     return;
   }
-  float* mine = reinterpret_cast<float*>(smem + kStateAt);
-  for (int e = threadIdx.x; e < G * D; e += NW * 32) {
-    const int h = e / D, d = e % D;
-    float M, o, l;
-    merged(NW, h, d, of_warp, M, o, l);
-    mine[h * kRow + d] = o;
-    if (d == 0) {
-      mine[8 * kRow + h] = M;
-      mine[8 * kRow + 8 + h] = l;
+  // CTA r merges elements [r * per, r * per + per) of the group's rows over
+  // the cluster: every CTA stores its part of them, and its heads' max and
+  // sum, into r's shared memory.
+  const int per = G * D / C;  // a multiple of 4: D is at least 64, C at most 8
+  float* inbox = reinterpret_cast<float*>(smem + kInboxAt);  // [C][per], then [C][8] max, [C][8] sum
+  float* inbox_m = inbox + 8 * D;
+  float* inbox_l = inbox_m + 8 * kSparseMaxCluster;
+  __syncwarp();
+  cluster_wait();  // every CTA has begun
+  for (int e = 4 * threadIdx.x; e < G * D; e += 4 * NW * 32) {
+    const int h = e / D, d = e % D, to = e / per;
+    float M, l;
+    float4 o;
+    merged(h, d, M, o, l);
+    cluster_store_float4(cluster_map(smem_u32(inbox + rank * per + (e - to * per)), to), o);
+    if (d / 4 < C) {  // head h's max and sum, to CTA d / 4
+      cluster_store_float(cluster_map(smem_u32(inbox_m + rank * 8 + h), d / 4), M);
+      cluster_store_float(cluster_map(smem_u32(inbox_l + rank * 8 + h), d / 4), l);
     }
   }
   cluster_sync();
-  const uint32_t at_mine = smem_u32(mine);
-  auto of_cta = [&](int r, int i) { return cluster_load_float(cluster_map(at_mine + 4 * i, r)); };
-  for (int e = rank * NW * 32 + threadIdx.x; e < G * D; e += C * NW * 32) {
-    float M, o, l;
-    merged(C, e / D, e % D, of_cta, M, o, l);
-    store_out(a.out, row0 + e, l > 0.f ? o / l : 0.f, a.out_dtype);
+  for (int k = 4 * threadIdx.x; k < per; k += 4 * NW * 32) {
+    const int e = rank * per + k, h = e / D;
+    float M = kNegInf, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < kSparseMaxCluster; ++r)
+      if (r < C) M = fmaxf(M, inbox_m[r * 8 + h]);
+    const float mu = M == kNegInf ? 0.f : M;
+#pragma unroll
+    for (int r = 0; r < kSparseMaxCluster; ++r)
+      if (r < C) {
+        const float c = exp2f(inbox_m[r * 8 + h] - mu);
+        const float4 v = *reinterpret_cast<const float4*>(inbox + r * per + k);
+        o.x += v.x * c;
+        o.y += v.y * c;
+        o.z += v.z * c;
+        o.w += v.w * c;
+        l += inbox_l[r * 8 + h] * c;
+      }
+    store4(e, o, l);
   }
-  cluster_sync();  // no CTA leaves while another reads its shared memory
 }
 
-// CTAs per unit: doubled while the batch fills at most half of the resident
-// CTAs (kSparsePerSm a SM) and a warp keeps at least kSparseLeast tiles.
-constexpr int kSparsePerSm = 2, kSparseLeast = 2, kSparseMaxCluster = 8;
+template <int D, bool BF16, bool FP8, int NW>
+cudaError_t launch_sparse_nw(const DecodeArgs& a, const SparseArgs& sp, int C, const CUtensorMap& tk,
+                             const CUtensorMap& tv, cudaStream_t stream) {
+  using Geom = TileGeom<D, FP8 ? 1 : 2>;
+  constexpr int NST = FP8 ? 4 : 3;
+  constexpr size_t smem = static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 8) +
+                          (8 * D + 16 * kSparseMaxCluster) * sizeof(float);
+  auto kern = decode_sparse_kernel<D, BF16, FP8, NW, NST>;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(a.num_seqs) * a.num_kv_heads * C), dim3(NW * 32), smem, C,
+                            stream, a, sp, tk, tv);
+}
+
+// Fewer units than SMs: 8-warp CTAs, doubled per unit while they fit the SMs
+// once and a warp keeps at least kSparseLeast tiles.  Otherwise one CTA of 4
+// warps per unit, two on an SM at a time, whose starts and ends overlap.
+// Microseconds with 8 / 4 warps a CTA at 8 units of 128 tiles: 5.5 / 6.1, at
+// 64 (FP8): 12.1 / 13.2, at 2048 of 64 (f16): 168 / 158.
+constexpr int kSparseLeast = 2;
 
 template <int D, bool BF16, bool FP8>
 cudaError_t launch_sparse_t(const DecodeArgs& a, const SparseArgs& sp, const CUtensorMap& tk, const CUtensorMap& tv,
                             cudaStream_t stream) {
-  using Geom = TileGeom<D, FP8 ? 1 : 2>;
-  constexpr int NW = kSparseWarps, NST = FP8 ? 4 : 3;
-  const size_t smem = static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 16) + (8 * (D + 4) + 16) * sizeof(float);
-  auto kern = decode_sparse_kernel<D, BF16, FP8, NW, NST>;
-  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
-  if (e != cudaSuccess) return e;
-  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads, sms = current_sm_count(152);
+  if (units > sms) return launch_sparse_nw<D, BF16, FP8, 4>(a, sp, 1, tk, tv, stream);
   const int64_t tiles = min((static_cast<int64_t>(a.max_context_len) + kTile - 1) / kTile,
                             static_cast<int64_t>(sp.keep) << (a.block_shift - 4));
   int C = 1;
-  while (C < kSparseMaxCluster && units * C * 2 <= kSparsePerSm * current_sm_count(152) &&
-         tiles >= 2 * C * NW * kSparseLeast)
-    C *= 2;
-  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(units * C)), dim3(NW * 32), smem, C, stream, a, sp, tk, tv);
+  while (C < kSparseMaxCluster && units * C * 2 <= sms && tiles >= 2 * C * 8 * kSparseLeast) C *= 2;
+  return launch_sparse_nw<D, BF16, FP8, 8>(a, sp, C, tk, tv, stream);
 }
 
 }  // namespace

@@ -314,6 +314,7 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
   __shared__ int found[3];  // the bin, how many keys lie above it and in it
   __shared__ uint2 list[kListed];  // candidates left: key and block
   __shared__ int listed;
+  cluster_arrive();  // see the wait before the scores
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -362,6 +363,7 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
   if (rank == 0 && tid == 0) a.counts[unit] = count;
   if (n <= a.keep) {  // the same for every CTA of the cluster
     for (int i = rank * NT + tid; i < a.keep; i += C * NT) out[i] = i < n ? i : -1;
+    cluster_wait();
     return;
   }
   // This CTA scores blocks [lo_b, hi_b), whole steps of 32; the first CTA's keys[] receives all keys.
@@ -434,6 +436,8 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
   const float scale_b = exp2_int(max(q_exp[2 * tq + 1] - emax - 22, -126));
 
   const uint32_t keys_at = cluster_map(smem_u32(keys), 0);
+  __syncwarp();
+  cluster_wait();  // the first CTA has begun
   auto score = [&](const Group& u, int half, int base, float scales) {
     int c[4] = {0, 0, 0, 0};
 #pragma unroll
