@@ -89,7 +89,7 @@ pkv_status prepare_summarize(SummarizeArgs* a, void* summary, float* summary_sca
                              int num_blocks, int32_t* dev_status) {
   if (num_ids < 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0) return PKV_ERR_INVALID_ARG;
   if ((head_dim != 64 && head_dim != 128) || block_shift_of(block_size) < 4) return PKV_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(num_ids) * num_kv_heads > (1LL << 33)) return PKV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_ids) * num_kv_heads > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
   if (num_ids == 0) return PKV_OK;
   if (!summary || !summary_scale || !k_pool || !block_ids) return PKV_ERR_INVALID_ARG;
   if (!aligned(summary, 16) || !aligned(summary_scale, 4) || !aligned(k_pool, 16) || !aligned(block_ids, 4) ||

@@ -96,35 +96,48 @@ __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeAr
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t tasks = static_cast<int64_t>(a.num_ids) * a.num_kv_heads;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
-  int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t row_bytes = static_cast<int64_t>(a.num_kv_heads) * D * EB;
+  const int H = a.num_kv_heads;
+  const uint32_t first = blockIdx.x * 8 + (threadIdx.x >> 5), stride = gridDim.x * 8;  // in (listed block, head) pairs
+  const int step_i = static_cast<int>(stride / H), step_g = static_cast<int>(stride % H);
+  const int64_t row_bytes = static_cast<int64_t>(H) * D * EB;
   const int64_t lane_at = (lane / LPR) * row_bytes + (lane % LPR) * 16;
 
-  auto id_of = [&](int64_t k) { return k < tasks ? a.block_ids[k / a.num_kv_heads] : -1; };
-  // The step's rows; none for a task that is not there (-1 or out of range).
-  auto load = [&](uint4 (&u)[NL], int64_t k, int id, int r0) {
+  struct Pair {
+    int64_t i;  // index into block_ids
+    int g;
+  };
+  auto after = [&](Pair p) {
+    p.i += step_i;
+    p.g += step_g;
+    if (p.g >= H) {
+      p.g -= H;
+      ++p.i;
+    }
+    return p;
+  };
+  auto id_of = [&](const Pair& p) { return p.i < a.num_ids ? __ldg(a.block_ids + p.i) : -1; };
+  // A step's rows; none for a pair that is not there (-1 or out of range).
+  auto load = [&](uint4 (&u)[NL], const Pair& p, int id, int r0) {
     if (id < 0 || id >= a.num_blocks) return;
-    const uint8_t* src = a.k_pool + id * a.block_bytes + static_cast<int>(k % a.num_kv_heads) * (D * EB) +
-                         r0 * row_bytes + lane_at;
+    const uint8_t* src = a.k_pool + id * a.block_bytes + p.g * (D * EB) + r0 * row_bytes + lane_at;
 #pragma unroll
     for (int i = 0; i < NL; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(src + i * RPL * row_bytes));
   };
 
-  int id = id_of(task), next_id = id_of(task + stride), r0 = 0;
+  Pair now{first / H, static_cast<int>(first % H)}, next = after(now), later = after(next);
+  int id = id_of(now), next_id = id_of(next), r0 = 0;
   uint4 cur[NL], nxt[NL];
-  load(cur, task, id, 0);
+  load(cur, now, id, 0);
   uint32_t lo[NW], hi[NW];
 #pragma unroll
   for (int i = 0; i < NW; ++i) lo[i] = hi[i] = kNone;
-  while (task < tasks) {
+  while (now.i < a.num_ids) {
     const bool last = r0 + 16 >= a.block_size;
-    const int id_after = last ? id_of(task + 2 * stride) : 0;
+    const int later_id = last ? id_of(later) : 0;
     if (last)
-      load(nxt, task + stride, next_id, 0);
+      load(nxt, next, next_id, 0);
     else
-      load(nxt, task, id, r0 + 16);
+      load(nxt, now, id, r0 + 16);
     const bool there = id >= 0 && id < a.num_blocks;
     if (there) {
 #pragma unroll
@@ -145,7 +158,7 @@ __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeAr
           }
         }
       }
-    } else if (id != -1 && r0 == 0 && task % a.num_kv_heads == 0 && lane == 0) {
+    } else if (id != -1 && r0 == 0 && now.g == 0 && lane == 0) {
       flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK
     }
     if (last && there) {
@@ -172,12 +185,11 @@ __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeAr
       }
       // Values p + r, exactly: the keys themselves (r = 0), or code * scale
       // as its float32 product and the remainder.
-      const int g = static_cast<int>(task % a.num_kv_heads);
-      const int64_t head = static_cast<int64_t>(id) * a.num_kv_heads + g;
+      const int64_t head = static_cast<int64_t>(id) * H + now.g;
       const float most = KIND == 0 ? 65504.f : KIND == 1 ? __uint_as_float(0x7f7f0000u) : 448.f;
       float sc = 1.f;
       if constexpr (KIND == 2) {
-        sc = __ldg(a.k_scale + id * a.scale_stride + g);
+        sc = __ldg(a.k_scale + id * a.scale_stride + now.g);
         if (!(sc > 0.f) || sc > 3.4028234e38f) sc = 0.f;  // no such scale: the block counts as zeros
       }
       float vl[CF], vh[CF], top = 0.f;
@@ -221,9 +233,11 @@ __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeAr
       if (lane == 0) a.summary_scale[head] = exp2_int(e);
     }
     if (last) {
-      task += stride;
+      now = next;
+      next = later;
+      later = after(later);
       id = next_id;
-      next_id = id_after;
+      next_id = later_id;
       r0 = 0;
 #pragma unroll
       for (int i = 0; i < NW; ++i) lo[i] = hi[i] = kNone;
@@ -683,13 +697,17 @@ cudaError_t launch_select_t(const SelectArgs& a, int64_t cap, cudaStream_t strea
                             32 * words, words);
 }
 
-// 256 threads where a sequence may have more blocks than 128 threads score in
-// four chunks each: the first CTA's search of the keys takes half the time.
+// More threads where a sequence may have more blocks: each warp still scores
+// four chunks or more, and the first CTA's search of the keys is shared among
+// more threads (8 sequences of up to 8192 blocks: 58 us with 128 threads, 33.5
+// with 256, 31.9 with 512).
 template <int D, bool BF16>
 cudaError_t launch_select_n(const SelectArgs& a, cudaStream_t stream) {
   const int64_t cap = min(static_cast<int64_t>(a.max_blocks_per_seq),
                           (static_cast<int64_t>(a.max_context_len) + (1 << a.block_shift) - 1) >> a.block_shift);
-  return cap <= 512 ? launch_select_t<D, BF16, 128>(a, cap, stream) : launch_select_t<D, BF16, 256>(a, cap, stream);
+  return cap <= 512    ? launch_select_t<D, BF16, 128>(a, cap, stream)
+         : cap <= 2048 ? launch_select_t<D, BF16, 256>(a, cap, stream)
+                       : launch_select_t<D, BF16, 512>(a, cap, stream);
 }
 
 template <int D, int KIND>
