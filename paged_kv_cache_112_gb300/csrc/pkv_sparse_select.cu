@@ -21,26 +21,30 @@ using namespace dev;
 
 // ------------------------------------------------------------------ summary
 
-// The smallest e >= -126 such that p + r <= 127 * 2^e, where p >= 0 and r is
-// the part of an exact product that its float32 rounding p left out.
+// The smallest e >= -126 such that p + r <= 127 * 2^e, where p >= 0 is finite
+// and r is the part of an exact product that its float32 rounding p left out;
+// 0 for p = 0.  p = m 2^x with m in [1/2, 1): x - 7 while m <= 127/128
+// (fraction bits 0x7e0000), else x - 6; a subnormal p is below 127 * 2^-126.
 __device__ __forceinline__ int bound_exponent(float p, float r) {
-  if (!(p > 0.f)) return 0;
-  int x;
-  const float m = frexpf(p, &x);  // p = m 2^x, m in [1/2, 1)
-  const int e = (m < 0.9921875f || (m == 0.9921875f && r <= 0.f)) ? x - 7 : x - 6;
-  return max(e, -126);
+  const uint32_t u = __float_as_uint(p), frac = u & 0x7fffffu;
+  const int x = static_cast<int>(u >> 23) - 126;
+  const int e = x - 7 + (frac > 0x7e0000u || (frac == 0x7e0000u && r > 0.f));
+  return u == 0 ? 0 : max(e, -126);
 }
 
-// floor of (p + r) * 2^-e, r as above (inv = 2^-e).  A power of two scales p
-// exactly, so p + r crosses an integer only where p sits on it; a product
-// that underflowed to zero keeps p's sign.
-__device__ __forceinline__ int step_down(float p, float r, float inv) {
-  const float y = p * inv;
-  int c = __float2int_rd(y);
-  if (static_cast<float>(c) == y && (r < 0.f || (c == 0 && p < 0.f))) --c;
-  return c;
+// floor (ceil) of x * f as a byte, |x f| <= 127: added to 1.5 * 2^23 with one
+// rounding downwards (upwards), the exact product's integer part is the sum's
+// low bits, in two's complement.
+__device__ __forceinline__ uint32_t floor_bits(float x, float f) {
+  return __float_as_uint(__fmaf_rd(x, f, 12582912.f));
 }
-__device__ __forceinline__ int step_up(float p, float r, float inv) { return -step_down(-p, -r, inv); }
+__device__ __forceinline__ uint32_t ceil_bits(float x, float f) {
+  return __float_as_uint(__fmaf_ru(x, f, 12582912.f));
+}
+// The low bytes of four words.
+__device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
 
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
@@ -70,8 +74,7 @@ __device__ __forceinline__ float2 widen2(uint32_t w) {
   return __half22float2(*reinterpret_cast<__half2*>(&w));
 }
 
-// A finite number for a bound: NaN (a channel without a number) counts as 0,
-// an infinity as the type's largest value.
+// A finite number: NaN counts as 0, an infinity as the type's largest value.
 __device__ __forceinline__ float finite_bound(float x, float most) {
   return x == x ? fminf(fmaxf(x, -most), most) : 0.f;
 }
@@ -183,52 +186,63 @@ __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeAr
           }
         kept += upper ? left : 0;
       }
-      // Values p + r, exactly: the keys themselves (r = 0), or code * scale
-      // as its float32 product and the remainder.
+      // The bounds in float32; a channel without a number counts as 0, an
+      // infinity as the type's largest value.
       const int64_t head = static_cast<int64_t>(id) * H + now.g;
-      const float most = KIND == 0 ? 65504.f : KIND == 1 ? __uint_as_float(0x7f7f0000u) : 448.f;
-      float sc = 1.f;
-      if constexpr (KIND == 2) {
-        sc = __ldg(a.k_scale + id * a.scale_stride + now.g);
-        if (!(sc > 0.f) || sc > 3.4028234e38f) sc = 0.f;  // no such scale: the block counts as zeros
-      }
+      constexpr float kMost = KIND == 0 ? 65504.f : 3.3895313892515355e38f;
       float vl[CF], vh[CF], top = 0.f;
 #pragma unroll
       for (int i = 0; i < CF / 2; ++i) {
         const float2 l = widen2<BF16>(lo[i]), h = widen2<BF16>(hi[i]);
-        vl[2 * i] = finite_bound(l.x, most);
-        vl[2 * i + 1] = finite_bound(l.y, most);
-        vh[2 * i] = finite_bound(h.x, most);
-        vh[2 * i + 1] = finite_bound(h.y, most);
-        top = fmaxf(top, fmaxf(fmaxf(-vl[2 * i], vh[2 * i]), fmaxf(-vl[2 * i + 1], vh[2 * i + 1])));
+        vl[2 * i] = l.x == l.x ? l.x : 0.f;
+        vl[2 * i + 1] = l.y == l.y ? l.y : 0.f;
+        vh[2 * i] = l.x == l.x ? h.x : 0.f;
+        vh[2 * i + 1] = l.y == l.y ? h.y : 0.f;
       }
-      top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));  // top >= 0: its bits order as it does
-      const float ptop = fminf(top * sc, 3.4028234e38f);
-      const int e = bound_exponent(ptop, KIND == 2 ? fmaf(top, sc, -ptop) : 0.f);
-      const float inv = exp2_int(-e);
-      uint32_t cl = 0, ch = 0;
 #pragma unroll
       for (int j = 0; j < CF; ++j) {
-        float pl = vl[j], ph = vh[j], rl = 0.f, rh = 0.f;
-        if constexpr (KIND == 2) {
-          pl = fmaxf(vl[j] * sc, -3.4028234e38f);
-          ph = fminf(vh[j] * sc, 3.4028234e38f);
-          pl = fminf(pl, 3.4028234e38f);
-          ph = fmaxf(ph, -3.4028234e38f);
-          rl = fmaf(vl[j], sc, -pl);
-          rh = fmaf(vh[j], sc, -ph);
+        if constexpr (KIND != 2) {
+          vl[j] = fminf(fmaxf(vl[j], -kMost), kMost);
+          vh[j] = fminf(fmaxf(vh[j], -kMost), kMost);
         }
-        cl |= (static_cast<uint32_t>(step_down(pl, rl, inv)) & 0xffu) << (8 * j);
-        ch |= (static_cast<uint32_t>(step_up(ph, rh, inv)) & 0xffu) << (8 * j);
+        top = fmaxf(top, fmaxf(-vl[j], vh[j]));
+      }
+      top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));  // top >= 0: its bits order as it does
+      float factor, ptop = top, rtop = 0.f;  // value = factor * v
+      if constexpr (KIND == 2) {
+        factor = __ldg(a.k_scale + id * a.scale_stride + now.g);
+        if (!(factor > 0.f) || factor > 3.4028234e38f) factor = 0.f;  // no such scale: the block counts as zeros
+        ptop = top * factor;
+        rtop = fmaf(top, factor, -ptop);
+        if (ptop > 3.4028234e38f) {  // values beyond float32 count as its largest
+          ptop = 3.4028234e38f;
+          rtop = 0.f;
+#pragma unroll
+          for (int j = 0; j < CF; ++j) {
+            vl[j] = fminf(fmaxf(vl[j] * factor, -3.4028234e38f), 3.4028234e38f);
+            vh[j] = fminf(fmaxf(vh[j] * factor, -3.4028234e38f), 3.4028234e38f);
+          }
+          factor = 1.f;
+        }
+      } else {
+        factor = 1.f;
+      }
+      const int e = bound_exponent(ptop, rtop);
+      factor *= exp2_int(-e);  // exact: a power of two that keeps top * factor within 127
+      uint32_t cl[CF], ch[CF];
+#pragma unroll
+      for (int j = 0; j < CF; ++j) {
+        cl[j] = floor_bits(vl[j], factor);
+        ch[j] = ceil_bits(vh[j], factor);
       }
       int8_t* dst = a.summary + head * (2 * D) + (lane % LPR) * (2 * NW) + 2 * kept;
       if constexpr (CF == 4) {
-        *reinterpret_cast<uint32_t*>(dst) = cl;
-        *reinterpret_cast<uint32_t*>(dst + D) = ch;
+        *reinterpret_cast<uint32_t*>(dst) = pack_bytes(cl[0], cl[1], cl[2], cl[3]);
+        *reinterpret_cast<uint32_t*>(dst + D) = pack_bytes(ch[0], ch[1], ch[2], ch[3]);
       } else {
         static_assert(CF == 2, "two or four channels a lane");
-        *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(cl);
-        *reinterpret_cast<uint16_t*>(dst + D) = static_cast<uint16_t>(ch);
+        *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(__byte_perm(cl[0], cl[1], 0x0040));
+        *reinterpret_cast<uint16_t*>(dst + D) = static_cast<uint16_t>(__byte_perm(ch[0], ch[1], 0x0040));
       }
       if (lane == 0) a.summary_scale[head] = exp2_int(e);
     }
