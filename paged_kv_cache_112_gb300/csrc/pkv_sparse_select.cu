@@ -350,6 +350,9 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
   const int64_t unit = blockIdx.x / C;
   const int s = static_cast<int>(unit / a.num_kv_heads), g = static_cast<int>(unit % a.num_kv_heads);
   int L = a.context_lens[s];
+  // The table entries of a lone CTA's first blocks do not need the length: read along with it.
+  const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
+  const int early = C == 1 && tid < a.max_blocks_per_seq ? __ldg(tbl + tid) : -1;
 
   // Query codes, a head per warp: 4 channels a lane (D = 64: the lower half-warp).
   for (int h = warp; h < 8; h += NWARP) {
@@ -401,11 +404,9 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
 
   // A warp takes 32 consecutive blocks at a time; lane j holds block j's
   // table entry, fetched two chunks ahead, and its scale, one chunk ahead.
-  const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
   auto entry = [&](int b) {
     if (b + lane >= hi_b) return -1;
-    const int p = __ldg(tbl + b + lane);
-    return p;
+    return __ldg(tbl + b + lane);
   };
   auto checked = [&](int p, int b) {  // PKV_DEV_ERR_BLOCK: the block is scored last
     if (p >= 0 && p < a.num_blocks) return p;
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
     }
   };
   int b0 = lo_b + warp * 32;
-  int phys = entry(b0), ahead = entry(b0 + NT);
+  int phys = C == 1 ? (tid < hi_b ? early : -1) : entry(b0), ahead = entry(b0 + NT);
   phys = checked(phys, b0);
   float sc = scale_of(phys);
   Group even, odd;

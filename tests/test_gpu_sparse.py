@@ -441,3 +441,29 @@ def test_refusals():
         with pytest.raises(pkv.PkvError):
             pool = torch.zeros(s.NB, 16, 2, 128, dtype=torch.bfloat16, device="cuda")
             pkv.summarize_blocks(kw.get("summary", s.summary), kw.get("scale", s.scale), pool, kw.get("ids", ids))
+
+
+@pytest.mark.parametrize("n,keep", [(300, 8), (300, 200), (2500, 100), (9000, 700)])
+def test_selection_among_unusable_entries(n, keep):
+    """Blocks whose table entries lie outside the pool are taken last, the lowest first, when there are not
+    enough others; never in place of a usable one."""
+    s = Select([n * 16], keep=keep, first=1, last=2, seed=n)
+    bad = torch.randperm(n, generator=torch.Generator().manual_seed(n))[:n - keep // 2]
+    s.tables[0, bad[bad < n].cuda()] = -5
+    s.call()
+    s.check(pkv.DEV_ERR_BLOCK)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_selection_on_random_shapes(seed):
+    rng = np.random.default_rng(100 + seed)
+    for _ in range(6):
+        Hkv = int(rng.integers(1, 5))
+        keep = int(rng.integers(3, 200))
+        kw = dict(Hq=Hkv * int(rng.integers(1, 9)), Hkv=Hkv, D=int(rng.choice([64, 128])), B=int(rng.choice([16, 32, 64])),
+                  keep=keep, first=int(rng.integers(0, 2)), last=int(rng.integers(1, 3)),
+                  dtype=str(rng.choice(["bf16", "f16"])), ties=bool(rng.random() < 0.3))
+        lens = rng.integers(0, int(np.exp(rng.uniform(3, 11))), size=int(rng.integers(1, 5)))
+        s = Select(lens, seed=int(rng.integers(1 << 30)), **kw)
+        s.call()
+        s.check()
