@@ -467,9 +467,9 @@ pkv_status pkv_decode_step_partitions_fp8(void* out, const void* q, const void* 
  *   interleaved  : 0: channel i pairs with i + rot_dim / 2; 1: 2i with 2i + 1.
  *   cos_sin      : float32 [max_positions][rot_dim]: the rot_dim / 2 cosines
  *                  of a position, then its sines (NULL when rot_dim is 0).
- *   positions    : int32[num_tokens] (NULL when rot_dim is 0).  -1: a
- *                  padding token, for which nothing is read or written
- *                  anywhere.  Any other position outside the table sets
+ *   positions    : int32[num_tokens] (may be NULL when rot_dim is 0).  -1: a
+ *                  padding token, for which nothing is written anywhere.
+ *                  Any other negative position, or one past the table, sets
  *                  PKV_DEV_ERR_POSITION and is treated alike.
  *   slot_mapping : as pkv_write_cache; -1: the pools are not written (q_out
  *                  and k_out are).

@@ -137,7 +137,7 @@ struct NormRopeArgs {
   const uint16_t* q_weight;  // null: no norm
   const uint16_t* k_weight;
   const float* cos_sin;      // [max_positions][rot_dim]: cosines, then sines
-  const int32_t* positions;  // null when rot_dim is 0
+  const int32_t* positions;  // may be null when rot_dim is 0
   const int32_t* slot_mapping;
   void* k_pool;
   void* v_pool;

@@ -139,11 +139,11 @@ struct LaneWork {
     heads = first_v + a.num_kv_heads;
   }
 
-  // Whether token t with this position is worked on: -1 marks a padding
+  // Whether a token with this position is worked on: -1 marks a padding
   // token, for which nothing is written; any other position outside the
-  // table is treated alike and reported.
+  // table (negative, where nothing is rotated) is treated alike and reported.
   __device__ __forceinline__ bool in_table(int pos) const {
-    return a.rot_dim == 0 || (pos >= 0 && pos < a.max_positions);
+    return pos >= 0 && (a.rot_dim == 0 || pos < a.max_positions);
   }
   __device__ __forceinline__ void report(int pos, int slot) const {
     if (!in_table(pos)) {
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(128) norm_rope_write_kernel(const NormRopeArgs
     u1 = *(reinterpret_cast<const uint4*>(src) + work.c1);
   }
   const int slot = __ldg(a.slot_mapping + t);
-  const int pos = a.rot_dim ? __ldg(a.positions + t) : 0;
+  const int pos = a.positions ? __ldg(a.positions + t) : 0;
   if (part == 0 && lane == 0) work.report(pos, slot);
   if (!work.in_table(pos)) return;
   work.begin(t, slot, a.cos_sin + static_cast<int64_t>(pos) * a.rot_dim);
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32) norm_rope_stream_kernel(con
   auto fetch = [&](uint32_t j) {  // task j's position and slot
     if (j >= count) return make_int2(-1, -1);
     const int64_t t = token_of(j);
-    return make_int2(a.rot_dim ? __ldg(a.positions + t) : 0, __ldg(a.slot_mapping + t));
+    return make_int2(a.positions ? __ldg(a.positions + t) : 0, __ldg(a.slot_mapping + t));
   };
   auto issue = [&](uint32_t j, int2 at) {  // lane 0
     if (j >= count) return;

@@ -272,3 +272,59 @@ def test_fp8_codes_are_those_of_the_division(dtype):
     pkv.write_cache_fp8(s.k, s.v, kp, vp, s.ks, s.vs, s.slots)
     torch.cuda.synchronize()
     assert torch.equal(s.kp, kp) and torch.equal(s.vp, vp)
+
+
+@pytest.mark.parametrize("T", [24, 3000])
+def test_padding_without_rotation(T):
+    """Positions count without an angle table too: -1 is padding, other negative ones are reported."""
+    s = Step(T=T, rot=0, Hq=32, Hkv=8)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 1000
+    pos[5] = pos[T - 1] = -1
+    pos[7] = -2
+    kp = s.kp.clone()
+    pkv.norm_rope_write(s.q, s.k, s.v, s.kp, s.vp, s.slots, q_out=s.q_out, q_weight=s.qw, k_weight=s.kw, eps=1e-5,
+                        positions=pos, status=s.status)
+    torch.cuda.synchronize()
+    assert int(s.status.item()) == pkv.DEV_ERR_POSITION
+    left = [5, 7, T - 1]
+    assert torch.all(s.q_out[left] == 7.0)
+    at = s.slots.long()[left]
+    same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))
+    assert same(s.kp[at // s.B, at % s.B], kp[at // s.B, at % s.B])
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[left] = False
+    y, m = R.norm_rope(s.in64[0], f64(s.qw), 1e-5, None, False)
+    assert np.all((np.abs(f64(s.q_out) - y) <= 2.0 ** -8 * np.abs(y) + 2.0 ** -18 * m)[rest.numpy()])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kw", [dict(T=3001, Hq=32, Hkv=8, fused=True), dict(T=2500, Hq=9, Hkv=3, rot=64, interleaved=True),
+                                dict(T=5000, Hq=15, Hkv=5, D=64, rot=48, dtype="f16"),
+                                dict(T=1500, Hq=70, Hkv=7, in_place=True, k_out=True, dtype="f16", rot=0, qw=False)])
+def test_long_prompts(kw, fp8):
+    """Lengths at which rows are streamed, with odd head counts whose last part is ragged, padding tokens and
+    bad positions among them."""
+    s = Step(seed=7, fp8=fp8, **kw)
+    if s.rot:
+        s.pos[::501] = -1
+        s.pos[17] = 1 << 20
+    s.slots[::77] = -1
+    s.call()
+    s.check(pkv.DEV_ERR_POSITION if s.rot else 0)
+
+
+def test_pools_past_four_gigabytes():
+    """Slots whose rows lie beyond 2^32 bytes and 2^31 elements of the pools."""
+    T, Hq, Hkv, D, B, NB = 40, 8, 8, 128, 16, 140000
+    s = Step(T=T, Hq=Hq, Hkv=Hkv)
+    kp, vp = (torch.empty((NB, B, Hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    slots = (torch.arange(T, device="cuda") * 55987 + 5).to(torch.int32)
+    slots[-1] = NB * B - 1
+    pkv.norm_rope_write(s.q, s.k, s.v, kp, vp, slots, q_out=s.q_out, q_weight=s.qw, k_weight=s.kw, cos_sin=s.cs,
+                        positions=s.pos, status=s.status)
+    pkv.norm_rope_write(s.q, s.k, s.v, s.kp, s.vp, s.slots, q_out=s.q_out, q_weight=s.qw, k_weight=s.kw, cos_sin=s.cs,
+                        positions=s.pos, status=s.status)
+    torch.cuda.synchronize()
+    assert int(s.status.item()) == 0
+    for big, small in ((kp, s.kp), (vp, s.vp)):
+        assert torch.equal(big.view(-1, Hkv, D)[slots.long()], small.reshape(-1, Hkv, D)[s.slots.long()])

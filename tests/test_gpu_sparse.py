@@ -467,3 +467,59 @@ def test_selection_on_random_shapes(seed):
         s = Select(lens, seed=int(rng.integers(1 << 30)), **kw)
         s.call()
         s.check()
+
+
+def test_selection_at_the_block_limit():
+    """49152 blocks of one sequence are scored and searched; one more is refused."""
+    n = 49152
+    s = Select([n * 16], Hq=2, Hkv=1, D=64, keep=300)
+    s.tables = s.tables[:, :n].contiguous()
+    s.call()
+    s.check()
+    s.tables = torch.nn.functional.pad(s.tables, (0, 1), value=-1)
+    s.max_len += 1
+    with pytest.raises(pkv.PkvError):
+        s.call()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pools_and_summaries_past_four_gigabytes(fp8):
+    """Blocks beyond 2^32 bytes and 2^31 elements of the pools (and 2^31 bytes of the summaries)."""
+    Hkv, D, B = 8, 128, 16
+    NB = 290000 if fp8 else 140000
+    ids = torch.tensor([NB - 1, 5, NB - 7, NB // 2, 131071, 131072], dtype=torch.int32).cuda()
+    n = len(ids)
+    a = Attend([n * B - 3], Hq=8, Hkv=Hkv, keep=n, fp8=fp8, poison=False)
+    make = lambda: torch.empty((NB, B, Hkv, D), dtype=a.kp.dtype, device="cuda")
+    kp, vp = make(), make()
+    own = a.tables[0, :n].long()
+    kp[ids.long()], vp[ids.long()] = a.kp[own], a.vp[own]
+    if fp8:
+        ks, vs = (torch.empty((NB, Hkv), device="cuda") for _ in range(2))
+        ks[ids.long()], vs[ids.long()] = a.ks[own], a.vs[own]
+    summary = torch.empty((NB, Hkv, 2, D), dtype=torch.int8, device="cuda")
+    scale = torch.empty((NB, Hkv), device="cuda")
+    if fp8:
+        pkv.summarize_blocks_fp8(summary, scale, kp, ks, ids, status=a.status)
+    else:
+        pkv.summarize_blocks(summary, scale, kp, ids, status=a.status)
+    torch.cuda.synchronize()
+    keys = R.E4M3[a.kp.cpu().numpy()] * f64(a.ks)[:, None, :, None] if fp8 else f64(a.kp)
+    for i in range(n):
+        for g in range(Hkv):
+            codes, unit = R.summarize(keys[int(own[i]), :, g], MOST["fp8" if fp8 else "bf16"] if not fp8 else 3.4e38)
+            assert np.array_equal(summary[int(ids[i]), g].cpu().numpy(), codes) and float(scale[int(ids[i]), g]) == unit
+    sel = torch.empty((1, Hkv, 4), dtype=torch.int32, device="cuda")
+    cnt = torch.empty((1, Hkv), dtype=torch.int32, device="cuda")
+    pkv.select_blocks(sel, cnt, a.q, summary, scale, ids[None].contiguous(), a.cl, block_size=B, max_context_len=n * B,
+                      status=a.status)
+    torch.cuda.synchronize()
+    q = f64(a.q)
+    for g in range(Hkv):
+        sc = R.scores(q[0, g:g + 1], summary[ids.long(), g].cpu().numpy(), f64(scale)[ids.cpu().numpy(), g], MOST["bf16"])
+        assert sel[0, g].tolist() == R.select(sc, n, 4, 1, 1)
+    a.tables, a.kp, a.vp, own_tables = ids[None].contiguous(), kp, vp, a.tables
+    if fp8:
+        a.ks, a.vs = ks, vs
+    a.call()
+    a.check()
