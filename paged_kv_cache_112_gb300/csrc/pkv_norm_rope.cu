@@ -84,23 +84,23 @@ __device__ __forceinline__ uint4 narrow8(const F2 (&x)[4]) {
   return make_uint4(narrow2<BF16>(x[0]), narrow2<BF16>(x[1]), narrow2<BF16>(x[2]), narrow2<BF16>(x[3]));
 }
 
-// Eight e4m3 codes of x / scale, the division in IEEE float32.  x * (1 / scale)
-// is within 2^-22 of it (three roundings, of 2^-24 each); where the codes of
-// that product moved by 2^-21 either way agree, the quotient's code lies
-// between them and is the same, and only elsewhere (one element in some
-// 10^5, next to a rounding border) is the division carried out.  Scales whose
-// reciprocal is not a normal number always divide.
+// Eight e4m3 codes of x / scale, the division in IEEE float32.  x times the
+// reciprocal moved by 2^-21 either way is below and above the quotient (the
+// reciprocal, its move and the product round by 2^-24 each, as the division
+// does).  Where both have the same code, the quotient has it too; only
+// elsewhere (one element in some 10^5, next to a rounding border) is the
+// division carried out.  Scales whose reciprocal is not a normal number always
+// divide.
 __device__ __forceinline__ uint2 codes8(const F2 (&x)[4], float scale) {
   const float inv = __frcp_rn(scale);
-  const F2 ii = pair(inv, inv), down = pair(1.f - 4.76837158203125e-7f, 1.f - 4.76837158203125e-7f);
-  const F2 up = pair(1.f + 4.76837158203125e-7f, 1.f + 4.76837158203125e-7f);
-  uint32_t c[4], differ = fabsf(inv) < 1.17549435e-38f || fabsf(inv) > 3.4028234e38f;
+  const float below = inv * (1.f - 4.76837158203125e-7f), above = inv * (1.f + 4.76837158203125e-7f);
+  const F2 lo = pair(below, below), hi = pair(above, above);
+  uint32_t c[4], differ = fabsf(inv) < 1.17549435e-38f || fabsf(inv) > 3.4e38f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const F2 y = mul2(x[i], ii);
-    const float2 lo = halves(mul2(y, down)), hi = halves(mul2(y, up));
-    c[i] = fp8::e4m3x2_satfinite(lo.x, lo.y);
-    differ |= c[i] ^ fp8::e4m3x2_satfinite(hi.x, hi.y);
+    const float2 p = halves(mul2(x[i], lo)), q = halves(mul2(x[i], hi));
+    c[i] = fp8::e4m3x2_satfinite(p.x, p.y);
+    differ |= c[i] ^ fp8::e4m3x2_satfinite(q.x, q.y);
   }
   if (differ) {
 #pragma unroll
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(128) norm_rope_write_kernel(const NormRopeArgs
 }
 
 // Many tokens: persistent warps, each streaming its share of the (token, part)
-// tasks -- a part is kGroups * HPW adjacent heads -- through a private ring of
+// tasks -- a part is up to kGroups * HPW adjacent heads -- through a private ring of
 // bulk copies into shared memory, a stage the part's rows and the token's
 // angle row.  What is in flight does not depend on registers then, the chain
 // position -> angles is off the path, and no warp waits for another.  (Loaded
@@ -304,9 +304,11 @@ template <int D>
 constexpr int kRingBytes = (kStages * (kStageBytes<D> + 16) + 127) / 128 * 128;
 
 template <int D, bool BF16, bool FP8>
-__global__ void __launch_bounds__(kStreamWarps * 32) norm_rope_stream_kernel(const NormRopeArgs a, uint32_t parts) {
+__global__ void __launch_bounds__(kStreamWarps * 32) norm_rope_stream_kernel(const NormRopeArgs a, uint32_t parts,
+                                                                                int part_groups) {
   using Work = LaneWork<D, BF16, FP8>;
-  constexpr int kHeads = kGroups * Work::HPW, kRowBytes = D * 2, kAngles = kHeads * kRowBytes;
+  constexpr int kRowBytes = D * 2, kAngles = kGroups * Work::HPW * kRowBytes;
+  const int part_heads = part_groups * Work::HPW;
   extern __shared__ __align__(128) uint8_t smem[];
   griddep_wait();
   griddep_launch_dependents();
@@ -326,6 +328,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32) norm_rope_stream_kernel(con
   const uint32_t step = gridDim.x * kStreamWarps, first = blockIdx.x * kStreamWarps + warp;
   const uint32_t count = first < total ? (total - first + step - 1) / step : 0;  // this warp's tasks
   auto token_of = [&](uint32_t j) { return static_cast<int64_t>((first + j * step) / parts); };
+  auto first_head = [&](uint32_t j) { return static_cast<int>((first + j * step) % parts) * part_heads; };
   auto fetch = [&](uint32_t j) {  // task j's position and slot
     if (j >= count) return make_int2(-1, -1);
     const int64_t t = token_of(j);
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32) norm_rope_stream_kernel(con
       return;
     }
     const int64_t t = token_of(j);
-    const int h0 = static_cast<int>((first + j * step) % parts) * kHeads, h1 = min(h0 + kHeads, work.heads);
+    const int h0 = first_head(j), h1 = min(h0 + part_heads, work.heads);
     mbar_arrive_expect_tx(bar, (h1 - h0) * kRowBytes + a.rot_dim * 4);
     auto copy = [&](const uint16_t* rows, int lo, int hi) {  // heads [lo, hi) of a kind whose first head `rows` is
       const int from = max(h0, lo), to = min(h1, hi);
@@ -371,14 +374,14 @@ __global__ void __launch_bounds__(kStreamWarps * 32) norm_rope_stream_kernel(con
     }
     const uint8_t* stage = ring + st * kStageBytes<D>;
     const int2 at = info[st];
-    const int h0 = static_cast<int>((first + i * step) % parts) * kHeads;
+    const int h0 = first_head(i);
     if (h0 == 0 && lane == 0) work.report(at.x, at.y);
     if (work.in_table(at.x)) {
       work.begin(token_of(i), at.y, reinterpret_cast<const float*>(stage + kAngles));
 #pragma unroll
       for (int k = 0; k < kGroups; ++k) {
         const int hh = k * Work::HPW + lane / Work::LPH;  // past the last head: the stage's old contents, not stored
-        if (h0 + k * Work::HPW >= work.heads) break;
+        if (k >= part_groups || h0 + k * Work::HPW >= work.heads) break;
         const uint4* row = reinterpret_cast<const uint4*>(stage + hh * kRowBytes);
         work.head(h0 + hh, row[work.c0], row[work.c1]);
       }
@@ -408,7 +411,7 @@ cudaError_t launch_t(const NormRopeArgs& a, cudaStream_t stream) {
     return launch_pdl(norm_rope_write_kernel<D, BF16, FP8>,
                       dim3(static_cast<unsigned>((a.num_tokens * groups + 3) / 4)), dim3(128), 0, stream, a,
                       static_cast<uint32_t>(groups));
-  const int64_t parts = (groups + kGroups - 1) / kGroups;
+  const int64_t parts = (groups + kGroups - 1) / kGroups, part_groups = (groups + parts - 1) / parts;
   auto kern = norm_rope_stream_kernel<D, BF16, FP8>;
   constexpr size_t smem = static_cast<size_t>(kStreamWarps) * kRingBytes<D>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
@@ -416,7 +419,7 @@ cudaError_t launch_t(const NormRopeArgs& a, cudaStream_t stream) {
   const int64_t ctas = (a.num_tokens * parts + kStreamWarps - 1) / kStreamWarps;
   const int64_t slots = resident_warp_slots(reinterpret_cast<const void*>(kern), kStreamWarps * 32, smem) / kStreamWarps;
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas < slots ? ctas : slots)), dim3(kStreamWarps * 32), smem,
-                    stream, a, static_cast<uint32_t>(parts));
+                    stream, a, static_cast<uint32_t>(parts), static_cast<int>(part_groups));
 }
 
 }  // namespace

@@ -287,6 +287,7 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
 constexpr int kBins = 2048;
 constexpr int kListed = 512;      // candidates that are listed once no more are left
 constexpr int kAhead = 8;         // keys a thread reads ahead of using them
+constexpr int kWarpBlocks = 1024;  // up to here one warp searches the threshold
 constexpr int kRankBlocks = 256;  // up to here every key is ranked directly
 
 // Exclusive prefix sums of a pair of counts over the CTA's threads.
@@ -314,8 +315,8 @@ __device__ __forceinline__ int2 block_scan(int2 v, int2* warp_sums) {
   return before;
 }
 
-// One cluster of C CTAs per (sequence, KV head).  Every CTA scores a contiguous
-// share of the blocks and stores the order keys into the first CTA's shared
+// One cluster of C CTAs per (sequence, KV head).  Every CTA scores its share
+// of the blocks and stores the order keys into the first CTA's shared
 // memory; then the first CTA alone finds the keep-th largest key by
 // histograms over ever narrower ranges (2048 bins each) and writes the chosen
 // block numbers in order.  (Histograms kept by every CTA and added up through
@@ -350,9 +351,12 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
   const int64_t unit = blockIdx.x / C;
   const int s = static_cast<int>(unit / a.num_kv_heads), g = static_cast<int>(unit % a.num_kv_heads);
   int L = a.context_lens[s];
-  // The table entries of a lone CTA's first blocks do not need the length: read along with it.
+  // The cluster's warps take chunks of 32 blocks in turn.  Where the first ones
+  // are does not depend on the length: their table entries are read along with it.
   const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
-  const int early = C == 1 && tid < a.max_blocks_per_seq ? __ldg(tbl + tid) : -1;
+  const int stride = C * NT;
+  int b0 = rank * NT + warp * 32;
+  const int early = b0 + lane < a.max_blocks_per_seq ? __ldg(tbl + b0 + lane) : -1;
 
   // Query codes, a head per warp: 4 channels a lane (D = 64: the lower half-warp).
   for (int h = warp; h < 8; h += NWARP) {
@@ -397,20 +401,16 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
     cluster_wait();
     return;
   }
-  // This CTA scores blocks [lo_b, hi_b), whole steps of 32; the first CTA's keys[] receives all keys.
-  const int share = ((n + C - 1) / C + 31) & ~31;
-  const int lo_b = min(n, rank * share), hi_b = min(n, lo_b + share);
   const int first = a.first_blocks, last = n - a.last_blocks;  // blocks outside [first, last) are always taken
 
-  // A warp takes 32 consecutive blocks at a time; lane j holds block j's
-  // table entry, fetched two chunks ahead, and its scale, one chunk ahead.
+  // Lane j holds block j's table entry, fetched two chunks ahead, and its scale, one chunk ahead.
   auto entry = [&](int b) {
-    if (b + lane >= hi_b) return -1;
+    if (b + lane >= n) return -1;
     return __ldg(tbl + b + lane);
   };
   auto checked = [&](int p, int b) {  // PKV_DEV_ERR_BLOCK: the block is scored last
     if (p >= 0 && p < a.num_blocks) return p;
-    if (b + lane < hi_b) flag(a.dev_status, 4u);
+    if (b + lane < n) flag(a.dev_status, 4u);
     return -1;
   };
   auto scale_of = [&](int p) {
@@ -433,8 +433,7 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
       }
     }
   };
-  int b0 = lo_b + warp * 32;
-  int phys = C == 1 ? (tid < hi_b ? early : -1) : entry(b0), ahead = entry(b0 + NT);
+  int phys = b0 + lane < n ? early : -1, ahead = entry(b0 + stride);
   phys = checked(phys, b0);
   float sc = scale_of(phys);
   Group even, odd;
@@ -489,20 +488,20 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
     const int row = 16 * half + gr + 8 * (tq & 1);
     const float psc = __shfl_sync(kFull, scales, row);
     const int b = base + row;
-    if (tq < 2 && b < hi_b)
+    if (tq < 2 && b < n)
       cluster_store_u32(keys_at + 4 * b, psc >= 0.f ? order_key((tq ? best[1] : best[0]) * psc) : 0u);
   };
-  while (b0 < hi_b) {
+  while (b0 < n) {
     load(odd, phys, 1);
-    const int next = checked(ahead, b0 + NT);
-    ahead = entry(b0 + 2 * NT);
+    const int next = checked(ahead, b0 + stride);
+    ahead = entry(b0 + 2 * stride);
     const float next_sc = scale_of(next);
     score(even, 0, b0, sc);
     load(even, next, 0);
     score(odd, 1, b0, sc);
     phys = next;
     sc = next_sc;
-    b0 += NT;
+    b0 += stride;
   }
   cluster_sync();  // every key has arrived
   if (rank != 0) return;
@@ -516,17 +515,47 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
   int ties = 0;
   auto forced = [&](int b) { return b < first || b >= last; };
   if (n <= kRankBlocks) {
-    // Few blocks: each thread counts the middle keys that come before its own.
+    // Few blocks: each thread counts the middle keys above its own.  Forced
+    // blocks' keys become 0 first, below every score.
+    for (int b = tid; b < words * 32; b += NT)
+      if (b >= n || forced(b)) keys[b] = 0;
+    if (tid == 0) listed = 0;
+    __syncthreads();
+    const uint4* all = reinterpret_cast<const uint4*>(keys);
     for (int b = tid; b < words * 32; b += NT) {
-      bool take = b < n && forced(b);
-      if (b < n && !take) {
+      const uint32_t k = keys[b];
+      int part[4] = {0, 0, 0, 0};  // independent sums: with one warp a scheduler only these overlap
+      for (int j = 0; j < words * 8; j += 8) {
+        uint4 o[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) o[u] = all[j + u];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          part[0] += o[u].x > k;
+          part[1] += o[u].y > k;
+          part[2] += o[u].z > k;
+          part[3] += o[u].w > k;
+        }
+      }
+      const int above = part[0] + part[1] + part[2] + part[3];
+      const bool middle = b < n && !forced(b);
+      const uint32_t w = __ballot_sync(kFull, middle && above < need);
+      const uint32_t f = __ballot_sync(kFull, b < n && !middle);
+      if (lane == 0) {
+        sure_bits[b / 32] = w | f;
+        atomicAdd(&listed, __popc(w));
+      }
+    }
+    __syncthreads();
+    if (listed > need) {  // equal keys at the threshold: the lowest blocks of them
+      for (int b = tid; b < words * 32; b += NT) {
         const uint32_t k = keys[b];
+        const bool middle = b < n && !forced(b);
         int before = 0;
         for (int j = first; j < last; ++j) before += keys[j] > k || (keys[j] == k && j < b);
-        take = before < need;
+        const uint32_t w = __ballot_sync(kFull, middle ? before < need : b < n);
+        if (lane == 0) sure_bits[b / 32] = w;
       }
-      const uint32_t w = __ballot_sync(kFull, take);
-      if (lane == 0) sure_bits[b / 32] = w;
     }
     __syncthreads();
     for (int b = tid; b < words * 32; b += NT) {
@@ -534,6 +563,96 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
       int at = __popc(w & ((1u << lane) - 1));
       for (int i = 0; i < b / 32; ++i) at += __popc(sure_bits[i]);
       if ((w >> lane) & 1) out[at] = b;
+    }
+    return;
+  }
+  if (n <= kWarpBlocks) {
+    // One warp holds all keys (0, below every score, for those not to be
+    // chosen among) and halves the range until a bound has exactly `need`
+    // keys at or above it, or a single value is left: no barrier until then.
+    // (1 us less than the histograms below at 400 to 700 blocks, 1 more at 1500.)
+    constexpr int GROUP = 8, GROUPS = kWarpBlocks / (32 * GROUP);
+    if (warp == 0 && need > 0) {
+      uint32_t k[GROUPS][GROUP], low = 0xffffffffu, top = 0;
+#pragma unroll
+      for (int i = 0; i < GROUPS; ++i)
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j) {
+          const int b = (i * GROUP + j) * 32 + lane;
+          const bool middle = b < n && !forced(b);
+          k[i][j] = i * GROUP * 32 < n && middle ? keys[b] : 0u;
+          low = min(low, middle ? k[i][j] : 0xffffffffu);
+          top = max(top, k[i][j]);
+        }
+      // At least `need` keys are >= lo, `above` (fewer than `need`) are >= hi.
+      uint32_t lo = __reduce_min_sync(kFull, low), hi = __reduce_max_sync(kFull, top) + 1;
+      int above = 0;
+      uint32_t threshold = 0;
+      for (;;) {
+        if (hi - lo == 1) {
+          threshold = hi;
+          ties = need - above;
+          break;
+        }
+        const uint32_t mid = lo + (hi - lo) / 2;
+        int part[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i)
+          if (i * GROUP * 32 < n) {
+#pragma unroll
+            for (int j = 0; j < GROUP; ++j) part[j % 4] += k[i][j] >= mid;
+          }
+        const int c = __reduce_add_sync(kFull, (part[0] + part[1]) + (part[2] + part[3]));
+        if (c == need) {
+          threshold = mid;
+          break;
+        }
+        if (c > need)
+          lo = mid;
+        else
+          hi = mid, above = c;
+      }
+      if (lane == 0) {
+        found[0] = static_cast<int>(threshold);
+        found[1] = ties;
+      }
+    } else if (tid == 0) {
+      found[0] = -1;  // need == 0: no key reaches it
+      found[1] = 0;
+    }
+    __syncthreads();
+    const uint32_t threshold = static_cast<uint32_t>(found[0]);
+    ties = found[1];
+    for (int b = tid; b < words * 32; b += NT) {
+      const bool middle = b < n && !forced(b);
+      const uint32_t k = middle ? keys[b] : 0u;
+      const uint32_t w = __ballot_sync(kFull, middle ? k >= threshold : b < n);
+      const uint32_t v = __ballot_sync(kFull, middle && k + 1 == threshold && ties > 0);
+      if (lane == 0) {
+        sure_bits[b / 32] = w;
+        tie_bits[b / 32] = v;
+      }
+    }
+    __syncthreads();
+    // Counts before each word of 32 blocks (at most 32 words, one a lane).
+    int2* before = reinterpret_cast<int2*>(hist);
+    if (warp == 0) {
+      const int2 x = lane < words ? make_int2(__popc(sure_bits[lane]), __popc(tie_bits[lane])) : make_int2(0, 0);
+      int2 sum = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int p = __shfl_up_sync(kFull, sum.x, o), q = __shfl_up_sync(kFull, sum.y, o);
+        if (lane >= o) sum.x += p, sum.y += q;
+      }
+      before[lane] = make_int2(sum.x - x.x, sum.y - x.y);
+    }
+    __syncthreads();
+    const uint32_t below = (1u << lane) - 1;
+    for (int b = tid; b < words * 32; b += NT) {
+      const uint32_t w = sure_bits[b / 32], v = tie_bits[b / 32];
+      const int2 p = before[b / 32];
+      const int at = p.x + __popc(w & below), tie = p.y + __popc(v & below);
+      if (((w >> lane) & 1) || (((v >> lane) & 1) && tie < ties)) out[at + min(tie, ties)] = b;
     }
     return;
   }
@@ -694,15 +813,15 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
 }
 
 // CTAs per (sequence, KV head): doubled while the batch has fewer than
-// kSelWarps warps a SM and a CTA keeps at least 4 chunks a warp.
-constexpr int kSelWarps = 12, kSelMaxCluster = 8;
+// kSelWarps warps a SM and one CTA cannot take the blocks in one pass.
+constexpr int kSelWarps = 8, kSelMaxCluster = 8;
 
 template <int D, bool BF16, int NT>
 cudaError_t launch_select_t(const SelectArgs& a, int64_t cap, cudaStream_t stream) {
   auto kern = select_blocks_kernel<D, BF16, NT>;
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   int C = 1;
-  while (C < kSelMaxCluster && units * C * (NT / 32) < kSelWarps * current_sm_count(152) && cap >= 2 * C * NT) C *= 2;
+  while (C < kSelMaxCluster && units * C * (NT / 32) < kSelWarps * current_sm_count(152) && cap > C * NT) C *= 2;
   // Keys of the longest sequence, then the two bitmaps.
   const int words = static_cast<int>((cap + 31) / 32);
   const size_t smem = static_cast<size_t>(34) * words * sizeof(uint32_t);
