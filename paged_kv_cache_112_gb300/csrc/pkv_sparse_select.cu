@@ -329,7 +329,11 @@ __device__ __forceinline__ int2 block_scan(int2 v, int2* warp_sums) {
 // q has the same, it reads 16-byte chunks 4x + tq of a bound straight from
 // global memory and uses words 2i, 2i + 1 of chunk x in k-step 2x + i.  The
 // next 16 blocks' summaries are loaded before the current ones are used.
-template <int D, bool BF16, int NT>
+// With at most 4 heads (FEW) half of the product's columns would be idle and
+// the slow integer tensor path bound the kernel (18 us of an SM's 21 at 8
+// sequences of up to 8192 blocks): there the lower bounds take dp4a on the
+// same registers instead, the query's words from shared memory.
+template <int D, bool BF16, int NT, bool FEW>
 __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, int a_keys, int words_max) {
   constexpr int X = D / 64;      // 16-byte chunks of one bound per lane and row
   constexpr int NWARP = NT / 32;
@@ -444,24 +448,25 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
   // 2^-(22 + the largest exponent): the order stays, and integer * scale *
   // summary scale neither overflows nor, for the head with that exponent,
   // loses a bit (2^-22 * 2^-126 is a subnormal float32).
-  uint32_t qf[2][X][4];
+  uint32_t qf[X][4], qn[X][4];  // positive, negative parts
 #pragma unroll
-  for (int sign = 0; sign < 2; ++sign)
-#pragma unroll
-    for (int x = 0; x < X; ++x) {
-      const uint4 w = *reinterpret_cast<const uint4*>(&q_codes[sign][gr][16 * x + 4 * tq]);
-      qf[sign][x][0] = w.x;
-      qf[sign][x][1] = w.y;
-      qf[sign][x][2] = w.z;
-      qf[sign][x][3] = w.w;
+  for (int x = 0; x < X; ++x) {
+    const uint4 w = *reinterpret_cast<const uint4*>(&q_codes[1][gr][16 * x + 4 * tq]);
+    qf[x][0] = w.x, qf[x][1] = w.y, qf[x][2] = w.z, qf[x][3] = w.w;
+    if constexpr (!FEW) {
+      const uint4 v = *reinterpret_cast<const uint4*>(&q_codes[0][gr][16 * x + 4 * tq]);
+      qn[x][0] = v.x, qn[x][1] = v.y, qn[x][2] = v.z, qn[x][3] = v.w;
     }
+  }
   int emax = -126;
 #pragma unroll
   for (int h = 0; h < 8; ++h) emax = max(emax, q_exp[h]);
-  // The scales of heads 2 tq and 2 tq + 1 (columns of this lane's sums).
-  const bool live_a = 2 * tq < a.group, live_b = 2 * tq + 1 < a.group;
-  const float scale_a = exp2_int(max(q_exp[2 * tq] - emax - 22, -126));
-  const float scale_b = exp2_int(max(q_exp[2 * tq + 1] - emax - 22, -126));
+  // The scales of the heads whose sums this lane ends up with: 2 tq and
+  // 2 tq + 1, the product's columns; FEW: 2 (tq & 1) and the next.
+  const int head_a = 2 * (FEW ? tq & 1 : tq);
+  const bool live_a = head_a < a.group, live_b = head_a + 1 < a.group;
+  const float scale_a = exp2_int(max(q_exp[head_a] - emax - 22, -126));
+  const float scale_b = exp2_int(max(q_exp[head_a + 1] - emax - 22, -126));
 
   const uint32_t keys_at = cluster_map(smem_u32(keys), 0);
   __syncwarp();
@@ -470,11 +475,55 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
     int c[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int x = 0; x < X; ++x) {
-      const uint4 l0 = u.lo[0][x], l1 = u.lo[1][x], h0 = u.hi[0][x], h1 = u.hi[1][x];
-      mma_s8(c, l0.x, l1.x, l0.y, l1.y, qf[0][x][0], qf[0][x][1]);
-      mma_s8(c, l0.z, l1.z, l0.w, l1.w, qf[0][x][2], qf[0][x][3]);
-      mma_s8(c, h0.x, h1.x, h0.y, h1.y, qf[1][x][0], qf[1][x][1]);
-      mma_s8(c, h0.z, h1.z, h0.w, h1.w, qf[1][x][2], qf[1][x][3]);
+      const uint4 h0 = u.hi[0][x], h1 = u.hi[1][x];
+      mma_s8(c, h0.x, h1.x, h0.y, h1.y, qf[x][0], qf[x][1]);
+      mma_s8(c, h0.z, h1.z, h0.w, h1.w, qf[x][2], qf[x][3]);
+      if constexpr (!FEW) {
+        const uint4 l0 = u.lo[0][x], l1 = u.lo[1][x];
+        mma_s8(c, l0.x, l1.x, l0.y, l1.y, qn[x][0], qn[x][1]);
+        mma_s8(c, l0.z, l1.z, l0.w, l1.w, qn[x][2], qn[x][3]);
+      }
+    }
+    if constexpr (FEW) {
+      int d[2][4];  // [row gr, gr + 8][head]: this lane's channels
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        d[0][h] = d[1][h] = 0;
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+          const int4 w = *reinterpret_cast<const int4*>(&q_codes[0][h][16 * x + 4 * tq]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint4 l = u.lo[r][x];
+            d[r][h] = __dp4a(static_cast<int>(l.x), w.x, d[r][h]);
+            d[r][h] = __dp4a(static_cast<int>(l.y), w.y, d[r][h]);
+            d[r][h] = __dp4a(static_cast<int>(l.z), w.z, d[r][h]);
+            d[r][h] = __dp4a(static_cast<int>(l.w), w.w, d[r][h]);
+          }
+        }
+      }
+      // Sums over the four lanes of a row pair, halved with each exchange:
+      // lane tq ends up with row (tq & 2 ? gr + 8 : gr), heads 2 (tq & 1) and + 1.
+      const bool low_row = !(tq & 2), low_pair = !(tq & 1);
+      int e[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        e[h] = (low_row ? d[0][h] : d[1][h]) + __shfl_xor_sync(kFull, low_row ? d[1][h] : d[0][h], 2);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        e[i] = (low_pair ? e[i] : e[2 + i]) + __shfl_xor_sync(kFull, low_pair ? e[2 + i] : e[i], 1);
+      // The product's sums of row gr + 8 move to lanes 2 and 3 (its columns 4 to 7 are padding).
+      const int p = __shfl_xor_sync(kFull, c[2], 2), q = __shfl_xor_sync(kFull, c[3], 2);
+      const int ta = e[0] + (low_row ? c[0] : p), tb = e[1] + (low_row ? c[1] : q);
+      float top = fmaxf(live_a ? static_cast<float>(ta) * scale_a : kNegInf,
+                        live_b ? static_cast<float>(tb) * scale_b : kNegInf);
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+      const int row = 16 * half + gr + (low_row ? 0 : 8);
+      const float psc = __shfl_sync(kFull, scales, row);
+      const int b = base + row;
+      // A power of two after the maximum: the same as before it.
+      if (low_pair && b < n) cluster_store_u32(keys_at + 4 * b, psc >= 0.f ? order_key(top * psc) : 0u);
+      return;
     }
     float best[2];
 #pragma unroll
@@ -818,7 +867,7 @@ constexpr int kSelWarps = 8, kSelMaxCluster = 8;
 
 template <int D, bool BF16, int NT>
 cudaError_t launch_select_t(const SelectArgs& a, int64_t cap, cudaStream_t stream) {
-  auto kern = select_blocks_kernel<D, BF16, NT>;
+  auto kern = a.group <= 4 ? select_blocks_kernel<D, BF16, NT, true> : select_blocks_kernel<D, BF16, NT, false>;
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   int C = 1;
   while (C < kSelMaxCluster && units * C * (NT / 32) < kSelWarps * current_sm_count(152) && cap > C * NT) C *= 2;
