@@ -523,22 +523,22 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
       const int b = base + row;
       // A power of two after the maximum: the same as before it.
       if (low_pair && b < n) cluster_store_u32(keys_at + 4 * b, psc >= 0.f ? order_key(top * psc) : 0u);
-      return;
-    }
-    float best[2];
+    } else {
+      float best[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      best[r] = fmaxf(live_a ? static_cast<float>(c[2 * r]) * scale_a : kNegInf,
-                      live_b ? static_cast<float>(c[2 * r + 1]) * scale_b : kNegInf);
-      best[r] = fmaxf(best[r], __shfl_xor_sync(kFull, best[r], 1));
-      best[r] = fmaxf(best[r], __shfl_xor_sync(kFull, best[r], 2));
+      for (int r = 0; r < 2; ++r) {
+        best[r] = fmaxf(live_a ? static_cast<float>(c[2 * r]) * scale_a : kNegInf,
+                        live_b ? static_cast<float>(c[2 * r + 1]) * scale_b : kNegInf);
+        best[r] = fmaxf(best[r], __shfl_xor_sync(kFull, best[r], 1));
+        best[r] = fmaxf(best[r], __shfl_xor_sync(kFull, best[r], 2));
+      }
+      // Lanes tq = 0 and 1 store rows gr and gr + 8 (a power of two after the maximum: the same as before it).
+      const int row = 16 * half + gr + 8 * (tq & 1);
+      const float psc = __shfl_sync(kFull, scales, row);
+      const int b = base + row;
+      if (tq < 2 && b < n)
+        cluster_store_u32(keys_at + 4 * b, psc >= 0.f ? order_key((tq ? best[1] : best[0]) * psc) : 0u);
     }
-    // Lanes tq = 0 and 1 store rows gr and gr + 8 (a power of two after the maximum: the same as before it).
-    const int row = 16 * half + gr + 8 * (tq & 1);
-    const float psc = __shfl_sync(kFull, scales, row);
-    const int b = base + row;
-    if (tq < 2 && b < n)
-      cluster_store_u32(keys_at + 4 * b, psc >= 0.f ? order_key((tq ? best[1] : best[0]) * psc) : 0u);
   };
   while (b0 < n) {
     load(odd, phys, 1);
@@ -783,38 +783,32 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
       if (in_bin == need || shift == 0) break;
       shift = max(0, shift - 11);
       if (!in_list && in_bin <= kListed) {
-        for (int i0 = tid; i0 < words * 32; i0 += kAhead * NT) {
-          uint32_t k[kAhead];
+        for (int i0 = tid; i0 < words * 32; i0 += 2 * kAhead * NT) {
+          uint32_t k[2 * kAhead], open = 0;  // keys; which of them are candidates
 #pragma unroll
-          for (int u = 0; u < kAhead; ++u) k[u] = keys[min(i0 + u * NT, n - 1)];
+          for (int u = 0; u < 2 * kAhead; ++u) k[u] = keys[min(i0 + u * NT, n - 1)];
 #pragma unroll
-          for (int u = 0; u < kAhead; ++u) {
+          for (int u = 0; u < 2 * kAhead; ++u) {
             const int b = i0 + u * NT;
-            if (b >= words * 32) break;  // the same for a whole warp
-            const bool mid = b < n && !forced(b);
-            const uint32_t w = __ballot_sync(kFull, (b < n && !mid) || (mid && k[u] > lo && k[u] - lo > width));
-            const uint32_t open = __ballot_sync(kFull, mid && k[u] >= lo && k[u] - lo <= width);
-            if (lane == 0) {
-              sure_bits[b / 32] = w;
-              tie_bits[b / 32] = open;
+            if (b < words * 32) {  // the same for a whole warp
+              const bool mid = b < n && !forced(b), in = mid && k[u] >= lo;
+              const bool above = in && k[u] - lo > width;
+              const uint32_t w = __ballot_sync(kFull, (b < n && !mid) || above);
+              if (lane == 0) {
+                sure_bits[b / 32] = w;
+                tie_bits[b / 32] = 0;
+              }
+              if (in && !above) open |= 1u << u;
             }
+          }
+          if (open) {  // one atomic a thread that has any; their order in the list does not matter
+            int at = atomicAdd(&listed, __popc(open));
+#pragma unroll
+            for (int u = 0; u < 2 * kAhead; ++u)
+              if ((open >> u) & 1) list[at++] = make_uint2(k[u], static_cast<uint32_t>(i0 + u * NT));
           }
         }
         __syncthreads();
-        for (int w0 = 0; w0 < words; w0 += NT) {
-          const int w = w0 + tid;
-          uint32_t open = w < words ? tie_bits[w] : 0u;
-          int at = listed + block_scan<NT>(make_int2(__popc(open), 0), warp_sums).x;
-          const int end = at + __popc(open);
-          for (; open; open &= open - 1, ++at) {
-            const int b = w * 32 + __ffs(open) - 1;
-            list[at] = make_uint2(keys[b], static_cast<uint32_t>(b));
-          }
-          if (w < words) tie_bits[w] = 0;
-          __syncthreads();
-          if (tid == NT - 1) listed = end;
-          __syncthreads();
-        }
         in_list = true;
       }
     }
