@@ -79,57 +79,61 @@ __device__ __forceinline__ float finite_bound(float x, float most) {
   return x == x ? fminf(fmaxf(x, -most), most) : 0.f;
 }
 
-// A warp takes (listed block, KV head) pairs in turn.  Rows of D * EB bytes
-// are read as 16-byte vectors, 32 / LPR rows at a time and 16 rows a step,
-// the next step's rows on their way while the current ones are compared.
-// Each lane keeps the packed min and max of its channels; the row groups then
-// halve their channels with every exchange, so each lane ends up with CF of
-// them, rounds their bounds and stores the codes.  KIND: 0 = f16, 1 = bf16,
-// 2 = FP8 (codes compared as f16, which holds every e4m3 value).
+// A warp takes (listed block, HPT adjacent KV heads) tasks in turn: as many
+// heads as make 256 bytes of a row.  The rows are read as 16-byte vectors, two
+// rows at a time and 16 rows a step, the next step's rows on their way while
+// the current ones are compared.  Each lane keeps the packed min and max of
+// its channels; the two row groups then exchange halves, so each lane ends up
+// with NW channels, rounds their bounds and stores the codes.  KIND: 0 = f16,
+// 1 = bf16, 2 = FP8 (codes compared as f16, which holds every e4m3 value).
+//
+// Bound: 16-bit pools HBM (8192 blocks of 8 heads in 46 us, 6.2 TB/s of keys);
+// FP8 pools the instruction rate (a code costs as many as a 16-bit key).
 template <int D, int KIND>
 __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeArgs a) {
   constexpr int EB = KIND == 2 ? 1 : 2;
   constexpr bool BF16 = KIND == 1;
-  constexpr int LPR = D * EB / 16;  // lanes per row
-  constexpr int RPL = 32 / LPR;     // rows per load
-  constexpr int NL = 16 / RPL;      // loads per step
-  constexpr int NW = KIND == 2 ? 8 : 4;  // packed pairs of channels per lane
-  constexpr int CF = 2 * NW / RPL;       // channels per lane in the end
+  constexpr int HPT = 256 / (D * EB);  // heads per task
+  constexpr int LPR = 16;              // lanes per row
+  constexpr int LPH = LPR / HPT;       // lanes per head and row
+  constexpr int NL = 8;                // loads per step of 16 rows
+  constexpr int NW = KIND == 2 ? 8 : 4;  // packed pairs of channels per lane; channels it ends up with
   constexpr uint32_t kNone = BF16 ? 0x7fc07fc0u : 0x7e007e00u;  // NaN: no number yet
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int H = a.num_kv_heads;
-  const uint32_t first = blockIdx.x * 8 + (threadIdx.x >> 5), stride = gridDim.x * 8;  // in (listed block, head) pairs
-  const int step_i = static_cast<int>(stride / H), step_g = static_cast<int>(stride % H);
+  const int H = a.num_kv_heads, GH = (H + HPT - 1) / HPT;  // tasks per block
+  const uint32_t first = blockIdx.x * 8 + (threadIdx.x >> 5), stride = gridDim.x * 8;
+  const int step_i = static_cast<int>(stride / GH), step_g = static_cast<int>(stride % GH);
   const int64_t row_bytes = static_cast<int64_t>(H) * D * EB;
   const int64_t lane_at = (lane / LPR) * row_bytes + (lane % LPR) * 16;
+  const int sub = (lane % LPR) / LPH;  // this lane's head within the task
 
-  struct Pair {
+  struct Task {
     int64_t i;  // index into block_ids
-    int g;
+    int g;      // group of HPT heads
   };
-  auto after = [&](Pair p) {
+  auto after = [&](Task p) {
     p.i += step_i;
     p.g += step_g;
-    if (p.g >= H) {
-      p.g -= H;
+    if (p.g >= GH) {
+      p.g -= GH;
       ++p.i;
     }
     return p;
   };
-  auto id_of = [&](const Pair& p) { return p.i < a.num_ids ? __ldg(a.block_ids + p.i) : -1; };
-  // A step's rows; none for a pair that is not there (-1 or out of range).
-  auto load = [&](uint4 (&u)[NL], const Pair& p, int id, int r0) {
-    if (id < 0 || id >= a.num_blocks) return;
-    const uint8_t* src = a.k_pool + id * a.block_bytes + p.g * (D * EB) + r0 * row_bytes + lane_at;
+  auto id_of = [&](const Task& p) { return p.i < a.num_ids ? __ldg(a.block_ids + p.i) : -1; };
+  // A step's rows; none for a block that is not there (-1 or out of range) or a head past the last.
+  auto load = [&](uint4 (&u)[NL], const Task& p, int id, int r0) {
+    if (id < 0 || id >= a.num_blocks || p.g * HPT + sub >= H) return;
+    const uint8_t* src = a.k_pool + id * a.block_bytes + p.g * 256 + r0 * row_bytes + lane_at;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(src + i * RPL * row_bytes));
+    for (int i = 0; i < NL; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(src + 2 * i * row_bytes));
   };
 
-  Pair now{first / H, static_cast<int>(first % H)}, next = after(now), later = after(next);
+  Task now{first / GH, static_cast<int>(first % GH)}, next = after(now), later = after(next);
   int id = id_of(now), next_id = id_of(next), r0 = 0;
-  uint4 cur[NL], nxt[NL];
+  uint4 cur[NL] = {}, nxt[NL] = {};
   load(cur, now, id, 0);
   uint32_t lo[NW], hi[NW];
 #pragma unroll
@@ -165,34 +169,27 @@ __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeAr
       flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK
     }
     if (last && there) {
-      // Row groups: each exchange keeps half of the pairs, picked by the lane's bit.
-      int kept = 0, left = NW;
+      // The row groups exchange halves of their pairs: lanes 16 and up keep the upper.
+      const bool upper = lane & 16;
 #pragma unroll
-      for (int o = 16; o >= LPR; o >>= 1) {
-        left /= 2;
-        const bool upper = lane & o;
-#pragma unroll
-        for (int i = 0; i < NW / 2; ++i)
-          if (i < left) {
-            uint32_t dump;
-            const uint32_t l = __shfl_xor_sync(kFull, upper ? lo[i] : lo[i + left], o);
-            const uint32_t h = __shfl_xor_sync(kFull, upper ? hi[i] : hi[i + left], o);
-            lo[i] = upper ? lo[i + left] : lo[i];
-            hi[i] = upper ? hi[i + left] : hi[i];
-            dump = lo[i];
-            min_max2<BF16>(lo[i], dump, l);
-            dump = hi[i];
-            min_max2<BF16>(dump, hi[i], h);
-          }
-        kept += upper ? left : 0;
+      for (int i = 0; i < NW / 2; ++i) {
+        const uint32_t l = __shfl_xor_sync(kFull, upper ? lo[i] : lo[i + NW / 2], 16);
+        const uint32_t h = __shfl_xor_sync(kFull, upper ? hi[i] : hi[i + NW / 2], 16);
+        lo[i] = upper ? lo[i + NW / 2] : lo[i];
+        hi[i] = upper ? hi[i + NW / 2] : hi[i];
+        uint32_t dump = lo[i];
+        min_max2<BF16>(lo[i], dump, l);
+        dump = hi[i];
+        min_max2<BF16>(dump, hi[i], h);
       }
       // The bounds in float32; a channel without a number counts as 0, an
       // infinity as the type's largest value.
-      const int64_t head = static_cast<int64_t>(id) * H + now.g;
+      const int head = now.g * HPT + sub;
+      const int64_t at = static_cast<int64_t>(id) * H + min(head, H - 1);
       constexpr float kMost = KIND == 0 ? 65504.f : 3.3895313892515355e38f;
-      float vl[CF], vh[CF], top = 0.f;
+      float vl[NW], vh[NW], top = 0.f;
 #pragma unroll
-      for (int i = 0; i < CF / 2; ++i) {
+      for (int i = 0; i < NW / 2; ++i) {
         const float2 l = widen2<BF16>(lo[i]), h = widen2<BF16>(hi[i]);
         vl[2 * i] = l.x == l.x ? l.x : 0.f;
         vl[2 * i + 1] = l.y == l.y ? l.y : 0.f;
@@ -200,17 +197,23 @@ __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeAr
         vh[2 * i + 1] = l.y == l.y ? h.y : 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < CF; ++j) {
+      for (int j = 0; j < NW; ++j) {
         if constexpr (KIND != 2) {
           vl[j] = fminf(fmaxf(vl[j], -kMost), kMost);
           vh[j] = fminf(fmaxf(vh[j], -kMost), kMost);
         }
         top = fmaxf(top, fmaxf(-vl[j], vh[j]));
       }
-      top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));  // top >= 0: its bits order as it does
+      if constexpr (HPT == 1) {
+        top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));  // top >= 0: its bits order as it does
+      } else {
+#pragma unroll
+        for (int o = 1; o < LPH; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+      }
       float factor, ptop = top, rtop = 0.f;  // value = factor * v
       if constexpr (KIND == 2) {
-        factor = __ldg(a.k_scale + id * a.scale_stride + now.g);
+        factor = __ldg(a.k_scale + id * a.scale_stride + min(head, H - 1));
         if (!(factor > 0.f) || factor > 3.4028234e38f) factor = 0.f;  // no such scale: the block counts as zeros
         ptop = top * factor;
         rtop = fmaf(top, factor, -ptop);
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeAr
           ptop = 3.4028234e38f;
           rtop = 0.f;
 #pragma unroll
-          for (int j = 0; j < CF; ++j) {
+          for (int j = 0; j < NW; ++j) {
             vl[j] = fminf(fmaxf(vl[j] * factor, -3.4028234e38f), 3.4028234e38f);
             vh[j] = fminf(fmaxf(vh[j] * factor, -3.4028234e38f), 3.4028234e38f);
           }
@@ -229,22 +232,25 @@ __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeAr
       }
       const int e = bound_exponent(ptop, rtop);
       factor *= exp2_int(-e);  // exact: a power of two that keeps top * factor within 127
-      uint32_t cl[CF], ch[CF];
+      uint32_t cl[NW], ch[NW];
 #pragma unroll
-      for (int j = 0; j < CF; ++j) {
+      for (int j = 0; j < NW; ++j) {
         cl[j] = floor_bits(vl[j], factor);
         ch[j] = ceil_bits(vh[j], factor);
       }
-      int8_t* dst = a.summary + head * (2 * D) + (lane % LPR) * (2 * NW) + 2 * kept;
-      if constexpr (CF == 4) {
-        *reinterpret_cast<uint32_t*>(dst) = pack_bytes(cl[0], cl[1], cl[2], cl[3]);
-        *reinterpret_cast<uint32_t*>(dst + D) = pack_bytes(ch[0], ch[1], ch[2], ch[3]);
-      } else {
-        static_assert(CF == 2, "two or four channels a lane");
-        *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(__byte_perm(cl[0], cl[1], 0x0040));
-        *reinterpret_cast<uint16_t*>(dst + D) = static_cast<uint16_t>(__byte_perm(ch[0], ch[1], 0x0040));
+      if (head < H) {
+        int8_t* dst = a.summary + at * (2 * D) + (lane % LPH) * (2 * NW) + (upper ? NW : 0);
+        if constexpr (NW == 4) {
+          *reinterpret_cast<uint32_t*>(dst) = pack_bytes(cl[0], cl[1], cl[2], cl[3]);
+          *reinterpret_cast<uint32_t*>(dst + D) = pack_bytes(ch[0], ch[1], ch[2], ch[3]);
+        } else {
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(pack_bytes(cl[0], cl[1], cl[2], cl[3]), pack_bytes(cl[4], cl[5], cl[6], cl[7]));
+          *reinterpret_cast<uint2*>(dst + D) =
+              make_uint2(pack_bytes(ch[0], ch[1], ch[2], ch[3]), pack_bytes(ch[4], ch[5], ch[6], ch[7]));
+        }
+        if (lane % LPH == 0 && !upper) a.summary_scale[at] = exp2_int(e);
       }
-      if (lane == 0) a.summary_scale[head] = exp2_int(e);
     }
     if (last) {
       now = next;
@@ -890,7 +896,8 @@ cudaError_t launch_select_n(const SelectArgs& a, cudaStream_t stream) {
 template <int D, int KIND>
 cudaError_t launch_summarize_t(const SummarizeArgs& a, cudaStream_t stream) {
   auto kern = summarize_blocks_kernel<D, KIND>;
-  const int64_t ctas = (static_cast<int64_t>(a.num_ids) * a.num_kv_heads + 7) / 8;
+  constexpr int HPT = 256 / (D * (KIND == 2 ? 1 : 2));
+  const int64_t ctas = (static_cast<int64_t>(a.num_ids) * ((a.num_kv_heads + HPT - 1) / HPT) + 7) / 8;
   const int64_t most = resident_warp_slots(reinterpret_cast<const void*>(kern), 256, 0) / 8;
   return launch_pdl(kern, dim3(static_cast<unsigned>(min(ctas, most))), dim3(256), 0, stream, a);
 }
