@@ -324,7 +324,7 @@ template <int D, bool BF16, bool FP8, int NW>
 cudaError_t launch_sparse_nw(const DecodeArgs& a, const SparseArgs& sp, int C, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t stream) {
   using Geom = TileGeom<D, FP8 ? 1 : 2>;
-  constexpr int NST = FP8 ? 4 : 3;
+  constexpr int NST = FP8 ? 4 : D == 64 ? 3 : 2;  // 12 to 16 KB of tiles a warp
   constexpr size_t smem = static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 8) +
                           (8 * D + 16 * kSparseMaxCluster) * sizeof(float);
   auto kern = decode_sparse_kernel<D, BF16, FP8, NW, NST>;
@@ -334,20 +334,28 @@ cudaError_t launch_sparse_nw(const DecodeArgs& a, const SparseArgs& sp, int C, c
                             stream, a, sp, tk, tv);
 }
 
-// Fewer units than SMs: 8-warp CTAs, doubled per unit while they fit the SMs
-// once and a warp keeps at least kSparseLeast tiles.  Otherwise one CTA of 4
-// warps per unit, two on an SM at a time, whose starts and ends overlap.
-// Microseconds with 8 / 4 warps a CTA at 8 units of 128 tiles: 5.5 / 6.1, at
-// 64 (FP8): 12.1 / 13.2, at 2048 of 64 (f16): 168 / 158.
-constexpr int kSparseLeast = 2;
+// Warps a CTA and CTAs a unit.  Units up to the SMs: 8-warp CTAs, doubled per
+// unit while they fit the SMs once and a warp keeps at least kSparseLeast
+// tiles.  More: one CTA of 4 warps a unit, whose starts and ends overlap with
+// the others' on the SM; of 2 where units queue and are short (the start, a
+// chain of reads, then takes most of a CTA's time) and for FP8 tiles, whose
+// arithmetic is the bound.  Microseconds with 8 / 4 / 2 warps:
+//   8 units of 128 tiles 5.4 / 6.1 / -, 64 of 128 (FP8) 12.1 / 13.2 / -,
+//   220 of 28: 10.0 / 8.2 / 11.6, 800 of up to 22: 26 / 17.4 / 16.3,
+//   904 of 6: 25 / 15.0 / 12.4, 504 of 90 (FP8): 51 / 51 / 45,
+//   2048 of 64: 171 / 156 / 160.
+constexpr int kSparseLeast = 1, kSparseShort = 32;
 
 template <int D, bool BF16, bool FP8>
 cudaError_t launch_sparse_t(const DecodeArgs& a, const SparseArgs& sp, const CUtensorMap& tk, const CUtensorMap& tv,
                             cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads, sms = current_sm_count(152);
-  if (units > sms) return launch_sparse_nw<D, BF16, FP8, 4>(a, sp, 1, tk, tv, stream);
   const int64_t tiles = min((static_cast<int64_t>(a.max_context_len) + kTile - 1) / kTile,
                             static_cast<int64_t>(sp.keep) << (a.block_shift - 4));
+  if (units > sms)
+    return FP8 || (units > 3 * sms && tiles <= kSparseShort)
+               ? launch_sparse_nw<D, BF16, FP8, 2>(a, sp, 1, tk, tv, stream)
+               : launch_sparse_nw<D, BF16, FP8, 4>(a, sp, 1, tk, tv, stream);
   int C = 1;
   while (C < kSparseMaxCluster && units * C * 2 <= sms && tiles >= 2 * C * 8 * kSparseLeast) C *= 2;
   return launch_sparse_nw<D, BF16, FP8, 8>(a, sp, C, tk, tv, stream);
