@@ -39,7 +39,10 @@ struct WarpAttentionFp8 : SoftmaxState<D / 16> {
   // Loads the group's query rows (heads >= G read as 0) in the permuted
   // order and returns the power of two by which they were scaled down (1
   // for f16; for bf16, 2^e with the group's max |q| / 2^e below 2^15).
-  template <bool QBF16>
+  // OWN: a power of two per head, that of head gr, from the head's largest
+  // finite |q|: a head beside one of far larger or infinite queries keeps its
+  // bits.
+  template <bool QBF16, bool OWN = false>
   __device__ __forceinline__ float load_q(const uint16_t* qhead0, int G, int lane) {
     const int gr = lane >> 2, tq = lane & 3;
     const bool live = gr < G;
@@ -59,13 +62,17 @@ struct WarpAttentionFp8 : SoftmaxState<D / 16> {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float2 f = unpack_bf16(w[i]);
-        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        const float x = fabsf(f.x), y = fabsf(f.y);
+        if constexpr (OWN)
+          amax = fmaxf(amax, fmaxf(x < INFINITY ? x : 0.f, y < INFINITY ? y : 0.f));
+        else
+          amax = fmaxf(amax, fmaxf(x, y));
       }
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+      for (int o = 1; o < (OWN ? 4 : 32); o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
       // 2^e >= amax / 2^14.99: exponent of amax minus 14, at least 0.
       const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127;
-      const int e = min(max(ex - 14, 0), 120);
+      const int e = min(max(ex - 14, OWN ? -100 : 0), 120);
       const float mul = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, exact
       down = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
@@ -86,10 +93,11 @@ struct WarpAttentionFp8 : SoftmaxState<D / 16> {
   // all of them).  Tile t: K at sK[t], V at sK[t] + VOFF, nv[t] valid
   // tokens (rows >= nv are masked, whatever they hold), sl2k[t] = log2(e) *
   // softmax scale * q prescale * K scale, pv[t] = V scale in the
-  // accumulator's unit (a power of two chosen per chunk of tiles).
-  template <int NT, int VOFF = 2048>
+  // accumulator's unit (a power of two chosen per chunk of tiles).  OWN: times
+  // up_a and up_b for this lane's heads 2tq and 2tq + 1 (load_q's powers).
+  template <int NT, int VOFF = 2048, bool OWN = false>
   __device__ __forceinline__ void tiles(const uint32_t (&sK)[NT], const int (&nv)[NT], const float (&sl2k)[NT],
-                                        const float (&pv)[NT], int lane) {
+                                        const float (&pv)[NT], int lane, float up_a = 1.f, float up_b = 1.f) {
     const int gr = lane >> 2, tq = lane & 3;
     // K: rows gr and gr+8 (same swizzle phase), chunks 2tq and 2tq+1.
     const uint32_t off0 = gr * 128 + (((2 * tq) ^ gr) << 4);
@@ -132,10 +140,11 @@ struct WarpAttentionFp8 : SoftmaxState<D / 16> {
     float sc[4 * NT], p[4 * NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      sc[4 * t] = (c[t][0][0] + c[t][1][0]) * sl2k[t];
-      sc[4 * t + 1] = (c[t][0][1] + c[t][1][1]) * sl2k[t];
-      sc[4 * t + 2] = (c[t][0][2] + c[t][1][2]) * sl2k[t];
-      sc[4 * t + 3] = (c[t][0][3] + c[t][1][3]) * sl2k[t];
+      const float fa = OWN ? sl2k[t] * up_a : sl2k[t], fb = OWN ? sl2k[t] * up_b : sl2k[t];
+      sc[4 * t] = (c[t][0][0] + c[t][1][0]) * fa;
+      sc[4 * t + 1] = (c[t][0][1] + c[t][1][1]) * fb;
+      sc[4 * t + 2] = (c[t][0][2] + c[t][1][2]) * fa;
+      sc[4 * t + 3] = (c[t][0][3] + c[t][1][3]) * fb;
       if (gr >= nv[t]) sc[4 * t] = sc[4 * t + 1] = kNegInf;
       if (gr + 8 >= nv[t]) sc[4 * t + 2] = sc[4 * t + 3] = kNegInf;
     }

@@ -80,9 +80,10 @@ def attend(q, k, v, scale):
 def attend_bound(q, k, v, scale, split):
     """Largest error of a float32 computation of attend() whose weights carry a relative error of
     `split`: a dot product of D terms is off by at most D * 2^-23 times the sum of its magnitudes (each
-    addition loses at most one unit in the last place, the accumulator may truncate), a weight by twice
-    its score's error and its own rounding, the sums by one rounding a token."""
+    addition loses at most one unit in the last place, the accumulator may truncate), a score by
+    |scale| times that (a negative scale makes no error negative), a weight by twice its score's error and
+    its own rounding, the sums by one rounding a token."""
     if not k.shape[0]:
         return 0.0
-    eps_s = q.shape[1] * 2.0 ** -23 * scale * (np.abs(q) @ np.abs(k).T).max()
+    eps_s = q.shape[1] * 2.0 ** -23 * abs(scale) * (np.abs(q) @ np.abs(k).T).max()
     return np.abs(v).max() * (2 * eps_s + 2 * split + (k.shape[0] + 64) * 2.0 ** -23)

@@ -523,3 +523,90 @@ def test_pools_and_summaries_past_four_gigabytes(fp8):
         a.ks, a.vs = ks, vs
     a.call()
     a.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kw", [dict(lens=[100, 17, 230, 90, 1] * 26, Hq=8, Hkv=4, keep=6),
+                                dict(lens=[1000, 300, 0, 65] * 12, Hq=12, Hkv=4, keep=50),
+                                dict(lens=[700] * 19, Hq=64, Hkv=8, keep=20, dtype="f16"),
+                                dict(lens=[400, 900] * 10, Hq=16, Hkv=16, keep=40, D=64, B=32)])
+def test_attention_of_many_units(kw, fp8):
+    """As many (sequence, KV head) units as SMs and more, short and long."""
+    if fp8 and kw.get("D") == 64:
+        kw = dict(kw, D=128, B=16)
+    a = Attend(seed=17, fp8=fp8, **kw)
+    a.call()
+    a.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("scale", [0.0, -0.05, 3.0])
+def test_attention_with_other_scales(scale, fp8):
+    a = Attend([300, 50], keep=10, fp8=fp8)
+    a.scale = scale
+    a.call()
+    a.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_query_that_is_not_finite_stays_in_its_row(fp8):
+    a, b = Attend([700, 90], keep=30, fp8=fp8), Attend([700, 90], keep=30, fp8=fp8)
+    a.q[0, 3, 7], a.q[1, 4, 0] = float("nan"), float("inf")
+    a.call()
+    b.call()
+    torch.cuda.synchronize()
+    rest = torch.ones(2, 8, dtype=torch.bool, device="cuda")
+    rest[0, 3] = rest[1, 4] = False
+    assert torch.equal(a.out[rest], b.out[rest]) and not torch.isfinite(a.out[0, 3]).any()
+
+
+def test_tables_of_no_blocks():
+    """A table of width 0 holds no token: zero rows and empty lists; a length above it is reported."""
+    s, a = Select([0, 0]), Attend([0, 0])
+    s.tables, a.tables = s.tables[:, :0].contiguous(), a.tables[:, :0].contiguous()
+    s.call()
+    s.check()
+    a.call()
+    a.check()
+    s.cl[1] = a.cl[1] = 5
+    s.call()
+    s.check(pkv.DEV_ERR_LENGTH)
+    a.call()
+    a.check(pkv.DEV_ERR_LENGTH)
+
+
+def test_equal_inputs_give_equal_bits():
+    """Repeated calls, alone and beside another stream's, agree bit for bit."""
+    s, a = Select([60000, 9000, 33], keep=99), Attend([20000, 300], keep=500)
+    busy = torch.cuda.Stream()
+    noise = Attend([5000] * 8, keep=200)
+    torch.cuda.synchronize()
+    first = None
+    for i in range(20):
+        if i % 2:
+            noise.call(busy)
+        s.call()
+        a.call()
+        torch.cuda.synchronize()
+        got = (s.sel.clone(), a.out.clone())
+        first = first or got
+        assert all(torch.equal(x, y) for x, y in zip(first, got))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_heads_of_far_apart_magnitudes(fp8):
+    """Each head is as exact as beside heads of its own size."""
+    a = Attend([500, 60], Hq=8, Hkv=1, keep=30, fp8=fp8)
+    a.q *= torch.exp2(torch.tensor([0.0, 60, -40, 17, -20, 100, 3, 30]))[:, None].to(a.q)
+    a.call()
+    torch.cuda.synchronize()
+    got, q = f64(a.out), f64(a.q)
+    for s, L in enumerate(a.lens):
+        blocks = a.tables[s].cpu().numpy()[a.sel[s, 0, :a.cnt[s, 0]].cpu().numpy()]
+        k, v = (np.concatenate([a.values(p, sc, int(b), 0) for b in blocks])
+                for p, sc in ((a.kp, getattr(a, "ks", None)), (a.vp, getattr(a, "vs", None))))
+        ok = ~np.isnan(k).any(1)  # the poisoned rows behind the sequence
+        for h in range(8):
+            want = R.attend(q[s, h:h + 1], k[ok], v[ok], a.scale)
+            tol = R.attend_bound(q[s, h:h + 1], k[ok], v[ok], a.scale, SPLIT["fp8" if fp8 else a.dtype])
+            assert np.all(np.abs(got[s, h] - want) <= tol + 2.0 ** -24 * np.abs(want) + 2.0 ** -25), (s, h)
