@@ -479,7 +479,13 @@ def _ext():
         spec = importlib.util.spec_from_loader("_pkv_torch", importlib.machinery.ExtensionFileLoader(
             "_pkv_torch", _build.EXT))
         ext = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(ext)
+        try:
+            spec.loader.exec_module(ext)
+        except ImportError as e:
+            raise PkvError(f"the torch extension does not load, rebuild it: {e}") from e
+        if ext.torch_version != torch.__version__:
+            raise PkvError(f"the torch extension was built for torch {ext.torch_version}, this is "
+                           f"{torch.__version__}: rebuild it")
         ext.set_error_type(PkvError)
         _EXT = ext
     return _EXT

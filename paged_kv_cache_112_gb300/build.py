@@ -79,16 +79,16 @@ def _torch_dirs() -> tuple:
     import torch
 
     root = os.path.dirname(os.path.abspath(torch.__file__))
-    return os.path.join(root, "include"), os.path.join(root, "lib")
+    return os.path.join(root, "include"), os.path.join(root, "lib"), torch.__version__
 
 
 def _compile_ext() -> str:
-    inc, _ = _torch_dirs()
+    inc, _, version = _torch_dirs()
     obj = os.path.join(OUT_DIR, "pkv_torch.o")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(ROOT, "include"), "-isystem", inc, "-isystem",
            os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-isystem",
-           sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj]
+           sysconfig.get_paths()["include"], f'-DPKV_TORCH_VERSION="{version}"', "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {EXT_SOURCE}:\n{r.stdout}\n{r.stderr}")
@@ -97,7 +97,7 @@ def _compile_ext() -> str:
 
 def _link_ext(obj: str) -> None:
     """Links against libpkv.so beside it and the installed torch."""
-    _, lib = _torch_dirs()
+    _, lib, _ = _torch_dirs()
     tmp = EXT + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-l:libpkv.so", "-L", lib, "-lc10", "-lc10_cuda",
            "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]

@@ -150,6 +150,15 @@ float number(PyObject* o, const char* name) {
   return static_cast<float>(v);
 }
 
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    throw Refused(std::string(name) + " must be true or false");
+  }
+  return v == 1;
+}
+
 void done(pkv_status st, const char* what) {
   if (st == PKV_OK) return;
   std::string text = std::string(what) + ": " + pkv_status_string(st);
@@ -215,7 +224,7 @@ PyObject* norm_rope_write(PyObject*, PyObject* const* o, Py_ssize_t n) {
     }
     need(!pos || (pos->dim() == 1 && pos->size(0) == T), "positions must be int32 [T]");
     const float eps = number(o[12], "eps");
-    const int inter = PyObject_IsTrue(o[15]) == 1;
+    const bool inter = truth(o[15], "interleaved");
     void* stream = stream_of(o[17], dev);
     if (fp8)
       done(pkv_norm_rope_write_fp8(ptr(&q_out), qos, ptr(k_out), kos, ptr(&q), qs, ptr(&k), ptr(&v), kvs, ptr(qw),
@@ -360,4 +369,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_pkv_torch", nullptr, -1, kMethod
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__pkv_torch(void) { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__pkv_torch(void) {
+  PyObject* m = PyModule_Create(&kModule);
+  // The torch it was compiled against (build.py): another one's tensors may be laid out differently.
+  if (m && PyModule_AddStringConstant(m, "torch_version", PKV_TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -246,6 +246,17 @@ def test_refusals():
             f(**kw)
 
 
+def test_arguments_of_the_wrong_kind():
+    s = Step(T=4)
+    for kw in (dict(interleaved=torch.zeros(2)), dict(eps="small"), dict(eps=None), dict(stream=7),
+               dict(status=torch.zeros(1)), dict(q_weight=1.0), dict(eps=float("nan"), q_weight=s.qw)):
+        with pytest.raises(pkv.PkvError):
+            pkv.norm_rope_write(s.q, s.k, s.v, s.kp, s.vp, s.slots, q_out=s.q_out, cos_sin=s.cs, positions=s.pos, **kw)
+    with pytest.raises(pkv.PkvError):
+        pkv.norm_rope_write(s.q, s.k, [1.0], s.kp, s.vp, s.slots, q_out=s.q_out, cos_sin=s.cs, positions=s.pos)
+    torch.cuda.synchronize()  # nothing was launched and no error is left behind
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_fp8_codes_are_those_of_the_division(dtype):
     """Values and scales whose quotients lie on, next to and far from rounding borders, beyond the largest
