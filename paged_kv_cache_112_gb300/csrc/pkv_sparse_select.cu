@@ -12,6 +12,11 @@
 // and q^+ = max(q, 0): two integer dot products, below 2^22 in magnitude and
 // free of any summation order.  A block's score is the largest over the
 // group's heads; the best ones are taken, equal scores by the lowest block.
+//
+// Bound: HBM bytes of the summaries, 2D + 4 a block and KV head (8 sequences of
+// 2048 to 8192 blocks: 29.0 us, 21 of them the scores at 5.2 TB/s, 6 the search
+// after them); with few blocks the latency of length -> table -> summary ->
+// ranks (64 sequences of up to 128 blocks: 6.2 us).
 #include "pkv_device.cuh"
 
 namespace pkv {
@@ -87,8 +92,9 @@ __device__ __forceinline__ float finite_bound(float x, float most) {
 // with NW channels, rounds their bounds and stores the codes.  KIND: 0 = f16,
 // 1 = bf16, 2 = FP8 (codes compared as f16, which holds every e4m3 value).
 //
-// Bound: 16-bit pools HBM (8192 blocks of 8 heads in 46 us, 6.2 TB/s of keys);
-// FP8 pools the instruction rate (a code costs as many as a 16-bit key).
+// Bound: 16-bit pools HBM (8192 blocks of 8 heads in 46.0 us, 6.2 TB/s);
+// FP8 pools the instruction rate (a code costs as many as a 16-bit key; 4001
+// blocks of 8 heads in 15.6 us, 4.7 TB/s).
 template <int D, int KIND>
 __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeArgs a) {
   constexpr int EB = KIND == 2 ? 1 : 2;
@@ -882,8 +888,8 @@ cudaError_t launch_select_t(const SelectArgs& a, int64_t cap, cudaStream_t strea
 
 // More threads where a sequence may have more blocks: each warp still scores
 // four chunks or more, and the first CTA's search of the keys is shared among
-// more threads (8 sequences of up to 8192 blocks: 58 us with 128 threads, 33.5
-// with 256, 31.9 with 512).
+// more threads (8 sequences of up to 8192 blocks: 57.7 us with 128 threads, 30.5
+// with 256, 29.0 with 512).
 template <int D, bool BF16>
 cudaError_t launch_select_n(const SelectArgs& a, cudaStream_t stream) {
   const int64_t cap = min(static_cast<int64_t>(a.max_blocks_per_seq),
