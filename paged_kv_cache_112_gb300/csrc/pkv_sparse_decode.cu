@@ -9,7 +9,7 @@
 // Bound: HBM bytes of the selected K and V rows (each read once; all query
 // heads of the group share them); with few units the latency of length ->
 // list -> table entry -> tile.  (256 sequences of 64 blocks, 8 KV heads: 155.4
-// us, 6.6 TB/s; 8 of 128 over FP8 pools: 12.0 us, 4 of them before the first
+// us, 6.6 TB/s; 8 of 128 over FP8 pools: 12.1 us, 4 of them before the first
 // tile and after the last; one of 128: 5.3 us.)
 //
 // One cluster of C CTAs of NW warps per (s, g).  The list's 16-token tiles are
