@@ -18,6 +18,8 @@
 // tensor cores (WarpAttention, WarpAttentionFp8).  The states meet in shared
 // memory, first a CTA's, then through distributed shared memory the
 // cluster's, so one launch writes final rows and no workspace is needed.
+#include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "pkv_fp8_attention.cuh"
@@ -323,45 +325,133 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
   }
 }
 
+// The kernel with NW warps a CTA, and what launching it in clusters of C takes.
 template <int D, bool BF16, bool FP8, int NW>
-cudaError_t launch_sparse_nw(const DecodeArgs& a, const SparseArgs& sp, int C, const CUtensorMap& tk,
-                             const CUtensorMap& tv, cudaStream_t stream) {
+struct SparseLaunch {
   using Geom = TileGeom<D, FP8 ? 1 : 2>;
-  constexpr int NST = FP8 ? 4 : D == 64 ? 3 : 2;  // 12 to 16 KB of tiles a warp
-  constexpr size_t smem = static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 8) +
-                          (8 * D + 16 * kSparseMaxCluster) * sizeof(float);
-  auto kern = decode_sparse_kernel<D, BF16, FP8, NW, NST>;
-  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(a.num_seqs) * a.num_kv_heads * C), dim3(NW * 32), smem, C,
-                            stream, a, sp, tk, tv);
-}
+  static constexpr int NST = FP8 ? 4 : D == 64 ? 3 : 2;  // 12 to 16 KB of tiles a warp
+  static constexpr auto kernel = decode_sparse_kernel<D, BF16, FP8, NW, NST>;
 
-// Warps a CTA and CTAs a unit.  Units up to the SMs: 8-warp CTAs, doubled per
-// unit while they fit the SMs once and a warp keeps at least one
-// tile.  More: one CTA of 4 warps a unit, whose starts and ends overlap with
-// the others' on the SM; of 2 where units queue and are short (the start, a
-// chain of reads, then takes most of a CTA's time) and for FP8 tiles, whose
-// arithmetic is the bound.  Microseconds with 8 / 4 / 2 warps:
-//   8 units of 128 tiles 5.4 / 6.1 / -, 64 of 128 (FP8) 12.1 / 13.2 / -,
-//   220 of 28: 10.0 / 8.2 / 11.6, 800 of up to 22: 26 / 17.4 / 16.3,
-//   904 of 6: 25 / 15.0 / 12.4, 504 of 90 (FP8): 51 / 51 / 45,
-//   2048 of 64: 171 / 156 / 160.
-constexpr int kSparseShort = 32;
+  static size_t smem(int C) {
+    return static_cast<size_t>(NW) * NST * (Geom::kStageBytes + 8) +
+           (C > 1 ? (8 * D + 16 * kSparseMaxCluster) * sizeof(float) : 0);
+  }
+
+  // Clusters of C that the current device holds at a time (a cluster stays
+  // within one of the GPU's groups of SMs, so fewer than SMs / C).
+  static int resident(int C) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> cache[kDevices][4];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) {
+      cudaGetLastError();
+      return 1;
+    }
+    std::atomic<int>& slot = cache[dev][C == 1 ? 0 : C == 2 ? 1 : C == 4 ? 2 : 3];
+    int n = slot.load(std::memory_order_acquire);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(NW * 32);
+    cfg.dynamicSmemBytes = smem(C);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem(kSparseMaxCluster)) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      return 1;
+    }
+    slot.store(n, std::memory_order_release);
+    return n;
+  }
+
+  static cudaError_t launch(const DecodeArgs& a, const SparseArgs& sp, int C, const CUtensorMap& tk,
+                            const CUtensorMap& tv, cudaStream_t stream) {
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem(kSparseMaxCluster));
+    if (e != cudaSuccess) return e;
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(a.num_seqs) * a.num_kv_heads * C), dim3(NW * 32),
+                              smem(C), C, stream, a, sp, tk, tv);
+  }
+};
+
+// Microseconds that `units` lists of up to `tiles` tiles take with NW warps a
+// CTA and C CTAs a list, `held` clusters at a time.  A wave of clusters starts
+// (length -> list -> table -> tile; the cluster's meeting), then a warp takes
+// kTileUs a tile, or longer where its SM's rate is what it waits for.  All
+// waves together are no faster than the memory; the last one, and some of each
+// one's start, stay exposed, the less the more CTAs a SM holds.  A quarter of
+// a wave is added in any case: a longer chain next to a full memory.  SMs fill
+// up with clusters one after another, with single CTAs evenly.
+// The constants are fitted to 458 measured shapes (2 to 2000 lists of 2 to 512
+// tiles, the three kinds of pool, each NW and C): the form with the lowest cost
+// is 1% slower than the best one in the mean, 16% at the most.  (Eight warps up
+// to the number of SMs and four or two above it: 11% and 130%.)  Microseconds:
+//   8 of 128 tiles: 5.4 with 8 warps in clusters of 8, 6.6 of 4, 9.4 of 2;
+//   16 of 128: 6.8 with 8 warps of 4 -- clusters of 8 no longer fit at once: 9.9;
+//   38 of 128: 10.8 with 4 warps of 8 -- 15.7 with 8 of 4, 11.8 with 8 of 2;
+//   64 of 128 (FP8): 11.8 with 8 warps of 2, 12.6 with 4 of 4;
+//   100 of 512 (FP8): 37.7 with 4 warps of 4, 51 with 8 alone;
+//   160 of 512 (FP8): 61 with 4 warps of 2, 87 with 4 alone, 142 with 2;
+//   912 of 5: 10.3 with 2 warps alone, 12.9 with 4; 2000 of 64: 153 with 4, 157
+//   with 2, 171 with 8, 180 with 1.
+template <int D, bool FP8>
+float sparse_cost(int64_t units, int64_t tiles, int group, int NW, int C, int held, int64_t sms) {
+  constexpr float kStartUs = 3.5f, kTileUs = FP8 ? 0.8f : D == 64 ? 0.6f : 0.9f;
+  constexpr float kSmBytes = FP8 ? 45e3f : D == 64 ? 60e3f : 75e3f, kBytes = 6.4e6f;  // a microsecond
+  constexpr float kTileBytes = TileGeom<D, FP8 ? 1 : 2>::kStageBytes;
+  const int64_t full = (static_cast<int64_t>(held) * C + sms - 1) / sms;  // CTAs a SM holds
+  const int64_t per_sm = C == 1 ? std::min((units + sms - 1) / sms, full) : units * C <= sms ? 1 : full;
+  int64_t n = (tiles + NW * C - 1) / (NW * C);  // tiles of a warp
+  if (FP8) n += n & 1;                          // taken in pairs
+  const float tile = std::max(kTileUs, static_cast<float>(per_sm * NW) * (kTileBytes / kSmBytes));
+  const float meet = 0.4f + 0.1f * static_cast<float>(group);  // rows of `group` heads to send
+  const float start = kStartUs + (C > 1 ? meet : 0.f), wave = start + tile * static_cast<float>(n);
+  const float waves = static_cast<float>(units) / static_cast<float>(held);
+  const float exposed = units > held ? wave * (0.5f + 0.15f * (waves - 1.f)) / static_cast<float>(full) : 0.f;
+  const float bytes = static_cast<float>(units) * static_cast<float>(tiles) * kTileBytes;
+  return std::max(static_cast<float>((units + held - 1) / held) * wave, start + bytes / kBytes + exposed) +
+         0.25f * wave;
+}
 
 template <int D, bool BF16, bool FP8>
 cudaError_t launch_sparse_t(const DecodeArgs& a, const SparseArgs& sp, const CUtensorMap& tk, const CUtensorMap& tv,
                             cudaStream_t stream) {
+  using One = SparseLaunch<D, BF16, FP8, 1>;
+  using Two = SparseLaunch<D, BF16, FP8, 2>;
+  using Four = SparseLaunch<D, BF16, FP8, 4>;
+  using Eight = SparseLaunch<D, BF16, FP8, 8>;
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads, sms = current_sm_count(152);
-  const int64_t tiles = min((static_cast<int64_t>(a.max_context_len) + kTile - 1) / kTile,
-                            static_cast<int64_t>(sp.keep) << (a.block_shift - 4));
-  if (units > sms)
-    return FP8 || (units > 3 * sms && tiles <= kSparseShort)
-               ? launch_sparse_nw<D, BF16, FP8, 2>(a, sp, 1, tk, tv, stream)
-               : launch_sparse_nw<D, BF16, FP8, 4>(a, sp, 1, tk, tv, stream);
-  int C = 1;
-  while (C < kSparseMaxCluster && units * C * 2 <= sms && tiles >= 2 * C * 8) C *= 2;
-  return launch_sparse_nw<D, BF16, FP8, 8>(a, sp, C, tk, tv, stream);
+  const int64_t tiles = std::max<int64_t>(1, std::min((static_cast<int64_t>(a.max_context_len) + kTile - 1) / kTile,
+                                                      static_cast<int64_t>(sp.keep) << (a.block_shift - 4)));
+  int best_nw = 8, best_c = 1;
+  float best = 0.f;
+  auto consider = [&](int NW, int C, int held) {
+    const float cost = sparse_cost<D, FP8>(units, tiles, a.group, NW, C, held, sms);
+    if (best > 0.f && cost >= best) return;
+    best = cost;
+    best_nw = NW;
+    best_c = C;
+  };
+  consider(4, 1, Four::resident(1));
+  consider(8, 1, Eight::resident(1));
+  if (units > sms) {
+    consider(2, 1, Two::resident(1));
+    consider(1, 1, One::resident(1));
+  }
+  for (int C = 2; C <= kSparseMaxCluster && units * C <= 4 * sms; C *= 2) {
+    consider(8, C, Eight::resident(C));
+    consider(4, C, Four::resident(C));
+  }
+  switch (best_nw) {
+    case 1: return One::launch(a, sp, 1, tk, tv, stream);
+    case 2: return Two::launch(a, sp, 1, tk, tv, stream);
+    case 4: return Four::launch(a, sp, best_c, tk, tv, stream);
+    default: return Eight::launch(a, sp, best_c, tk, tv, stream);
+  }
 }
 
 }  // namespace
