@@ -867,16 +867,21 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
   }
 }
 
-// CTAs per (sequence, KV head): doubled while the batch has fewer than
-// kSelWarps warps a SM and one CTA cannot take the blocks in one pass.
-constexpr int kSelWarps = 8, kSelMaxCluster = 8;
+// CTAs per (sequence, KV head): doubled while all clusters stay resident at 16
+// warps a SM and one CTA cannot take the blocks in one pass.  A cluster stays
+// within one of the GPU's groups of 18 to 20 SMs: where a CTA takes a whole SM,
+// 76 clusters of two fit, 36 of four, but 15 of eight (a sixteenth waits for
+// another to end).
+constexpr int kSelWarps = 16, kSelMaxCluster = 8;
 
 template <int D, bool BF16, int NT>
 cudaError_t launch_select_t(const SelectArgs& a, int64_t cap, cudaStream_t stream) {
   auto kern = a.group <= 4 ? select_blocks_kernel<D, BF16, NT, true> : select_blocks_kernel<D, BF16, NT, false>;
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   int C = 1;
-  while (C < kSelMaxCluster && units * C * (NT / 32) < kSelWarps * current_sm_count(152) && cap > C * NT) C *= 2;
+  const int64_t warps = static_cast<int64_t>(kSelWarps) * current_sm_count(152);
+  auto fits = [&](int c) { return units * c * (NT / 32) * 100 <= warps * (c == 8 ? 79 : c == 4 ? 95 : 100); };
+  while (C < kSelMaxCluster && fits(2 * C) && cap > C * NT) C *= 2;
   // Keys of the longest sequence, then the two bitmaps.
   const int words = static_cast<int>((cap + 31) / 32);
   const size_t smem = static_cast<size_t>(34) * words * sizeof(uint32_t);
