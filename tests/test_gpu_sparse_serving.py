@@ -4,6 +4,10 @@ copy-on-write, a swap to host memory and back), each step one captured graph
 of norm + rotation + write, summaries of the blocks it filled, selection and
 sparse attention, over a padded batch.  Every step's queries, selection and
 attention are compared with the float64 statements over the pools' contents."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -216,3 +220,37 @@ def test_two_captured_layers_replay_side_by_side():
         for layer, rows in zip((a, b), new):
             assert int(layer.status.item()) == 0
             layer.check(rows, [L - 1 for L in lens], lens, tables)
+
+
+FIRST_CALLS = """
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+import paged_kv_cache_112_gb300 as pkv
+from tests.test_gpu_norm_rope import Step
+from tests.test_gpu_sparse import Attend, Select
+
+calls = [Select([70000, 900, 20], keep=40), Attend([700, 900], keep=20), Attend([700, 20], keep=20, fp8=True),
+         Step(T=33), Step(T=3000, Hq=32, Hkv=8)]
+pool = torch.randn(9, 16, 2, 128, device="cuda").bfloat16()
+summary, scale = torch.zeros(9, 2, 2, 128, dtype=torch.int8, device="cuda"), torch.zeros(9, 2, device="cuda")
+ids = torch.arange(9, dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    for c in calls:
+        c.call()
+    pkv.summarize_blocks(summary, scale, pool, ids)
+g.replay()
+torch.cuda.synchronize()
+for c in calls:
+    c.check()
+print("ok")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing has to run before a capture: attributes, occupancy and descriptors are found within it."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS, root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
