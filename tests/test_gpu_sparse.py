@@ -610,3 +610,13 @@ def test_heads_of_far_apart_magnitudes(fp8):
             want = R.attend(q[s, h:h + 1], k[ok], v[ok], a.scale)
             tol = R.attend_bound(q[s, h:h + 1], k[ok], v[ok], a.scale, SPLIT["fp8" if fp8 else a.dtype])
             assert np.all(np.abs(got[s, h] - want) <= tol + 2.0 ** -24 * np.abs(want) + 2.0 ** -25), (s, h)
+
+
+@pytest.mark.parametrize("kind", [dict(), dict(fp8=True), dict(D=64, dtype="f16")])
+@pytest.mark.parametrize("units,tiles", [(1, 3), (1, 10), (1, 24), (2, 48), (3, 100), (40, 9), (153, 18), (77, 33),
+                                         (38, 49), (330, 3), (330, 30), (700, 2), (1300, 4), (2100, 1)])
+def test_attention_by_number_and_length_of_lists(units, tiles, kind):
+    """Every number of warps a CTA and of CTAs a list, with tiles that do not fill the last round."""
+    a = Attend([16 * tiles - i % 16 for i in range(units)], Hq=2, Hkv=1, keep=tiles, seed=units, **kind)
+    a.call()
+    a.check()
