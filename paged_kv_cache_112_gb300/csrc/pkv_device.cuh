@@ -205,10 +205,16 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // shared-memory writes before it are seen by the cluster's CTAs after it.  A
 // CTA's shared memory may be written from another only once it has begun to
 // run: kernels arrive first thing and wait before their first remote store.
+// The .aligned forms need a warp's lanes together, which a loop with a trip
+// count of each lane's own before them does not leave to be so.
 __device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
   cluster_arrive();
   cluster_wait();

@@ -288,7 +288,6 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
   float* inbox = reinterpret_cast<float*>(smem + kInboxAt);  // [C][per], then [C][8] max, [C][8] sum
   float* inbox_m = inbox + 8 * D;
   float* inbox_l = inbox_m + 8 * kSparseMaxCluster;
-  __syncwarp();
   cluster_wait();  // every CTA has begun
   for (int e = 4 * threadIdx.x; e < G * D; e += 4 * NW * 32) {
     const int h = e / D, d = e % D, to = e / per;

@@ -481,7 +481,6 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
   const float scale_b = exp2_int(max(q_exp[head_a + 1] - emax - 22, -126));
 
   const uint32_t keys_at = cluster_map(smem_u32(keys), 0);
-  __syncwarp();
   cluster_wait();  // the first CTA has begun
   auto score = [&](const Group& u, int half, int base, float scales) {
     int c[4] = {0, 0, 0, 0};
