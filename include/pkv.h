@@ -553,7 +553,8 @@ pkv_status pkv_summarize_blocks_fp8(void* summary, float* summary_scale, const v
  *   q            : [num_seqs][num_q_heads][head_dim] of q_dtype, 16-byte aligned.
  *   first_blocks >= 0, last_blocks >= 1, their sum <= keep <= 2^20.
  * Lengths are clamped and flagged as in pkv_decode_attention; a table entry
- * outside the pool sets PKV_DEV_ERR_BLOCK and is taken last.  head_dim 64 or
+ * outside the pool sets PKV_DEV_ERR_BLOCK and is taken last, as is a block
+ * whose summary_scale is negative, infinite or NaN.  head_dim 64 or
  * 128, 1 <= group <= 8, block sizes 16, 32 and 64, at most 49152 blocks a
  * sequence (min of max_context_len's and max_blocks_per_seq).
  */

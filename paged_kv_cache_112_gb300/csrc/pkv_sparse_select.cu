@@ -429,8 +429,12 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
     if (b + lane < n) flag(a.dev_status, 4u);
     return -1;
   };
+  // -1 for a block that is scored last: no table entry, or a scale that no
+  // summary has (0 times an infinite one is NaN, whose key would end the
+  // order of the floats that the searches below rely on).
   auto scale_of = [&](int p) {
-    return p >= 0 ? __ldg(a.summary_scale + static_cast<int64_t>(p) * a.num_kv_heads + g) : -1.f;
+    const float x = p >= 0 ? __ldg(a.summary_scale + static_cast<int64_t>(p) * a.num_kv_heads + g) : -1.f;
+    return x >= 0.f && x <= 3.4028234e38f ? x : -1.f;
   };
   const int gr = lane >> 2, tq = lane & 3;
   struct Group {
@@ -645,6 +649,7 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
           top = max(top, k[i][j]);
         }
       // At least `need` keys are >= lo, `above` (fewer than `need`) are >= hi.
+      // (hi does not wrap: a finite float's key is below 0xff800000.)
       uint32_t lo = __reduce_min_sync(kFull, low), hi = __reduce_max_sync(kFull, top) + 1;
       int above = 0;
       uint32_t threshold = 0;
