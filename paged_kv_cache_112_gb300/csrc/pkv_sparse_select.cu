@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
   constexpr int X = D / 64;      // 16-byte chunks of one bound per lane and row
   constexpr int NWARP = NT / 32;
   constexpr int BPT = kBins / NT;  // bins per thread
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];  // read as 16-byte vectors too
   __shared__ __align__(16) int hist[kBins];
   __shared__ __align__(16) uint32_t q_codes[2][8][D / 4];  // negative and positive parts; heads past the group are 0
   __shared__ int q_exp[8];
