@@ -441,13 +441,26 @@ struct SoftmaxState {
   // only when some head's running max grows (the common case once a
   // sequence is under way skips it; a warp-uniform branch).  Exponentials
   // by ex2.approx.ftz (results below 2^-126 flush to 0).
-  template <int NT>
-  __device__ __forceinline__ void online_update_lazy(const float (&s)[4 * NT], float (&p)[4 * NT]) {
+  // LIFTED: the running max is that of s + lift[t] (log2 of a bound on what
+  // tile t's weights are multiplied with), so that the products p * 2^lift,
+  // not the weights, stay at 1 and below; the row is the same for any shift.
+  template <int NT, bool LIFTED = false>
+  __device__ __forceinline__ void online_update_lazy(const float (&s)[4 * NT], float (&p)[4 * NT],
+                                                     const float* lift = nullptr) {
     float mx_a = fmaxf(s[0], s[2]), mx_b = fmaxf(s[1], s[3]);
+    if constexpr (LIFTED) {
+      mx_a += lift[0];
+      mx_b += lift[0];
+    }
 #pragma unroll
     for (int t = 1; t < NT; ++t) {
-      mx_a = fmaxf(mx_a, fmaxf(s[4 * t], s[4 * t + 2]));
-      mx_b = fmaxf(mx_b, fmaxf(s[4 * t + 1], s[4 * t + 3]));
+      float a = fmaxf(s[4 * t], s[4 * t + 2]), b = fmaxf(s[4 * t + 1], s[4 * t + 3]);
+      if constexpr (LIFTED) {
+        a += lift[t];
+        b += lift[t];
+      }
+      mx_a = fmaxf(mx_a, a);
+      mx_b = fmaxf(mx_b, b);
     }
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
@@ -556,13 +569,18 @@ struct SoftmaxState {
 //   O^T[D x 8 heads]     += V^T[D x 16] P^T[16 x 8]  (head_dim on M)
 // V^T comes from ldmatrix.trans; P^T is S^T's C fragment transposed in
 // registers with movmatrix.  P is rounded to the KV type for the MMA; with
-// SPLIT (bf16 always) it is split into hi + lo parts (two MMAs), keeping the
-// rounding error near 2^-17 relative for bf16 and 2^-22 for fp16 (fp16 alone
-// is 2^-11).  Lane (gr = lane/4, tq = lane%4)
+// SPLIT (bf16 always) it is split into hi + lo parts (two MMAs): bf16 parts
+// are off by 2^-17 of the weight, f16 parts by 2^-22 of it or, where their
+// subnormals end, by 2^-25 absolutely (one f16 alone: 2^-11, 2^-25).  The f16
+// parts therefore hold the weight times kWeightUp (P <= 1, so the upper half
+// of f16's exponents is free): their floor is 2^-39 of the largest weight, and
+// `acc` is kWeightUp times the sum it stands for; the caller scales it back.
+// Lane (gr = lane/4, tq = lane%4)
 // owns heads 2tq and 2tq+1 (a, b) and the output rows d = 16mt + gr (+8).
 template <int D, bool BF16, bool SPLIT = BF16>
 struct WarpAttention : SoftmaxState<D / 16> {
   static_assert(SPLIT || !BF16, "bf16 weights alone (2^-9) are too coarse");
+  static constexpr float kWeightUp = SPLIT && !BF16 ? 16384.f : 1.f;
   static constexpr int KT = D / 16;
   using Base = SoftmaxState<KT>;
   using Base::acc;
@@ -619,7 +637,7 @@ struct WarpAttention : SoftmaxState<D / 16> {
     if (gr + 8 >= nv) s2 = s3 = kNegInf;
     float sc[4] = {s0, s1, s2, s3}, pw[4];
     this->template online_update_lazy<1>(sc, pw);
-    const float p0 = pw[0], p1 = pw[1], p2 = pw[2], p3 = pw[3];
+    const float p0 = pw[0] * kWeightUp, p1 = pw[1] * kWeightUp, p2 = pw[2] * kWeightUp, p3 = pw[3] * kWeightUp;
 
     uint32_t pb0, pb1, pl0 = 0, pl1 = 0;
     if constexpr (BF16) {

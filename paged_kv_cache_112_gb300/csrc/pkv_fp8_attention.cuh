@@ -93,11 +93,17 @@ struct WarpAttentionFp8 : SoftmaxState<D / 16> {
   // all of them).  Tile t: K at sK[t], V at sK[t] + VOFF, nv[t] valid
   // tokens (rows >= nv are masked, whatever they hold), sl2k[t] = log2(e) *
   // softmax scale * q prescale * K scale, pv[t] = V scale in the
-  // accumulator's unit (a power of two chosen per chunk of tiles).  OWN: times
-  // up_a and up_b for this lane's heads 2tq and 2tq + 1 (load_q's powers).
+  // accumulator's unit (a power of two chosen per chunk of tiles).  OWN: sl2k
+  // times up_a and up_b for this lane's heads 2tq and 2tq + 1 (load_q's
+  // powers); pv[t] times kWeightUp, and lift[t] bounds log2 of pv[t] /
+  // kWeightUp: a weight times the V scale is at most 1 then, whatever the
+  // scales, so that a tile of large scale and little weight costs the others
+  // no bits.
+  static constexpr int kWeightUpLog2 = 14;
   template <int NT, int VOFF = 2048, bool OWN = false>
   __device__ __forceinline__ void tiles(const uint32_t (&sK)[NT], const int (&nv)[NT], const float (&sl2k)[NT],
-                                        const float (&pv)[NT], int lane, float up_a = 1.f, float up_b = 1.f) {
+                                        const float (&pv)[NT], int lane, float up_a = 1.f, float up_b = 1.f,
+                                        const float* lift = nullptr) {
     const int gr = lane >> 2, tq = lane & 3;
     // K: rows gr and gr+8 (same swizzle phase), chunks 2tq and 2tq+1.
     const uint32_t off0 = gr * 128 + (((2 * tq) ^ gr) << 4);
@@ -148,10 +154,12 @@ struct WarpAttentionFp8 : SoftmaxState<D / 16> {
       if (gr >= nv[t]) sc[4 * t] = sc[4 * t + 1] = kNegInf;
       if (gr + 8 >= nv[t]) sc[4 * t + 2] = sc[4 * t + 3] = kNegInf;
     }
-    this->template online_update_lazy<NT>(sc, p);
+    this->template online_update_lazy<NT, OWN>(sc, p, lift);
 
-    // P^T (times the V scale) as f16 hi + lo parts, two MMAs per tile, so
-    // the weights keep ~2^-22 relative precision.
+    // P^T (times the V scale) as f16 hi + lo parts, two MMAs per tile: off by
+    // 2^-22 of itself or, where f16's subnormals end, by 2^-25 in the
+    // accumulator's unit (OWN: 2^-39 of a unit at most twice the largest
+    // weight times V scale).
     uint32_t pb[NT][4];  // hi (tokens 0-7, 8-15), lo (tokens 0-7, 8-15)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {

@@ -121,11 +121,14 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
   auto scale_of = [&](const float* sc, int phys) {
     return phys >= 0 ? __ldg(sc + static_cast<int64_t>(phys) * a.scale_stride + g) : 0.f;
   };
-  float ks = 0.f, vs = 0.f, ks_prev = 0.f, vs_prev = 0.f;
+  // With each V scale goes its exponent: |v scale| < 2^ve.
+  auto exponent_of = [](float x) { return static_cast<float>(static_cast<int>((__float_as_uint(x) >> 23) & 0xff) - 126); };
+  float ks = 0.f, vs = 0.f, ve = 0.f, ks_prev = 0.f, vs_prev = 0.f, ve_prev = 0.f;
   int chunk = 0;
   if constexpr (FP8) {
     ks = scale_of(a.k_scale, cur.phys);
     vs = scale_of(a.v_scale, cur.phys);
+    ve = exponent_of(vs);
   }
   uint32_t stage_nv = 0;  // 8 bits per stage: valid rows of its tile
   static_assert(NST <= 4, "stage_nv");
@@ -136,8 +139,10 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
       if constexpr (FP8) {
         ks_prev = ks;
         vs_prev = vs;
+        ve_prev = ve;
         ks = scale_of(a.k_scale, cur.phys);
         vs = scale_of(a.v_scale, cur.phys);
+        ve = exponent_of(vs);
         chunk = j >> 5;
       }
     }
@@ -168,13 +173,21 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
       __syncwarp();
       if (i + NST < cnt) issue(i + NST);
     }
+    if constexpr (!BF16) at.scale_acc(1.f / Att::kWeightUp);
   } else {
-    // Two tiles a step; the accumulator's unit is a power of two at least
-    // the largest V scale seen (it only grows).
+    // Two tiles a step.  2^top is above every V scale seen so far; weights and
+    // scales enter the product in its unit, times 2^14.  The softmax's shift m
+    // follows weight times V scale in that unit (`lift`), so the products keep
+    // their f16 bits although scales lie far apart.  When the unit grows by
+    // 2^d, lowering m by d (times 2^d for the sum) leaves the accumulator's
+    // numbers as they are.  Weights without their scales then exceed 1: lift
+    // >= -kSpread and at most kSpread of lowering keep their sum below 2^97 a
+    // token.
+    constexpr int kSpread = 48;
     const float up = at.template load_q<BF16, true>(q0, G, lane);
     const float up_a = __shfl_sync(kFull, up, 8 * (lane & 3)), up_b = __shfl_sync(kFull, up, 8 * (lane & 3) + 4);
-    int vexp = -126;
-    float inv_unit = exp2i(126);
+    int vexp = -100, room = kSpread;
+    float top = -100.f, unit = exp2i(Att::kWeightUpLog2 + 100);
     for (int i = 0; i < cnt; i += 2) {
       const bool two = i + 1 < cnt;
       const bool ok = ring.wait(i, a.timeout_ns) && (!two || ring.wait(i + 1, a.timeout_ns));
@@ -184,34 +197,49 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
         break;
       }
       const bool now = (i >> 5) == chunk;  // both tiles of a pair lie in one chunk
-      const float ksel = now ? ks : ks_prev, vsel = now ? vs : vs_prev;
+      const float ksel = now ? ks : ks_prev, vsel = now ? vs : vs_prev, vesel = now ? ve : ve_prev;
       uint32_t sK[2];
       int nv[2];
-      float sl2k[2], vsc[2], pv[2];
+      float sl2k[2], pv[2], lift[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int j = two ? i + u : i;  // a missing second tile reuses the first one's stage, no valid token
-        const float kj = __shfl_sync(kFull, ksel, j & 31), vj = __shfl_sync(kFull, vsel, j & 31);
+        sl2k[u] = a.scale_log2 * __shfl_sync(kFull, ksel, j & 31);
+        pv[u] = __shfl_sync(kFull, vsel, j & 31);
+        lift[u] = __shfl_sync(kFull, vesel, j & 31);
         nv[u] = u == 1 && !two ? 0 : nv_of(j);
         sK[u] = ring.k_tile(j);
-        sl2k[u] = a.scale_log2 * kj;
-        vsc[u] = nv[u] > 0 ? vj : 0.f;
       }
-      const float vmax = fmaxf(vsc[0], vsc[1]);
-      const int e = min(max(static_cast<int>((__float_as_uint(vmax) >> 23) & 0xff) - 127, -126), 126);
-      if (e > vexp) {
-        at.scale_acc(unit_change(vexp, e));
+      if (fmaxf(lift[0], lift[1]) > top && vexp < 126) {  // the same for the whole warp
+        const int e = min(static_cast<int>(fmaxf(lift[0], lift[1])), 126), d = i > 0 ? min(e - vexp, room) : 0;
+        at.m_a -= static_cast<float>(d);
+        at.m_b -= static_cast<float>(d);
+        at.l_a *= exp2i(d);
+        at.l_b *= exp2i(d);
+        at.scale_acc(unit_change(vexp + d, e));
+        room -= d;
         vexp = e;
-        inv_unit = exp2i(-e);
+        top = static_cast<float>(e);
+        unit = exp2i(Att::kWeightUpLog2 - e);
       }
-      pv[0] = vsc[0] * inv_unit;
-      pv[1] = vsc[1] * inv_unit;
-      at.template tiles<2, Geom::kTileBytes, true>(sK, nv, sl2k, pv, lane, up_a, up_b);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        pv[u] = nv[u] > 0 ? pv[u] * unit : 0.f;
+        lift[u] = fmaxf(lift[u] - top, -static_cast<float>(kSpread));
+      }
+      at.template tiles<2, Geom::kTileBytes, true>(sK, nv, sl2k, pv, lane, up_a, up_b, lift);
       __syncwarp();
       if (i + NST < cnt) issue(i + NST);
       if (i + 1 + NST < cnt) issue(i + 1 + NST);
     }
-    at.scale_acc(exp2i(vexp));
+    // Out of the unit.  Of a very large one (2^60 and more) a part stays in m
+    // and the sum: the accumulator adds up tokens before it is divided.
+    const int stay = max(vexp - Att::kWeightUpLog2 - 60, 0);
+    at.m_a += static_cast<float>(stay);
+    at.m_b += static_cast<float>(stay);
+    at.l_a *= exp2i(-stay);
+    at.l_b *= exp2i(-stay);
+    at.scale_acc(exp2i(vexp - Att::kWeightUpLog2 - stay));
   }
   at.finish_sums();
 

@@ -68,3 +68,107 @@ def test_scales_that_no_summary_has(n, zero_query):
         sc = R.scores(q[0, 4 * g:4 * g + 4], codes[at, g], unit, 3.3895313892515355e38)
         want = R.select(np.where(ok, sc, -np.inf), n, keep, 1, 2)
         assert s.sel[0, g].tolist() == want and int(s.cnt[0, g]) == keep
+
+
+def check_channels(a, split, floor):
+    """a's rows against the float64 statement, each channel to the magnitudes that meet in it.
+
+    A weight p_t (the largest of the row is 1) is off by 2 eps_t of itself for its score's error eps_t
+    (layer_ref.attend_bound, of this token), by `split` for the two parts that hold it, and by `floor`, of the
+    largest weight times value scale, where the parts' subnormals end (c: the values without their scale u).  Sums
+    lose at most 2^-23 a token and merge, above and below the line:
+        |err_d| <= sum_t p_t (r_t + r) |v_td| / l + floor max_t(p_t u_t) sum_t |c_td| / l,
+        r_t = 2 eps_t + split + (n + 64) 2^-23,  r = sum_t p_t r_t / l."""
+    torch.cuda.synchronize()
+    assert int(a.status.item()) == 0
+    got, q, tables = f64(a.out), f64(a.q), a.tables.cpu().numpy()
+    G, worst = a.Hq // a.Hkv, 0.0
+    for s, L in enumerate(a.lens):
+        for g in range(a.Hkv):
+            blocks = a.sel[s, g, :int(a.cnt[s, g])].tolist()
+            k, v = (np.concatenate([a.values(p, sc, int(tables[s, b]), g)[:min(a.B, int(L) - b * a.B)]
+                                    for b in blocks])
+                    for p, sc in ((a.kp, getattr(a, "ks", None)), (a.vp, getattr(a, "vs", None))))
+            u = np.ones(k.shape[0])
+            if a.fp8:
+                u = np.repeat(f64(a.vs)[tables[s, blocks], g], a.B)[:k.shape[0]]
+            for h in range(g * G, (g + 1) * G):
+                logit = a.scale * (k @ q[s, h])
+                p = np.exp(logit - logit.max())
+                eps = a.D * 2.0 ** -23 * a.scale * (np.abs(k) @ np.abs(q[s, h]))
+                want, l = p @ v / p.sum(), p.sum()
+                r = 2 * eps + split + (k.shape[0] + 64) * 2.0 ** -23
+                tol = (p * (r + p @ r / l)) @ np.abs(v) / l + floor * (p * u).max() * (np.abs(v).T / u).sum(1) / l
+                err = np.abs(got[s, h] - want)
+                tol = tol + 2.0 ** -24 * np.abs(want)
+                worst = max(worst, float((err / tol).max()))
+    assert worst <= 1.0, worst
+
+
+def _scored(a, blocks, code):
+    """Gives the keys of sequence 0's listed blocks `code` (FP8) or its value in channel 0, other keys 0 there."""
+    phys = a.tables[0].long()
+    a.kp[..., 0] = 0
+    for b in blocks:
+        a.kp[phys[b], :, :, 0] = code
+
+
+# Two f16 parts of a weight (times value scale) times 2^14: half a step of the second part, and half of f16's
+# smallest number, in a unit at most twice the largest.
+F16_PARTS = dict(split=2.0 ** -22, floor=2.0 ** -38)
+
+
+@pytest.mark.parametrize("e", [0, 8, 12, 16, 20, 40])
+@pytest.mark.parametrize("low", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_weights_under_far_apart_value_scales(dtype, low, e):
+    """low: the first half of the blocks has values 2^e times as large and next to no weight, in every warp's
+    first tiles.  Else: the first block has most of the weight and values 2^e times smaller than the rest."""
+    a = Attend([2048], Hq=8, Hkv=2, keep=128, fp8=True, dtype=dtype, seed=e)
+    phys = a.tables[0, :128].long()
+    a.q *= 0.125
+    a.vs[:] = 2.0 ** -6
+    a.ks[:] = 1 / 32
+    if low:  # a score of -448 / 32 * 40 / sqrt(128) = -49.5 in channel 0
+        _scored(a, range(64), 0xFE)
+        a.q[..., 0] = 40.0
+        a.vs[phys[:64]] = 2.0 ** (e - 6)
+    else:  # 12.4
+        _scored(a, [0], 0x7E)
+        a.q[..., 0] = 10.0
+        a.vs[phys[0]] = 2.0 ** (-6 - e)
+    a.call()
+    check_channels(a, **F16_PARTS)
+
+
+@pytest.mark.parametrize("base", [-90, -6, 100])
+@pytest.mark.parametrize("first", [True, False])
+def test_long_lists_under_far_apart_value_scales(first, base):
+    """Some 65 tiles a warp: half of the blocks, the first or the last, has values far larger than the others,
+    which are about 2^base, and next to no weight."""
+    a = Attend([67200], Hq=2, Hkv=1, keep=4200, fp8=True, seed=5)
+    phys = a.tables[0, :4200].long()
+    a.q *= 0.125
+    a.vs[:] = 2.0 ** base * (1 + torch.rand(a.vs.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(1)))
+    a.ks[:] = 1 / 32
+    low = range(2100) if first else range(2100, 4200)
+    _scored(a, low, 0xFE)
+    a.q[..., 0] = 40.0
+    a.vs[phys[low.start:low.stop]] = 2.0 ** min(base + 24, 112)
+    a.call()
+    check_channels(a, **F16_PARTS)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,q0", [(128, 10.0), (64, 11.0), (128, 15.0)])
+def test_small_weights_keep_their_bits(dtype, D, q0):
+    """16-bit pools: one block has nearly all the weight and no values, so the rows are made of weights
+    that are all about exp(-14 q0 / sqrt(D)), 2^-18 to 2^-28."""
+    a = Attend([1500, 40], Hq=8, Hkv=2, D=D, keep=94, dtype=dtype, seed=D)
+    _scored(a, [2], 14.0)
+    a.q *= 0.125
+    a.q[0, :, 0] = q0
+    a.vp[a.tables[0, 2].long()] = 0
+    a.call()
+    # bf16 has float32's exponents: a second part of 2^-17 and no floor.
+    check_channels(a, **(F16_PARTS if dtype == "f16" else dict(split=2.0 ** -16, floor=0.0)))
