@@ -547,7 +547,9 @@ pkv_status pkv_summarize_blocks_fp8(void* summary, float* summary_scale, const v
  *   (the power of two that summaries use; nearest, ties to even): an upper
  *   bound of the scores of the block's keys for the rounded q.  The sum is
  *   an integer, so equal inputs give equal choices everywhere; equal scores
- *   go to the lowest block.
+ *   go to the lowest block.  (Scores are compared in float32 divided by the
+ *   group's largest q_scale: exact where q_scale / largest * summary_scale is
+ *   at least 2^-127, rounded below.)
  *   selected     : int32 [num_seqs][num_kv_heads][keep] logical blocks, ascending, then -1.
  *   counts       : int32 [num_seqs][num_kv_heads] = min(n, keep).
  *   q            : [num_seqs][num_q_heads][head_dim] of q_dtype, 16-byte aligned.

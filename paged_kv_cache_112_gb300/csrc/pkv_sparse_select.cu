@@ -461,9 +461,10 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
   __syncthreads();  // q_codes
 
   // Query fragments: this lane's words of head gr.  All heads' scales times
-  // 2^-(22 + the largest exponent): the order stays, and integer * scale *
-  // summary scale neither overflows nor, for the head with that exponent,
-  // loses a bit (2^-22 * 2^-126 is a subnormal float32).
+  // 2^-(22 + the largest exponent), down to float32's subnormals: integer *
+  // scale * summary scale does not overflow and is exact while scale times
+  // summary scale is 2^-149 or more, 2^-22 * 2^-126 for the head with that
+  // exponent; below, it rounds, which swaps no two scores.
   uint32_t qf[X][4], qn[X][4];  // positive, negative parts
 #pragma unroll
   for (int x = 0; x < X; ++x) {
@@ -481,8 +482,8 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
   // 2 tq + 1, the product's columns; FEW: 2 (tq & 1) and the next.
   const int head_a = 2 * (FEW ? tq & 1 : tq);
   const bool live_a = head_a < a.group, live_b = head_a + 1 < a.group;
-  const float scale_a = exp2_int(max(q_exp[head_a] - emax - 22, -126));
-  const float scale_b = exp2_int(max(q_exp[head_a + 1] - emax - 22, -126));
+  const float scale_a = ldexpf(1.f, q_exp[head_a] - emax - 22);
+  const float scale_b = ldexpf(1.f, q_exp[head_a + 1] - emax - 22);
 
   const uint32_t keys_at = cluster_map(smem_u32(keys), 0);
   cluster_wait();  // the first CTA has begun

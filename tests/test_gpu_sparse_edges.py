@@ -172,3 +172,22 @@ def test_small_weights_keep_their_bits(dtype, D, q0):
     a.call()
     # bf16 has float32's exponents: a second part of 2^-17 and no floor.
     check_channels(a, **(F16_PARTS if dtype == "f16" else dict(split=2.0 ** -16, floor=0.0)))
+
+
+def test_heads_scored_far_apart():
+    """One head's positive score decides against another's whose queries are 2^120 times smaller, in blocks
+    whose summaries are far apart too."""
+    s = Select([40 * 16], Hq=2, Hkv=1, keep=4, first=0, last=1)
+    phys = s.tables[0, :40].long()
+    s.q.zero_()
+    s.q[0, 0, 0], s.q[0, 1, 64:] = 1.0, 2.0 ** -120
+    s.summary.zero_()
+    s.summary[phys, 0, :, 0] = -1  # the first head: negative everywhere,
+    s.summary[phys, 0, :, 64:] = 100  # the second: the same positive score in every block
+    s.scale[phys] = 1.0
+    for b in (11, 23, 38):  # but here the first head's is positive, and larger than the second's elsewhere
+        s.summary[phys[b], 0, :, 0] = 1
+        s.scale[phys[b]] = 2.0 ** -95
+    s.call()
+    s.check()
+    assert s.sel[0, 0].tolist() == [11, 23, 38, 39]
