@@ -37,19 +37,45 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libpkv")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(EXT):
+def _older(target: str, deps: list) -> bool:
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [EXT_SOURCE]] + [os.path.abspath(__file__)]
-    return any(os.path.getmtime(p) > t for p in deps)
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(p) > t for p in deps + [os.path.abspath(__file__)])
+
+
+def _lib_stale() -> bool:
+    return _older(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS])
+
+
+def _ext_stale() -> bool:
+    return _older(EXT, [os.path.join(CSRC, EXT_SOURCE), os.path.join(ROOT, "include", "pkv.h")])
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    if not force and not _stale():
+    """Builds what is missing or older than its sources.  The library needs no torch: where torch does not
+    import, the extension is left out and stderr says so."""
+    lib, ext = force or _lib_stale(), force or _ext_stale()
+    torch_dirs = None
+    if ext:
+        try:
+            torch_dirs = _torch_dirs()
+        except Exception as e:  # not installed, or installed and broken
+            sys.stderr.write(f"{os.path.basename(EXT)} is not built: torch does not import ({e})\n")
+    if not lib and not torch_dirs:
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ext_obj = ex.submit(_compile_ext, torch_dirs) if torch_dirs else None
+        if lib:
+            _build_lib(nvcc, ex, verbose, ptxas_verbose)
+        if ext_obj:
+            _link_ext(ext_obj.result(), torch_dirs)
+    return LIB
+
+
+def _build_lib(nvcc: str, ex: ThreadPoolExecutor, verbose: bool, ptxas_verbose: bool) -> None:
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
 
     def compile_one(src):
@@ -62,17 +88,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ext_obj = ex.submit(_compile_ext)
-        objs = list(ex.map(compile_one, SOURCES))
-        ext_obj = ext_obj.result()
+    objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_ext(ext_obj)
-    return LIB
 
 
 def _torch_dirs() -> tuple:
@@ -82,8 +103,8 @@ def _torch_dirs() -> tuple:
     return os.path.join(root, "include"), os.path.join(root, "lib"), torch.__version__
 
 
-def _compile_ext() -> str:
-    inc, _, version = _torch_dirs()
+def _compile_ext(torch_dirs: tuple) -> str:
+    inc, _, version = torch_dirs
     obj = os.path.join(OUT_DIR, "pkv_torch.o")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(ROOT, "include"), "-isystem", inc, "-isystem",
@@ -95,9 +116,9 @@ def _compile_ext() -> str:
     return obj
 
 
-def _link_ext(obj: str) -> None:
+def _link_ext(obj: str, torch_dirs: tuple) -> None:
     """Links against libpkv.so beside it and the installed torch."""
-    _, lib, _ = _torch_dirs()
+    _, lib, _ = torch_dirs
     tmp = EXT + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-l:libpkv.so", "-L", lib, "-lc10", "-lc10_cuda",
            "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
