@@ -48,20 +48,26 @@ def _lib_stale() -> bool:
     return _older(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS])
 
 
-def _ext_stale() -> bool:
-    return _older(EXT, [os.path.join(CSRC, EXT_SOURCE), os.path.join(ROOT, "include", "pkv.h")])
+def _ext_stale(version: str) -> bool:
+    """Older than its sources, or built for another torch than `version`."""
+    if _older(EXT, [os.path.join(CSRC, EXT_SOURCE), os.path.join(ROOT, "include", "pkv.h")]):
+        return True
+    if not os.path.exists(EXT + ".torch"):
+        return True
+    with open(EXT + ".torch") as f:
+        return f.read() != version
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Builds what is missing or older than its sources.  The library needs no torch: where torch does not
-    import, the extension is left out and stderr says so."""
-    lib, ext = force or _lib_stale(), force or _ext_stale()
-    torch_dirs = None
-    if ext:
-        try:
-            torch_dirs = _torch_dirs()
-        except Exception as e:  # not installed, or installed and broken
-            sys.stderr.write(f"{os.path.basename(EXT)} is not built: torch does not import ({e})\n")
+    """Builds what is missing, older than its sources or made for another torch.  The library needs no torch:
+    where torch does not import, the extension is left out and stderr says so."""
+    lib, torch_dirs = force or _lib_stale(), None
+    try:
+        torch_dirs = _torch_dirs()
+    except Exception as e:  # not installed, or installed and broken
+        sys.stderr.write(f"{os.path.basename(EXT)} is not built: torch does not import ({e})\n")
+    if torch_dirs and not (force or _ext_stale(torch_dirs[2])):
+        torch_dirs = None
     if not lib and not torch_dirs:
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
@@ -118,7 +124,7 @@ def _compile_ext(torch_dirs: tuple) -> str:
 
 def _link_ext(obj: str, torch_dirs: tuple) -> None:
     """Links against libpkv.so beside it and the installed torch."""
-    _, lib, _ = torch_dirs
+    _, lib, version = torch_dirs
     tmp = EXT + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-l:libpkv.so", "-L", lib, "-lc10", "-lc10_cuda",
            "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
@@ -126,6 +132,8 @@ def _link_ext(obj: str, torch_dirs: tuple) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, EXT)
+    with open(EXT + ".torch", "w") as f:
+        f.write(version)
 
 
 if __name__ == "__main__":

@@ -71,3 +71,38 @@ def test_library_beside_an_extension_that_does_not_compile(compilers):
     with pytest.raises(RuntimeError, match="pkv_torch.cpp"):
         B.build()
     assert built(compilers)[0] == [True, False]
+
+
+def test_extension_of_another_torch(compilers, monkeypatch):
+    """Another installed torch makes the extension stale, whatever the files' times; the library is not."""
+    import torch
+
+    B.build()
+    built(compilers)
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1+other")
+        B.build()
+        assert built(compilers) == ([True, True], {"pkv_torch.o", "_pkv_torch.so"})
+        assert '-DPKV_TORCH_VERSION="0.0.1+other"' in open(os.path.join(B.OUT_DIR, "pkv_torch.o")).read()
+        B.build()
+        assert built(compilers)[1] == set()
+    B.build()
+    assert built(compilers)[1] == {"pkv_torch.o", "_pkv_torch.so"}
+
+
+def test_an_extension_of_another_torch_is_refused(monkeypatch):
+    """One that was built before torch changed: the first layer operator says what to do."""
+    import torch
+
+    import paged_kv_cache_112_gb300 as pkv
+    from paged_kv_cache_112_gb300 import _binding
+
+    try:
+        B.build()
+    except RuntimeError as e:  # no nvcc on this machine
+        pytest.skip(str(e))
+    monkeypatch.setattr(_binding, "_EXT", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    with pytest.raises(pkv.PkvError, match="rebuild"):
+        _binding._ext()
+    assert _binding._EXT is None
