@@ -575,9 +575,12 @@ pkv_status pkv_select_blocks(int32_t* selected, int32_t* counts, const void* q, 
  *   selected, counts, keep : as pkv_select_blocks writes them, or a list of
  *                  the caller's own: logical blocks of the sequence, strictly
  *                  ascending.  An entry that is not larger than the one
- *                  before it or lies outside the sequence sets
- *                  PKV_DEV_ERR_SELECT and is passed over; so does a count
- *                  outside [0, keep], which is clamped.
+ *                  before it (whether that one counted or not) or lies
+ *                  outside the sequence sets PKV_DEV_ERR_SELECT and is passed
+ *                  over; so does a count outside [0, keep], which is clamped.
+ *                  Only neighbours are compared: a block that comes again
+ *                  behind another one ([5, 3, 5]) is flagged by the entry
+ *                  between, and counts twice.
  * A row without tokens is zero.  One kernel, no workspace.  q 16-byte
  * aligned; head_dim 64 or 128, 1 <= group <= 8, block sizes 16, 32 and 64;
  * other arguments and flags as in pkv_decode_attention.

@@ -93,7 +93,10 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
   const int cnt = tiles > w0 ? (tiles - w0 + W - 1) / W : 0;
 
   // Place of this warp's tile i.  A list entry counts when it is larger than
-  // its predecessor and inside the sequence, so no token counts twice.
+  // its predecessor and inside the sequence: every entry of an ascending list,
+  // no token twice.  A list that is not ascending is flagged where it descends
+  // or repeats; as nothing is known of the entries further back, a block that
+  // comes again behind another one counts again.
   auto place = [&](int i, const Entry& r) {
     TilePlace p{-1, 0, 0};
     if (i >= cnt) return p;

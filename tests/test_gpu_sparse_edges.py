@@ -191,3 +191,14 @@ def test_heads_scored_far_apart():
     s.call()
     s.check()
     assert s.sel[0, 0].tolist() == [11, 23, 38, 39]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("given,counted", [([5, 3, 5], [5, 5]), ([5, -1, 5], [5, 5]), ([1, 50, 20], [1]),
+                                           ([7, 7, 7], [7]), ([9, 8, 7], [9]), ([2, 4, 3, 4], [2, 4, 4])])
+def test_lists_that_do_not_ascend(given, counted, fp8):
+    """Flagged, and what counts is what the comparison of neighbours leaves."""
+    a = Attend([800, 33], Hq=4, Hkv=1, keep=len(given), fp8=fp8)
+    a.sel[0, 0] = torch.tensor(given)
+    a.call()
+    a.check(pkv.DEV_ERR_SELECT, {(0, 0): counted})
