@@ -202,3 +202,14 @@ def test_lists_that_do_not_ascend(given, counted, fp8):
     a.sel[0, 0] = torch.tensor(given)
     a.call()
     a.check(pkv.DEV_ERR_SELECT, {(0, 0): counted})
+
+
+@pytest.mark.parametrize("kind", [dict(), dict(fp8=True), dict(D=64, dtype="f16")])
+@pytest.mark.parametrize("units,tiles", [(20, 70), (50, 60), (76, 300), (100, 128), (200, 90)])
+def test_attention_of_long_lists_on_small_clusters(units, tiles, kind):
+    """From twenty lists to a few more than SMs, long enough that CTAs share them: at head size 128 these are
+    8 warps in clusters of 4, 4 of 8, 8 of 2, 4 of 4 and 4 of 2."""
+    a = Attend([16 * tiles - i % 16 if i % 5 else 16 for i in range(units)], Hq=2, Hkv=1, keep=tiles, seed=units,
+               **kind)
+    a.call()
+    a.check()
