@@ -8,9 +8,9 @@
 //
 // Bound: HBM bytes of the selected K and V rows (each read once; all query
 // heads of the group share them); with few units the latency of length ->
-// list -> table entry -> tile.  (256 sequences of 64 blocks, 8 KV heads: 155.4
-// us, 6.6 TB/s; 8 of 128 over FP8 pools: 12.1 us, 4 of them before the first
-// tile and after the last; one of 128: 5.3 us.)
+// list -> table entry -> tile.  (256 sequences of 64 blocks, 8 KV heads: 155.6
+// us, 6.6 TB/s; 8 of 128 over FP8 pools: 12.3 us, 4 of them before the first
+// tile and after the last, on 128 of the SMs; one of 128: 5.4 us.)
 //
 // One cluster of C CTAs of NW warps per (s, g).  The list's 16-token tiles are
 // dealt to the cluster's warps in turn; each warp streams its tiles through a
@@ -185,12 +185,14 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
     // 2^d, lowering m by d (times 2^d for the sum) leaves the accumulator's
     // numbers as they are.  Weights without their scales then exceed 1: lift
     // >= -kSpread and at most kSpread of lowering keep their sum below 2^97 a
-    // token.
-    constexpr int kSpread = 48;
+    // token.  (Up to the first scale of 2^kLeast and more, zeros among the
+    // smaller ones, m is lowered to lift = -kSpread at most and none of that
+    // counts.)
+    constexpr int kSpread = 48, kLeast = -100;
     const float up = at.template load_q<BF16, true>(q0, G, lane);
     const float up_a = __shfl_sync(kFull, up, 8 * (lane & 3)), up_b = __shfl_sync(kFull, up, 8 * (lane & 3) + 4);
-    int vexp = -100, room = kSpread;
-    float top = -100.f, unit = exp2i(Att::kWeightUpLog2 + 100);
+    int vexp = kLeast, room = kSpread;
+    float top = kLeast, unit = exp2i(Att::kWeightUpLog2 - kLeast);
     for (int i = 0; i < cnt; i += 2) {
       const bool two = i + 1 < cnt;
       const bool ok = ring.wait(i, a.timeout_ns) && (!two || ring.wait(i + 1, a.timeout_ns));
@@ -214,13 +216,15 @@ __global__ void __launch_bounds__(NW * 32) decode_sparse_kernel(const DecodeArgs
         sK[u] = ring.k_tile(j);
       }
       if (fmaxf(lift[0], lift[1]) > top && vexp < 126) {  // the same for the whole warp
-        const int e = min(static_cast<int>(fmaxf(lift[0], lift[1])), 126), d = i > 0 ? min(e - vexp, room) : 0;
+        const int e = min(static_cast<int>(fmaxf(lift[0], lift[1])), 126);
+        const bool begun = vexp > kLeast;
+        const int d = min(e - vexp, begun ? room : kSpread - (126 + kLeast));
         at.m_a -= static_cast<float>(d);
         at.m_b -= static_cast<float>(d);
         at.l_a *= exp2i(d);
         at.l_b *= exp2i(d);
         at.scale_acc(unit_change(vexp + d, e));
-        room -= d;
+        if (begun) room -= d;
         vexp = e;
         top = static_cast<float>(e);
         unit = exp2i(Att::kWeightUpLog2 - e);
@@ -425,7 +429,7 @@ struct SparseLaunch {
 //   38 of 128: 10.8 with 4 warps of 8 -- 15.7 with 8 of 4, 11.8 with 8 of 2;
 //   64 of 128 (FP8): 11.8 with 8 warps of 2, 12.6 with 4 of 4;
 //   100 of 512 (FP8): 37.7 with 4 warps of 4, 51 with 8 alone;
-//   160 of 512 (FP8): 61 with 4 warps of 2, 87 with 4 alone, 142 with 2;
+//   160 of 512 (FP8): 64 with 4 warps of 2, 87 with 4 alone, 142 with 2;
 //   912 of 5: 10.3 with 2 warps alone, 12.9 with 4; 2000 of 64: 153 with 4, 157
 //   with 2, 171 with 8, 180 with 1.
 template <int D, bool FP8>

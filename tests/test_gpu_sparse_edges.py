@@ -89,16 +89,17 @@ def check_channels(a, split, floor):
             k, v = (np.concatenate([a.values(p, sc, int(tables[s, b]), g)[:min(a.B, int(L) - b * a.B)]
                                     for b in blocks])
                     for p, sc in ((a.kp, getattr(a, "ks", None)), (a.vp, getattr(a, "vs", None))))
-            u = np.ones(k.shape[0])
+            u, c = np.ones(k.shape[0]), v
             if a.fp8:
                 u = np.repeat(f64(a.vs)[tables[s, blocks], g], a.B)[:k.shape[0]]
+                c = np.where(u[:, None] > 0, v / np.where(u > 0, u, 1)[:, None], 448.0)
             for h in range(g * G, (g + 1) * G):
                 logit = a.scale * (k @ q[s, h])
                 p = np.exp(logit - logit.max())
                 eps = a.D * 2.0 ** -23 * a.scale * (np.abs(k) @ np.abs(q[s, h]))
                 want, l = p @ v / p.sum(), p.sum()
                 r = 2 * eps + split + (k.shape[0] + 64) * 2.0 ** -23
-                tol = (p * (r + p @ r / l)) @ np.abs(v) / l + floor * (p * u).max() * (np.abs(v).T / u).sum(1) / l
+                tol = (p * (r + p @ r / l)) @ np.abs(v) / l + floor * (p * u).max() * np.abs(c).sum(0) / l
                 err = np.abs(got[s, h] - want)
                 tol = tol + 2.0 ** -24 * np.abs(want)
                 worst = max(worst, float((err / tol).max()))
@@ -142,10 +143,11 @@ def test_weights_under_far_apart_value_scales(dtype, low, e):
 
 
 @pytest.mark.parametrize("base", [-90, -6, 100])
-@pytest.mark.parametrize("first", [True, False])
-def test_long_lists_under_far_apart_value_scales(first, base):
+@pytest.mark.parametrize("first,zeros", [(True, False), (False, False), (False, True)])
+def test_long_lists_under_far_apart_value_scales(first, zeros, base):
     """Some 65 tiles a warp: half of the blocks, the first or the last, has values far larger than the others,
-    which are about 2^base, and next to no weight."""
+    which are about 2^base, and next to no weight.  zeros: each warp's first two tiles have most of the weight,
+    and value scales of zero."""
     a = Attend([67200], Hq=2, Hkv=1, keep=4200, fp8=True, seed=5)
     phys = a.tables[0, :4200].long()
     a.q *= 0.125
@@ -155,6 +157,9 @@ def test_long_lists_under_far_apart_value_scales(first, base):
     _scored(a, low, 0xFE)
     a.q[..., 0] = 40.0
     a.vs[phys[low.start:low.stop]] = 2.0 ** min(base + 24, 112)
+    if zeros:
+        a.kp[phys[:128], :, :, 0] = 0x6C  # 96: e^10.6 times the weight
+        a.vs[phys[:128]] = 0
     a.call()
     check_channels(a, **F16_PARTS)
 
