@@ -581,7 +581,9 @@ pkv_status pkv_select_blocks(int32_t* selected, int32_t* counts, const void* q, 
  *                  Only neighbours are compared: a block that comes again
  *                  behind another one ([5, 3, 5]) is flagged by the entry
  *                  between, and counts twice.
- * A row without tokens is zero.  One kernel, no workspace.  q 16-byte
+ * A row without tokens is zero.  A channel that meets an infinite value in a
+ * listed block's tokens is infinite or NaN (weights are held in two parts).
+ * One kernel, no workspace.  q 16-byte
  * aligned; head_dim 64 or 128, 1 <= group <= 8, block sizes 16, 32 and 64;
  * other arguments and flags as in pkv_decode_attention.
  */

@@ -9,10 +9,14 @@
 // divided by the block's scale and rounded once to e4m3.
 //
 // Bound: HBM bytes (each row read and written once, ~3 flops a byte): 16384
-// tokens of 32 + 16 heads in 64.7 us, 6.35 TB/s; 4097 tokens into FP8 pools,
-// bound by the instructions of two e4m3 conversions an element, in 19.9 us, 4.1
-// TB/s.  With few tokens the latency of position -> angle row -> store (1.7 us
-// for one, 3.4 for 256).
+// tokens of 32 + 16 heads in 64.7 us, 6.35 TB/s.  Head counts whose groups do
+// not divide into equal parts stay further from it, as a streaming warp then
+// has parts of unequal size (8192 tokens: 32 + 16 heads 1.13 times the bytes'
+// time, 40 + 16 1.24, 16 + 4 1.67, 6 + 12 1.85).  4097 tokens of 32 + 8 heads
+// into FP8 pools take 20.0 us, 1.65 times their bytes' time, on the direct
+// kernel: 52% of the issue slots, 28% of DRAM, and loads that wait for one
+// another (position -> angles, sum -> weights, slot -> scale) as the largest
+// stall.  With few tokens that latency alone (1.7 us for one, 3.4 for 256).
 //
 // Layout: D/16 lanes share a head, each holding two 16-byte chunks chosen so
 // that both members of every rotated pair (i, i + rot_dim/2) sit in one lane:

@@ -14,8 +14,8 @@
 // group's heads; the best ones are taken, equal scores by the lowest block.
 //
 // Bound: HBM bytes of the summaries, 2D + 4 a block and KV head (8 sequences of
-// 2048 to 8192 blocks: 29.0 us, 21 of them the scores at 5.2 TB/s, 6 the search
-// after them); with few blocks the latency of length -> table -> summary ->
+// 2048 to 8192 blocks: 27.8 us, 20 of them the scores at 5.2 TB/s, 6 the search
+// after them; every sequence has as many CTAs, so the longest ones end last); with few blocks the latency of length -> table -> summary ->
 // ranks (64 sequences of up to 128 blocks: 6.2 us).
 #include "pkv_device.cuh"
 
@@ -93,8 +93,9 @@ __device__ __forceinline__ float finite_bound(float x, float most) {
 // 1 = bf16, 2 = FP8 (codes compared as f16, which holds every e4m3 value).
 //
 // Bound: 16-bit pools HBM (8192 blocks of 8 heads in 46.0 us, 6.2 TB/s);
-// FP8 pools the instruction rate (a code costs as many as a 16-bit key; 4001
-// blocks of 8 heads in 15.6 us, 4.7 TB/s).
+// FP8 pools neither memory nor the issue rate alone (4001 blocks of 8 heads in
+// 15.6 us, 4.7 TB/s: a code costs as many instructions as a 16-bit key of
+// twice its bytes, 41% of the issue slots with two CTAs of 120 registers a SM).
 template <int D, int KIND>
 __global__ void __launch_bounds__(256) summarize_blocks_kernel(const SummarizeArgs a) {
   constexpr int EB = KIND == 2 ? 1 : 2;
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
       const int row = 16 * half + gr + (low_row ? 0 : 8);
       const float psc = __shfl_sync(kFull, scales, row);
       const int b = base + row;
-      // A power of two after the maximum: the same as before it.
+      // The block's scale after the maximum over heads: it is their common factor.
       if (low_pair && b < n) cluster_store_u32(keys_at + 4 * b, psc >= 0.f ? order_key(top * psc) : 0u);
     } else {
       float best[2];
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(NT) select_blocks_kernel(const SelectArgs a, i
         best[r] = fmaxf(best[r], __shfl_xor_sync(kFull, best[r], 1));
         best[r] = fmaxf(best[r], __shfl_xor_sync(kFull, best[r], 2));
       }
-      // Lanes tq = 0 and 1 store rows gr and gr + 8 (a power of two after the maximum: the same as before it).
+      // Lanes tq = 0 and 1 store rows gr and gr + 8 (the block's scale is the heads' common factor).
       const int row = 16 * half + gr + 8 * (tq & 1);
       const float psc = __shfl_sync(kFull, scales, row);
       const int b = base + row;
@@ -899,7 +900,7 @@ cudaError_t launch_select_t(const SelectArgs& a, int64_t cap, cudaStream_t strea
 // More threads where a sequence may have more blocks: each warp still scores
 // four chunks or more, and the first CTA's search of the keys is shared among
 // more threads (8 sequences of up to 8192 blocks: 57.7 us with 128 threads, 30.5
-// with 256, 29.0 with 512).
+// with 256, 27.8 with 512).
 template <int D, bool BF16>
 cudaError_t launch_select_n(const SelectArgs& a, cudaStream_t stream) {
   const int64_t cap = min(static_cast<int64_t>(a.max_blocks_per_seq),
