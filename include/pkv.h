@@ -604,6 +604,106 @@ pkv_status pkv_decode_sparse_fp8(void* out, const void* q, const void* k_pool, c
                                  void* stream);
 
 /*
+ * -------------------------------------------------------------- 4-bit pools
+ *
+ * Pools of 4-bit e2m1 codes (1 sign, 2 exponent bits, 1 mantissa bit: 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6) with an e4m3 scale for every 16 channels of a token:
+ * 4.5 bits an element.  Element value = code * scale * (k|v)_scale[KV head].
+ *   pools            : uint8 [num_blocks][num_kv_heads][block_size / 16][9 * head_dim]:
+ *                      a record per KV head and 16 tokens, its codes [16][head_dim / 2]
+ *                      (the even channel in a byte's low half), then its scales
+ *                      [16][head_dim / 16].  16-byte aligned.
+ *   k_scale, v_scale : float32 [num_kv_heads], 4-byte aligned, positive and finite, or NULL
+ *                      (1): the head's range, set by the caller (e.g. from a calibrated
+ *                      amax) so that the e4m3 scales, 2^-9 to 448, cover its values.  They
+ *                      belong to the layer: reads and writes take the same ones.
+ *   num_layers       : as for FP8 pools: block b of a layer starts num_layers blocks'
+ *                      bytes further apart; pass the layer's base pointers.
+ * Rows are quantised when they are written, each on its own: appending changes
+ * nothing of the tokens written before.  head_dim 64 or 128; block sizes 16, 32
+ * and 64.  pkv_swap_blocks moves such pools as it does any blocks of bytes.
+ */
+
+/*
+ * pkv_write_cache_fp4 -- the write path into 4-bit pools: for every token i
+ * with a slot, KV head g and 16 adjacent channels x,
+ *     z = float32(x) * r,  r = 1 / k_scale[g] rounded to float32,
+ *     s = e4m3(max |z| / 6),  code = e2m1(z / s),
+ * divisions and products in IEEE float32, both roundings to the nearest with
+ * ties to even, magnitudes beyond 448 and 6 saturating.  s = 0: codes of zero.
+ * (The sign of a zero is not specified.)
+ * A group with a NaN gets the scale NaN: its 16 values are.
+ * Other arguments and flags as pkv_write_cache_fp8.
+ */
+pkv_status pkv_write_cache_fp4(const void* k_new, const void* v_new, void* k_pool, void* v_pool, const float* k_scale,
+                               const float* v_scale, const int32_t* slot_mapping, int num_tokens,
+                               int64_t new_row_stride, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                               int num_layers, pkv_dtype new_dtype, int32_t* dev_status, void* stream);
+
+/* pkv_norm_rope_write_fp4 -- pkv_norm_rope_write into 4-bit pools: the float32 key after norm and rotation, not
+ * rounded to 16 bits before, and the value are quantised as in pkv_write_cache_fp4. */
+pkv_status pkv_norm_rope_write_fp4(void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, const void* q,
+                                   int64_t q_stride, const void* k, const void* v, int64_t new_row_stride,
+                                   const void* q_weight, const void* k_weight, float eps, const float* cos_sin,
+                                   const int32_t* positions, int max_positions, int rot_dim, int interleaved,
+                                   void* k_pool, void* v_pool, const float* k_scale, const float* v_scale,
+                                   const int32_t* slot_mapping, int num_tokens, int num_q_heads, int num_kv_heads,
+                                   int head_dim, int block_size, int num_blocks, int num_layers, pkv_dtype new_dtype,
+                                   int32_t* dev_status, void* stream);
+
+/* pkv_copy_blocks_fp4 -- copy-on-write over 4-bit pools, codes and scales of every layer; rules and errors as
+ * pkv_copy_blocks. */
+pkv_status pkv_copy_blocks_fp4(void* k_pool, void* v_pool, const int32_t* pairs, int num_pairs, int num_layers,
+                               int num_kv_heads, int head_dim, int block_size, int num_blocks, int32_t* dev_status,
+                               void* stream);
+
+/*
+ * pkv_decode_attention_fp4 -- pkv_decode_attention over 4-bit pools; q has
+ * q_dtype and is 16-byte aligned.  Fixed partitions (workspace of
+ * pkv_decode_workspace_bytes); PKV_PARTITION_BALANCED returns
+ * PKV_ERR_UNSUPPORTED.  Rows of tokens >= L, NaN scales included, are never
+ * used.  Softmax weights enter the product with V rounded to f16 (2^-12 of
+ * each).  1 <= group <= 8.
+ */
+pkv_status pkv_decode_attention_fp4(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                    const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                    int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                    int num_kv_heads, int head_dim, int block_size, int num_blocks, int num_layers,
+                                    float scale, int partition_size, int max_context_len, void* workspace,
+                                    size_t workspace_bytes, pkv_dtype q_dtype, pkv_dtype out_dtype,
+                                    int32_t* dev_status, void* stream);
+
+/*
+ * ------------------------------------------------- windows with first tokens
+ */
+
+/*
+ * pkv_decode_window -- pkv_decode_attention over a sliding window and the
+ * first tokens, which stay visible:
+ *     out[s][h] = sum_t softmax_t(scale * q[s][h] . k_t) v_t,
+ *                 t in [0, L) with t < sinks or t >= L - window.
+ * Blocks without a visible token are not read: their table entries may be
+ * anything (a caller may free them).  window >= 1, sinks >= 0.  One kernel, no
+ * workspace.  Blocks of 16, 32 and 64 tokens, head_dim 64 or 128, 1 <= group
+ * <= 8; q 16-byte aligned; other arguments and flags as pkv_decode_attention.
+ * A channel that meets an infinite value in a visible token is infinite or NaN
+ * (weights are held in two parts).
+ */
+pkv_status pkv_decode_window(void* out, const void* q, const void* k_pool, const void* v_pool, int64_t block_stride,
+                             const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                             int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                             int num_blocks, float scale, int window, int sinks, int max_context_len,
+                             pkv_dtype kv_dtype, pkv_dtype out_dtype, int32_t* dev_status, void* stream);
+
+/* pkv_decode_window_fp4 -- the same over 4-bit pools, as pkv_decode_attention_fp4. */
+pkv_status pkv_decode_window_fp4(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                 const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                 int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                 int num_kv_heads, int head_dim, int block_size, int num_blocks, int num_layers,
+                                 float scale, int window, int sinks, int max_context_len, pkv_dtype q_dtype,
+                                 pkv_dtype out_dtype, int32_t* dev_status, void* stream);
+
+/*
  * ------------------------------------------------------------ block manager
  *
  * Host-side allocator of a pool's blocks (host functions, no GPU call): the

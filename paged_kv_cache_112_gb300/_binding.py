@@ -72,6 +72,14 @@ _SIGS["pkv_decode_sparse"] = ([_c_void_p] * 4 + [_c_int64, _c_void_p, _c_int] + 
                               [_c_float] + [_c_int] * 3 + [_c_void_p] * 2)
 _SIGS["pkv_decode_sparse_fp8"] = ([_c_void_p] * 7 + [_c_int] + [_c_void_p] * 3 + [_c_int] * 8 + [_c_float] +
                                   [_c_int] * 3 + [_c_void_p] * 2)
+_SIGS["pkv_write_cache_fp4"] = _SIGS["pkv_write_cache_fp8"]
+_SIGS["pkv_norm_rope_write_fp4"] = _SIGS["pkv_norm_rope_write_fp8"]
+_SIGS["pkv_copy_blocks_fp4"] = [_c_void_p] * 3 + [_c_int] * 6 + [_c_void_p] * 2
+_SIGS["pkv_decode_attention_fp4"] = _SIGS["pkv_decode_attention_fp8"]
+_SIGS["pkv_decode_window"] = ([_c_void_p] * 4 + [_c_int64, _c_void_p, _c_int, _c_void_p] + [_c_int] * 6 + [_c_float] +
+                              [_c_int] * 5 + [_c_void_p] * 2)
+_SIGS["pkv_decode_window_fp4"] = ([_c_void_p] * 7 + [_c_int, _c_void_p] + [_c_int] * 7 + [_c_float] + [_c_int] * 5 +
+                                  [_c_void_p] * 2)
 _SIGS["pkv_last_cuda_error"] = []
 _SIGS["pkv_cuda_error_name"] = [_c_int]
 
@@ -500,7 +508,7 @@ def norm_rope_write(q, k, v, k_pool, v_pool, slot_mapping, *, q_out, k_out=None,
     q_out (and k_out, optional) receive the rotated rows and may be q and k themselves; pools as
     write_cache.  Tokens with position -1 are padding and are left alone; slot -1 writes no pool row."""
     (_EXT or _ext()).norm_rope_write(q, k, v, k_pool, v_pool, None, None, slot_mapping, q_out, k_out, q_weight,
-                                     k_weight, eps, cos_sin, positions, interleaved, status, stream, False)
+                                     k_weight, eps, cos_sin, positions, interleaved, status, stream, 16)
 
 
 def norm_rope_write_fp8(q, k, v, k_pool, v_pool, k_scale, v_scale, slot_mapping, *, q_out, k_out=None, q_weight=None,
@@ -508,7 +516,7 @@ def norm_rope_write_fp8(q, k, v, k_pool, v_pool, k_scale, v_scale, slot_mapping,
                         stream=None):
     """pkv_norm_rope_write_fp8: norm_rope_write into FP8 pools (uint8 codes, scales as write_cache_fp8)."""
     (_EXT or _ext()).norm_rope_write(q, k, v, k_pool, v_pool, k_scale, v_scale, slot_mapping, q_out, k_out, q_weight,
-                                     k_weight, eps, cos_sin, positions, interleaved, status, stream, True)
+                                     k_weight, eps, cos_sin, positions, interleaved, status, stream, 8)
 
 
 def summarize_blocks(summary, summary_scale, k_pool, block_ids, *, status=None, stream=None):
@@ -543,6 +551,57 @@ def decode_sparse_fp8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, co
     """pkv_decode_sparse_fp8: decode_sparse over FP8 pools (q f16/bf16)."""
     (_EXT or _ext()).decode_sparse(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, selected,
                                    counts, scale, max_context_len, status, stream, True)
+
+
+# ------------------------------------------------------------------ 4-bit pools
+
+# A 4-bit pool: uint8 [NB, H_kv, block_size / 16, 9 * D], per KV head and 16 tokens the e2m1 codes
+# [16, D / 2] and then the e4m3 scales [16, D / 16] (or one layer's view of [NB, layers, ...]);
+# k_scale and v_scale float32 [H_kv], or None.
+
+
+def write_cache_fp4(k_new, v_new, k_pool, v_pool, k_scale, v_scale, slot_mapping, *, status=None, stream=None):
+    """pkv_write_cache_fp4: new rows [T, H_kv, D] f16/bf16 quantised into 4-bit pools through slot_mapping int32 [T]."""
+    (_EXT or _ext()).write_cache_fp4(k_new, v_new, k_pool, v_pool, k_scale, v_scale, slot_mapping, status, stream)
+
+
+def norm_rope_write_fp4(q, k, v, k_pool, v_pool, k_scale, v_scale, slot_mapping, *, q_out, k_out=None, q_weight=None,
+                        k_weight=None, eps=1e-6, cos_sin=None, positions=None, interleaved=False, status=None,
+                        stream=None):
+    """pkv_norm_rope_write_fp4: norm_rope_write into 4-bit pools (quantised as by write_cache_fp4)."""
+    (_EXT or _ext()).norm_rope_write(q, k, v, k_pool, v_pool, k_scale, v_scale, slot_mapping, q_out, k_out, q_weight,
+                                     k_weight, eps, cos_sin, positions, interleaved, status, stream, 4)
+
+
+def copy_blocks_fp4(k_pool, v_pool, pairs, *, status=None, stream=None):
+    """pkv_copy_blocks_fp4: block pairs[i][1] := block pairs[i][0] of whole pools (every layer's)."""
+    (_EXT or _ext()).copy_blocks_fp4(k_pool, v_pool, pairs, status, stream)
+
+
+def decode_attention_fp4(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale, *,
+                         partition_size=0, max_context_len, workspace=None, status=None, stream=None):
+    """pkv_decode_attention_fp4: decode_attention over 4-bit pools (partition kernel + reduce kernel; workspace of
+    decode_workspace_bytes)."""
+    (_EXT or _ext()).decode_attention_fp4(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
+                                          partition_size, max_context_len, workspace, status, stream)
+
+
+# ------------------------------------------------------------------ windows
+
+
+def decode_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, *, window, sinks=0, max_context_len,
+                  status=None, stream=None):
+    """pkv_decode_window: decode_attention over the last `window` tokens and the first `sinks`; one kernel, no
+    workspace."""
+    (_EXT or _ext()).decode_window(out, q, k_pool, v_pool, None, None, block_tables, context_lens, scale, window,
+                                   sinks, max_context_len, status, stream, 16)
+
+
+def decode_window_fp4(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale, *, window, sinks=0,
+                      max_context_len, status=None, stream=None):
+    """pkv_decode_window_fp4: decode_window over 4-bit pools."""
+    (_EXT or _ext()).decode_window(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale, window,
+                                   sinks, max_context_len, status, stream, 4)
 
 
 # ------------------------------------------------------------------ swap

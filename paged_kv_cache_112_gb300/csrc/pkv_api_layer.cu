@@ -27,8 +27,8 @@ pkv_status prepare_norm_rope(NormRopeArgs* a, void* q_out, int64_t q_out_stride,
                              const int32_t* positions, int max_positions, int rot_dim, int interleaved, void* k_pool,
                              void* v_pool, const int32_t* slot_mapping, int num_tokens, int num_q_heads,
                              int num_kv_heads, int head_dim, int block_size, int num_blocks, pkv_dtype dtype,
-                             int32_t* dev_status) {
-  if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0 || rot_dim < 0 ||
+                             int32_t* dev_status, bool kv_alone = false) {  // kv_alone: no queries (0 heads, null)
+  if (num_tokens < 0 || (kv_alone ? num_q_heads != 0 : num_q_heads <= 0) || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0 || rot_dim < 0 ||
       rot_dim > head_dim || (interleaved != 0 && interleaved != 1) || !value_dtype_ok(dtype))
     return PKV_ERR_INVALID_ARG;
   if ((q_weight || k_weight) && !(std::isfinite(eps) && eps > 0.f)) return PKV_ERR_INVALID_ARG;
@@ -45,7 +45,7 @@ pkv_status prepare_norm_rope(NormRopeArgs* a, void* q_out, int64_t q_out_stride,
   const int64_t kvs = row_stride(new_row_stride, kv_row), kos = row_stride(k_out_stride, kv_row);
   if (qs < 0 || qos < 0 || kvs < 0 || kos < 0) return PKV_ERR_INVALID_ARG;
   if (num_tokens == 0) return PKV_OK;
-  if (!q_out || !q || !k || !v || !k_pool || !v_pool || !slot_mapping) return PKV_ERR_INVALID_ARG;
+  if ((!kv_alone && (!q_out || !q)) || !k || !v || !k_pool || !v_pool || !slot_mapping) return PKV_ERR_INVALID_ARG;
   if (rot_dim > 0 && (!cos_sin || !positions || max_positions <= 0)) return PKV_ERR_INVALID_ARG;
   for (const void* p : {static_cast<const void*>(q_out), static_cast<const void*>(k_out), q, k, v, q_weight, k_weight,
                         static_cast<const void*>(cos_sin), static_cast<const void*>(k_pool),
@@ -53,7 +53,7 @@ pkv_status prepare_norm_rope(NormRopeArgs* a, void* q_out, int64_t q_out_stride,
     if (!aligned(p, 16)) return PKV_ERR_INVALID_ARG;
   if (!aligned(positions, 4) || !aligned(slot_mapping, 4) || !aligned(dev_status, 4)) return PKV_ERR_INVALID_ARG;
   // Rows rewritten in place keep their places.
-  if ((q_out == q && qos != qs) || (k_out == k && kos != kvs)) return PKV_ERR_INVALID_ARG;
+  if ((!kv_alone && q_out == q && qos != qs) || (k_out == k && kos != kvs)) return PKV_ERR_INVALID_ARG;
   a->q = static_cast<const uint16_t*>(q);
   a->k = static_cast<const uint16_t*>(k);
   a->v = static_cast<const uint16_t*>(v);
@@ -104,6 +104,60 @@ pkv_status prepare_summarize(SummarizeArgs* a, void* summary, float* summary_sca
   a->num_kv_heads = num_kv_heads;
   a->num_blocks = num_blocks;
   a->block_size = block_size;
+  return PKV_OK;
+}
+
+// 4-bit pools: bytes between consecutive blocks; their checks shared by every
+// call.  num_layers as for FP8 pools.
+int64_t fp4_block_bytes(int num_layers, int block_size, int num_kv_heads, int head_dim) {
+  return static_cast<int64_t>(num_layers) * (block_size / 16) * num_kv_heads * (9 * head_dim);
+}
+pkv_status check_fp4(int num_layers, int block_size, const float* k_scale, const float* v_scale) {
+  if (num_layers <= 0 || num_layers > kMaxLayers) return PKV_ERR_INVALID_ARG;
+  if (block_shift_of(block_size) < 4) return PKV_ERR_UNSUPPORTED;
+  return aligned(k_scale, 4) && aligned(v_scale, 4) ? PKV_OK : PKV_ERR_INVALID_ARG;
+}
+
+// What the decode calls of this file share: sizes, pointers, alignment.
+pkv_status prepare_rows(DecodeArgs* a, void* out, const void* q, const void* k_pool, const void* v_pool,
+                        const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                        int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                        float scale, int max_context_len, pkv_dtype q_dtype, pkv_dtype out_dtype,
+                        int32_t* dev_status) {
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq < 0 || num_blocks <= 0 ||
+      max_context_len < 0 || !std::isfinite(scale))
+    return PKV_ERR_INVALID_ARG;
+  if (!value_dtype_ok(q_dtype) || (out_dtype != PKV_F32 && out_dtype != PKV_F16 && out_dtype != PKV_BF16))
+    return PKV_ERR_INVALID_ARG;
+  const int shift = block_shift_of(block_size);
+  if (shift < 4 || (head_dim != 64 && head_dim != 128) || num_q_heads % num_kv_heads != 0 ||
+      num_q_heads / num_kv_heads > 8 || static_cast<int64_t>(num_seqs) * num_kv_heads > kMaxUnits ||
+      (static_cast<int64_t>(max_blocks_per_seq) << shift) > 0x7fffffff)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PKV_OK;
+  if (!out || !q || !k_pool || !v_pool || !context_lens || (!block_tables && max_blocks_per_seq))
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(q, 16) || !aligned(out, out_dtype == PKV_F32 ? 4 : 2) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(dev_status, 4))
+    return PKV_ERR_INVALID_ARG;
+  a->out = out;
+  a->q = static_cast<const uint16_t*>(q);
+  a->block_tables = block_tables;
+  a->context_lens = context_lens;
+  a->dev_status = dev_status;
+  a->num_seqs = num_seqs;
+  a->num_q_heads = num_q_heads;
+  a->num_kv_heads = num_kv_heads;
+  a->group = num_q_heads / num_kv_heads;
+  a->max_blocks_per_seq = max_blocks_per_seq;
+  a->num_blocks = num_blocks;
+  a->max_context_len = max_context_len;
+  a->block_shift = shift;
+  a->scale_log2 = scale * 1.4426950408889634f;
+  a->out_dtype = static_cast<int>(out_dtype);
+  a->max_parts = 1;
+  a->heads_per_box = 1;
+  a->timeout_ns = kWaitTimeoutNs;
   return PKV_OK;
 }
 
@@ -177,7 +231,7 @@ pkv_status pkv_norm_rope_write(void* q_out, int64_t q_out_stride, void* k_out, i
   a.block_stride = resolve_block_stride(block_stride, block_size, num_kv_heads, head_dim);
   if (a.block_stride < 0) return PKV_ERR_INVALID_ARG;
   return cuda_status(
-      launch_norm_rope_write(a, head_dim, kv_dtype == PKV_BF16, false, static_cast<cudaStream_t>(stream)));
+      launch_norm_rope_write(a, head_dim, kv_dtype == PKV_BF16, 16, static_cast<cudaStream_t>(stream)));
 }
 
 pkv_status pkv_norm_rope_write_fp8(void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, const void* q,
@@ -202,7 +256,7 @@ pkv_status pkv_norm_rope_write_fp8(void* q_out, int64_t q_out_stride, void* k_ou
   a.block_stride = static_cast<int64_t>(num_layers) * kBlockSize * num_kv_heads * head_dim;
   a.scale_stride = static_cast<int64_t>(num_layers) * num_kv_heads;
   return cuda_status(
-      launch_norm_rope_write(a, head_dim, new_dtype == PKV_BF16, true, static_cast<cudaStream_t>(stream)));
+      launch_norm_rope_write(a, head_dim, new_dtype == PKV_BF16, 8, static_cast<cudaStream_t>(stream)));
 }
 
 pkv_status pkv_summarize_blocks(void* summary, float* summary_scale, const void* k_pool, int64_t block_stride,
@@ -333,6 +387,156 @@ pkv_status pkv_decode_sparse_fp8(void* out, const void* q, const void* k_pool, c
     return PKV_ERR_CUDA;
   return cuda_status(
       launch_decode_sparse(a, sp, tk, tv, head_dim, q_dtype == PKV_BF16, true, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_write_cache_fp4(const void* k_new, const void* v_new, void* k_pool, void* v_pool, const float* k_scale,
+                               const float* v_scale, const int32_t* slot_mapping, int num_tokens,
+                               int64_t new_row_stride, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                               int num_layers, pkv_dtype new_dtype, int32_t* dev_status, void* stream) {
+  pkv_status st = check_fp4(num_layers, block_size, k_scale, v_scale);
+  if (st != PKV_OK) return st;
+  NormRopeArgs a{};
+  st = prepare_norm_rope(&a, nullptr, 0, nullptr, 0, nullptr, 0, k_new, v_new, new_row_stride, nullptr, nullptr, 0.f,
+                         nullptr, nullptr, 0, 0, 0, k_pool, v_pool, slot_mapping, num_tokens, 0, num_kv_heads, head_dim,
+                         block_size, num_blocks, new_dtype, dev_status, true);
+  if (st != PKV_OK || num_tokens == 0) return st;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_stride = fp4_block_bytes(num_layers, block_size, num_kv_heads, head_dim);
+  return cuda_status(
+      launch_norm_rope_write(a, head_dim, new_dtype == PKV_BF16, 4, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_norm_rope_write_fp4(void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, const void* q,
+                                   int64_t q_stride, const void* k, const void* v, int64_t new_row_stride,
+                                   const void* q_weight, const void* k_weight, float eps, const float* cos_sin,
+                                   const int32_t* positions, int max_positions, int rot_dim, int interleaved,
+                                   void* k_pool, void* v_pool, const float* k_scale, const float* v_scale,
+                                   const int32_t* slot_mapping, int num_tokens, int num_q_heads, int num_kv_heads,
+                                   int head_dim, int block_size, int num_blocks, int num_layers, pkv_dtype new_dtype,
+                                   int32_t* dev_status, void* stream) {
+  pkv_status st = check_fp4(num_layers, block_size, k_scale, v_scale);
+  if (st != PKV_OK) return st;
+  NormRopeArgs a{};
+  st = prepare_norm_rope(&a, q_out, q_out_stride, k_out, k_out_stride, q, q_stride, k, v, new_row_stride, q_weight,
+                         k_weight, eps, cos_sin, positions, max_positions, rot_dim, interleaved, k_pool, v_pool,
+                         slot_mapping, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                         new_dtype, dev_status);
+  if (st != PKV_OK || num_tokens == 0) return st;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_stride = fp4_block_bytes(num_layers, block_size, num_kv_heads, head_dim);
+  return cuda_status(
+      launch_norm_rope_write(a, head_dim, new_dtype == PKV_BF16, 4, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_copy_blocks_fp4(void* k_pool, void* v_pool, const int32_t* pairs, int num_pairs, int num_layers,
+                               int num_kv_heads, int head_dim, int block_size, int num_blocks, int32_t* dev_status,
+                               void* stream) {
+  if (num_pairs < 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0) return PKV_ERR_INVALID_ARG;
+  const pkv_status st = check_fp4(num_layers, block_size, nullptr, nullptr);
+  if (st != PKV_OK) return st;
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  if (num_pairs == 0) return PKV_OK;
+  if (!k_pool || !v_pool || !pairs || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(pairs, 4) ||
+      !aligned(dev_status, 4))
+    return PKV_ERR_INVALID_ARG;
+  CopyBlocksArgs a{};
+  a.k_pool = static_cast<uint16_t*>(k_pool);
+  a.v_pool = static_cast<uint16_t*>(v_pool);
+  a.pairs = pairs;
+  a.dev_status = dev_status;
+  a.block_elems = fp4_block_bytes(num_layers, block_size, num_kv_heads, head_dim) / 2;  // counted in 16-bit units
+  a.num_pairs = num_pairs;
+  a.num_blocks = num_blocks;
+  return cuda_status(launch_copy_blocks(a, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_decode_attention_fp4(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                    const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                    int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                    int num_kv_heads, int head_dim, int block_size, int num_blocks, int num_layers,
+                                    float scale, int partition_size, int max_context_len, void* workspace,
+                                    size_t workspace_bytes, pkv_dtype q_dtype, pkv_dtype out_dtype,
+                                    int32_t* dev_status, void* stream) {
+  pkv_status st = check_fp4(num_layers, block_size, k_scale, v_scale);
+  if (st != PKV_OK) return st;
+  if (partition_size == PKV_PARTITION_BALANCED) return PKV_ERR_UNSUPPORTED;
+  if (partition_size < 0) return PKV_ERR_INVALID_ARG;
+  if (partition_size % kTile != 0) return PKV_ERR_UNSUPPORTED;
+  DecodeArgs a{};
+  st = prepare_rows(&a, out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                    num_kv_heads, head_dim, block_size, num_blocks, scale, max_context_len, q_dtype, out_dtype,
+                    dev_status);
+  if (st != PKV_OK || num_seqs == 0) return st;
+  const int64_t len = max_context_len > 0 ? max_context_len : 1;
+  const int64_t whole = (len + kTile - 1) / kTile * kTile, size = partition_size > 0 ? partition_size : whole;
+  const int64_t parts = (len + size - 1) / size;
+  if (parts * num_seqs * num_kv_heads > 0x7fffffff || size > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+  a.partition_size = static_cast<int>(size);
+  a.max_parts = static_cast<int>(parts);
+  if (parts > 1) {
+    const WorkspaceLayout ws = workspace_layout(num_seqs, num_q_heads, head_dim, a.max_parts);
+    if (!workspace || workspace_bytes < ws.total || !aligned(workspace, 16)) return PKV_ERR_WORKSPACE;
+    a.ws_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.acc_offset);
+    a.ws_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ws.ml_offset);
+  }
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_stride = fp4_block_bytes(num_layers, block_size, num_kv_heads, head_dim);
+  const WindowArgs w{0, 0, static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool)};
+  const CUtensorMap none{};
+  st = cuda_status(
+      launch_decode_window(a, w, none, none, head_dim, q_dtype == PKV_BF16, true, static_cast<cudaStream_t>(stream)));
+  if (st != PKV_OK || parts == 1) return st;
+  return cuda_status(launch_decode_reduce(a, head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_decode_window(void* out, const void* q, const void* k_pool, const void* v_pool, int64_t block_stride,
+                             const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                             int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                             int num_blocks, float scale, int window, int sinks, int max_context_len,
+                             pkv_dtype kv_dtype, pkv_dtype out_dtype, int32_t* dev_status, void* stream) {
+  if (window <= 0 || sinks < 0) return PKV_ERR_INVALID_ARG;
+  DecodeArgs a{};
+  const pkv_status st =
+      prepare_rows(&a, out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                   num_kv_heads, head_dim, block_size, num_blocks, scale, max_context_len, kv_dtype, out_dtype,
+                   dev_status);
+  if (st != PKV_OK) return st;
+  a.block_stride = resolve_block_stride(block_stride, block_size, num_kv_heads, head_dim);
+  if (a.block_stride < 0) return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PKV_OK;
+  CUtensorMap tk, tv;
+  if (!encode_pool_map(&tk, k_pool, num_blocks, block_size, num_kv_heads, head_dim, 2, a.block_stride) ||
+      !encode_pool_map(&tv, v_pool, num_blocks, block_size, num_kv_heads, head_dim, 2, a.block_stride))
+    return PKV_ERR_CUDA;
+  const WindowArgs w{window, sinks, nullptr, nullptr};
+  return cuda_status(
+      launch_decode_window(a, w, tk, tv, head_dim, kv_dtype == PKV_BF16, false, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_decode_window_fp4(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                 const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                 int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                 int num_kv_heads, int head_dim, int block_size, int num_blocks, int num_layers,
+                                 float scale, int window, int sinks, int max_context_len, pkv_dtype q_dtype,
+                                 pkv_dtype out_dtype, int32_t* dev_status, void* stream) {
+  if (window <= 0 || sinks < 0) return PKV_ERR_INVALID_ARG;
+  pkv_status st = check_fp4(num_layers, block_size, k_scale, v_scale);
+  if (st != PKV_OK) return st;
+  DecodeArgs a{};
+  st = prepare_rows(&a, out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                    num_kv_heads, head_dim, block_size, num_blocks, scale, max_context_len, q_dtype, out_dtype,
+                    dev_status);
+  if (st != PKV_OK || num_seqs == 0) return st;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_stride = fp4_block_bytes(num_layers, block_size, num_kv_heads, head_dim);
+  const WindowArgs w{window, sinks, static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool)};
+  const CUtensorMap none{};
+  return cuda_status(
+      launch_decode_window(a, w, none, none, head_dim, q_dtype == PKV_BF16, true, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

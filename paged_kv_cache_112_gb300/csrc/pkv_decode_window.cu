@@ -1,0 +1,395 @@
+// Single-token attention over a range of a sequence's tokens: a sliding
+// window and the first tokens (16-bit and 4-bit pools), or a partition of the
+// whole history (4-bit pools).
+//
+// For sequence s of L tokens and each query head h of KV head g's group,
+//     out[s][h] = sum_t softmax_t(scale * q[s][h] . k_t) v_t,
+//     windows:    t < sinks or t >= L - window     (t < L),
+//     partitions: t in [part * size, part * size + size).
+//
+// Bound: HBM bytes of the visible K and V (each read once, for all query heads
+// of the group); over 4-bit pools the issue slots come close behind: a tile's
+// 4 D values cost two instructions for every three of their bits.
+//
+// A cluster of C CTAs of NW warps serves one (s, g, partition).  The visible
+// 16-token tiles are dealt to its warps in turn; each streams its tiles
+// through a private ring of bulk copies (16 bits: TMA boxes; 4 bits: one
+// record for K and one for V) and keeps its own online-softmax state on the
+// tensor cores.  The states meet in shared memory, first a CTA's, then through
+// distributed shared memory the cluster's.  Windows need no workspace then;
+// partitions write the partial records that the reduce kernel merges.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "pkv_fp4.cuh"
+
+namespace pkv {
+namespace {
+
+using namespace dev;
+
+constexpr int kMaxCluster = 8;
+
+// The visible part of a sequence: tokens [0, sinks) and [low, L), as a list of
+// tiles [0, head) and [head + skip, ...), `count` in all.
+struct Visible {
+  int sinks, low, head, skip, count;
+
+  __device__ __forceinline__ Visible(int L, int window, int first) {
+    low = max(0, L - window);
+    sinks = min(first, low);
+    head = (sinks + kTile - 1) / kTile;
+    skip = max(0, low / kTile - head);
+    count = (L + kTile - 1) / kTile - skip;
+  }
+  __device__ __forceinline__ int tile(int j) const { return j < head ? j : j + skip; }
+  // Bit r: token 16 T + r is visible.
+  __device__ __forceinline__ uint32_t mask(int T, int L) const {
+    auto below = [&](int x) { return (1u << max(0, min(kTile, x - T * kTile))) - 1u; };
+    return below(L) & (below(sinks) | ~below(low));
+  }
+};
+
+// POOL: 16 or 4 bits.  Warps a CTA NW, stages a warp NST.
+template <int D, bool BF16, int POOL, int NW, int NST>
+struct Ring {
+  static constexpr int kTileBytes = POOL == 4 ? fp4::Record<D>::kBytes : kTile * D * 2;
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kState = 8 * (D + 4) + 16;  // a warp's saved state: 8 rows, running max and sum of each head
+  static constexpr int kWarpBytes = NST * kStageBytes > kState * 4 ? NST * kStageBytes : kState * 4;
+  static constexpr size_t kInboxAt = static_cast<size_t>(NW) * (kWarpBytes + 8 * NST);
+  static constexpr size_t smem(int C) {
+    return kInboxAt + (C > 1 ? (8 * D + 16 * kMaxCluster) * sizeof(float) : 0);
+  }
+  static_assert(POOL == 4 || kWarpBytes % 1024 == 0, "TMA tiles sit on 1024-byte boundaries");
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+template <int D, bool BF16, int POOL, int NW, int NST>
+__global__ void __launch_bounds__(NW * 32) decode_window_kernel(const DecodeArgs a, const WindowArgs wa,
+                                                                const __grid_constant__ CUtensorMap tmap_k,
+                                                                const __grid_constant__ CUtensorMap tmap_v) {
+  using R = Ring<D, BF16, POOL, NW, NST>;
+  using Att = std::conditional_t<POOL == 4, WarpAttentionFp4<D>, WarpAttention<D, BF16, true>>;
+  constexpr int kRow = D + 4;              // floats between a saved state's head rows
+  constexpr int NT = POOL == 4 ? 2 : 1;    // tiles a step
+  static_assert(NST * 16 <= 64 && NST % NT == 0, "stage masks; whole steps");
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  if (C > 1) cluster_arrive();  // see the wait before the merge
+  griddep_wait();
+  griddep_launch_dependents();
+  if (POOL != 4 && smem_misaligned(smem, a.dev_status)) return;  // the same for every CTA
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Units in ascending partition index: those past a sequence's end come last.
+  const int64_t unit = blockIdx.x / C;
+  const int g = static_cast<int>(unit % a.num_kv_heads);
+  const int64_t rest = unit / a.num_kv_heads;
+  const int s = static_cast<int>(rest % a.num_seqs), part = static_cast<int>(rest / a.num_seqs);
+  const int G = a.group;
+  const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
+  const int tshift = a.block_shift - 4;         // log2 of tiles per block
+  const int W = C * NW, w0 = rank * NW + warp;  // this warp's tiles of the list: w0, w0 + W, ...
+
+  const int L = clamp_len(a, a.context_lens[s], part == 0 && g == 0 && rank == 0 && threadIdx.x == 0);
+  const int nparts = wa.window > 0 ? 1 : max(1, (L + a.partition_size - 1) / a.partition_size);
+  if (part >= nparts) return;  // never with windows or clusters: max_parts is 1 there
+  const Visible vis(L, wa.window > 0 ? wa.window : L, wa.sinks);
+  const int tile0 = wa.window > 0 ? 0 : part * (a.partition_size / kTile);
+  const int tiles = wa.window > 0 ? vis.count : min(vis.count - tile0, a.partition_size / kTile);
+  const int cnt = tiles > w0 ? (tiles - w0 + W - 1) / W : 0;
+  auto tile_of = [&](int i) { return vis.tile(tile0 + i * W + w0); };
+  // The table entry of the warp's tile i.
+  auto fetch = [&](int i) {
+    if (i >= cnt) return -1;
+    const int b = tile_of(i) >> tshift;  // below max_blocks_per_seq: L is clamped to the table
+    return __ldg(tbl + b);
+  };
+
+  uint8_t* mine = smem + static_cast<size_t>(warp) * R::kWarpBytes;
+  const uint32_t buf = smem_u32(mine), bars = smem_u32(smem + static_cast<size_t>(NW) * R::kWarpBytes) + 8 * NST * warp;
+  if (lane == 0) {
+    for (int st = 0; st < NST; ++st) mbar_init(bars + 8 * st, 1);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncwarp();
+  // Lane j holds the table entry of the warp's tile j of a chunk of 32.
+  int cur = fetch(lane), ahead = fetch(32 + lane);
+  uint64_t stage_mask = 0;  // 16 bits a stage: rows of its tile that count
+  auto issue = [&](int j) {
+    if ((j & 31) == 0 && j > 0) {
+      cur = ahead;
+      ahead = fetch(j + 32 + lane);
+    }
+    const int st = j % NST, T = tile_of(j);
+    int phys = __shfl_sync(kFull, cur, j & 31);
+    uint32_t m = vis.mask(T, L);
+    if (static_cast<unsigned>(phys) >= static_cast<unsigned>(a.num_blocks)) {
+      if (lane == 0) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK; the tile is masked
+      phys = 0;
+      m = 0;
+    }
+    stage_mask = (stage_mask & ~(0xffffull << (16 * st))) | (static_cast<uint64_t>(m) << (16 * st));
+    if (lane != 0) return;
+    const uint32_t bar = bars + 8 * st, dst = buf + st * R::kStageBytes;
+    const int in_block = T & ((1 << tshift) - 1);
+    mbar_arrive_expect_tx(bar, R::kStageBytes);
+    if constexpr (POOL == 4) {
+      const int64_t at = phys * a.block_stride + ((static_cast<int64_t>(g) << tshift) + in_block) * R::kTileBytes;
+      bulk_load(dst, wa.k4 + at, R::kTileBytes, bar);
+      bulk_load(dst + R::kTileBytes, wa.v4 + at, R::kTileBytes, bar);
+    } else {
+      tma_tile<D>(dst, &tmap_k, in_block * kTile, g, phys, bar);
+      tma_tile<D>(dst + R::kTileBytes, &tmap_v, in_block * kTile, g, phys, bar);
+    }
+  };
+  auto wait = [&](int i) { return mbar_wait_bounded(bars + 8 * (i % NST), (i / NST) & 1, a.timeout_ns); };
+  auto mask_of = [&](int j) { return static_cast<uint32_t>(stage_mask >> (16 * (j % NST))) & 0xffffu; };
+
+  Att at;
+  at.reset();
+  for (int j = 0; j < min(cnt, NST); ++j) issue(j);
+  const uint16_t* q0 = a.q + (static_cast<int64_t>(s) * a.num_q_heads + g * G) * D;
+  float sl2 = a.scale_log2, post = 1.f / Att::kWeightUp;
+  if constexpr (POOL == 4) {
+    at.template load_q<BF16>(q0, G, lane);
+    if (a.k_scale) sl2 *= __ldg(a.k_scale + g);
+    if (a.v_scale) post *= __ldg(a.v_scale + g);
+  } else {
+    at.load_q(q0, G, lane);
+  }
+  for (int i = 0; i < cnt; i += NT) {
+    const int n = min(NT, cnt - i);
+    bool ok = true;
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+      if (u < n) ok = ok && wait(i + u);
+    if (!__all_sync(kFull, ok)) {
+      for (int j = i; j < min(cnt, i + NST); ++j) wait(j);  // copies in flight land before the warp goes on
+      if (lane == 0) flag(a.dev_status, 16u);               // PKV_DEV_ERR_TIMEOUT; the output is undefined
+      break;
+    }
+    if constexpr (POOL == 4) {
+      uint32_t sK[NT], m[NT];
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {  // a missing second tile reuses the first one's stage, no token counts
+        const int j = u < n ? i + u : i;
+        sK[u] = buf + (j % NST) * R::kStageBytes;
+        m[u] = u < n ? mask_of(j) : 0u;
+      }
+      at.template tiles<NT>(sK, m, sl2, lane);
+    } else {
+      const uint32_t sK = buf + (i % NST) * R::kStageBytes, m = mask_of(i);
+      if (m) at.template tile<true>(sK, sK + R::kTileBytes, static_cast<int>(m), sl2, lane);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+      if (i + NST + u < cnt) issue(i + NST + u);
+  }
+  at.finish_sums();
+
+  // Save this warp's state: rows [8][kRow], running max [8], running sum [8].
+  {
+    float* st = reinterpret_cast<float*>(mine);
+    const int gr = lane >> 2, tq = lane & 3;
+    float* ra = st + (2 * tq) * kRow;
+    float* rb = ra + kRow;
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt) {
+      const int d0 = POOL == 4 ? D / 8 * gr + 2 * mt : 16 * mt + gr, d1 = POOL == 4 ? d0 + 1 : d0 + 8;
+      ra[d0] = at.acc[mt][0];
+      rb[d0] = at.acc[mt][1];
+      ra[d1] = at.acc[mt][2];
+      rb[d1] = at.acc[mt][3];
+    }
+    if (gr == 0) {
+      st[8 * kRow + 2 * tq] = at.m_a;
+      st[8 * kRow + 2 * tq + 1] = at.m_b;
+      st[8 * kRow + 8 + 2 * tq] = at.l_a;
+      st[8 * kRow + 8 + 2 * tq + 1] = at.l_b;
+    }
+  }
+  __syncthreads();
+  // Merge over the warps, four channels a thread:
+  //     M = max m_w, acc = sum 2^(m_w - M) acc_w, l = sum 2^(m_w - M) l_w.
+  auto merged = [&](int h, int d, float& M, float4& o, float& l) {
+    const float* st[NW];
+    float m[NW];
+    M = kNegInf;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      st[w] = reinterpret_cast<const float*>(smem + static_cast<size_t>(w) * R::kWarpBytes);
+      m[w] = st[w][8 * kRow + h];
+      M = fmaxf(M, m[w]);
+    }
+    const float mu = M == kNegInf ? 0.f : M;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float c = exp2f(m[w] - mu);
+      const float4 v = *reinterpret_cast<const float4*>(st[w] + h * kRow + d);
+      o.x += v.x * c;
+      o.y += v.y * c;
+      o.z += v.z * c;
+      o.w += v.w * c;
+      l += st[w][8 * kRow + 8 + h] * c;
+    }
+  };
+  const int64_t head0 = static_cast<int64_t>(s) * a.num_q_heads + g * G;
+  auto store4 = [&](int e, float4 o, float l) {
+    const float inv = l > 0.f ? post / l : 0.f;
+    store_out(a.out, head0 * D + e, o.x * inv, a.out_dtype);
+    store_out(a.out, head0 * D + e + 1, o.y * inv, a.out_dtype);
+    store_out(a.out, head0 * D + e + 2, o.z * inv, a.out_dtype);
+    store_out(a.out, head0 * D + e + 3, o.w * inv, a.out_dtype);
+  };
+  if (C == 1) {
+    for (int e = 4 * threadIdx.x; e < G * D; e += 4 * NW * 32) {
+      const int h = e / D, d = e % D;
+      float M, l;
+      float4 o;
+      merged(h, d, M, o, l);
+      if (nparts == 1) {
+        store4(e, o, l);
+      } else {
+        const int64_t rec = (head0 + h) * a.max_parts + part;
+        *reinterpret_cast<float4*>(a.ws_acc + rec * D + d) = make_float4(o.x * post, o.y * post, o.z * post, o.w * post);
+        if (d == 0) a.ws_ml[rec] = make_float2(M, l);
+      }
+    }
+    return;
+  }
+  // CTA r merges elements [r * per, r * per + per) of the group's rows over
+  // the cluster: every CTA stores its part of them, and its heads' max and
+  // sum, into r's shared memory.
+  const int per = G * D / C;  // a multiple of 4: D is at least 64, C at most 8
+  float* inbox = reinterpret_cast<float*>(smem + R::kInboxAt);  // [C][per], then [C][8] max, [C][8] sum
+  float* inbox_m = inbox + 8 * D;
+  float* inbox_l = inbox_m + 8 * kMaxCluster;
+  cluster_wait();  // every CTA has begun
+  for (int e = 4 * threadIdx.x; e < G * D; e += 4 * NW * 32) {
+    const int h = e / D, d = e % D, to = e / per;
+    float M, l;
+    float4 o;
+    merged(h, d, M, o, l);
+    cluster_store_float4(cluster_map(smem_u32(inbox + rank * per + (e - to * per)), to), o);
+    if (d / 4 < C) {  // head h's max and sum, to CTA d / 4
+      cluster_store_float(cluster_map(smem_u32(inbox_m + rank * 8 + h), d / 4), M);
+      cluster_store_float(cluster_map(smem_u32(inbox_l + rank * 8 + h), d / 4), l);
+    }
+  }
+  cluster_sync();
+  for (int k = 4 * threadIdx.x; k < per; k += 4 * NW * 32) {
+    const int e = rank * per + k, h = e / D;
+    float M = kNegInf, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < C) M = fmaxf(M, inbox_m[r * 8 + h]);
+    const float mu = M == kNegInf ? 0.f : M;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < C) {
+        const float c = exp2f(inbox_m[r * 8 + h] - mu);
+        const float4 v = *reinterpret_cast<const float4*>(inbox + r * per + k);
+        o.x += v.x * c;
+        o.y += v.y * c;
+        o.z += v.z * c;
+        o.w += v.w * c;
+        l += inbox_l[r * 8 + h] * c;
+      }
+    store4(e, o, l);
+  }
+}
+
+// The kernel with NW warps a CTA, and what launching it in clusters of C takes.
+template <int D, bool BF16, int POOL, int NW>
+struct Launch {
+  static constexpr int NST = POOL == 4 ? 4 : D == 64 ? 3 : 2;
+  using R = Ring<D, BF16, POOL, NW, NST>;
+  static constexpr auto kernel = decode_window_kernel<D, BF16, POOL, NW, NST>;
+
+  // Clusters of C that the current device holds at a time (a cluster stays
+  // within one of the GPU's groups of SMs, so fewer than SMs / C).
+  static int resident(int C) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> cache[kDevices][4];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) {
+      cudaGetLastError();
+      return 1;
+    }
+    std::atomic<int>& slot = cache[dev][C == 1 ? 0 : C == 2 ? 1 : C == 4 ? 2 : 3];
+    int n = slot.load(std::memory_order_acquire);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(NW * 32);
+    cfg.dynamicSmemBytes = R::smem(C);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), R::smem(kMaxCluster)) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      return 1;
+    }
+    slot.store(n, std::memory_order_release);
+    return n;
+  }
+
+  static cudaError_t launch(const DecodeArgs& a, const WindowArgs& w, int C, const CUtensorMap& tk,
+                            const CUtensorMap& tv, cudaStream_t stream) {
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), R::smem(kMaxCluster));
+    if (e != cudaSuccess) return e;
+    const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * a.max_parts;
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(units * C)), dim3(NW * 32), R::smem(C), C, stream, a,
+                              w, tk, tv);
+  }
+};
+
+template <int D, bool BF16, int POOL>
+cudaError_t launch_t(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tk, const CUtensorMap& tv,
+                     cudaStream_t stream) {
+  using Four = Launch<D, BF16, POOL, 4>;
+  using Eight = Launch<D, BF16, POOL, 8>;
+  if (a.max_parts > 1 || w.window == 0) return Four::launch(a, w, 1, tk, tv, stream);
+  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads, sms = current_sm_count(152);
+  int C = 1;
+  while (C < kMaxCluster && units * C * 2 <= sms) C *= 2;
+  while (C > 1 && units > Eight::resident(C)) C /= 2;
+  return Eight::launch(a, w, C, tk, tv, stream);
+}
+
+template <int POOL>
+cudaError_t launch_p(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tk, const CUtensorMap& tv,
+                     int head_dim, bool bf16, cudaStream_t stream) {
+  if (head_dim == 128)
+    return bf16 ? launch_t<128, true, POOL>(a, w, tk, tv, stream) : launch_t<128, false, POOL>(a, w, tk, tv, stream);
+  if (head_dim == 64)
+    return bf16 ? launch_t<64, true, POOL>(a, w, tk, tv, stream) : launch_t<64, false, POOL>(a, w, tk, tv, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_decode_window(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tmap_k,
+                                 const CUtensorMap& tmap_v, int head_dim, bool bf16, bool fp4, cudaStream_t stream) {
+  if (a.num_seqs == 0) return cudaSuccess;
+  return fp4 ? launch_p<4>(a, w, tmap_k, tmap_v, head_dim, bf16, stream)
+             : launch_p<16>(a, w, tmap_k, tmap_v, head_dim, bf16, stream);
+}
+
+}  // namespace pkv

@@ -611,7 +611,9 @@ struct WarpAttention : SoftmaxState<D / 16> {
     }
   }
 
-  // One tile: nv valid tokens (rows >= nv are masked, whatever they hold).
+  // One tile: nv valid tokens (rows >= nv are masked, whatever they hold); with
+  // ROWS, bit r of nv set where row r is valid.
+  template <bool ROWS = false>
   __device__ __forceinline__ void tile(uint32_t sK, uint32_t sV, int nv, float sl2, int lane) {
     const int gr = lane >> 2, tq = lane & 3;
     const int rowK = (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -633,8 +635,9 @@ struct WarpAttention : SoftmaxState<D / 16> {
     }
     float s0 = (c[0] + c2[0]) * sl2, s1 = (c[1] + c2[1]) * sl2;
     float s2 = (c[2] + c2[2]) * sl2, s3 = (c[3] + c2[3]) * sl2;
-    if (gr >= nv) s0 = s1 = kNegInf;
-    if (gr + 8 >= nv) s2 = s3 = kNegInf;
+    auto valid = [&](int r) { return ROWS ? ((nv >> r) & 1) != 0 : r < nv; };
+    if (!valid(gr)) s0 = s1 = kNegInf;
+    if (!valid(gr + 8)) s2 = s3 = kNegInf;
     float sc[4] = {s0, s1, s2, s3}, pw[4];
     this->template online_update_lazy<1>(sc, pw);
     const float p0 = pw[0] * kWeightUp, p1 = pw[1] * kWeightUp, p2 = pw[2] * kWeightUp, p3 = pw[3] * kWeightUp;
@@ -659,12 +662,12 @@ struct WarpAttention : SoftmaxState<D / 16> {
       }
     }
 
-    // V rows past the valid tokens may hold anything (even NaN): zero them in
+    // V rows of tokens that are not valid may hold anything (even NaN): zero them in
     // the A fragment (lane holds tokens 2tq, 2tq+1 and 8+2tq, 9+2tq).
     uint32_t m01 = kFull, m23 = kFull;
-    if (nv < kTile) {
-      m01 = (2 * tq < nv ? 0x0000ffffu : 0u) | (2 * tq + 1 < nv ? 0xffff0000u : 0u);
-      m23 = (2 * tq + 8 < nv ? 0x0000ffffu : 0u) | (2 * tq + 9 < nv ? 0xffff0000u : 0u);
+    if (ROWS ? nv != 0xffff : nv < kTile) {
+      m01 = (valid(2 * tq) ? 0x0000ffffu : 0u) | (valid(2 * tq + 1) ? 0xffff0000u : 0u);
+      m23 = (valid(2 * tq + 8) ? 0x0000ffffu : 0u) | (valid(2 * tq + 9) ? 0xffff0000u : 0u);
     }
 #pragma unroll
     for (int mt = 0; mt < KT; ++mt) {

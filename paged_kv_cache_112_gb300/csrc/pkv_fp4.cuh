@@ -1,0 +1,268 @@
+// 4-bit pools: e2m1 codes (sign, two exponent bits, one mantissa bit: 0, 1/2,
+// 1, 3/2, 2, 3, 4, 6) with an e4m3 scale for every 16 channels of a token.
+//
+// Layout.  A block holds, per KV head and per 16 tokens, one record
+//     [16 tokens][D / 2] bytes of codes (the even channel in the low half),
+//     [16 tokens][D / 16] bytes of scales,
+// 9 D bytes.  A tile (16 tokens of a head) is then one contiguous, 64-byte
+// aligned copy, codes and scales together; the records of a block's heads
+// follow one another, so the CTAs of neighbouring heads read one range.
+#pragma once
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+namespace fp4 {
+
+template <int D>
+struct Record {
+  static constexpr int kRowBytes = D / 2;    // codes of a token
+  static constexpr int kRowScales = D / 16;  // scales of a token
+  static constexpr int kScalesAt = 16 * kRowBytes;
+  static constexpr int kBytes = 9 * D;
+};
+
+// Two values to codes: lo in the low half of the byte.  Nearest, ties to the
+// even code, magnitudes beyond 6 saturate.
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t, z;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
+      "mov.b32 %0, {t, t, t, t};\n\t}"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return r & 0xffu;
+}
+
+// Four bytes of codes to four pairs of f16 (the low half's value in the lower half).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+}  // namespace fp4
+
+namespace dev {
+
+// Attention state of one warp serving the G <= 8 query heads of one KV head
+// over 4-bit tiles (see SoftmaxState; mma.sync m16n8k16 as WarpAttention).
+//
+// A value is code * scale: two significant bits times four, at most 2688 and
+// a multiple of 2^-10, so the f16 product that enters the MMA is exact.  The
+// softmax weights enter as one f16 part (2^-12 of the weight at most; times
+// 2^14, so that small ones keep it): the values are themselves rounded by
+// up to 2^-3.
+//
+// Order of the fragments: within an MMA, channels, tokens and output dims may
+// be permuted as long as both operands agree.  Lane (gr, tq) takes channels
+// [D/4 tq, + D/4) of K: 16 bytes a token for D = 128, and the two quantisation
+// groups they hold.  MMA row r of a half tile is token r/2 + 4 (r & 1), so a
+// lane's V tokens are tq, tq + 4 (+ 8): the four lanes of a quad read adjacent
+// rows.  Of V it takes dims [D/8 gr, + D/8): one group's scale a token.  A
+// dim's codes of two tokens are brought into one byte by a select, which one
+// conversion turns into the f16 pair the MMA wants.
+template <int D>
+struct WarpAttentionFp4 : SoftmaxState<D / 16> {
+  static constexpr int KT = D / 16;
+  static constexpr float kWeightUp = 16384.f;
+  using Rec = fp4::Record<D>;
+  using Base = SoftmaxState<KT>;
+  using Base::acc;
+  uint32_t qf[KT][2];  // f16x2: q[head gr][D/4 tq + 4kk + {0,1}] and {2,3}
+  float up_a, up_b;    // the powers of two by which heads 2tq and 2tq + 1 were scaled down
+
+  // The group's query rows (heads >= G read as 0).  bf16 queries become f16
+  // with a power of two per head, from its largest finite |q|.
+  template <bool QBF16>
+  __device__ __forceinline__ void load_q(const uint16_t* qhead0, int G, int lane) {
+    const int gr = lane >> 2, tq = lane & 3;
+    const bool live = gr < G;
+    const uint4* src = reinterpret_cast<const uint4*>(qhead0 + (live ? gr : 0) * D + D / 4 * tq);
+    uint32_t w[2 * KT];
+#pragma unroll
+    for (int i = 0; i < KT / 2; ++i) {
+      const uint4 v = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+    float down = 1.f;
+    if constexpr (QBF16) {
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2 * KT; ++i) {
+        const float2 f = unpack_bf16(w[i]);
+        const float x = fabsf(f.x), y = fabsf(f.y);
+        amax = fmaxf(amax, fmaxf(x < INFINITY ? x : 0.f, y < INFINITY ? y : 0.f));
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+      const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127;
+      const int e = min(max(ex - 14, -100), 120);  // |q| 2^-e is below 2^15
+      const float mul = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      down = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < 2 * KT; ++i) {
+        const float2 f = unpack_bf16(w[i]);
+        w[i] = pack_f16(f.x * mul, f.y * mul);
+      }
+    }
+#pragma unroll
+    for (int kk = 0; kk < KT; ++kk) {
+      qf[kk][0] = w[2 * kk];
+      qf[kk][1] = w[2 * kk + 1];
+    }
+    up_a = __shfl_sync(kFull, down, 8 * tq);
+    up_b = __shfl_sync(kFull, down, 8 * tq + 4);
+  }
+
+  __device__ __forceinline__ static uint32_t lds32(uint32_t addr) {
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr));
+    return r;
+  }
+  __device__ __forceinline__ static uint32_t lds8(uint32_t addr) {
+    uint32_t r;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr));
+    return r;
+  }
+  template <int N>
+  __device__ __forceinline__ static void lds(uint32_t (&r)[N], uint32_t addr) {
+    if constexpr (N == 4)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                   : "r"(addr));
+    else if constexpr (N == 2)
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+    else
+      r[0] = lds32(addr);
+  }
+
+  // NT tiles at once: K records at sK[t], V records Rec::kBytes further, bit r
+  // of mask[t] set where token r counts (the others are masked whatever they
+  // hold), sl2 = log2(e) * softmax scale * the head's K scale.
+  template <int NT>
+  __device__ __forceinline__ void tiles(const uint32_t (&sK)[NT], const uint32_t (&mask)[NT], float sl2, int lane) {
+    const int gr = lane >> 2, tq = lane & 3;
+    const int tok = (gr >> 1) + 4 * (gr & 1);
+    constexpr int KW = D / 32, VW = D / 64;  // words of a lane's codes a K row and a V row
+    uint32_t kw[NT][2][KW], ks[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        lds<KW>(kw[t][r], sK[t] + (tok + 8 * r) * Rec::kRowBytes + tq * (D / 8));
+        const uint32_t at = sK[t] + Rec::kScalesAt + (tok + 8 * r) * Rec::kRowScales;
+        if constexpr (D == 128) {
+          asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
+                       : "=r"(ks[t][r])
+                       : "r"(at + 2 * tq));
+        } else {
+          ks[t][r] = lds8(at + tq);
+        }
+      }
+    float c[NT][2][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[t][0][j] = c[t][1][j] = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t s[2][D / 64];  // scales of rows tok, tok + 8: of the lane's groups, twice
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t f = fp4::e4m3x2_to_f16(ks[t][r]);
+        s[r][0] = __byte_perm(f, f, 0x1010);
+        if constexpr (D == 128) s[r][1] = __byte_perm(f, f, 0x3232);
+      }
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        uint32_t x[4], y[4];
+        fp4::e2m1x8_to_f16(kw[t][0][w], x);
+        fp4::e2m1x8_to_f16(kw[t][1][w], y);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // k-step 2w + h
+          const uint32_t s0 = s[0][w / 2], s1 = s[1][w / 2];
+          const uint32_t a[4] = {fp4::mul_f16x2(x[2 * h], s0), fp4::mul_f16x2(y[2 * h], s1),
+                                 fp4::mul_f16x2(x[2 * h + 1], s0), fp4::mul_f16x2(y[2 * h + 1], s1)};
+          mma_16816<false>(c[t][h], a, qf[2 * w + h][0], qf[2 * w + h][1]);
+        }
+      }
+    }
+    // V: tokens tq, tq + 4, tq + 8, tq + 12, dims [D/8 gr, + D/8).
+    uint32_t vw[NT][4][VW], vs[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const uint32_t sV = sK[t] + Rec::kBytes;
+      uint32_t b[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        lds<VW>(vw[t][r], sV + (tq + 4 * r) * Rec::kRowBytes + gr * (D / 16));
+        b[r] = lds8(sV + Rec::kScalesAt + (tq + 4 * r) * Rec::kRowScales + (D == 128 ? gr : gr >> 1));
+        // A token that does not count may hold anything: its scale is 0.
+        if (!((mask[t] >> (tq + 4 * r)) & 1u)) b[r] = 0u;
+      }
+      vs[t][0] = fp4::e4m3x2_to_f16(b[0] | (b[1] << 8));
+      vs[t][1] = fp4::e4m3x2_to_f16(b[2] | (b[3] << 8));
+    }
+    float sc[4 * NT], p[4 * NT];
+    const float fa = sl2 * up_a, fb = sl2 * up_b;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const bool lo = (mask[t] >> tok) & 1u, hi = (mask[t] >> (tok + 8)) & 1u;
+      sc[4 * t] = lo ? (c[t][0][0] + c[t][1][0]) * fa : kNegInf;
+      sc[4 * t + 1] = lo ? (c[t][0][1] + c[t][1][1]) * fb : kNegInf;
+      sc[4 * t + 2] = hi ? (c[t][0][2] + c[t][1][2]) * fa : kNegInf;
+      sc[4 * t + 3] = hi ? (c[t][0][3] + c[t][1][3]) * fb : kNegInf;
+    }
+    this->template online_update_lazy<NT>(sc, p);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const uint32_t p0 = movmatrix_trans(pack_f16(p[4 * t] * kWeightUp, p[4 * t + 1] * kWeightUp));
+      const uint32_t p1 = movmatrix_trans(pack_f16(p[4 * t + 2] * kWeightUp, p[4 * t + 3] * kWeightUp));
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        constexpr uint32_t kLow = 0x0f0f0f0fu;
+        uint32_t x[4][4];  // even dims, odd dims of tokens tq and tq + 4; of tq + 8 and tq + 12
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t A = vw[t][2 * h][w], B = vw[t][2 * h + 1][w];
+          fp4::e2m1x8_to_f16((A & kLow) | ((B << 4) & ~kLow), x[2 * h]);
+          fp4::e2m1x8_to_f16(((A >> 4) & kLow) | (B & ~kLow), x[2 * h + 1]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // M-tile 4w + j: rows gr, gr + 8 are dims D/8 gr + 2 (4w + j), + 1
+          const uint32_t a[4] = {fp4::mul_f16x2(x[0][j], vs[t][0]), fp4::mul_f16x2(x[1][j], vs[t][0]),
+                                 fp4::mul_f16x2(x[2][j], vs[t][1]), fp4::mul_f16x2(x[3][j], vs[t][1])};
+          mma_16816<false>(acc[4 * w + j], a, p0, p1);
+        }
+      }
+    }
+  }
+};
+
+}  // namespace dev
+}  // namespace pkv

@@ -127,7 +127,7 @@ struct DecodeArgs {
 
 // Norms of queries and keys per head, position rotation and the scatter of K
 // and V (pkv_norm_rope.cu).  Row strides in elements; pool strides in pool
-// elements (FP8: bytes).
+// elements (FP8, 4-bit: bytes).  num_q_heads 0 and q null: K and V alone.
 struct NormRopeArgs {
   const uint16_t* q;
   const uint16_t* k;
@@ -141,7 +141,7 @@ struct NormRopeArgs {
   const int32_t* slot_mapping;
   void* k_pool;
   void* v_pool;
-  const float* k_scale;  // FP8 pools only
+  const float* k_scale;  // FP8 pools: [block][head]; 4-bit pools: [head], or null
   const float* v_scale;
   int32_t* dev_status;
   int64_t q_stride, kv_stride, q_out_stride, k_out_stride;
@@ -187,6 +187,15 @@ struct SparseArgs {
   const int32_t* selected;
   const int32_t* counts;
   int keep;
+};
+
+// What a decode call sees of each sequence, and 4-bit pools, beside its
+// DecodeArgs (pkv_decode_window.cu).  4-bit pools: block_stride in bytes,
+// k_scale and v_scale float [num_kv_heads] or null.
+struct WindowArgs {
+  int window, sinks;  // window 0: all tokens, in partitions
+  const uint8_t* k4;
+  const uint8_t* v4;
 };
 
 // Split-K workspace layout (regions 256-byte aligned).  Fixed partitions:
@@ -304,8 +313,9 @@ cudaError_t launch_decode_balanced(const DecodeArgs& a, const CUtensorMap& tmap_
 cudaError_t launch_decode_reduce_balanced(const DecodeArgs& a, int head_dim, cudaStream_t stream);
 
 
-// head_dim 64 or 128; bf16: 0 = f16 values, 1 = bf16; fp8: e4m3 pools.
-cudaError_t launch_norm_rope_write(const NormRopeArgs& a, int head_dim, bool bf16, bool fp8, cudaStream_t stream);
+// head_dim 64 or 128; bf16: 0 = f16 values, 1 = bf16; pool_bits 16, 8 (e4m3) or 4 (e2m1, pkv_fp4.cuh).
+cudaError_t launch_norm_rope_write(const NormRopeArgs& a, int head_dim, bool bf16, int pool_bits,
+                                   cudaStream_t stream);
 cudaError_t launch_summarize_blocks(const SummarizeArgs& a, int head_dim, bool bf16, bool fp8, cudaStream_t stream);
 // Largest number of blocks a sequence may have for launch_select_blocks.
 constexpr int kSelectMaxBlocks = 49152;
@@ -316,6 +326,11 @@ cudaError_t launch_select_blocks(const SelectArgs& a, int head_dim, bool bf16, c
 // `a` as for launch_decode_partitions(_fp8) with one head a box; blocks of 16 tokens or more.
 cudaError_t launch_decode_sparse(const DecodeArgs& a, const SparseArgs& sp, const CUtensorMap& tmap_k,
                                  const CUtensorMap& tmap_v, int head_dim, bool bf16, bool fp8, cudaStream_t stream);
+
+// The visible tiles of each sequence, over 16-bit pools (tensor maps as for
+// launch_decode_sparse) or 4-bit pools (maps unused).
+cudaError_t launch_decode_window(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tmap_k,
+                                 const CUtensorMap& tmap_v, int head_dim, bool bf16, bool fp4, cudaStream_t stream);
 
 // Argument helpers shared by the entry points (pkv_api.cu).
 constexpr long long kWaitTimeoutNs = 2000000000LL;  // 2 s per bounded wait

@@ -6,7 +6,10 @@
 //            (a, b) -> (a cos - b sin, b cos + a sin)      (the first rot_dim channels)
 //     q -> q_out;  k -> its slot of the K pool (and k_out);  v -> its slot of the V pool.
 // One rounding to 16 bits at the end; into FP8 pools the float32 value is
-// divided by the block's scale and rounded once to e4m3.
+// divided by the block's scale and rounded once to e4m3; into 4-bit pools each
+// 16 channels get the e4m3 scale that brings the largest of them to 6, and
+// their quotients are rounded once to e2m1.  Writes alone (no queries, no
+// norm, no rotation) run here too for 4-bit pools.
 //
 // Bound: HBM bytes (each row read and written once, ~3 flops a byte): 16384
 // tokens of 32 + 16 heads in 64.7 us, 6.35 TB/s.  Head counts whose groups do
@@ -27,6 +30,7 @@
 #include <cuda_fp16.h>
 
 #include "pkv_device.cuh"
+#include "pkv_fp4.cuh"
 #include "pkv_fp8.cuh"
 
 namespace pkv {
@@ -119,10 +123,49 @@ __device__ __forceinline__ uint2 codes8(const F2 (&x)[4], float scale) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// 4-bit rows.  The largest magnitude of a chunk; NaN where it holds one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float top8(const F2 (&x)[4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = halves(x[i]);
+    m = max_nan(m, max_nan(fabsf(f.x), fabsf(f.y)));
+  }
+  return m;
+}
+
+// Eight e2m1 codes (element i in bits 4i ..) of x / s, s the value of an e4m3
+// scale, the quotient as IEEE float32 division gives it: with y = RN(1 / s)
+// and q = RN(x y), RN(q + (x - q s) y) is the rounded quotient (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990; x - q s is exact).  16-bit values often lie on a border
+// exactly, so an approximate quotient would not do.  Where a quotient is not
+// finite it saturates as it is; a scale of 0 (or NaN, when the values mean
+// nothing) gives zeros.
+__device__ __forceinline__ uint32_t codes8_e2m1(const F2 (&x)[4], float s, float top) {
+  const bool usable = s > 0.f;
+  const float inv = usable ? __frcp_rn(s) : 0.f, div = usable ? s : 0.f;
+  const F2 y = pair(inv, inv), d = pair(-div, -div);
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    F2 q = mul2(x[i], y);
+    if (top < 3e38f) q = fma2(fma2(q, d, x[i]), y, q);
+    const float2 f = halves(q);
+    r |= fp4::e2m1x2(f.x, f.y) << (8 * i);
+  }
+  return r;
+}
+
 // One lane's work on a head: the norm, the rotation and the stores of its two
 // chunks of the head's D values, with the token's angles and the norm weights
 // kept from head to head.  All lanes of a warp call together.
-template <int D, bool BF16, bool FP8>
+template <int D, bool BF16, int POOL>  // POOL: bits of a pool's elements
 struct LaneWork {
   static constexpr int LPH = D / 16;    // lanes per head
   static constexpr int HPW = 32 / LPH;  // heads per warp
@@ -130,10 +173,13 @@ struct LaneWork {
   int l, rc, c0, c1;  // lane of the head; rotated chunks / 2; this lane's chunks
   int first_k, first_v, heads;
   int64_t t, at, block;  // token; its row in the pools and its block
+  int row_in_tile = 0;
   bool writes;
   F2 cs[4], sn[4], ns[4];
   const uint16_t* w_now = nullptr;  // whose weights w0 and w1 hold
   F2 w0[4], w1[4];
+  int mate0, mate1;  // 4-bit pools: the lane with the other half of chunk c0's and c1's group
+  bool second0, second1;  // and whether it is that lane's second chunk
 
   __device__ __forceinline__ LaneWork(const NormRopeArgs& args, int lane) : a(args) {
     l = lane % LPH;
@@ -144,6 +190,14 @@ struct LaneWork {
     first_k = a.num_q_heads;
     first_v = first_k + a.num_kv_heads;
     heads = first_v + a.num_kv_heads;
+    auto mate = [&](int c, int& who, bool& second) {
+      const int p = c ^ 1;
+      const int in_head = p < rc ? p : p < 2 * rc ? p - rc : rc + (p - 2 * rc) / 2;
+      who = lane - l + in_head;
+      second = p < rc ? false : p < 2 * rc ? true : p & 1;
+    };
+    mate(c0, mate0, second0);
+    mate(c1, mate1, second1);
   }
 
   // Whether a token with this position is worked on: -1 marks a padding
@@ -167,8 +221,13 @@ struct LaneWork {
     t = token;
     writes = slot >= 0 && slot < a.num_slots;  // -1: the token has no slot
     block = writes ? slot >> a.block_shift : 0;
-    at = block * a.block_stride +
-         static_cast<int64_t>(writes ? slot & ((1 << a.block_shift) - 1) : 0) * a.num_kv_heads * D;
+    const int offset = writes ? slot & ((1 << a.block_shift) - 1) : 0;
+    if constexpr (POOL == 4) {  // the record of head 0, and the row in it
+      at = block * a.block_stride + (offset >> 4) * fp4::Record<D>::kBytes;
+      row_in_tile = offset & 15;
+    } else {
+      at = block * a.block_stride + static_cast<int64_t>(offset) * a.num_kv_heads * D;
+    }
     if (l >= rc) return;
     const int i0 = a.interleaved ? 4 * c0 : 8 * c0, i1 = a.interleaved ? 4 * c1 : 8 * c0 + 4;
     const float4 x = *reinterpret_cast<const float4*>(row + i0), y = *reinterpret_cast<const float4*>(row + i1);
@@ -183,6 +242,7 @@ struct LaneWork {
     const bool is_q = h < first_k, is_v = h >= first_v;
     const int g = is_q ? h : is_v ? h - first_v : h - first_k;
     F2 x0[4], x1[4];
+    [[maybe_unused]] F2 z0[4], z1[4];  // 4-bit pools: over the head's scale
     widen8<BF16>(u0, x0);
     widen8<BF16>(u1, x1);
     const uint16_t* w = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
@@ -231,26 +291,65 @@ struct LaneWork {
         }
       }
     }
+    [[maybe_unused]] float top0 = 0.f, top1 = 0.f;  // the largest magnitudes of the two chunks' groups
+    if constexpr (POOL == 4) {
+      if (!is_q) {
+        const float* hs = is_v ? a.v_scale : a.k_scale;
+        if (hs && h < heads) {
+          const float inv = __frcp_rn(__ldg(hs + g));
+          const F2 m = pair(inv, inv);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            z0[j] = mul2(x0[j], m);
+            z1[j] = mul2(x1[j], m);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            z0[j] = x0[j];
+            z1[j] = x1[j];
+          }
+        }
+        top0 = top8(z0);
+        top1 = top8(z1);
+      }
+      const float a0 = __shfl_sync(kFull, top0, mate0), a1 = __shfl_sync(kFull, top1, mate0);
+      const float b0 = __shfl_sync(kFull, top0, mate1), b1 = __shfl_sync(kFull, top1, mate1);
+      top0 = max_nan(top0, second0 ? a1 : a0);
+      top1 = max_nan(top1, second1 ? b1 : b0);
+    }
     if (h >= heads) return;
-    if (is_q || (a.k_out && !is_v) || (!FP8 && !is_v && writes)) {
+    if (is_q || (a.k_out && !is_v) || (POOL == 16 && !is_v && writes)) {
       const uint4 y0 = narrow8<BF16>(x0), y1 = narrow8<BF16>(x1);
       if (is_q || a.k_out) {
         uint16_t* dst = is_q ? a.q_out + t * a.q_out_stride + g * D : a.k_out + t * a.k_out_stride + g * D;
         reinterpret_cast<uint4*>(dst)[c0] = y0;
         reinterpret_cast<uint4*>(dst)[c1] = y1;
       }
-      if (!FP8 && !is_q && writes) {
+      if (POOL == 16 && !is_q && writes) {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_pool) + at + g * D);
         dst[c0] = y0;
         dst[c1] = y1;
       }
     }
     if (is_q || !writes) return;
-    if constexpr (FP8) {
+    if constexpr (POOL == 8) {
       const float sc = __ldg((is_v ? a.v_scale : a.k_scale) + block * a.scale_stride + g);
       uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) + at + g * D);
       dst[c0] = codes8(x0, sc);
       dst[c1] = codes8(x1, sc);
+    } else if constexpr (POOL == 4) {
+      uint8_t* rec = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) + at +
+                     (static_cast<int64_t>(g) << (a.block_shift - 4)) * fp4::Record<D>::kBytes;
+      uint8_t* codes = rec + row_in_tile * fp4::Record<D>::kRowBytes;
+      uint8_t* scales = rec + fp4::Record<D>::kScalesAt + row_in_tile * fp4::Record<D>::kRowScales;
+      const uint32_t s01 = fp8::e4m3x2_satfinite(__fdiv_rn(top0, 6.f), __fdiv_rn(top1, 6.f));
+      const uint32_t sf = fp4::e4m3x2_to_f16(s01);
+      const float2 sv = __half22float2(*reinterpret_cast<const __half2*>(&sf));
+      *reinterpret_cast<uint32_t*>(codes + 4 * c0) = codes8_e2m1(z0, sv.x, top0);
+      *reinterpret_cast<uint32_t*>(codes + 4 * c1) = codes8_e2m1(z1, sv.y, top1);
+      if (!(c0 & 1)) scales[c0 / 2] = static_cast<uint8_t>(s01);
+      if (!(c1 & 1)) scales[c1 / 2] = static_cast<uint8_t>(s01 >> 8);
     } else if (is_v) {  // moves bit by bit
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v_pool) + at + g * D);
       dst[c0] = u0;
@@ -260,7 +359,7 @@ struct LaneWork {
 };
 
 // Few tokens: a warp per (token, HPW heads), everything straight from global memory.
-template <int D, bool BF16, bool FP8>
+template <int D, bool BF16, int POOL>  // POOL: bits of a pool's elements
 __global__ void __launch_bounds__(128) norm_rope_write_kernel(const NormRopeArgs a, uint32_t parts) {
   griddep_wait();
   griddep_launch_dependents();
@@ -268,7 +367,7 @@ __global__ void __launch_bounds__(128) norm_rope_write_kernel(const NormRopeArgs
   const uint32_t task = blockIdx.x * 4 + (threadIdx.x >> 5);
   const uint32_t token = task / parts;
   if (token >= static_cast<uint32_t>(a.num_tokens)) return;
-  LaneWork<D, BF16, FP8> work(a, lane);
+  LaneWork<D, BF16, POOL> work(a, lane);
   const int part = static_cast<int>(task - token * parts);
   const int h = part * work.HPW + lane / work.LPH;
   const int64_t t = token;
@@ -310,10 +409,10 @@ constexpr int kStageBytes = kGroups * (32 / (D / 16)) * D * 2 + D * 4;
 template <int D>
 constexpr int kRingBytes = (kStages * (kStageBytes<D> + 16) + 127) / 128 * 128;
 
-template <int D, bool BF16, bool FP8>
+template <int D, bool BF16, int POOL>  // POOL: bits of a pool's elements
 __global__ void __launch_bounds__(kStreamWarps * 32) norm_rope_stream_kernel(const NormRopeArgs a, uint32_t parts,
                                                                                 int part_groups) {
-  using Work = LaneWork<D, BF16, FP8>;
+  using Work = LaneWork<D, BF16, POOL>;
   constexpr int kRowBytes = D * 2, kAngles = kGroups * Work::HPW * kRowBytes;
   const int part_heads = part_groups * Work::HPW;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -407,19 +506,19 @@ __global__ void __launch_bounds__(kStreamWarps * 32) norm_rope_stream_kernel(con
 // 81, 162, 323 and 647 groups a SM (32 + 16 heads, 16 bits): 5.8 / 7.1,
 // 13.0 / 13.1, 24.0 / 20.2, 45.3 / 34.8; FP8 pools (32 + 8 heads) at 135,
 // 270 and 539: 11.0 / 13.1, 20.2 / 21.1, 37.2 / 35.5.
-template <bool FP8>
-constexpr int kManyTasks = FP8 ? 320 : 160;
+template <int POOL>
+constexpr int kManyTasks = POOL == 8 ? 320 : 160;
 
-template <int D, bool BF16, bool FP8>
+template <int D, bool BF16, int POOL>  // POOL: bits of a pool's elements
 cudaError_t launch_t(const NormRopeArgs& a, cudaStream_t stream) {
   constexpr int HPW = 32 / (D / 16);
   const int64_t heads = a.num_q_heads + 2LL * a.num_kv_heads, groups = (heads + HPW - 1) / HPW;
-  if (a.num_tokens * groups < static_cast<int64_t>(kManyTasks<FP8>) * current_sm_count(152))
-    return launch_pdl(norm_rope_write_kernel<D, BF16, FP8>,
+  if (a.num_tokens * groups < static_cast<int64_t>(kManyTasks<POOL>) * current_sm_count(152))
+    return launch_pdl(norm_rope_write_kernel<D, BF16, POOL>,
                       dim3(static_cast<unsigned>((a.num_tokens * groups + 3) / 4)), dim3(128), 0, stream, a,
                       static_cast<uint32_t>(groups));
   const int64_t parts = (groups + kGroups - 1) / kGroups, part_groups = (groups + parts - 1) / parts;
-  auto kern = norm_rope_stream_kernel<D, BF16, FP8>;
+  auto kern = norm_rope_stream_kernel<D, BF16, POOL>;
   constexpr size_t smem = static_cast<size_t>(kStreamWarps) * kRingBytes<D>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
@@ -429,17 +528,21 @@ cudaError_t launch_t(const NormRopeArgs& a, cudaStream_t stream) {
                     stream, a, static_cast<uint32_t>(parts), static_cast<int>(part_groups));
 }
 
+template <int POOL>
+cudaError_t launch_p(const NormRopeArgs& a, int head_dim, bool bf16, cudaStream_t stream) {
+  if (head_dim == 128) return bf16 ? launch_t<128, true, POOL>(a, stream) : launch_t<128, false, POOL>(a, stream);
+  if (head_dim == 64) return bf16 ? launch_t<64, true, POOL>(a, stream) : launch_t<64, false, POOL>(a, stream);
+  return cudaErrorInvalidValue;
+}
+
 }  // namespace
 
-cudaError_t launch_norm_rope_write(const NormRopeArgs& a, int head_dim, bool bf16, bool fp8, cudaStream_t stream) {
+cudaError_t launch_norm_rope_write(const NormRopeArgs& a, int head_dim, bool bf16, int pool_bits,
+                                   cudaStream_t stream) {
   if (a.num_tokens == 0) return cudaSuccess;
-  if (head_dim == 128)
-    return fp8 ? (bf16 ? launch_t<128, true, true>(a, stream) : launch_t<128, false, true>(a, stream))
-               : (bf16 ? launch_t<128, true, false>(a, stream) : launch_t<128, false, false>(a, stream));
-  if (head_dim == 64)
-    return fp8 ? (bf16 ? launch_t<64, true, true>(a, stream) : launch_t<64, false, true>(a, stream))
-               : (bf16 ? launch_t<64, true, false>(a, stream) : launch_t<64, false, false>(a, stream));
-  return cudaErrorInvalidValue;
+  return pool_bits == 4   ? launch_p<4>(a, head_dim, bf16, stream)
+         : pool_bits == 8 ? launch_p<8>(a, head_dim, bf16, stream)
+                          : launch_p<16>(a, head_dim, bf16, stream);
 }
 
 }  // namespace pkv

@@ -105,6 +105,28 @@ Pool pool_of(const at::Tensor& k, const at::Tensor* v, const at::Tensor* ks, con
   return p;
 }
 
+// A 4-bit pool of records, uint8 [NB, H, B / 16, 9 D], with dense blocks.
+Pool pool4_of(const at::Tensor& k, const at::Tensor& v, const at::Tensor* ks, const at::Tensor* vs) {
+  need(k.scalar_type() == at::kByte && k.dim() == 4 && k.size(3) % 9 == 0,
+       "4-bit pools must be uint8 [NB, H_kv, block_size / 16, 9 * D]");
+  need(k.size(2) <= 4, "4-bit pool blocks hold 16, 32 or 64 tokens");
+  Pool p{size(k, 0), size(k, 2) * 16, size(k, 1), size(k, 3) / 9};
+  const int64_t tiles = k.size(2) * k.size(3), block = tiles * p.H;
+  need(k.stride(3) == 1 && k.stride(2) == k.size(3) && k.stride(1) == tiles && k.stride(0) >= block,
+       "4-bit pool blocks must be dense [H_kv, block_size / 16, 9 * D] slices");
+  need(v.sizes() == k.sizes() && v.strides() == k.strides() && v.scalar_type() == at::kByte,
+       "k_pool and v_pool must share shape, strides and dtype");
+  need(block > 0 && k.stride(0) % block == 0 && k.stride(0) / block <= 0x7fffffff,
+       "4-bit pool blocks must be whole blocks apart");
+  p.layers = static_cast<int>(k.stride(0) / block);
+  p.stride = k.stride(0);
+  for (const at::Tensor* sc : {ks, vs})
+    if (sc)
+      need(sc->scalar_type() == at::kFloat && sc->dim() == 1 && sc->size(0) == p.H && sc->is_contiguous(),
+           "scales of 4-bit pools must be float32 [H_kv]");
+  return p;
+}
+
 // Row stride of [T, heads, D] rows, dense within a token; 0 where one row or none makes it meaningless.
 int64_t rows(const at::Tensor* t, int64_t T, int64_t heads, int64_t D, at::ScalarType type, const char* name) {
   if (!t) return 0;
@@ -187,10 +209,11 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F call) {
 }
 
 // (q, k, v, k_pool, v_pool, k_scale, v_scale, slot_mapping, q_out, k_out, q_weight, k_weight, eps, cos_sin,
-//  positions, interleaved, status, stream, fp8)
+//  positions, interleaved, status, stream, bits)
 PyObject* norm_rope_write(PyObject*, PyObject* const* o, Py_ssize_t n) {
   return guarded(n, 19, [&](int dev) {
-    const bool fp8 = o[18] == Py_True;
+    const int bits = integer(o[18], "bits");
+    const bool fp8 = bits == 8;
     const at::Tensor &q = *tensor(o[0], "q", dev), &k = *tensor(o[1], "k", dev), &v = *tensor(o[2], "v", dev);
     const at::Tensor &kp = *tensor(o[3], "k_pool", dev), &vp = *tensor(o[4], "v_pool", dev);
     const at::Tensor *ks = tensor(o[5], "k_scale", dev, !fp8), *vs = tensor(o[6], "v_scale", dev, !fp8);
@@ -201,10 +224,10 @@ PyObject* norm_rope_write(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const at::Tensor* cs = dense(tensor(o[13], "cos_sin", dev, true), "cos_sin", at::kFloat);
     const at::Tensor* pos = int32s(o[14], "positions", dev, true);
     const at::Tensor* status = int32s(o[16], "status", dev, true);
-    const Pool p = pool_of(kp, &vp, ks, vs, fp8);
+    const Pool p = bits == 4 ? pool4_of(kp, vp, ks, vs) : pool_of(kp, &vp, ks, vs, fp8);
     const pkv_dtype dt = value_dtype(q);
     const at::ScalarType type = q.scalar_type();
-    need(fp8 || kp.scalar_type() == type, "rows and pools must share a dtype");
+    need(bits != 16 || kp.scalar_type() == type, "rows and pools must share a dtype");
     need(q.dim() == 3, "q must be [T, H_q, D]");
     const int T = size(q, 0), Hq = size(q, 1);
     const int64_t qs = rows(&q, T, Hq, p.D, type, "q"), qos = rows(&q_out, T, Hq, p.D, type, "q_out");
@@ -226,7 +249,13 @@ PyObject* norm_rope_write(PyObject*, PyObject* const* o, Py_ssize_t n) {
     const float eps = number(o[12], "eps");
     const bool inter = truth(o[15], "interleaved");
     void* stream = stream_of(o[17], dev);
-    if (fp8)
+    if (bits == 4)
+      done(pkv_norm_rope_write_fp4(ptr(&q_out), qos, ptr(k_out), kos, ptr(&q), qs, ptr(&k), ptr(&v), kvs, ptr(qw),
+                                   ptr(kw), eps, ptr_of<float>(cs), ptr_of<int32_t>(pos), top, rot, inter, ptr(&kp),
+                                   ptr(&vp), ptr_of<float>(ks), ptr_of<float>(vs), ptr_of<int32_t>(&slots), T, Hq, p.H,
+                                   p.D, p.B, p.NB, p.layers, dt, ptr_of<int32_t>(status), stream),
+           "pkv_norm_rope_write_fp4");
+    else if (fp8)
       done(pkv_norm_rope_write_fp8(ptr(&q_out), qos, ptr(k_out), kos, ptr(&q), qs, ptr(&k), ptr(&v), kvs, ptr(qw),
                                    ptr(kw), eps, ptr_of<float>(cs), ptr_of<int32_t>(pos), top, rot, inter, ptr(&kp),
                                    ptr(&vp), ptr_of<float>(ks), ptr_of<float>(vs), ptr_of<int32_t>(&slots), T, Hq, p.H,
@@ -345,6 +374,113 @@ PyObject* decode_sparse(PyObject*, PyObject* const* o, Py_ssize_t n) {
   });
 }
 
+// (k_new, v_new, k_pool, v_pool, k_scale, v_scale, slot_mapping, status, stream)
+PyObject* write_cache_fp4(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  return guarded(n, 9, [&](int dev) {
+    const at::Tensor &k = *tensor(o[0], "k_new", dev), &v = *tensor(o[1], "v_new", dev);
+    const at::Tensor &kp = *tensor(o[2], "k_pool", dev), &vp = *tensor(o[3], "v_pool", dev);
+    const at::Tensor *ks = tensor(o[4], "k_scale", dev, true), *vs = tensor(o[5], "v_scale", dev, true);
+    const at::Tensor& slots = *int32s(o[6], "slot_mapping", dev);
+    const at::Tensor* status = int32s(o[7], "status", dev, true);
+    const Pool p = pool4_of(kp, vp, ks, vs);
+    const pkv_dtype dt = value_dtype(k);
+    need(k.dim() == 3, "k_new must be [T, H_kv, D]");
+    const int T = size(k, 0);
+    const int64_t kvs = rows(&k, T, p.H, p.D, k.scalar_type(), "k_new");
+    need(rows(&v, T, p.H, p.D, k.scalar_type(), "v_new") == kvs, "k_new and v_new must share a row stride");
+    need(slots.dim() == 1 && slots.size(0) == T, "slot_mapping must be int32 [T]");
+    done(pkv_write_cache_fp4(ptr(&k), ptr(&v), ptr(&kp), ptr(&vp), ptr_of<float>(ks), ptr_of<float>(vs),
+                             ptr_of<int32_t>(&slots), T, kvs, p.H, p.D, p.B, p.NB, p.layers, dt,
+                             ptr_of<int32_t>(status), stream_of(o[8], dev)),
+         "pkv_write_cache_fp4");
+  });
+}
+
+// (k_pool, v_pool, pairs, status, stream): whole pools, [NB, H, tiles, 9 D] or [NB, layers, H, tiles, 9 D]
+PyObject* copy_blocks_fp4(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  return guarded(n, 5, [&](int dev) {
+    const at::Tensor &kp = *tensor(o[0], "k_pool", dev), &vp = *tensor(o[1], "v_pool", dev);
+    const at::Tensor& pairs = *int32s(o[2], "pairs", dev);
+    const at::Tensor* status = int32s(o[3], "status", dev, true);
+    const bool all = kp.dim() == 5;
+    need(kp.scalar_type() == at::kByte && (kp.dim() == 4 || all) && kp.is_contiguous() && kp.size(-1) % 9 == 0 &&
+             kp.size(-2) <= 4 && vp.is_contiguous() && vp.sizes() == kp.sizes() && vp.scalar_type() == at::kByte,
+         "4-bit pools must be contiguous uint8 [NB, (layers,) H_kv, block_size / 16, 9 * D]");
+    need(pairs.dim() == 2 && pairs.size(1) == 2, "pairs must be int32 [P, 2]");
+    done(pkv_copy_blocks_fp4(ptr(&kp), ptr(&vp), ptr_of<int32_t>(&pairs), size(pairs, 0), all ? size(kp, 1) : 1,
+                             size(kp, kp.dim() - 3), size(kp, kp.dim() - 1) / 9, size(kp, kp.dim() - 2) * 16,
+                             size(kp, 0), ptr_of<int32_t>(status), stream_of(o[4], dev)),
+         "pkv_copy_blocks_fp4");
+  });
+}
+
+// What the decode calls over a whole or windowed history share.
+struct Rows {
+  int S, Hq;
+  pkv_dtype dt, od;
+};
+Rows rows_of(const at::Tensor& out, const at::Tensor& q, const at::Tensor& bt, const at::Tensor& cl, const Pool& p) {
+  need(q.dim() == 3 && q.size(2) == p.D && q.is_contiguous() && out.sizes() == q.sizes() && out.is_contiguous(),
+       "q and out must be contiguous [S, H_q, D] with the pools' D");
+  Rows r{size(q, 0), size(q, 1), value_dtype(q), out_dtype(out)};
+  need(bt.dim() == 2 && bt.size(0) == r.S && cl.dim() == 1 && cl.size(0) == r.S,
+       "block_tables [S, blocks] and context_lens [S] are needed");
+  return r;
+}
+
+// (out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale, partition_size, max_context_len,
+//  workspace, status, stream)
+PyObject* decode_attention_fp4(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  return guarded(n, 14, [&](int dev) {
+    const at::Tensor &out = *tensor(o[0], "out", dev), &q = *tensor(o[1], "q", dev);
+    const at::Tensor &kp = *tensor(o[2], "k_pool", dev), &vp = *tensor(o[3], "v_pool", dev);
+    const at::Tensor *ks = tensor(o[4], "k_scale", dev, true), *vs = tensor(o[5], "v_scale", dev, true);
+    const at::Tensor &bt = *int32s(o[6], "block_tables", dev), &cl = *int32s(o[7], "context_lens", dev);
+    const at::Tensor* ws = tensor(o[11], "workspace", dev, true);
+    const at::Tensor* status = int32s(o[12], "status", dev, true);
+    const Pool p = pool4_of(kp, vp, ks, vs);
+    const Rows r = rows_of(out, q, bt, cl, p);
+    need(!ws || ws->is_contiguous(), "workspace must be contiguous");
+    done(pkv_decode_attention_fp4(ptr(&out), ptr(&q), ptr(&kp), ptr(&vp), ptr_of<float>(ks), ptr_of<float>(vs),
+                                  ptr_of<int32_t>(&bt), size(bt, 1), ptr_of<int32_t>(&cl), r.S, r.Hq, p.H, p.D, p.B,
+                                  p.NB, p.layers, number(o[8], "scale"), integer(o[9], "partition_size"),
+                                  integer(o[10], "max_context_len"), ptr(ws), ws ? ws->nbytes() : 0, r.dt, r.od,
+                                  ptr_of<int32_t>(status), stream_of(o[13], dev)),
+         "pkv_decode_attention_fp4");
+  });
+}
+
+// (out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale, window, sinks, max_context_len,
+//  status, stream, bits)
+PyObject* decode_window(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  return guarded(n, 15, [&](int dev) {
+    const bool fp4 = integer(o[14], "bits") == 4;
+    const at::Tensor &out = *tensor(o[0], "out", dev), &q = *tensor(o[1], "q", dev);
+    const at::Tensor &kp = *tensor(o[2], "k_pool", dev), &vp = *tensor(o[3], "v_pool", dev);
+    const at::Tensor *ks = tensor(o[4], "k_scale", dev, true), *vs = tensor(o[5], "v_scale", dev, true);
+    const at::Tensor &bt = *int32s(o[6], "block_tables", dev), &cl = *int32s(o[7], "context_lens", dev);
+    const at::Tensor* status = int32s(o[12], "status", dev, true);
+    const Pool p = fp4 ? pool4_of(kp, vp, ks, vs) : pool_of(kp, &vp, nullptr, nullptr, false);
+    const Rows r = rows_of(out, q, bt, cl, p);
+    need(fp4 || kp.scalar_type() == q.scalar_type(), "q, k_pool and v_pool must share a dtype");
+    const float scale = number(o[8], "scale");
+    const int window = integer(o[9], "window"), sinks = integer(o[10], "sinks");
+    const int longest = integer(o[11], "max_context_len");
+    void* stream = stream_of(o[13], dev);
+    if (fp4)
+      done(pkv_decode_window_fp4(ptr(&out), ptr(&q), ptr(&kp), ptr(&vp), ptr_of<float>(ks), ptr_of<float>(vs),
+                                 ptr_of<int32_t>(&bt), size(bt, 1), ptr_of<int32_t>(&cl), r.S, r.Hq, p.H, p.D, p.B,
+                                 p.NB, p.layers, scale, window, sinks, longest, r.dt, r.od, ptr_of<int32_t>(status),
+                                 stream),
+           "pkv_decode_window_fp4");
+    else
+      done(pkv_decode_window(ptr(&out), ptr(&q), ptr(&kp), ptr(&vp), p.stride, ptr_of<int32_t>(&bt), size(bt, 1),
+                             ptr_of<int32_t>(&cl), r.S, r.Hq, p.H, p.D, p.B, p.NB, scale, window, sinks, longest, r.dt,
+                             r.od, ptr_of<int32_t>(status), stream),
+           "pkv_decode_window");
+  });
+}
+
 PyObject* set_error_type(PyObject*, PyObject* type) {
   Py_INCREF(type);
   Py_XSETREF(g_error, type);
@@ -361,6 +497,10 @@ PyMethodDef kMethods[] = {
     {"summarize_blocks", fast(summarize_blocks), METH_FASTCALL, nullptr},
     {"select_blocks", fast(select_blocks), METH_FASTCALL, nullptr},
     {"decode_sparse", fast(decode_sparse), METH_FASTCALL, nullptr},
+    {"write_cache_fp4", fast(write_cache_fp4), METH_FASTCALL, nullptr},
+    {"copy_blocks_fp4", fast(copy_blocks_fp4), METH_FASTCALL, nullptr},
+    {"decode_attention_fp4", fast(decode_attention_fp4), METH_FASTCALL, nullptr},
+    {"decode_window", fast(decode_window), METH_FASTCALL, nullptr},
     {"set_error_type", set_error_type, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
