@@ -704,6 +704,44 @@ pkv_status pkv_decode_window_fp4(void* out, const void* q, const void* k_pool, c
                                  pkv_dtype out_dtype, int32_t* dev_status, void* stream);
 
 /*
+ * ------------------------------------------------------------------- prompts
+ */
+
+/*
+ * pkv_prefill_attention -- attention of many tokens of each sequence over its
+ * paged history, causal, with or without a window: prompts, chunks of prompts
+ * behind a cached prefix, drafted tokens.  The new tokens' K and V are in the
+ * pools already (pkv_write_cache, pkv_norm_rope_write).  With n =
+ * query_start[s + 1] - query_start[s] new tokens, the last n of the sequence's
+ * L = context_lens[s], row query_start[s] + i sits at position p = L - n + i:
+ *     out[row][h] = sum_t softmax_t(scale * q[row][h] . k_t) v_t,
+ *                   t <= p and (window == 0, or t > p - window, or t < sinks).
+ *   out          : [num_tokens][num_q_heads][head_dim], out_dtype, 16-byte aligned.
+ *   q            : [num_tokens][num_q_heads][head_dim] of kv_dtype, 16-byte aligned,
+ *                  consecutive tokens q_stride elements apart (0 = dense, else a
+ *                  multiple of 8 and at least a row).
+ *   query_start  : int32[num_seqs + 1], ascending from 0 to at most num_tokens (device).
+ *                  Rows at and behind query_start[num_seqs] are left as they are.
+ *                  Entries that descend or lie outside are clamped and set
+ *                  PKV_DEV_ERR_LENGTH, as does n > L (rows with p < 0 are zero).
+ *   window, sinks: >= 0; window 0: all of the history (sinks then mean nothing).
+ * Blocks without a token that some new one sees are not read.  A table entry
+ * outside the pool, of a block that is seen, sets PKV_DEV_ERR_BLOCK; the block
+ * then counts as zero keys and values.  Tokens that no new token of the
+ * sequence sees may hold anything; V of a token that some of them see has to be
+ * finite, as it meets weights of zero in the others' rows.  Weights enter the
+ * product with V in kv_dtype (half a step of it each).  Block sizes 8 to 64,
+ * head_dim 64 or 128, 1 <= group <= 8.  One kernel, no workspace; other
+ * arguments and flags as in pkv_decode_attention.
+ */
+pkv_status pkv_prefill_attention(void* out, const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
+                                 int64_t block_stride, const int32_t* block_tables, int max_blocks_per_seq,
+                                 const int32_t* context_lens, const int32_t* query_start, int num_seqs, int num_tokens,
+                                 int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                 float scale, int window, int sinks, int max_context_len, pkv_dtype kv_dtype,
+                                 pkv_dtype out_dtype, int32_t* dev_status, void* stream);
+
+/*
  * ------------------------------------------------------------ block manager
  *
  * Host-side allocator of a pool's blocks (host functions, no GPU call): the

@@ -80,6 +80,8 @@ _SIGS["pkv_decode_window"] = ([_c_void_p] * 4 + [_c_int64, _c_void_p, _c_int, _c
                               [_c_int] * 5 + [_c_void_p] * 2)
 _SIGS["pkv_decode_window_fp4"] = ([_c_void_p] * 7 + [_c_int, _c_void_p] + [_c_int] * 7 + [_c_float] + [_c_int] * 5 +
                                   [_c_void_p] * 2)
+_SIGS["pkv_prefill_attention"] = ([_c_void_p] * 2 + [_c_int64] + [_c_void_p] * 2 + [_c_int64, _c_void_p, _c_int] +
+                                  [_c_void_p] * 2 + [_c_int] * 7 + [_c_float] + [_c_int] * 5 + [_c_void_p] * 2)
 _SIGS["pkv_last_cuda_error"] = []
 _SIGS["pkv_cuda_error_name"] = [_c_int]
 
@@ -602,6 +604,20 @@ def decode_window_fp4(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, co
     """pkv_decode_window_fp4: decode_window over 4-bit pools."""
     (_EXT or _ext()).decode_window(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale, window,
                                    sinks, max_context_len, status, stream, 4)
+
+
+# ------------------------------------------------------------------ prompts
+
+
+def prefill_attention(out, q, k_pool, v_pool, block_tables, context_lens, query_start, scale, *, window=0, sinks=0,
+                      max_context_len, status=None, stream=None):
+    """pkv_prefill_attention: causal attention of new tokens over their sequences' paged history.
+
+    q [T, H_q, D] f16/bf16 (may be slices of a fused projection), rows query_start[s] .. query_start[s + 1]
+    (int32 [S + 1]) the last tokens of sequence s; their K and V are in the pools already.  window > 0: the
+    last `window` tokens of each position and the first `sinks` of the sequence."""
+    (_EXT or _ext()).prefill_attention(out, q, k_pool, v_pool, block_tables, context_lens, query_start, scale, window,
+                                       sinks, max_context_len, status, stream)
 
 
 # ------------------------------------------------------------------ swap

@@ -22,9 +22,9 @@ EXT = os.path.join(OUT_DIR, "_pkv_torch.so")  # CPython extension over libpkv an
 EXT_SOURCE = "pkv_torch.cpp"
 SOURCES = ["pkv_api.cu", "pkv_cache_ops.cu", "pkv_decode.cu", "pkv_decode_hg.cu", "pkv_decode_balanced.cu",
            "pkv_decode_fp8.cu", "pkv_norm_rope.cu", "pkv_sparse_select.cu", "pkv_sparse_decode.cu", "pkv_decode_window.cu",
-           "pkv_api_layer.cu",
+           "pkv_prefill.cu", "pkv_api_layer.cu",
            "pkv_static_ws.cu", "pkv_checks.cu", "pkv_block_manager.cpp"]
-HEADERS = ["pkv_internal.h", "pkv_device.cuh", "pkv_balanced.cuh", "pkv_fp4.cuh", "pkv_fp8.cuh", "pkv_fp8_attention.cuh",
+HEADERS = ["pkv_internal.h", "pkv_device.cuh", "pkv_balanced.cuh", "pkv_fp4.cuh", "pkv_fp8.cuh", "pkv_fp8_attention.cuh", "pkv_tcgen05.cuh",
            os.path.join("..", "..", "include", "pkv.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

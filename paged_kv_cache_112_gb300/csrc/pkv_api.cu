@@ -254,6 +254,46 @@ bool encode_pool_map(CUtensorMap* map, const void* pool, int num_blocks, int blo
   return true;
 }
 
+namespace {
+
+// A four-dimensional map of 16-bit elements in the 128-byte swizzle; strides in bytes, box rows of 64 elements.
+bool encode_lines(CUtensorMap* map, const void* base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
+                  const cuuint32_t (&box)[4]) {
+  auto fn = encode_fn();
+  if (!fn) {
+    t_last_cuda_error = static_cast<int>(cudaErrorSymbolNotFound);
+    return false;
+  }
+  if (!bind_context_if_none()) return false;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) t_last_cuda_error = -static_cast<int>(r);
+  return r == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool encode_block_map(CUtensorMap* map, const void* pool, int num_blocks, int block_size, int num_kv_heads,
+                      int head_dim, int64_t block_stride) {
+  const cuuint64_t lines = static_cast<cuuint64_t>(num_kv_heads) * (head_dim / 64);
+  return encode_lines(map, pool,
+                      {64, static_cast<cuuint64_t>(block_size), lines, static_cast<cuuint64_t>(num_blocks)},
+                      {lines * 128, 128, static_cast<cuuint64_t>(block_stride) * 2},
+                      {64, static_cast<cuuint32_t>(block_size), 1, 1});
+}
+
+bool encode_query_map(CUtensorMap* map, const void* q, int num_tokens, int num_heads, int head_dim, int64_t stride,
+                      int heads_per_box, int tokens_per_box) {
+  return encode_lines(map, q,
+                      {64, static_cast<cuuint64_t>(head_dim / 64), static_cast<cuuint64_t>(num_heads),
+                       static_cast<cuuint64_t>(num_tokens)},
+                      {128, static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(stride) * 2},
+                      {64, 1, static_cast<cuuint32_t>(heads_per_box), static_cast<cuuint32_t>(tokens_per_box)});
+}
+
 // log2 of a supported block size (8, 16, 32 or 64 tokens), else -1.
 int block_shift_of(int block_size) {
   switch (block_size) {

@@ -123,14 +123,14 @@ pkv_status prepare_rows(DecodeArgs* a, void* out, const void* q, const void* k_p
                         const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
                         int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
                         float scale, int max_context_len, pkv_dtype q_dtype, pkv_dtype out_dtype,
-                        int32_t* dev_status) {
+                        int32_t* dev_status, int least_shift = 4) {
   if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq < 0 || num_blocks <= 0 ||
       max_context_len < 0 || !std::isfinite(scale))
     return PKV_ERR_INVALID_ARG;
   if (!value_dtype_ok(q_dtype) || (out_dtype != PKV_F32 && out_dtype != PKV_F16 && out_dtype != PKV_BF16))
     return PKV_ERR_INVALID_ARG;
   const int shift = block_shift_of(block_size);
-  if (shift < 4 || (head_dim != 64 && head_dim != 128) || num_q_heads % num_kv_heads != 0 ||
+  if (shift < least_shift || (head_dim != 64 && head_dim != 128) || num_q_heads % num_kv_heads != 0 ||
       num_q_heads / num_kv_heads > 8 || static_cast<int64_t>(num_seqs) * num_kv_heads > kMaxUnits ||
       (static_cast<int64_t>(max_blocks_per_seq) << shift) > 0x7fffffff)
     return PKV_ERR_UNSUPPORTED;
@@ -537,6 +537,39 @@ pkv_status pkv_decode_window_fp4(void* out, const void* q, const void* k_pool, c
   const CUtensorMap none{};
   return cuda_status(
       launch_decode_window(a, w, none, none, head_dim, q_dtype == PKV_BF16, true, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_prefill_attention(void* out, const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
+                                 int64_t block_stride, const int32_t* block_tables, int max_blocks_per_seq,
+                                 const int32_t* context_lens, const int32_t* query_start, int num_seqs, int num_tokens,
+                                 int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                 float scale, int window, int sinks, int max_context_len, pkv_dtype kv_dtype,
+                                 pkv_dtype out_dtype, int32_t* dev_status, void* stream) {
+  if (num_tokens < 0 || window < 0 || sinks < 0) return PKV_ERR_INVALID_ARG;
+  DecodeArgs a{};
+  const pkv_status st =
+      prepare_rows(&a, out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, context_lens,
+                   num_tokens == 0 && num_seqs > 0 ? 0 : num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                   num_blocks, scale, max_context_len, kv_dtype, out_dtype, dev_status, 3);
+  if (st != PKV_OK) return st;
+  a.block_stride = resolve_block_stride(block_stride, block_size, num_kv_heads, head_dim);
+  const int64_t row = static_cast<int64_t>(num_q_heads) * head_dim, stride = row_stride(q_stride, row);
+  if (a.block_stride < 0 || stride < 0) return PKV_ERR_INVALID_ARG;
+  // Clusters of up to eight CTAs a pair of tiles and KV head, numbered in 32 bits.
+  if ((num_tokens / 2 + static_cast<int64_t>(num_seqs)) * num_kv_heads > 0x7fffffff / 8 || row > 0x7fffffff)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
+  if (!query_start || !aligned(query_start, 4) || !aligned(out, 16)) return PKV_ERR_INVALID_ARG;
+  if (scale < 0.f) a.scale_log2 = -a.scale_log2;
+  if (a.scale_log2 < 1e-30f) a.scale_log2 = 1e-30f;  // 0: every score alike, and masked ones stay -infinity
+  CUtensorMap tq, tk, tv;
+  if (!encode_query_map(&tq, q, num_tokens, num_q_heads, head_dim, stride, a.group, 128 / a.group) ||
+      !encode_block_map(&tk, k_pool, num_blocks, block_size, num_kv_heads, head_dim, a.block_stride) ||
+      !encode_block_map(&tv, v_pool, num_blocks, block_size, num_kv_heads, head_dim, a.block_stride))
+    return PKV_ERR_CUDA;
+  const PrefillArgs pa{query_start, num_tokens, window, sinks, scale < 0.f};
+  return cuda_status(
+      launch_prefill(a, pa, tq, tk, tv, head_dim, kv_dtype == PKV_BF16, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

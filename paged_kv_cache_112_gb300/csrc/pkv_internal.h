@@ -198,6 +198,14 @@ struct WindowArgs {
   const uint8_t* v4;
 };
 
+// New tokens of a prompt attention call, beside its DecodeArgs (pkv_prefill.cu).
+struct PrefillArgs {
+  const int32_t* query_start;  // [num_seqs + 1]: rows of each sequence's new tokens
+  int num_tokens;              // rows of q
+  int window, sinks;           // window 0: none
+  int negate;                  // the softmax scale is negative: scale_log2 is its magnitude's
+};
+
 // Split-K workspace layout (regions 256-byte aligned).  Fixed partitions:
 // records [S][H_q][max_parts].  Balanced split: per-pair metadata [S][<=H_q]
 // then records [W warps][2 slots][<= 8 heads].
@@ -332,6 +340,12 @@ cudaError_t launch_decode_sparse(const DecodeArgs& a, const SparseArgs& sp, cons
 cudaError_t launch_decode_window(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tmap_k,
                                  const CUtensorMap& tmap_v, int head_dim, bool bf16, bool fp4, cudaStream_t stream);
 
+// Prompt attention over 16-bit pools: maps of encode_query_map (boxes of a group's heads and 128 / group tokens) and
+// encode_block_map.
+cudaError_t launch_prefill(const DecodeArgs& a, const PrefillArgs& pa, const CUtensorMap& tmap_q,
+                           const CUtensorMap& tmap_k, const CUtensorMap& tmap_v, int head_dim, bool bf16,
+                           cudaStream_t stream);
+
 // Argument helpers shared by the entry points (pkv_api.cu).
 constexpr long long kWaitTimeoutNs = 2000000000LL;  // 2 s per bounded wait
 inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
@@ -342,5 +356,11 @@ int64_t resolve_block_stride(int64_t block_stride, int block_size, int num_kv_he
 // Tensor map of a pool for TMA tile loads; false (and the thread's CUDA error set) on failure.
 bool encode_pool_map(CUtensorMap* map, const void* pool, int num_blocks, int block_size, int num_kv_heads,
                      int head_dim, int eb, int64_t block_stride, int heads_per_box = 1);
+// Map of a 16-bit pool whose box is one 128-byte line of a whole block's rows.
+bool encode_block_map(CUtensorMap* map, const void* pool, int num_blocks, int block_size, int num_kv_heads,
+                      int head_dim, int64_t block_stride);
+// Map of query rows [tokens][heads][head_dim]: a box is one line of `heads_per_box` heads of `tokens_per_box` tokens.
+bool encode_query_map(CUtensorMap* map, const void* q, int num_tokens, int num_heads, int head_dim, int64_t stride,
+                      int heads_per_box, int tokens_per_box);
 
 }  // namespace pkv

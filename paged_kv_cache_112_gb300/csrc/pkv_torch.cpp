@@ -481,6 +481,32 @@ PyObject* decode_window(PyObject*, PyObject* const* o, Py_ssize_t n) {
   });
 }
 
+// (out, q, k_pool, v_pool, block_tables, context_lens, query_start, scale, window, sinks, max_context_len, status,
+//  stream)
+PyObject* prefill_attention(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  return guarded(n, 13, [&](int dev) {
+    const at::Tensor &out = *tensor(o[0], "out", dev), &q = *tensor(o[1], "q", dev);
+    const at::Tensor &kp = *tensor(o[2], "k_pool", dev), &vp = *tensor(o[3], "v_pool", dev);
+    const at::Tensor &bt = *int32s(o[4], "block_tables", dev), &cl = *int32s(o[5], "context_lens", dev);
+    const at::Tensor& qs = *int32s(o[6], "query_start", dev);
+    const at::Tensor* status = int32s(o[11], "status", dev, true);
+    const Pool p = pool_of(kp, &vp, nullptr, nullptr, false);
+    need(kp.scalar_type() == q.scalar_type(), "q, k_pool and v_pool must share a dtype");
+    need(q.dim() == 3, "q must be [T, H_q, D]");
+    const int T = size(q, 0), Hq = size(q, 1);
+    const int64_t stride = rows(&q, T, Hq, p.D, q.scalar_type(), "q");
+    need(out.sizes() == q.sizes() && out.is_contiguous(), "out must be contiguous [T, H_q, D]");
+    need(bt.dim() == 2 && cl.dim() == 1 && cl.size(0) == bt.size(0) && qs.dim() == 1 && qs.size(0) == bt.size(0) + 1,
+         "block_tables [S, blocks], context_lens [S] and query_start [S + 1] are needed");
+    done(pkv_prefill_attention(ptr(&out), ptr(&q), stride, ptr(&kp), ptr(&vp), p.stride, ptr_of<int32_t>(&bt),
+                               size(bt, 1), ptr_of<int32_t>(&cl), ptr_of<int32_t>(&qs), size(bt, 0), T, Hq, p.H, p.D,
+                               p.B, p.NB, number(o[7], "scale"), integer(o[8], "window"), integer(o[9], "sinks"),
+                               integer(o[10], "max_context_len"), value_dtype(q), out_dtype(out),
+                               ptr_of<int32_t>(status), stream_of(o[12], dev)),
+         "pkv_prefill_attention");
+  });
+}
+
 PyObject* set_error_type(PyObject*, PyObject* type) {
   Py_INCREF(type);
   Py_XSETREF(g_error, type);
@@ -501,6 +527,7 @@ PyMethodDef kMethods[] = {
     {"copy_blocks_fp4", fast(copy_blocks_fp4), METH_FASTCALL, nullptr},
     {"decode_attention_fp4", fast(decode_attention_fp4), METH_FASTCALL, nullptr},
     {"decode_window", fast(decode_window), METH_FASTCALL, nullptr},
+    {"prefill_attention", fast(prefill_attention), METH_FASTCALL, nullptr},
     {"set_error_type", set_error_type, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -99,3 +99,21 @@ def test_window_refusals(lib):
         assert call(q=FAKE + 4) == call(kd=pkv.PKV_F32) == call(maxlen=-1) == call(S=-1) == pkv.PKV_ERR_INVALID_ARG
     assert d(bs=16 * 2 * 128 - 8) == pkv.PKV_ERR_INVALID_ARG
     assert f(L=0) == f(vs=FAKE + 2) == pkv.PKV_ERR_INVALID_ARG
+
+
+def test_prefill_refusals(lib):
+    def c(**kw):
+        a = dict(out=FAKE, q=FAKE, qst=0, k=FAKE, bs=0, bt=FAKE, cl=FAKE, qs=FAKE, S=2, T=10, Hq=8, Hkv=2, D=128, B=16,
+                 scale=0.1, window=0, sinks=0, maxlen=64, kd=pkv.PKV_BF16, od=pkv.PKV_F32)
+        a.update(kw)
+        return lib.pkv_prefill_attention(a["out"], a["q"], a["qst"], a["k"], FAKE, a["bs"], a["bt"], 4, a["cl"], a["qs"],
+                                         a["S"], a["T"], a["Hq"], a["Hkv"], a["D"], a["B"], 10, a["scale"], a["window"],
+                                         a["sinks"], a["maxlen"], a["kd"], a["od"], None, None)
+
+    assert c(S=0) == c(T=0) == c(T=0, out=None) == pkv.PKV_OK
+    assert c(B=12) == c(D=96) == c(Hq=7) == c(Hq=18) == c(T=2 ** 31 - 1, Hkv=8) == pkv.PKV_ERR_UNSUPPORTED
+    assert c(window=-1) == c(sinks=-1) == c(T=-1) == c(S=-1) == c(maxlen=-1) == pkv.PKV_ERR_INVALID_ARG
+    assert c(q=None) == c(out=None) == c(qs=None) == c(cl=None) == c(bt=None) == pkv.PKV_ERR_INVALID_ARG
+    assert c(q=FAKE + 8) == c(out=FAKE + 8) == c(qs=FAKE + 2) == c(k=FAKE + 8) == pkv.PKV_ERR_INVALID_ARG
+    assert c(qst=1000) == c(qst=1028) == c(bs=8) == c(kd=pkv.PKV_F32) == pkv.PKV_ERR_INVALID_ARG
+    assert c(scale=float("nan")) == pkv.PKV_ERR_INVALID_ARG
