@@ -38,32 +38,6 @@ namespace {
 
 using namespace dev;
 
-// Pairs of floats, two operations an instruction (the kernel is as near the
-// issue limit as the memory's).
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 pair(float x, float y) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 halves(F2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
 template <bool BF16>
 __device__ __forceinline__ void widen8(const uint4& u, F2 (&x)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};

@@ -40,7 +40,10 @@ using namespace dev;
 
 constexpr int kRows = 128;     // query rows a tile
 constexpr int kKeys = 128;     // history tokens a tile
-constexpr int kThreads = 320;  // two tiles' threads, the loading warp, the issuing warp
+constexpr int kThreads = 384;  // two tiles' threads; the loading warp, the issuing warp and two that only wait
+// Registers: 168 a thread at launch; the tiles' threads hold a row of scores.
+constexpr int kRowRegs = 208, kOtherRegs = 80;
+static_assert(256 * kRowRegs + 128 * kOtherRegs <= 384 * 168, "shares of the launch's registers");
 constexpr int kMaxCluster = 8;
 
 template <int D>
@@ -190,7 +193,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
     }
   };
 
-  if (warp == 8) {
+  if (warp >= 8) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+   if (warp == 8) {
     // ---------------------------------------------------------------- loads
     const int B = 1 << a.block_shift, nblk = kKeys >> a.block_shift;  // blocks of a tile: 2 to 16, one a lane
     const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
@@ -326,194 +331,204 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
     __syncwarp();
   }
 
-  // ---------------------------------------------------------------- softmax
-  const int t = warp >> 2, r = tid & (kRows - 1);  // tile and row (warps 0 to 7)
-  const int token = r / G, pos = p0 + t * per_tile + token;
-  const bool live = warp < 8 && token < per_tile && t * per_tile + token < tokens;
-  const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
-  const uint32_t s_at = tmem + t * kKeys + lanes, o_at = tmem + 256 + t * D + lanes;
-  constexpr float kGrow = 8.f;
-  // f16 weights: times 2^7, so that small ones keep their bits (f16 ends at 2^-24).
-  constexpr float kUp = BF16 ? 0.f : 7.f;
-  float m = kNegInf, l = 0.f;  // the row's reference, in scores; the sum of its weights
-  if (warp < 8 && t < ntiles) {
-    const float sl2 = a.scale_log2, grow = kGrow / sl2;
-    const int my_low = pa.window > 0 ? max(0, pos - pa.window + 1) : 0, my_sinks = pa.window > 0 ? pa.sinks : 0;
-    // The tile's rows: positions first .. last, the widest and the narrowest view.
-    const int first = p0 + t * per_tile, last = first + per_tile - 1;
-    const int last_low = pa.window > 0 ? max(0, last - pa.window + 1) : 0;
-    bool ok = true;
-    for (int j = 0; j < cnt; ++j) {
-      ok = __all_sync(kFull, wait(s_bar + 8 * t, j & 1));
-      if (!ok) break;
+   if (C > 1) {  // the barriers of the cluster's meeting
+    __syncthreads();
+    cluster_sync();
+    cluster_sync();
+    cluster_sync();
+   }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
+    // -------------------------------------------------------------- softmax
+    const int t = warp >> 2, r = tid & (kRows - 1);  // tile and row
+    const int token = r / G, pos = p0 + t * per_tile + token;
+    const bool live = token < per_tile && t * per_tile + token < tokens;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+    const uint32_t s_at = tmem + t * kKeys + lanes, o_at = tmem + 256 + t * D + lanes;
+    constexpr float kGrow = 8.f;
+    // f16 weights: times 2^7, so that small ones keep their bits (f16 ends at 2^-24).
+    constexpr float kUp = BF16 ? 0.f : 7.f;
+    float m = kNegInf, l = 0.f;  // the row's reference, in scores; the sum of its weights
+    if (t < ntiles) {
+      const float sl2 = a.scale_log2, grow = kGrow / sl2;
+      const int my_low = pa.window > 0 ? max(0, pos - pa.window + 1) : 0, my_sinks = pa.window > 0 ? pa.sinks : 0;
+      // The tile's rows: positions first .. last, the widest and the narrowest view.
+      const int first = p0 + t * per_tile, last = first + per_tile - 1;
+      const int last_low = pa.window > 0 ? max(0, last - pa.window + 1) : 0;
+      bool ok = true;
+      for (int j = 0; j < cnt; ++j) {
+        ok = __all_sync(kFull, wait(s_bar + 8 * t, j & 1));
+        if (!ok) break;
+        tc::fence_after();
+        uint32_t x[kKeys];
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) tc::ld32(x + c, s_at + c);
+        tc::wait_ld();
+        float* v = reinterpret_cast<float*>(x);
+        const int t0 = tile_of(j) * kKeys;
+        if (!(t0 + kKeys - 1 <= first && (t0 >= last_low || t0 + kKeys <= my_sinks))) {
+          auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; };
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) {
+            const int at = t0 + c;
+            const uint32_t see = below(pos + 1 - at) & (~below(my_low - at) | below(my_sinks - at));
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[c + i] = (see >> i) & 1u ? v[c + i] : kNegInf;
+          }
+        }
+        float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int i = 4; i < kKeys - 4; i += 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], v[i + k]), v[i + 4 + k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], v[kKeys - 4 + k]);
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const bool raise = mx > m + grow;  // a first one counts: m is -infinity
+        if (__any_sync(kFull, raise)) {
+          const float mn = raise ? mx : m;
+          const float f = raise ? ex2_approx((m - mn) * sl2) : 1.f;  // 0 for a first one
+          l *= f;
+          m = mn;
+          if (j > 0) {  // O is at rest: its last product came before these scores
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tc::ld32(o, o_at + c);
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tc::st32(o_at + c, o);
+            }
+          }
+        }
+        const float shift = m == kNegInf ? 0.f : kUp - m * sl2;
+        const F2 scale2 = pair(sl2, sl2), shift2 = pair(shift, shift);
+        F2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < kKeys; i += 2) {
+          const float2 e = halves(fma2(pair(v[i], v[i + 1]), scale2, shift2));
+          const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
+          sum[(i / 2) & 1] = add2(sum[(i / 2) & 1], pair(p0, p1));
+          x[i / 2] = BF16 ? pack_bf16(p0, p1) : pack_f16(p0, p1);
+        }
+        const float2 s0 = halves(sum[0]), s1 = halves(sum[1]);
+        l += (s0.x + s0.y) + (s1.x + s1.y);
+        tc::st32(s_at, x);
+        tc::st32(s_at + 32, x + 32);
+        tc::wait_st();
+        tc::fence_before();
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_bar + 8 * t) : "memory");
+      }
+      if (cnt > 0 && ok) ok = __all_sync(kFull, wait(o_bar + 8 * t, 0));
       tc::fence_after();
-      uint32_t x[kKeys];
+    }
+
+    // ----------------------------------------------------------------- rows
+    auto store_row = [&](int64_t at, const float* o, float f) {  // 32 channels
+      if (a.out_dtype == 0) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
 #pragma unroll
-      for (int c = 0; c < kKeys; c += 32) tc::ld32(x + c, s_at + c);
-      tc::wait_ld();
-      float* v = reinterpret_cast<float*>(x);
-      const int t0 = tile_of(j) * kKeys;
-      if (!(t0 + kKeys - 1 <= first && (t0 >= last_low || t0 + kKeys <= my_sinks))) {
-        auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; };
+        for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
+        return;
+      }
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at);
+      auto two = [&](int i) {
+        return a.out_dtype == 1 ? pack_f16(o[i] * f, o[i + 1] * f) : pack_bf16(o[i] * f, o[i + 1] * f);
+      };
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 32) {
-          const int at = t0 + c;
-          const uint32_t see = below(pos + 1 - at) & (~below(my_low - at) | below(my_sinks - at));
+      for (int i = 0; i < 4; ++i) dst[i] = make_uint4(two(8 * i), two(8 * i + 2), two(8 * i + 4), two(8 * i + 6));
+    };
+    auto row_at = [&](int tile, int row) {  // element index of a live row's first channel
+      const int tok = row / G;
+      return ((static_cast<int64_t>(row0) + unit.first + tile * per_tile + tok) * a.num_q_heads + g * G + (row - tok * G)) * D;
+    };
+    if (C == 1) {
+      if (t < ntiles) {
+        const float f = l > 0.f ? 1.f / l : 0.f;
+        const int64_t at = row_at(t, r);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[c + i] = (see >> i) & 1u ? v[c + i] : kNegInf;
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tc::ld32(o, o_at + c);
+          tc::wait_ld();
+          if (l == 0.f) {  // no visible token: whatever tensor memory holds
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
+          if (live) store_row(at + c, reinterpret_cast<const float*>(o), f);
         }
       }
-      float top[4] = {v[0], v[1], v[2], v[3]};
+    } else {
+      // The cluster's rows: each CTA scales its part to the rows' common maximum
+      // and leaves it in its shared memory; CTA r adds up rows r, r + C, ...
+      float2* state = reinterpret_cast<float2*>(smem + SM::kRowState);
+      float* rows = reinterpret_cast<float*>(smem + SM::kRowsAt);
+      __syncthreads();  // the tiles are no longer read
+      state[tid] = make_float2(m, l);
+      cluster_sync();
+      auto remote = [&](uint32_t addr, int from) {
+        float2 v;
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(v.x), "=f"(v.y)
+                     : "r"(cluster_map(addr, from))
+                     : "memory");
+        return v;
+      };
+      if (t < ntiles) {
+        float top = kNegInf, sum = 0.f;
+        for (int k = 0; k < C; ++k) top = fmaxf(top, remote(smem_u32(state + tid), k).x);
+        const float ref = top == kNegInf ? 0.f : top;
+        for (int k = 0; k < C; ++k) {
+          const float2 v = remote(smem_u32(state + tid), k);
+          sum += v.y * ex2_approx((v.x - ref) * a.scale_log2);
+        }
+        const float f = l > 0.f ? ex2_approx((m - ref) * a.scale_log2) / sum : 0.f;
 #pragma unroll
-      for (int i = 4; i < kKeys; i += 8) {
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tc::ld32(o, o_at + c);
+          tc::wait_ld();
+          // Rotated by the row, so that a warp's stores meet different banks.
 #pragma unroll
-        for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], fmaxf(v[i + k], i + 4 + k < kKeys ? v[i + 4 + k] : v[i + k]));
-      }
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      const bool raise = mx > m + grow;  // a first one counts: m is -infinity
-      if (__any_sync(kFull, raise)) {
-        const float mn = raise ? mx : m;
-        const float f = raise ? ex2_approx((m - mn) * sl2) : 1.f;  // 0 for a first one
-        l *= f;
-        m = mn;
-        if (j > 0) {  // O is at rest: its last product came before these scores
-#pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tc::ld32(o, o_at + c);
-            tc::wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tc::st32(o_at + c, o);
+          for (int i = 0; i < 32; i += 4) {
+            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (l > 0.f)
+              w = make_float4(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f, __uint_as_float(o[i + 2]) * f,
+                              __uint_as_float(o[i + 3]) * f);
+            *reinterpret_cast<float4*>(rows + tid * D + ((c + i + 4 * r) & (D - 1))) = w;
           }
         }
       }
-      const float shift = m == kNegInf ? 0.f : kUp - m * sl2;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < kKeys; i += 4) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[i + k] = ex2_approx(fmaf(v[i + k], sl2, shift));
-          sum[k] += v[i + k];
+      cluster_sync();
+      // 4 channels a thread, D / 4 threads a row.
+      const int rows_in = ntiles * kRows, width = D / 4;
+      for (int e = tid; e < rows_in / C * width; e += 2 * kRows) {
+        const int row = (e / width) * C + rank, ch = 4 * (e % width);
+        const int tile = row / kRows, in = row & (kRows - 1), tok = in / G;
+        if (tok >= per_tile || tile * per_tile + tok >= tokens) continue;
+        const uint32_t addr = smem_u32(rows + row * D + ((ch + 4 * in) & (D - 1)));
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < C; ++k) {
+          float4 v;
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                       : "r"(cluster_map(addr, k))
+                       : "memory");
+          sum.x += v.x;
+          sum.y += v.y;
+          sum.z += v.z;
+          sum.w += v.w;
         }
-        x[i / 2] = BF16 ? pack_bf16(v[i], v[i + 1]) : pack_f16(v[i], v[i + 1]);
-        x[i / 2 + 1] = BF16 ? pack_bf16(v[i + 2], v[i + 3]) : pack_f16(v[i + 2], v[i + 3]);
+        const int64_t at = row_at(tile, in) + ch;
+        store_out(a.out, at, sum.x, a.out_dtype);
+        store_out(a.out, at + 1, sum.y, a.out_dtype);
+        store_out(a.out, at + 2, sum.z, a.out_dtype);
+        store_out(a.out, at + 3, sum.w, a.out_dtype);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tc::st32(s_at, x);
-      tc::st32(s_at + 32, x + 32);
-      tc::wait_st();
-      tc::fence_before();
-      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_bar + 8 * t) : "memory");
+      cluster_sync();  // no CTA leaves while its rows are read
     }
-    if (cnt > 0 && ok) ok = __all_sync(kFull, wait(o_bar + 8 * t, 0));
-    tc::fence_after();
-  }
-
-  // ------------------------------------------------------------------- rows
-  auto store_row = [&](int64_t at, const float* o, float f) {  // 32 channels
-    if (a.out_dtype == 0) {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
-      return;
-    }
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at);
-    auto two = [&](int i) {
-      return a.out_dtype == 1 ? pack_f16(o[i] * f, o[i + 1] * f) : pack_bf16(o[i] * f, o[i + 1] * f);
-    };
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dst[i] = make_uint4(two(8 * i), two(8 * i + 2), two(8 * i + 4), two(8 * i + 6));
-  };
-  auto row_at = [&](int tile, int row) {  // element index of a live row's first channel
-    const int tok = row / G;
-    return ((static_cast<int64_t>(row0) + unit.first + tile * per_tile + tok) * a.num_q_heads + g * G + (row - tok * G)) * D;
-  };
-  if (C == 1) {
-    if (warp < 8 && t < ntiles) {
-      const float f = l > 0.f ? 1.f / l : 0.f;
-      const int64_t at = row_at(t, r);
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        tc::ld32(o, o_at + c);
-        tc::wait_ld();
-        if (l == 0.f) {  // no visible token: whatever tensor memory holds
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0u;
-        }
-        if (live) store_row(at + c, reinterpret_cast<const float*>(o), f);
-      }
-    }
-  } else {
-    // The cluster's rows: each CTA scales its part to the rows' common maximum
-    // and leaves it in its shared memory; CTA r adds up rows r, r + C, ...
-    float2* state = reinterpret_cast<float2*>(smem + SM::kRowState);
-    float* rows = reinterpret_cast<float*>(smem + SM::kRowsAt);
-    __syncthreads();  // the tiles are no longer read
-    if (warp < 8) state[tid] = make_float2(m, l);
-    cluster_sync();
-    auto remote = [&](uint32_t addr, int from) {
-      float2 v;
-      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                   : "=f"(v.x), "=f"(v.y)
-                   : "r"(cluster_map(addr, from))
-                   : "memory");
-      return v;
-    };
-    if (warp < 8 && t < ntiles) {
-      float top = kNegInf, sum = 0.f;
-      for (int k = 0; k < C; ++k) top = fmaxf(top, remote(smem_u32(state + tid), k).x);
-      const float ref = top == kNegInf ? 0.f : top;
-      for (int k = 0; k < C; ++k) {
-        const float2 v = remote(smem_u32(state + tid), k);
-        sum += v.y * ex2_approx((v.x - ref) * a.scale_log2);
-      }
-      const float f = l > 0.f ? ex2_approx((m - ref) * a.scale_log2) / sum : 0.f;
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        tc::ld32(o, o_at + c);
-        tc::wait_ld();
-        // Rotated by the row, so that a warp's stores meet different banks.
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (l > 0.f)
-            w = make_float4(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f, __uint_as_float(o[i + 2]) * f,
-                            __uint_as_float(o[i + 3]) * f);
-          *reinterpret_cast<float4*>(rows + tid * D + ((c + i + 4 * r) & (D - 1))) = w;
-        }
-      }
-    }
-    cluster_sync();
-    // 4 channels a thread, D / 4 threads a row.
-    const int rows_in = ntiles * kRows, width = D / 4;
-    for (int e = tid; e < rows_in / C * width; e += kThreads) {
-      const int row = (e / width) * C + rank, ch = 4 * (e % width);
-      const int tile = row / kRows, in = row & (kRows - 1), tok = in / G;
-      if (tok >= per_tile || tile * per_tile + tok >= tokens) continue;
-      const uint32_t addr = smem_u32(rows + row * D + ((ch + 4 * in) & (D - 1)));
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < C; ++k) {
-        float4 v;
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                     : "r"(cluster_map(addr, k))
-                     : "memory");
-        sum.x += v.x;
-        sum.y += v.y;
-        sum.z += v.z;
-        sum.w += v.w;
-      }
-      const int64_t at = row_at(tile, in) + ch;
-      store_out(a.out, at, sum.x, a.out_dtype);
-      store_out(a.out, at + 1, sum.y, a.out_dtype);
-      store_out(a.out, at + 2, sum.z, a.out_dtype);
-      store_out(a.out, at + 3, sum.w, a.out_dtype);
-    }
-    cluster_sync();  // no CTA leaves while its rows are read
   }
   tc::fence_before();
   __syncthreads();
