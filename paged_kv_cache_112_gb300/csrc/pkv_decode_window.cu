@@ -43,6 +43,10 @@ struct Visible {
     skip = max(0, low / kTile - head);
     count = (L + kTile - 1) / kTile - skip;
   }
+  // Whether tiles [T, T + n) are neighbours in the list (n is 1 or 2) and wholly visible.
+  __device__ __forceinline__ bool all(int T, int n, int L) const {
+    return (T + n) * kTile <= L && (T * kTile >= low || (T + n) * kTile <= sinks);
+  }
   __device__ __forceinline__ int tile(int j) const { return j < head ? j : j + skip; }
   // Bit r: token 16 T + r is visible.
   __device__ __forceinline__ uint32_t mask(int T, int L) const {
@@ -51,11 +55,11 @@ struct Visible {
   }
 };
 
-// POOL: 16 or 4 bits.  Warps a CTA NW, stages a warp NST.
-template <int D, bool BF16, int POOL, int NW, int NST>
+// POOL: 16 or 4 bits.  Warps a CTA NW, stages a warp NST; a stage is NT tiles.
+template <int D, int POOL, int NW, int NST, int NT>
 struct Ring {
   static constexpr int kTileBytes = POOL == 4 ? fp4::Record<D>::kBytes : kTile * D * 2;
-  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStageBytes = 2 * NT * kTileBytes;
   static constexpr int kState = 8 * (D + 4) + 16;  // a warp's saved state: 8 rows, running max and sum of each head
   static constexpr int kWarpBytes = NST * kStageBytes > kState * 4 ? NST * kStageBytes : kState * 4;
   static constexpr size_t kInboxAt = static_cast<size_t>(NW) * (kWarpBytes + 8 * NST);
@@ -71,15 +75,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+template <int POOL>
+constexpr int kTilesAStep = POOL == 4 ? 2 : 1;
+
 template <int D, bool BF16, int POOL, int NW, int NST>
 __global__ void __launch_bounds__(NW * 32) decode_window_kernel(const DecodeArgs a, const WindowArgs wa,
                                                                 const __grid_constant__ CUtensorMap tmap_k,
                                                                 const __grid_constant__ CUtensorMap tmap_v) {
-  using R = Ring<D, BF16, POOL, NW, NST>;
+  constexpr int NT = kTilesAStep<POOL>;
+  using R = Ring<D, POOL, NW, NST, NT>;
   using Att = std::conditional_t<POOL == 4, WarpAttentionFp4<D>, WarpAttention<D, BF16, true>>;
-  constexpr int kRow = D + 4;              // floats between a saved state's head rows
-  constexpr int NT = POOL == 4 ? 2 : 1;    // tiles a step
-  static_assert(NST * 16 <= 64 && NST % NT == 0, "stage masks; whole steps");
+  constexpr int kRow = D + 4;  // floats between a saved state's head rows
   extern __shared__ __align__(1024) uint8_t smem[];
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   if (C > 1) cluster_arrive();  // see the wait before the merge
@@ -95,7 +101,7 @@ __global__ void __launch_bounds__(NW * 32) decode_window_kernel(const DecodeArgs
   const int G = a.group;
   const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
   const int tshift = a.block_shift - 4;         // log2 of tiles per block
-  const int W = C * NW, w0 = rank * NW + warp;  // this warp's tiles of the list: w0, w0 + W, ...
+  const int W = C * NW, w0 = rank * NW + warp;  // this warp's steps of NT tiles of the list: w0, w0 + W, ...
 
   const int L = clamp_len(a, a.context_lens[s], part == 0 && g == 0 && rank == 0 && threadIdx.x == 0);
   const int nparts = wa.window > 0 ? 1 : max(1, (L + a.partition_size - 1) / a.partition_size);
@@ -103,13 +109,14 @@ __global__ void __launch_bounds__(NW * 32) decode_window_kernel(const DecodeArgs
   const Visible vis(L, wa.window > 0 ? wa.window : L, wa.sinks);
   const int tile0 = wa.window > 0 ? 0 : part * (a.partition_size / kTile);
   const int tiles = wa.window > 0 ? vis.count : min(vis.count - tile0, a.partition_size / kTile);
-  const int cnt = tiles > w0 ? (tiles - w0 + W - 1) / W : 0;
-  auto tile_of = [&](int i) { return vis.tile(tile0 + i * W + w0); };
-  // The table entry of the warp's tile i.
-  auto fetch = [&](int i) {
-    if (i >= cnt) return -1;
-    const int b = tile_of(i) >> tshift;  // below max_blocks_per_seq: L is clamped to the table
-    return __ldg(tbl + b);
+  const int steps = (tiles + NT - 1) / NT, cnt = steps > w0 ? (steps - w0 + W - 1) / W : 0;
+  auto tile_of = [&](int i, int u) { return vis.tile(tile0 + (i * W + w0) * NT + u); };
+  auto there = [&](int i, int u) { return u == 0 || (i * W + w0) * NT + u < tiles; };  // the last step may be short
+  // The table entry of the warp's tile n (tile n % NT of its step n / NT).
+  auto fetch = [&](int n) {
+    const int i = n / NT, u = n % NT;
+    if (i >= cnt || !there(i, u)) return -1;
+    return __ldg(tbl + (tile_of(i, u) >> tshift));  // below max_blocks_per_seq: L is clamped to the table
   };
 
   uint8_t* mine = smem + static_cast<size_t>(warp) * R::kWarpBytes;
@@ -122,36 +129,38 @@ __global__ void __launch_bounds__(NW * 32) decode_window_kernel(const DecodeArgs
   __syncwarp();
   // Lane j holds the table entry of the warp's tile j of a chunk of 32.
   int cur = fetch(lane), ahead = fetch(32 + lane);
-  uint64_t stage_mask = 0;  // 16 bits a stage: rows of its tile that count
-  auto issue = [&](int j) {
-    if ((j & 31) == 0 && j > 0) {
+  uint32_t bad = 0;  // bit st * NT + u: tile u in stage st came from an unusable entry
+  // Lane 2u + kv issues the copy of tile u's K or V.
+  auto issue = [&](int i) {
+    if (((i * NT) & 31) == 0 && i > 0) {
       cur = ahead;
-      ahead = fetch(j + 32 + lane);
+      ahead = fetch(i * NT + 32 + lane);
     }
-    const int st = j % NST, T = tile_of(j);
-    int phys = __shfl_sync(kFull, cur, j & 31);
-    uint32_t m = vis.mask(T, L);
-    if (static_cast<unsigned>(phys) >= static_cast<unsigned>(a.num_blocks)) {
-      if (lane == 0) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK; the tile is masked
-      phys = 0;
-      m = 0;
+    const int st = i % NST, u = (lane >> 1) % NT, kv = lane & 1;
+    int phys = __shfl_sync(kFull, cur, (i * NT + u) & 31);
+    const uint32_t bar = bars + 8 * st;
+    const bool copies = lane < 2 * NT && there(i, u), usable = static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks);
+    const uint32_t n = __popc(__ballot_sync(kFull, copies && usable));
+    uint32_t broken = __ballot_sync(kFull, copies && !usable && kv == 0);
+    bad &= ~(((1u << NT) - 1u) << (st * NT));
+    if (broken) {  // such a tile is left out
+      if (lane == 0) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK
+#pragma unroll
+      for (int v = 0; v < NT; ++v)
+        if ((broken >> (2 * v)) & 1u) bad |= 1u << (st * NT + v);
     }
-    stage_mask = (stage_mask & ~(0xffffull << (16 * st))) | (static_cast<uint64_t>(m) << (16 * st));
-    if (lane != 0) return;
-    const uint32_t bar = bars + 8 * st, dst = buf + st * R::kStageBytes;
-    const int in_block = T & ((1 << tshift) - 1);
-    mbar_arrive_expect_tx(bar, R::kStageBytes);
-    if constexpr (POOL == 4) {
-      const int64_t at = phys * a.block_stride + ((static_cast<int64_t>(g) << tshift) + in_block) * R::kTileBytes;
-      bulk_load(dst, wa.k4 + at, R::kTileBytes, bar);
-      bulk_load(dst + R::kTileBytes, wa.v4 + at, R::kTileBytes, bar);
-    } else {
-      tma_tile<D>(dst, &tmap_k, in_block * kTile, g, phys, bar);
-      tma_tile<D>(dst + R::kTileBytes, &tmap_v, in_block * kTile, g, phys, bar);
-    }
+    if (lane == 0) mbar_arrive_expect_tx(bar, n * R::kTileBytes);
+    __syncwarp();
+    if (!copies || !usable) return;
+    const int T = tile_of(i, u), in_block = T & ((1 << tshift) - 1);
+    const uint32_t dst = buf + st * R::kStageBytes + (2 * u + kv) * R::kTileBytes;
+    if constexpr (POOL == 4)
+      bulk_load(dst, (kv ? wa.v4 : wa.k4) + phys * a.block_stride + ((static_cast<int64_t>(g) << tshift) + in_block) * R::kTileBytes,
+                R::kTileBytes, bar);
+    else
+      tma_tile<D>(dst, kv ? &tmap_v : &tmap_k, in_block * kTile, g, phys, bar);
   };
   auto wait = [&](int i) { return mbar_wait_bounded(bars + 8 * (i % NST), (i / NST) & 1, a.timeout_ns); };
-  auto mask_of = [&](int j) { return static_cast<uint32_t>(stage_mask >> (16 * (j % NST))) & 0xffffu; };
 
   Att at;
   at.reset();
@@ -165,34 +174,36 @@ __global__ void __launch_bounds__(NW * 32) decode_window_kernel(const DecodeArgs
   } else {
     at.load_q(q0, G, lane);
   }
-  for (int i = 0; i < cnt; i += NT) {
-    const int n = min(NT, cnt - i);
-    bool ok = true;
-#pragma unroll
-    for (int u = 0; u < NT; ++u)
-      if (u < n) ok = ok && wait(i + u);
-    if (!__all_sync(kFull, ok)) {
+  for (int i = 0; i < cnt; ++i) {
+    if (!__all_sync(kFull, wait(i))) {
       for (int j = i; j < min(cnt, i + NST); ++j) wait(j);  // copies in flight land before the warp goes on
       if (lane == 0) flag(a.dev_status, 16u);               // PKV_DEV_ERR_TIMEOUT; the output is undefined
       break;
     }
-    if constexpr (POOL == 4) {
-      uint32_t sK[NT], m[NT];
+    const int st = i % NST, T0 = tile_of(i, 0);
+    const uint32_t stage = buf + st * R::kStageBytes, broken = (bad >> (st * NT)) & ((1u << NT) - 1u);
+    // Whole tiles, side by side, each token visible: no masks.
+    const bool plain = vis.all(T0, NT, L) && !broken && there(i, NT - 1);
+    uint32_t m[NT], sK[NT];
 #pragma unroll
-      for (int u = 0; u < NT; ++u) {  // a missing second tile reuses the first one's stage, no token counts
-        const int j = u < n ? i + u : i;
-        sK[u] = buf + (j % NST) * R::kStageBytes;
-        m[u] = u < n ? mask_of(j) : 0u;
-      }
-      at.template tiles<NT>(sK, m, sl2, lane);
+    for (int u = 0; u < NT; ++u) {
+      sK[u] = stage + 2 * u * R::kTileBytes;
+      m[u] = 0xffffu;
+    }
+    if (!plain) {
+#pragma unroll
+      for (int u = 0; u < NT; ++u) m[u] = there(i, u) && !((broken >> u) & 1u) ? vis.mask(tile_of(i, u), L) : 0u;
+    }
+    if constexpr (POOL == 4) {
+      if (plain)
+        at.template tiles<NT, false>(sK, m, sl2, lane);
+      else
+        at.template tiles<NT, true>(sK, m, sl2, lane);
     } else {
-      const uint32_t sK = buf + (i % NST) * R::kStageBytes, m = mask_of(i);
-      if (m) at.template tile<true>(sK, sK + R::kTileBytes, static_cast<int>(m), sl2, lane);
+      if (m[0]) at.template tile<true>(stage, stage + R::kTileBytes, static_cast<int>(m[0]), sl2, lane);
     }
     __syncwarp();
-#pragma unroll
-    for (int u = 0; u < NT; ++u)
-      if (i + NST + u < cnt) issue(i + NST + u);
+    if (i + NST < cnt) issue(i + NST);
   }
   at.finish_sums();
 
@@ -314,8 +325,8 @@ __global__ void __launch_bounds__(NW * 32) decode_window_kernel(const DecodeArgs
 // The kernel with NW warps a CTA, and what launching it in clusters of C takes.
 template <int D, bool BF16, int POOL, int NW>
 struct Launch {
-  static constexpr int NST = POOL == 4 ? 4 : D == 64 ? 3 : 2;
-  using R = Ring<D, BF16, POOL, NW, NST>;
+  static constexpr int NST = POOL == 4 ? 2 : D == 64 ? 3 : 2;
+  using R = Ring<D, POOL, NW, NST, kTilesAStep<POOL>>;
   static constexpr auto kernel = decode_window_kernel<D, BF16, POOL, NW, NST>;
 
   // Clusters of C that the current device holds at a time (a cluster stays

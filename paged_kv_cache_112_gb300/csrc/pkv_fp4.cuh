@@ -56,11 +56,11 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 
 }  // namespace fp4
 
@@ -86,7 +86,8 @@ namespace dev {
 template <int D>
 struct WarpAttentionFp4 : SoftmaxState<D / 16> {
   static constexpr int KT = D / 16;
-  static constexpr float kWeightUp = 16384.f;
+  static constexpr float kWeightUpLog2 = 14.f;
+  static constexpr float kWeightUp = 1.f;  // of the accumulator against the sum
   using Rec = fp4::Record<D>;
   using Base = SoftmaxState<KT>;
   using Base::acc;
@@ -161,10 +162,12 @@ struct WarpAttentionFp4 : SoftmaxState<D / 16> {
       r[0] = lds32(addr);
   }
 
-  // NT tiles at once: K records at sK[t], V records Rec::kBytes further, bit r
-  // of mask[t] set where token r counts (the others are masked whatever they
-  // hold), sl2 = log2(e) * softmax scale * the head's K scale.
-  template <int NT>
+  // NT tiles at once: K records at sK[t], V records Rec::kBytes further.  With
+  // MASKED, bit r of mask[t] is set where token r counts (the others are left
+  // out whatever they hold); without, every token does.  sl2 = log2(e) *
+  // softmax scale * the head's K scale.  The weights' factor of 2^14 is in the
+  // sums too, so it cancels.
+  template <int NT, bool MASKED>
   __device__ __forceinline__ void tiles(const uint32_t (&sK)[NT], const uint32_t (&mask)[NT], float sl2, int lane) {
     const int gr = lane >> 2, tq = lane & 3;
     const int tok = (gr >> 1) + 4 * (gr & 1);
@@ -191,58 +194,82 @@ struct WarpAttentionFp4 : SoftmaxState<D / 16> {
       for (int j = 0; j < 4; ++j) c[t][0][j] = c[t][1][j] = 0.f;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      uint32_t s[2][D / 64];  // scales of rows tok, tok + 8: of the lane's groups, twice
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t f = fp4::e4m3x2_to_f16(ks[t][r]);
-        s[r][0] = __byte_perm(f, f, 0x1010);
-        if constexpr (D == 128) s[r][1] = __byte_perm(f, f, 0x3232);
-      }
+      const __half2 s0 = fp4::as_half2(fp4::e4m3x2_to_f16(ks[t][0])), s1 = fp4::as_half2(fp4::e4m3x2_to_f16(ks[t][1]));
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
         uint32_t x[4], y[4];
         fp4::e2m1x8_to_f16(kw[t][0][w], x);
         fp4::e2m1x8_to_f16(kw[t][1][w], y);
+        const __half2 f0 = w < 2 ? __low2half2(s0) : __high2half2(s0), f1 = w < 2 ? __low2half2(s1) : __high2half2(s1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // k-step 2w + h
-          const uint32_t s0 = s[0][w / 2], s1 = s[1][w / 2];
-          const uint32_t a[4] = {fp4::mul_f16x2(x[2 * h], s0), fp4::mul_f16x2(y[2 * h], s1),
-                                 fp4::mul_f16x2(x[2 * h + 1], s0), fp4::mul_f16x2(y[2 * h + 1], s1)};
+          const uint32_t a[4] = {fp4::mul_f16x2(x[2 * h], f0), fp4::mul_f16x2(y[2 * h], f1),
+                                 fp4::mul_f16x2(x[2 * h + 1], f0), fp4::mul_f16x2(y[2 * h + 1], f1)};
           mma_16816<false>(c[t][h], a, qf[2 * w + h][0], qf[2 * w + h][1]);
         }
       }
     }
     // V: tokens tq, tq + 4, tq + 8, tq + 12, dims [D/8 gr, + D/8).
-    uint32_t vw[NT][4][VW], vs[NT][2];
+    uint32_t vw[NT][4][VW], vs[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const uint32_t sV = sK[t] + Rec::kBytes;
-      uint32_t b[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         lds<VW>(vw[t][r], sV + (tq + 4 * r) * Rec::kRowBytes + gr * (D / 16));
-        b[r] = lds8(sV + Rec::kScalesAt + (tq + 4 * r) * Rec::kRowScales + (D == 128 ? gr : gr >> 1));
+        vs[t][r] = lds8(sV + Rec::kScalesAt + (tq + 4 * r) * Rec::kRowScales + (D == 128 ? gr : gr >> 1));
         // A token that does not count may hold anything: its scale is 0.
-        if (!((mask[t] >> (tq + 4 * r)) & 1u)) b[r] = 0u;
+        if (MASKED && !((mask[t] >> (tq + 4 * r)) & 1u)) vs[t][r] = 0u;
       }
-      vs[t][0] = fp4::e4m3x2_to_f16(b[0] | (b[1] << 8));
-      vs[t][1] = fp4::e4m3x2_to_f16(b[2] | (b[3] << 8));
     }
-    float sc[4 * NT], p[4 * NT];
+    float sc[NT][4];
     const float fa = sl2 * up_a, fb = sl2 * up_b;
+    float mx_a = kNegInf, mx_b = kNegInf;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const bool lo = (mask[t] >> tok) & 1u, hi = (mask[t] >> (tok + 8)) & 1u;
-      sc[4 * t] = lo ? (c[t][0][0] + c[t][1][0]) * fa : kNegInf;
-      sc[4 * t + 1] = lo ? (c[t][0][1] + c[t][1][1]) * fb : kNegInf;
-      sc[4 * t + 2] = hi ? (c[t][0][2] + c[t][1][2]) * fa : kNegInf;
-      sc[4 * t + 3] = hi ? (c[t][0][3] + c[t][1][3]) * fb : kNegInf;
+      const bool lo = !MASKED || ((mask[t] >> tok) & 1u), hi = !MASKED || ((mask[t] >> (tok + 8)) & 1u);
+      sc[t][0] = lo ? (c[t][0][0] + c[t][1][0]) * fa : kNegInf;
+      sc[t][1] = lo ? (c[t][0][1] + c[t][1][1]) * fb : kNegInf;
+      sc[t][2] = hi ? (c[t][0][2] + c[t][1][2]) * fa : kNegInf;
+      sc[t][3] = hi ? (c[t][0][3] + c[t][1][3]) * fb : kNegInf;
+      mx_a = fmaxf(fmaxf(mx_a, sc[t][0]), sc[t][2]);
+      mx_b = fmaxf(fmaxf(mx_b, sc[t][1]), sc[t][3]);
     }
-    this->template online_update_lazy<NT>(sc, p);
+    // The shift follows the running maximum only where a score lies above it
+    // (most steps of a long history leave it alone): no exchange between the
+    // lanes otherwise.
+    if (__any_sync(kFull, (mx_a > this->m_a) | (mx_b > this->m_b))) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        mx_a = fmaxf(mx_a, __shfl_xor_sync(kFull, mx_a, o));
+        mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, o));
+      }
+      const float mn_a = fmaxf(this->m_a, mx_a), mn_b = fmaxf(this->m_b, mx_b);
+      const float al_a = mn_a > this->m_a ? ex2_approx(this->m_a - mn_a) : 1.f;  // m = -inf: 0
+      const float al_b = mn_b > this->m_b ? ex2_approx(this->m_b - mn_b) : 1.f;
+      this->l_a *= al_a;
+      this->l_b *= al_b;
+#pragma unroll
+      for (int mt = 0; mt < KT; ++mt) {
+        acc[mt][0] *= al_a;
+        acc[mt][1] *= al_b;
+        acc[mt][2] *= al_a;
+        acc[mt][3] *= al_b;
+      }
+      this->m_a = mn_a;
+      this->m_b = mn_b;
+    }
+    const float u_a = this->m_a == kNegInf ? 0.f : this->m_a - kWeightUpLog2;
+    const float u_b = this->m_b == kNegInf ? 0.f : this->m_b - kWeightUpLog2;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const uint32_t p0 = movmatrix_trans(pack_f16(p[4 * t] * kWeightUp, p[4 * t + 1] * kWeightUp));
-      const uint32_t p1 = movmatrix_trans(pack_f16(p[4 * t + 2] * kWeightUp, p[4 * t + 3] * kWeightUp));
+      const float q0 = ex2_approx(sc[t][0] - u_a), q1 = ex2_approx(sc[t][1] - u_b);
+      const float q2 = ex2_approx(sc[t][2] - u_a), q3 = ex2_approx(sc[t][3] - u_b);
+      this->l_a += q0 + q2;
+      this->l_b += q1 + q3;
+      const uint32_t p0 = movmatrix_trans(pack_f16(q0, q1)), p1 = movmatrix_trans(pack_f16(q2, q3));
+      const __half2 s0 = fp4::as_half2(fp4::e4m3x2_to_f16(__byte_perm(vs[t][0], vs[t][1], 0x0040)));
+      const __half2 s1 = fp4::as_half2(fp4::e4m3x2_to_f16(__byte_perm(vs[t][2], vs[t][3], 0x0040)));
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
         constexpr uint32_t kLow = 0x0f0f0f0fu;
@@ -255,8 +282,8 @@ struct WarpAttentionFp4 : SoftmaxState<D / 16> {
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {  // M-tile 4w + j: rows gr, gr + 8 are dims D/8 gr + 2 (4w + j), + 1
-          const uint32_t a[4] = {fp4::mul_f16x2(x[0][j], vs[t][0]), fp4::mul_f16x2(x[1][j], vs[t][0]),
-                                 fp4::mul_f16x2(x[2][j], vs[t][1]), fp4::mul_f16x2(x[3][j], vs[t][1])};
+          const uint32_t a[4] = {fp4::mul_f16x2(x[0][j], s0), fp4::mul_f16x2(x[1][j], s0),
+                                 fp4::mul_f16x2(x[2][j], s1), fp4::mul_f16x2(x[3][j], s1)};
           mma_16816<false>(acc[4 * w + j], a, p0, p1);
         }
       }
