@@ -13,8 +13,8 @@
 //
 // A cluster of C CTAs of NW warps serves one (s, g, partition).  The visible
 // 16-token tiles are dealt to its warps in turn; each streams its tiles
-// through a private ring of bulk copies (16 bits: TMA boxes; 4 bits: one
-// record for K and one for V) and keeps its own online-softmax state on the
+// through a private ring of copies (16 bits: TMA boxes; 4 bits: records, by
+// asynchronous copies of 16 bytes a lane) and keeps its own online-softmax state on the
 // tensor cores.  The states meet in shared memory, first a CTA's, then through
 // distributed shared memory the cluster's.  Windows need no workspace then;
 // partitions write the partial records that the reduce kernel merges.
@@ -43,10 +43,6 @@ struct Visible {
     skip = max(0, low / kTile - head);
     count = (L + kTile - 1) / kTile - skip;
   }
-  // Whether tiles [T, T + n) are neighbours in the list (n is 1 or 2) and wholly visible.
-  __device__ __forceinline__ bool all(int T, int n, int L) const {
-    return (T + n) * kTile <= L && (T * kTile >= low || (T + n) * kTile <= sinks);
-  }
   __device__ __forceinline__ int tile(int j) const { return j < head ? j : j + skip; }
   // Bit r: token 16 T + r is visible.
   __device__ __forceinline__ uint32_t mask(int T, int L) const {
@@ -69,10 +65,13 @@ struct Ring {
   static_assert(POOL == 4 || kWarpBytes % 1024 == 0, "TMA tiles sit on 1024-byte boundaries");
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the last N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int POOL>
@@ -110,102 +109,137 @@ __global__ void __launch_bounds__(NW * 32) decode_window_kernel(const DecodeArgs
   const int tile0 = wa.window > 0 ? 0 : part * (a.partition_size / kTile);
   const int tiles = wa.window > 0 ? vis.count : min(vis.count - tile0, a.partition_size / kTile);
   const int steps = (tiles + NT - 1) / NT, cnt = steps > w0 ? (steps - w0 + W - 1) / W : 0;
-  auto tile_of = [&](int i, int u) { return vis.tile(tile0 + (i * W + w0) * NT + u); };
-  auto there = [&](int i, int u) { return u == 0 || (i * W + w0) * NT + u < tiles; };  // the last step may be short
-  // The table entry of the warp's tile n (tile n % NT of its step n / NT).
+  // The place in the list of tile n of the warp (tile n % NT of its step n / NT).
+  auto place = [&](int n) { return (n / NT * W + w0) * NT + n % NT; };
+  // Its table entry: the physical block, or -1: none there, or unusable and left out.
   auto fetch = [&](int n) {
-    const int i = n / NT, u = n % NT;
-    if (i >= cnt || !there(i, u)) return -1;
-    return __ldg(tbl + (tile_of(i, u) >> tshift));  // below max_blocks_per_seq: L is clamped to the table
+    const int j = place(n);
+    if (n >= cnt * NT || j >= tiles) return -1;
+    const int phys = __ldg(tbl + (vis.tile(tile0 + j) >> tshift));  // inside the table: L is clamped to it
+    if (static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks)) return phys;
+    flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK
+    return -1;
   };
-
   uint8_t* mine = smem + static_cast<size_t>(warp) * R::kWarpBytes;
-  const uint32_t buf = smem_u32(mine), bars = smem_u32(smem + static_cast<size_t>(NW) * R::kWarpBytes) + 8 * NST * warp;
-  if (lane == 0) {
-    for (int st = 0; st < NST; ++st) mbar_init(bars + 8 * st, 1);
-    fence_barrier_init();
-    fence_proxy_async_smem();
-  }
-  __syncwarp();
-  // Lane j holds the table entry of the warp's tile j of a chunk of 32.
-  int cur = fetch(lane), ahead = fetch(32 + lane);
-  uint32_t bad = 0;  // bit st * NT + u: tile u in stage st came from an unusable entry
-  // Lane 2u + kv issues the copy of tile u's K or V.
-  auto issue = [&](int i) {
-    if (((i * NT) & 31) == 0 && i > 0) {
-      cur = ahead;
-      ahead = fetch(i * NT + 32 + lane);
-    }
-    const int st = i % NST, u = (lane >> 1) % NT, kv = lane & 1;
-    int phys = __shfl_sync(kFull, cur, (i * NT + u) & 31);
-    const uint32_t bar = bars + 8 * st;
-    const bool copies = lane < 2 * NT && there(i, u), usable = static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks);
-    const uint32_t n = __popc(__ballot_sync(kFull, copies && usable));
-    uint32_t broken = __ballot_sync(kFull, copies && !usable && kv == 0);
-    bad &= ~(((1u << NT) - 1u) << (st * NT));
-    if (broken) {  // such a tile is left out
-      if (lane == 0) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK
-#pragma unroll
-      for (int v = 0; v < NT; ++v)
-        if ((broken >> (2 * v)) & 1u) bad |= 1u << (st * NT + v);
-    }
-    if (lane == 0) mbar_arrive_expect_tx(bar, n * R::kTileBytes);
-    __syncwarp();
-    if (!copies || !usable) return;
-    const int T = tile_of(i, u), in_block = T & ((1 << tshift) - 1);
-    const uint32_t dst = buf + st * R::kStageBytes + (2 * u + kv) * R::kTileBytes;
-    if constexpr (POOL == 4)
-      bulk_load(dst, (kv ? wa.v4 : wa.k4) + phys * a.block_stride + ((static_cast<int64_t>(g) << tshift) + in_block) * R::kTileBytes,
-                R::kTileBytes, bar);
-    else
-      tma_tile<D>(dst, kv ? &tmap_v : &tmap_k, in_block * kTile, g, phys, bar);
-  };
-  auto wait = [&](int i) { return mbar_wait_bounded(bars + 8 * (i % NST), (i / NST) & 1, a.timeout_ns); };
-
+  const uint32_t buf = smem_u32(mine);
+  const uint16_t* q0 = a.q + (static_cast<int64_t>(s) * a.num_q_heads + g * G) * D;
+  float sl2 = a.scale_log2, post = 1.f;
+  uint32_t gone = 0;  // bit st * NT + u: tile u of stage st is not there
   Att at;
   at.reset();
-  for (int j = 0; j < min(cnt, NST); ++j) issue(j);
-  const uint16_t* q0 = a.q + (static_cast<int64_t>(s) * a.num_q_heads + g * G) * D;
-  float sl2 = a.scale_log2, post = 1.f / Att::kWeightUp;
   if constexpr (POOL == 4) {
-    at.template load_q<BF16>(q0, G, lane);
+    // Records by 16-byte asynchronous copies of all lanes: a warp's addresses
+    // differ by the lane alone, and a step is waited for without a barrier.
+    // (Bulk copies take their operands from uniform registers: some 20
+    // instructions to issue one, 40 a tile of the 370 there were.)
+    const int per_block = static_cast<int>(a.block_stride / R::kTileBytes);
+    auto record = [&](int n) {  // the tile's record in the pool, or -1
+      const int phys = fetch(n);
+      return phys < 0 ? -1 : phys * per_block + (g << tshift) + (vis.tile(tile0 + place(n)) & ((1 << tshift) - 1));
+    };
+    const uint8_t* k4 = wa.k4 + 16 * lane;
+    const uint8_t* v4 = wa.v4 + 16 * lane;
+    // Lane j holds the record of the warp's tile j of a chunk of 32.
+    int cur = record(lane), ahead = record(32 + lane);
+    auto issue = [&](int i) {
+      if (((i * NT) & 31) == 0 && i > 0) {
+        cur = ahead;
+        ahead = record(i * NT + 32 + lane);
+      }
+      const int st = i % NST;
+      gone &= ~(((1u << NT) - 1u) << (st * NT));
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        const int rec = __shfl_sync(kFull, cur, (i * NT + u) & 31);
+        if (rec < 0) {
+          gone |= 1u << (st * NT + u);
+          continue;
+        }
+        const int64_t off = static_cast<int64_t>(rec) * R::kTileBytes;
+        const uint32_t dst = buf + st * R::kStageBytes + 2 * u * R::kTileBytes + 16 * lane;
+#pragma unroll
+        for (int c = 0; c < R::kTileBytes; c += 512)
+          if (c + 512 <= R::kTileBytes || c + 16 * lane < R::kTileBytes) {
+            copy16(dst + c, k4 + off + c);
+            copy16(dst + R::kTileBytes + c, v4 + off + c);
+          }
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < NST; ++i) {
+      if (i < cnt) issue(i);
+      copies_commit();
+    }
     if (a.k_scale) sl2 *= __ldg(a.k_scale + g);
     if (a.v_scale) post *= __ldg(a.v_scale + g);
+    at.template load_q<BF16>(q0, G, lane, sl2);
+    // Places in the list between which every token is visible: [0, plain_first) and [plain_from, plain_to).
+    const int plain_first = vis.sinks / kTile, plain_from = vis.head + ((vis.low & (kTile - 1)) ? 1 : 0);
+    const int plain_to = L / kTile - vis.skip;
+    for (int i = 0; i < cnt; ++i) {
+      copies_wait<NST - 1>();
+      __syncwarp();
+      const int st = i % NST, j = place(i * NT), jj = tile0 + j;
+      const uint32_t absent = (gone >> (st * NT)) & ((1u << NT) - 1u);
+      uint32_t m[NT], sK[NT];
+#pragma unroll
+      for (int u = 0; u < NT; ++u) sK[u] = buf + st * R::kStageBytes + 2 * u * R::kTileBytes;
+      if (absent == 0 && jj + NT <= plain_to && (jj >= plain_from || jj + NT <= plain_first)) {
+        at.template tiles<NT, false>(sK, m, lane);
+      } else {
+#pragma unroll
+        for (int u = 0; u < NT; ++u) m[u] = (absent >> u) & 1u ? 0u : vis.mask(vis.tile(jj + u), L);
+        at.template tiles<NT, true>(sK, m, lane);
+      }
+      __syncwarp();
+      if (i + NST < cnt) issue(i + NST);
+      copies_commit();
+    }
+    copies_wait<0>();
+    at.finish();
   } else {
-    at.load_q(q0, G, lane);
-  }
-  for (int i = 0; i < cnt; ++i) {
-    if (!__all_sync(kFull, wait(i))) {
-      for (int j = i; j < min(cnt, i + NST); ++j) wait(j);  // copies in flight land before the warp goes on
-      if (lane == 0) flag(a.dev_status, 16u);               // PKV_DEV_ERR_TIMEOUT; the output is undefined
-      break;
-    }
-    const int st = i % NST, T0 = tile_of(i, 0);
-    const uint32_t stage = buf + st * R::kStageBytes, broken = (bad >> (st * NT)) & ((1u << NT) - 1u);
-    // Whole tiles, side by side, each token visible: no masks.
-    const bool plain = vis.all(T0, NT, L) && !broken && there(i, NT - 1);
-    uint32_t m[NT], sK[NT];
-#pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      sK[u] = stage + 2 * u * R::kTileBytes;
-      m[u] = 0xffffu;
-    }
-    if (!plain) {
-#pragma unroll
-      for (int u = 0; u < NT; ++u) m[u] = there(i, u) && !((broken >> u) & 1u) ? vis.mask(tile_of(i, u), L) : 0u;
-    }
-    if constexpr (POOL == 4) {
-      if (plain)
-        at.template tiles<NT, false>(sK, m, sl2, lane);
-      else
-        at.template tiles<NT, true>(sK, m, sl2, lane);
-    } else {
-      if (m[0]) at.template tile<true>(stage, stage + R::kTileBytes, static_cast<int>(m[0]), sl2, lane);
+    const uint32_t bars = smem_u32(smem + static_cast<size_t>(NW) * R::kWarpBytes) + 8 * NST * warp;
+    if (lane == 0) {
+      for (int st = 0; st < NST; ++st) mbar_init(bars + 8 * st, 1);
+      fence_barrier_init();
+      fence_proxy_async_smem();
     }
     __syncwarp();
-    if (i + NST < cnt) issue(i + NST);
+    // Lane j holds the table entry of the warp's tile j of a chunk of 32.
+    int cur = fetch(lane), ahead = fetch(32 + lane);
+    auto issue = [&](int i) {
+      if ((i & 31) == 0 && i > 0) {
+        cur = ahead;
+        ahead = fetch(i + 32 + lane);
+      }
+      const int st = i % NST;
+      const int phys = __shfl_sync(kFull, cur, i & 31);
+      gone = (gone & ~(1u << st)) | (phys < 0 ? 1u << st : 0u);
+      if (lane != 0) return;
+      const uint32_t bar = bars + 8 * st, dst = buf + st * R::kStageBytes;
+      const int row0 = (vis.tile(tile0 + place(i)) & ((1 << tshift) - 1)) * kTile;
+      mbar_arrive_expect_tx(bar, R::kStageBytes);
+      tma_tile<D>(dst, &tmap_k, row0, g, max(phys, 0), bar);
+      tma_tile<D>(dst + R::kTileBytes, &tmap_v, row0, g, max(phys, 0), bar);
+    };
+    auto wait = [&](int i) { return mbar_wait_bounded(bars + 8 * (i % NST), (i / NST) & 1, a.timeout_ns); };
+    for (int i = 0; i < min(cnt, NST); ++i) issue(i);
+    at.load_q(q0, G, lane);
+    for (int i = 0; i < cnt; ++i) {
+      if (!__all_sync(kFull, wait(i))) {
+        for (int j = i; j < min(cnt, i + NST); ++j) wait(j);  // copies in flight land before the warp goes on
+        if (lane == 0) flag(a.dev_status, 16u);               // PKV_DEV_ERR_TIMEOUT; the output is undefined
+        break;
+      }
+      const uint32_t stage = buf + (i % NST) * R::kStageBytes;
+      const uint32_t m = (gone >> (i % NST)) & 1u ? 0u : vis.mask(vis.tile(tile0 + place(i)), L);
+      if (m) at.template tile<true>(stage, stage + R::kTileBytes, static_cast<int>(m), sl2, lane);
+      __syncwarp();
+      if (i + NST < cnt) issue(i + NST);
+    }
+    at.finish_sums();
+    post = 1.f / Att::kWeightUp;
   }
-  at.finish_sums();
 
   // Save this warp's state: rows [8][kRow], running max [8], running sum [8].
   {

@@ -71,9 +71,8 @@ namespace dev {
 //
 // A value is code * scale: two significant bits times four, at most 2688 and
 // a multiple of 2^-10, so the f16 product that enters the MMA is exact.  The
-// softmax weights enter as one f16 part (2^-12 of the weight at most; times
-// 2^14, so that small ones keep it): the values are themselves rounded by
-// up to 2^-3.
+// softmax weights enter as one f16 part (off by 2^-11 of the weight at most):
+// the values are themselves rounded by up to 2^-3.
 //
 // Order of the fragments: within an MMA, channels, tokens and output dims may
 // be permuted as long as both operands agree.  Lane (gr, tq) takes channels
@@ -86,18 +85,22 @@ namespace dev {
 template <int D>
 struct WarpAttentionFp4 : SoftmaxState<D / 16> {
   static constexpr int KT = D / 16;
-  static constexpr float kWeightUpLog2 = 14.f;
-  static constexpr float kWeightUp = 1.f;  // of the accumulator against the sum
   using Rec = fp4::Record<D>;
   using Base = SoftmaxState<KT>;
   using Base::acc;
   uint32_t qf[KT][2];  // f16x2: q[head gr][D/4 tq + 4kk + {0,1}] and {2,3}
-  float up_a, up_b;    // the powers of two by which heads 2tq and 2tq + 1 were scaled down
+  float fa, fb;          // log2 units a product with heads 2tq and 2tq + 1
+  float grow_a, grow_b;  // kGrow in products
+  // Weights lie up to 2^kGrow above the reference m and enter the product
+  // times 2^kUp: below 2^15, and f16's floor of 2^-25 is 2^-33 of the largest
+  // weight at most.
+  static constexpr float kGrow = 7.f, kUp = 8.f;
 
-  // The group's query rows (heads >= G read as 0).  bf16 queries become f16
-  // with a power of two per head, from its largest finite |q|.
+  // The group's query rows (heads >= G read as 0), the sign of sl2 = log2(e) *
+  // softmax scale * the head's K scale with them.  bf16 queries become f16 with
+  // a power of two per head, from its largest finite |q|.
   template <bool QBF16>
-  __device__ __forceinline__ void load_q(const uint16_t* qhead0, int G, int lane) {
+  __device__ __forceinline__ void load_q(const uint16_t* qhead0, int G, int lane, float sl2) {
     const int gr = lane >> 2, tq = lane & 3;
     const bool live = gr < G;
     const uint4* src = reinterpret_cast<const uint4*>(qhead0 + (live ? gr : 0) * D + D / 4 * tq);
@@ -136,8 +139,18 @@ struct WarpAttentionFp4 : SoftmaxState<D / 16> {
       qf[kk][0] = w[2 * kk];
       qf[kk][1] = w[2 * kk + 1];
     }
-    up_a = __shfl_sync(kFull, down, 8 * tq);
-    up_b = __shfl_sync(kFull, down, 8 * tq + 4);
+    const uint32_t flip = sl2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int kk = 0; kk < KT; ++kk) {
+      qf[kk][0] ^= flip;
+      qf[kk][1] ^= flip;
+    }
+    // A factor of 0 would make a masked score 0 times infinity.
+    const float mag = fmaxf(fabsf(sl2), 1e-30f);
+    fa = fmaxf(mag * __shfl_sync(kFull, down, 8 * tq), 1e-36f);
+    fb = fmaxf(mag * __shfl_sync(kFull, down, 8 * tq + 4), 1e-36f);
+    grow_a = kGrow / fa;
+    grow_b = kGrow / fb;
   }
 
   __device__ __forceinline__ static uint32_t lds32(uint32_t addr) {
@@ -164,11 +177,10 @@ struct WarpAttentionFp4 : SoftmaxState<D / 16> {
 
   // NT tiles at once: K records at sK[t], V records Rec::kBytes further.  With
   // MASKED, bit r of mask[t] is set where token r counts (the others are left
-  // out whatever they hold); without, every token does.  sl2 = log2(e) *
-  // softmax scale * the head's K scale.  The weights' factor of 2^14 is in the
-  // sums too, so it cancels.
+  // out whatever they hold); without, every token does.  m_a and m_b are in
+  // products, not in log2 units, until finish().
   template <int NT, bool MASKED>
-  __device__ __forceinline__ void tiles(const uint32_t (&sK)[NT], const uint32_t (&mask)[NT], float sl2, int lane) {
+  __device__ __forceinline__ void tiles(const uint32_t (&sK)[NT], const uint32_t (&mask)[NT], int lane) {
     const int gr = lane >> 2, tq = lane & 3;
     const int tok = (gr >> 1) + 4 * (gr & 1);
     constexpr int KW = D / 32, VW = D / 64;  // words of a lane's codes a K row and a V row
@@ -187,11 +199,7 @@ struct WarpAttentionFp4 : SoftmaxState<D / 16> {
           ks[t][r] = lds8(at + tq);
         }
       }
-    float c[NT][2][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c[t][0][j] = c[t][1][j] = 0.f;
+    float c[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const __half2 s0 = fp4::as_half2(fp4::e4m3x2_to_f16(ks[t][0])), s1 = fp4::as_half2(fp4::e4m3x2_to_f16(ks[t][1]));
@@ -205,7 +213,10 @@ struct WarpAttentionFp4 : SoftmaxState<D / 16> {
         for (int h = 0; h < 2; ++h) {  // k-step 2w + h
           const uint32_t a[4] = {fp4::mul_f16x2(x[2 * h], f0), fp4::mul_f16x2(y[2 * h], f1),
                                  fp4::mul_f16x2(x[2 * h + 1], f0), fp4::mul_f16x2(y[2 * h + 1], f1)};
-          mma_16816<false>(c[t][h], a, qf[2 * w + h][0], qf[2 * w + h][1]);
+          if (w + h == 0)
+            mma_16816_first(c[t], a, qf[0][0], qf[0][1]);
+          else
+            mma_16816<false>(c[t], a, qf[2 * w + h][0], qf[2 * w + h][1]);
         }
       }
     }
@@ -222,31 +233,27 @@ struct WarpAttentionFp4 : SoftmaxState<D / 16> {
         if (MASKED && !((mask[t] >> (tq + 4 * r)) & 1u)) vs[t][r] = 0u;
       }
     }
-    float sc[NT][4];
-    const float fa = sl2 * up_a, fb = sl2 * up_b;
     float mx_a = kNegInf, mx_b = kNegInf;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const bool lo = !MASKED || ((mask[t] >> tok) & 1u), hi = !MASKED || ((mask[t] >> (tok + 8)) & 1u);
-      sc[t][0] = lo ? (c[t][0][0] + c[t][1][0]) * fa : kNegInf;
-      sc[t][1] = lo ? (c[t][0][1] + c[t][1][1]) * fb : kNegInf;
-      sc[t][2] = hi ? (c[t][0][2] + c[t][1][2]) * fa : kNegInf;
-      sc[t][3] = hi ? (c[t][0][3] + c[t][1][3]) * fb : kNegInf;
-      mx_a = fmaxf(fmaxf(mx_a, sc[t][0]), sc[t][2]);
-      mx_b = fmaxf(fmaxf(mx_b, sc[t][1]), sc[t][3]);
+      if constexpr (MASKED) {
+        if (!((mask[t] >> tok) & 1u)) c[t][0] = c[t][1] = kNegInf;
+        if (!((mask[t] >> (tok + 8)) & 1u)) c[t][2] = c[t][3] = kNegInf;
+      }
+      mx_a = fmaxf(fmaxf(mx_a, c[t][0]), c[t][2]);
+      mx_b = fmaxf(fmaxf(mx_b, c[t][1]), c[t][3]);
     }
-    // The shift follows the running maximum only where a score lies above it
-    // (most steps of a long history leave it alone): no exchange between the
-    // lanes otherwise.
-    if (__any_sync(kFull, (mx_a > this->m_a) | (mx_b > this->m_b))) {
+    // The reference follows the running maximum only where a score lies more
+    // than kGrow above it: few steps exchange maxima and scale the sums.
+    if (__any_sync(kFull, (mx_a > this->m_a + grow_a) | (mx_b > this->m_b + grow_b))) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         mx_a = fmaxf(mx_a, __shfl_xor_sync(kFull, mx_a, o));
         mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, o));
       }
       const float mn_a = fmaxf(this->m_a, mx_a), mn_b = fmaxf(this->m_b, mx_b);
-      const float al_a = mn_a > this->m_a ? ex2_approx(this->m_a - mn_a) : 1.f;  // m = -inf: 0
-      const float al_b = mn_b > this->m_b ? ex2_approx(this->m_b - mn_b) : 1.f;
+      const float al_a = mn_a > this->m_a ? ex2_approx((this->m_a - mn_a) * fa) : 1.f;  // m = -inf: 0
+      const float al_b = mn_b > this->m_b ? ex2_approx((this->m_b - mn_b) * fb) : 1.f;
       this->l_a *= al_a;
       this->l_b *= al_b;
 #pragma unroll
@@ -259,12 +266,12 @@ struct WarpAttentionFp4 : SoftmaxState<D / 16> {
       this->m_a = mn_a;
       this->m_b = mn_b;
     }
-    const float u_a = this->m_a == kNegInf ? 0.f : this->m_a - kWeightUpLog2;
-    const float u_b = this->m_b == kNegInf ? 0.f : this->m_b - kWeightUpLog2;
+    const float u_a = this->m_a == kNegInf ? 0.f : kUp - this->m_a * fa;
+    const float u_b = this->m_b == kNegInf ? 0.f : kUp - this->m_b * fb;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const float q0 = ex2_approx(sc[t][0] - u_a), q1 = ex2_approx(sc[t][1] - u_b);
-      const float q2 = ex2_approx(sc[t][2] - u_a), q3 = ex2_approx(sc[t][3] - u_b);
+      const float q0 = ex2_approx(fmaf(c[t][0], fa, u_a)), q1 = ex2_approx(fmaf(c[t][1], fb, u_b));
+      const float q2 = ex2_approx(fmaf(c[t][2], fa, u_a)), q3 = ex2_approx(fmaf(c[t][3], fb, u_b));
       this->l_a += q0 + q2;
       this->l_b += q1 + q3;
       const uint32_t p0 = movmatrix_trans(pack_f16(q0, q1)), p1 = movmatrix_trans(pack_f16(q2, q3));
@@ -288,6 +295,13 @@ struct WarpAttentionFp4 : SoftmaxState<D / 16> {
         }
       }
     }
+  }
+
+  // The sums of all lanes; the maxima in log2 units.
+  __device__ __forceinline__ void finish() {
+    this->finish_sums();
+    this->m_a *= fa;
+    this->m_b *= fb;
   }
 };
 

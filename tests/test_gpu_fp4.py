@@ -219,7 +219,8 @@ class Decode:
             blocks = self.tables[i, :-(-L // self.B)]
             k, v = (x[blocks].reshape(-1, *x.shape[2:])[:L] for x in self.vals)
             want, extra = R.attend(q[i], k, v, self.scale, R.visible(L - 1, L, window, sinks))
-            far = R.bound(want, extra, self.D, L, self.weights, STEP[self.out.dtype])
+            far = R.bound(want, extra, self.D, L, self.weights, STEP[self.out.dtype],
+                          2.0 ** -33 if self.bits == 4 else 2.0 ** -39)
             assert np.all(np.abs(got[i] - want) <= far), (i, L, np.nanmax(np.abs(got[i] - want) / far))
 
 
@@ -391,7 +392,7 @@ def test_serving_loop_with_graph_replay():
             for got, w, f in ((out, 0, 0), (win, 20, 3)):
                 n = len(vals[0])
                 want, extra = R.attend(q[s].double().cpu().numpy(), *vals, D ** -0.5, R.visible(n - 1, n, w, f))
-                far = R.bound(want, extra, D, n, 2.0 ** -11, 2.0 ** -8)
+                far = R.bound(want, extra, D, n, 2.0 ** -11, 2.0 ** -8, 2.0 ** -33)
                 assert np.all(np.abs(got[s].double().cpu().numpy() - want) <= far)
 
 

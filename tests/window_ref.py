@@ -88,8 +88,8 @@ def bound(out, extra, D, n, weights, out_step, floor=2.0 ** -39):
     by twice that relative to the row's sum, by 2^-21 for its exponential and by `weights` for the type that holds
     it; sums of n tokens lose at most n 2^-23 (and the rows' merging as much again); the row is rounded once.
     Where f16 holds the weights, times 2^14, its subnormals' half step of 2^-25 is 2^-39 of the largest weight: a
-    weight far below the largest is off by that absolutely, which matters where the largest one's value is 0 (prompts:
-    `floor` 2^-32, times 2^7)."""
+    weight far below the largest is off by that absolutely, which matters where the largest one's value is 0 (`floor`:
+    prompts hold them times 2^7, 2^-32; 4-bit pools times 2^8, 2^-33)."""
     mass, total, terms = extra
     rel = 4 * (D + 8) * 2.0 ** -23 * terms[:, None] + 2.0 ** -20 + weights + 4 * (n + 64) * 2.0 ** -23
     return mass * rel + total * floor + np.abs(out) * out_step + 1e-30
