@@ -60,6 +60,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// The bits of a where m has ones, those of b elsewhere.
+__device__ __forceinline__ uint32_t select(uint32_t a, uint32_t b, uint32_t m) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xe4;" : "=r"(r) : "r"(a), "r"(b), "r"(m));
+  return r;
+}
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 
 }  // namespace fp4
@@ -284,8 +290,8 @@ struct WarpAttentionFp4 : SoftmaxState<D / 16> {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t A = vw[t][2 * h][w], B = vw[t][2 * h + 1][w];
-          fp4::e2m1x8_to_f16((A & kLow) | ((B << 4) & ~kLow), x[2 * h]);
-          fp4::e2m1x8_to_f16(((A >> 4) & kLow) | (B & ~kLow), x[2 * h + 1]);
+          fp4::e2m1x8_to_f16(fp4::select(A, B << 4, kLow), x[2 * h]);
+          fp4::e2m1x8_to_f16(fp4::select(A >> 4, B, kLow), x[2 * h + 1]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {  // M-tile 4w + j: rows gr, gr + 8 are dims D/8 gr + 2 (4w + j), + 1

@@ -17,9 +17,10 @@
 //                      registers; P goes back over S as 16-bit pairs;
 //     O += P V         tcgen05.mma, P from tensor memory.
 // Warps 0 to 3 and 4 to 7 are the threads of the two tiles: while one tile's
-// are at the exponentials, the tensor cores work on the other's products.  Warp
-// 8 loads: TMA boxes of a block's rows of a head, scattered by the block table,
-// into a ring of K and V tiles.  Warp 9 issues the products.
+// are at the exponentials, the tensor cores work on the other's products.
+// Warps 8 and 10 load K and V: TMA boxes of a block's rows of a head, scattered
+// by the block table, into a ring of tiles; warp 11 passes a tile on, once it
+// has zeroed what nobody sees of it; a thread of warp 9 issues the products.
 //
 // m is raised, and O scaled in tensor memory, only when the row's maximum has
 // grown by more than 2^8 since: weights up to 2^8 do as well (a weight is
@@ -40,7 +41,7 @@ using namespace dev;
 
 constexpr int kRows = 128;     // query rows a tile
 constexpr int kKeys = 128;     // history tokens a tile
-constexpr int kThreads = 384;  // two tiles' threads; the loading warp, the issuing warp and two that only wait
+constexpr int kThreads = 384;  // two tiles' threads, and four warps that load, pass on and multiply
 // Registers: 168 a thread at launch; the tiles' threads hold a row of scores.
 constexpr int kRowRegs = 208, kOtherRegs = 80;
 static_assert(256 * kRowRegs + 128 * kOtherRegs <= 384 * 168, "shares of the launch's registers");
@@ -56,8 +57,9 @@ struct Smem {
   static constexpr int kRowState = 0;                   // the cluster's meeting, over the tiles: max and sum of 256 rows,
   static constexpr int kRowsAt = 2048;                  // then [256][D] floats
   static constexpr int kBars = kRing + kSlots * kTileBytes;
-  // full[kSlots], empty[kSlots], q, s[2], p[2], o[2], drain; bad blocks of each slot, tensor memory, abort, unit
-  static constexpr int kBytes = kBars + 8 * (2 * kSlots + 8) + 4 * kSlots + 64;
+  // full[kSlots], ready[kSlots], empty[kSlots], q, s[2], p[2][2], o[2], drain; bad blocks of each slot, tensor
+  // memory, abort, unit
+  static constexpr int kBytes = kBars + 8 * (3 * kSlots + 10) + 4 * kSlots + 64;
   static_assert(kRowsAt + 2 * kRows * D * 4 <= kBars, "the cluster's rows fit over the tiles");
 };
 
@@ -79,9 +81,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const uint32_t base = smem_u32(smem);
-  const uint32_t full = base + SM::kBars, empty = full + 8 * NS, q_bar = empty + 8 * NS, s_bar = q_bar + 8,
-                 p_bar = s_bar + 16, o_bar = p_bar + 16, drain_bar = o_bar + 16;
-  uint32_t* bad_blocks = reinterpret_cast<uint32_t*>(smem + SM::kBars + 8 * (2 * NS + 8));
+  const uint32_t full = base + SM::kBars, ready = full + 8 * NS, empty = ready + 8 * NS, q_bar = empty + 8 * NS,
+                 s_bar = q_bar + 8, p_bar = s_bar + 16, o_bar = p_bar + 32, drain_bar = o_bar + 16;
+  uint32_t* bad_blocks = reinterpret_cast<uint32_t*>(smem + SM::kBars + 8 * (3 * NS + 10));
   volatile uint32_t* tmem_at = bad_blocks + NS;
   volatile uint32_t* abort_at = tmem_at + 1;
   Unit* unit_at = reinterpret_cast<Unit*>(bad_blocks + NS + 2);
@@ -131,12 +133,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
       *abort_at = 0;
       for (int i = 0; i < NS; ++i) {
         mbar_init(full + 8 * i, 1);
+        mbar_init(ready + 8 * i, 1);
         mbar_init(empty + 8 * i, 1);
       }
       mbar_init(q_bar, 1);
       for (int t = 0; t < 2; ++t) {
         mbar_init(s_bar + 8 * t, 1);
-        mbar_init(p_bar + 8 * t, kRows);
+        mbar_init(p_bar + 16 * t, kRows);
+        mbar_init(p_bar + 16 * t + 8, kRows);
         mbar_init(o_bar + 8 * t, 1);
       }
       mbar_init(drain_bar, 1);
@@ -194,107 +198,110 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
   };
 
   if (warp >= 8) {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-   if (warp == 8) {
-    // ---------------------------------------------------------------- loads
-    const int B = 1 << a.block_shift, nblk = kKeys >> a.block_shift;  // blocks of a tile: 2 to 16, one a lane
-    const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
-    auto entry = [&](int j) {  // this lane's block of tile j: physical block, -1 where no row sees it, -2 outside the pool
-      if (j >= cnt || lane >= nblk) return -1;
-      const int t = tile_of(j) * kKeys + lane * B;
-      if (t > p1 || !(t + B > low || t < sinks)) return -1;
-      const int phys = __ldg(tbl + (t >> a.block_shift));
-      return static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks) ? phys : -2;
-    };
-    int phys = entry(0), issued = 0;
-    fence_proxy_async_smem();  // the search's sums lay where the queries go
-    if (lane == 0 && cnt > 0) {
-      mbar_arrive_expect_tx(q_bar, ntiles * NL * per_tile * G * 128);
-      for (int t = 0; t < ntiles; ++t)
-        for (int l = 0; l < NL; ++l)
-          tma_load_4d(base + t * SM::kTileBytes + l * SM::kLineBytes, &tmap_q, 0, l, g * G,
-                      row0 + unit.first + t * per_tile, q_bar);
-    }
-    bool ok = true;
-    for (int j = 0; j < cnt && ok; ++j) {
-      const uint32_t bad = __ballot_sync(kFull, phys == -2), n = __popc(__ballot_sync(kFull, phys >= 0));
-      if (bad && lane == 0) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK; the block counts as zeros
-      for (int kv = 0; kv < 2 && ok; ++kv) {
-        const int slot = issued % NS;
-        ok = __all_sync(kFull, wait(empty + 8 * slot, ((issued / NS) & 1) ^ 1));
-        if (!ok) break;
-        if (lane == 0) {
-          bad_blocks[slot] = bad;
-          mbar_arrive_expect_tx(full + 8 * slot, n * NL * B * 128);
-        }
-        __syncwarp();
-        if (phys >= 0) {
-          const uint32_t dst = base + SM::kRing + slot * SM::kTileBytes + lane * B * 128;
-#pragma unroll
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8 || warp == 10) {
+      // -------------------------------------------------------------- loads
+      // K tiles are 0, 2, 4, ... of the ring, V tiles 1, 3, 5, ...
+      const bool is_v = warp == 10;
+      const int B = 1 << a.block_shift, nblk = kKeys >> a.block_shift;  // blocks of a tile: 2 to 16, one a lane
+      const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
+      auto entry = [&](int j) {  // this lane's block of tile j: physical block, -1 where no row sees it, -2 outside the pool
+        if (j >= cnt || lane >= nblk) return -1;
+        const int t = tile_of(j) * kKeys + lane * B;
+        if (t > p1 || !(t + B > low || t < sinks)) return -1;
+        const int phys = __ldg(tbl + (t >> a.block_shift));
+        return static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks) ? phys : -2;
+      };
+      int phys = entry(0), j = 0;
+      fence_proxy_async_smem();  // the search's sums lay where the queries go
+      if (!is_v && cnt > 0 && tc::elect_one()) {
+        mbar_arrive_expect_tx(q_bar, ntiles * NL * per_tile * G * 128);
+        for (int t = 0; t < ntiles; ++t)
           for (int l = 0; l < NL; ++l)
-            tma_load_4d(dst + l * SM::kLineBytes, kv ? &tmap_v : &tmap_k, 0, 0, g * NL + l, phys, full + 8 * slot);
-        }
-        ++issued;
-      }
-      phys = entry(j + 1);
-    }
-    if (!ok) {  // copies in flight land before the CTA leaves
-      if (lane == 0) {
-        mbar_wait_bounded(q_bar, 0, a.timeout_ns);
-        for (int i = max(0, issued - NS); i < issued; ++i)
-          mbar_wait_bounded(full + 8 * (i % NS), (i / NS) & 1, a.timeout_ns);
+            tma_load_4d(base + t * SM::kTileBytes + l * SM::kLineBytes, &tmap_q, 0, l, g * G,
+                        row0 + unit.first + t * per_tile, q_bar);
       }
       __syncwarp();
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------- products
-    const uint32_t qk = tc::instr_desc(BF16, kKeys, false, pa.negate != 0), pv = tc::instr_desc(BF16, D, true, false);
-    auto slot_addr = [&](int i) { return base + SM::kRing + (i % NS) * SM::kTileBytes; };
-    // Tile i of the ring is there; rows that no row of queries sees, and (of K
-    // too) blocks outside the pool, are zeroed: their weights are zero, but
-    // what the pool holds there may be anything, and zero times NaN is NaN.
-    auto arrive = [&](int i, int j, bool is_v) {
-      if (!__all_sync(kFull, wait(full + 8 * (i % NS), (i / NS) & 1))) return false;
-      const uint32_t bad = bad_blocks[i % NS];
-      const int t0 = tile_of(j) * kKeys;
-      const bool edge = is_v && (t0 + kKeys - 1 > p1 || (t0 < low && t0 + kKeys > sinks));
-      if (bad || edge) {
-        const uint32_t at = slot_addr(i);
-        for (int r = lane; r < kKeys; r += 32) {
-          const int t = t0 + r;
-          const bool seen = t <= p1 && (t >= low || t < sinks);
-          if (((bad >> (r >> a.block_shift)) & 1u) || (is_v && !seen))
+      const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
+      for (; j < cnt; ++j) {
+        const uint32_t bad = __ballot_sync(kFull, phys == -2), there = __ballot_sync(kFull, phys >= 0);
+        if (bad && lane == 0) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK; the block counts as zeros
+        const int i = 2 * j + is_v, slot = i % NS;
+        const uint32_t bar = full + 8 * slot, dst = base + SM::kRing + slot * SM::kTileBytes;
+        if (!__all_sync(kFull, wait(empty + 8 * slot, ((i / NS) & 1) ^ 1))) break;
+        if (lane == 0) {
+          bad_blocks[slot] = bad;
+          mbar_arrive_expect_tx(bar, __popc(there) * NL * B * 128);
+        }
+        __syncwarp();
+        for (int k = 0; k < nblk; ++k) {
+          if (!((there >> k) & 1u)) continue;
+          const int block = __shfl_sync(kFull, phys, k);
+          if (tc::elect_one()) {
 #pragma unroll
             for (int l = 0; l < NL; ++l)
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + l * SM::kLineBytes + r * 128 + c * 16),
-                             "r"(0)
-                             : "memory");
+              tma_load_4d(dst + l * SM::kLineBytes + k * B * 128, map, 0, 0, g * NL + l, block, bar);
+          }
         }
-        fence_proxy_async_smem();
+        phys = entry(j + 1);
+      }
+      if (j < cnt && lane == 0) {  // copies in flight land before the CTA leaves
+        if (!is_v) mbar_wait_bounded(q_bar, 0, a.timeout_ns);
+        for (int k = max(0, j - NS); k < j; ++k) {
+          const int i = 2 * k + is_v;
+          if (i + NS > 2 * j + is_v) mbar_wait_bounded(full + 8 * (i % NS), (i / NS) & 1, a.timeout_ns);
+        }
+      }
+    } else if (warp == 11) {
+      // --------------------------------------------------------- what is there
+      // Rows that no row of queries sees and blocks outside the pool become
+      // zeros: their weights are zero, but what the pool holds there may be
+      // anything, and zero times NaN is NaN.
+      for (int i = 0; i < 2 * cnt; ++i) {
+        const int slot = i % NS;
+        const bool is_v = i & 1;
+        if (!__all_sync(kFull, wait(full + 8 * slot, (i / NS) & 1))) break;
+        const uint32_t bad = bad_blocks[slot];
+        const int t0 = tile_of(i >> 1) * kKeys;
+        const bool edge = is_v && (t0 + kKeys - 1 > p1 || (t0 < low && t0 + kKeys > sinks));
+        if (bad || edge) {
+          const uint32_t at = base + SM::kRing + slot * SM::kTileBytes;
+          for (int r = lane; r < kKeys; r += 32) {
+            const int t = t0 + r;
+            const bool seen = t <= p1 && (t >= low || t < sinks);
+            if (!((bad >> (r >> a.block_shift)) & 1u) && (!is_v || seen)) continue;
+            for (int c = 0; c < NL * 8; ++c)  // rotated by the row: other banks for other lanes
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                               at + (c >> 3) * SM::kLineBytes + r * 128 + ((c + r) & 7) * 16),
+                           "r"(0)
+                           : "memory");
+          }
+          fence_proxy_async_smem();
+        }
         __syncwarp();
+        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(ready + 8 * slot) : "memory");
       }
-      return true;
-    };
-    auto scores = [&](int t, int i) {  // S_t = Q_t K^T (lane 0)
-      const uint64_t qd = tc::smem_desc(base + t * SM::kTileBytes, 16, 1024), kd = tc::smem_desc(slot_addr(i), 16, 1024);
+    } else if (tc::elect_one()) {
+      // ----------------------------------------------------------- products
+      const uint32_t qk = tc::instr_desc(BF16, kKeys, false, pa.negate != 0), pv = tc::instr_desc(BF16, D, true, false);
+      auto slot_addr = [&](int i) { return base + SM::kRing + (i % NS) * SM::kTileBytes; };
+      auto arrive = [&](int i) { return wait(ready + 8 * (i % NS), (i / NS) & 1); };
+      auto scores = [&](int t, int i) {  // S_t = Q_t K^T
+        const uint64_t qd = tc::smem_desc(base + t * SM::kTileBytes, 16, 1024), kd = tc::smem_desc(slot_addr(i), 16, 1024);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = ((k / 4) * SM::kLineBytes + (k % 4) * 32) >> 4;
-        tc::mma_ss(tmem + t * kKeys, qd + off, kd + off, qk, k > 0);
-      }
-    };
-    auto output = [&](int t, int i, bool add) {  // O_t += P_t V
-      const uint64_t vd = tc::smem_desc(slot_addr(i), SM::kLineBytes, 1024);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k / 4) * SM::kLineBytes + (k % 4) * 32) >> 4;
+          tc::mma_ss(tmem + t * kKeys, qd + off, kd + off, qk, k > 0);
+        }
+      };
+      auto output = [&](int t, int i, int half, bool add) {  // O_t += P_t V, keys 64 half .. + 63
+        const uint64_t vd = tc::smem_desc(slot_addr(i), SM::kLineBytes, 1024);
 #pragma unroll
-      for (int k = 0; k < kKeys / 16; ++k)
-        tc::mma_ts(tmem + 256 + t * D, tmem + t * kKeys + 8 * k, vd + ((k * 2048) >> 4), pv, add || k > 0);
-    };
-    bool ok = cnt > 0;
-    if (ok) {
-      ok = __all_sync(kFull, wait(q_bar, 0)) && arrive(0, 0, false);
-      if (ok && lane == 0) {
+        for (int k = 4 * half; k < 4 * half + 4; ++k)
+          tc::mma_ts(tmem + 256 + t * D, tmem + t * kKeys + 8 * k, vd + ((k * 2048) >> 4), pv, add || k > 0);
+      };
+      bool ok = cnt > 0 && wait(q_bar, 0) && arrive(0);
+      if (ok) {
         tc::fence_after();
         for (int t = 0; t < ntiles; ++t) {
           scores(t, 0);
@@ -302,41 +309,37 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
         }
         tc::commit(empty);
       }
-      __syncwarp();
-    }
-    for (int j = 0; j < cnt && ok; ++j) {
-      const int vi = 2 * j + 1, ki = 2 * j + 2;
-      ok = arrive(vi, j, true) && (j + 1 == cnt || arrive(ki, j + 1, false));
-      for (int t = 0; t < ntiles && ok; ++t) {
-        ok = __all_sync(kFull, wait(p_bar + 8 * t, j & 1));
-        if (!ok) break;
-        if (lane == 0) {
+      for (int j = 0; j < cnt && ok; ++j) {
+        const int vi = 2 * j + 1, ki = 2 * j + 2;
+        ok = arrive(vi) && (j + 1 == cnt || arrive(ki));
+        for (int t = 0; t < ntiles && ok; ++t) {
+          ok = wait(p_bar + 16 * t, j & 1);
+          if (!ok) break;
           tc::fence_after();
-          output(t, vi, j > 0);
+          output(t, vi, 0, j > 0);
+          ok = wait(p_bar + 16 * t + 8, j & 1);
+          if (!ok) break;
+          tc::fence_after();
+          output(t, vi, 1, true);
           if (j + 1 < cnt) scores(t, ki);
           tc::commit(j + 1 < cnt ? s_bar + 8 * t : o_bar + 8 * t);
         }
-        __syncwarp();
+        if (ok) {
+          tc::commit(empty + 8 * (vi % NS));
+          if (j + 1 < cnt) tc::commit(empty + 8 * (ki % NS));
+        }
       }
-      if (ok && lane == 0) {
-        tc::commit(empty + 8 * (vi % NS));
-        if (j + 1 < cnt) tc::commit(empty + 8 * (ki % NS));
-      }
-      __syncwarp();
-    }
-    if (lane == 0) {  // every product has completed before tensor memory is freed
+      // Every product has completed before tensor memory is freed.
       tc::commit(drain_bar);
       mbar_wait_bounded(drain_bar, 0, a.timeout_ns);
     }
     __syncwarp();
-  }
-
-   if (C > 1) {  // the barriers of the cluster's meeting
-    __syncthreads();
-    cluster_sync();
-    cluster_sync();
-    cluster_sync();
-   }
+    if (C > 1) {  // the barriers of the cluster's meeting
+      __syncthreads();
+      cluster_sync();
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
     // -------------------------------------------------------------- softmax
@@ -407,19 +410,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
         const F2 scale2 = pair(sl2, sl2), shift2 = pair(shift, shift);
         F2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
-        for (int i = 0; i < kKeys; i += 2) {
-          const float2 e = halves(fma2(pair(v[i], v[i + 1]), scale2, shift2));
-          const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
-          sum[(i / 2) & 1] = add2(sum[(i / 2) & 1], pair(p0, p1));
-          x[i / 2] = BF16 ? pack_bf16(p0, p1) : pack_f16(p0, p1);
+        for (int half = 0; half < 2; ++half) {  // the product with V begins on the first half
+#pragma unroll
+          for (int i = 64 * half; i < 64 * half + 64; i += 2) {
+            const float2 e = halves(fma2(pair(v[i], v[i + 1]), scale2, shift2));
+            const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
+            sum[(i / 2) & 1] = add2(sum[(i / 2) & 1], pair(p0, p1));
+            x[i / 2] = BF16 ? pack_bf16(p0, p1) : pack_f16(p0, p1);
+          }
+          tc::st32(s_at + 32 * half, x + 32 * half);
+          tc::wait_st();
+          tc::fence_before();
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_bar + 16 * t + 8 * half) : "memory");
         }
         const float2 s0 = halves(sum[0]), s1 = halves(sum[1]);
         l += (s0.x + s0.y) + (s1.x + s1.y);
-        tc::st32(s_at, x);
-        tc::st32(s_at + 32, x + 32);
-        tc::wait_st();
-        tc::fence_before();
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_bar + 8 * t) : "memory");
       }
       if (cnt > 0 && ok) ok = __all_sync(kFull, wait(o_bar + 8 * t, 0));
       tc::fence_after();

@@ -8,6 +8,15 @@
 namespace pkv {
 namespace tc {
 
+// One thread of the warp, which the compiler knows to be alone in the branch:
+// operands of tensor and copy instructions then go to uniform registers once,
+// not in a loop over the lanes.  All lanes call together.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Tensor memory: 128 lanes of 512 32-bit columns a SM; an address is (lane
 // << 16) | column, and a warp reaches the 32 lanes of its rank modulo 4.
 __device__ __forceinline__ void alloc(uint32_t result, uint32_t columns) {  // one whole warp
