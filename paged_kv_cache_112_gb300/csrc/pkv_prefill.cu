@@ -9,18 +9,28 @@
 // Bound: the two products, 4 D flops a visible (query, head, token) on the
 // tensor cores; and next to them 32 exponentials a SM and cycle.
 //
-// A CTA owns two tiles of 128 query rows of one KV head: the group's G heads of
-// 128 / G tokens, rows ordered (token, head), so that K and V are read once for
-// the whole group.  It walks the visible 128-token tiles of the history:
+// A CTA works on two tiles of 128 query rows of one KV head: the group's G heads
+// of 128 / G tokens, rows ordered (token, head), so that K and V are read once
+// for the whole group.  It walks the visible 128-token tiles of the history:
 //     S = Q K^T        tcgen05.mma, both from shared memory, S in tensor memory;
 //     P = 2^(S - m)    one thread a row, the running maximum and sum in
-//                      registers; P goes back over S as 16-bit pairs;
+//                      registers; P goes back as 16-bit pairs;
 //     O += P V         tcgen05.mma, P from tensor memory.
 // Warps 0 to 3 and 4 to 7 are the threads of the two tiles: while one tile's
 // are at the exponentials, the tensor cores work on the other's products.
 // Warps 8 and 10 load K and V: TMA boxes of a block's rows of a head, scattered
 // by the block table, into a ring of tiles; warp 11 passes a tile on, once it
 // has zeroed what nobody sees of it; a thread of warp 9 issues the products.
+//
+// P overwrites the first half of S.  (With S of the next keys issued in halves,
+// one of them beside the exponentials, the products take 48 instructions an
+// iteration in place of 32, and the issuing thread is what everybody waits for:
+// 690 us for 8192 tokens instead of 400.)  Halves of 64 keys that no row of a
+// tile sees are left out.
+//
+// The grid has a CTA for each pair of tiles; those on the SMs take over the
+// others' work one after another (clusterlaunchcontrol), so that the next
+// pair's loads and first products run beside the last rows' stores.
 //
 // m is raised, and O scaled in tensor memory, only when the row's maximum has
 // grown by more than 2^8 since: weights up to 2^8 do as well (a weight is
@@ -43,7 +53,7 @@ constexpr int kRows = 128;     // query rows a tile
 constexpr int kKeys = 128;     // history tokens a tile
 constexpr int kThreads = 384;  // two tiles' threads, and four warps that load, pass on and multiply
 // Registers: 168 a thread at launch; the tiles' threads hold a row of scores.
-constexpr int kRowRegs = 208, kOtherRegs = 80;
+constexpr int kRowRegs = 216, kOtherRegs = 72;
 static_assert(256 * kRowRegs + 128 * kOtherRegs <= 384 * 168, "shares of the launch's registers");
 constexpr int kMaxCluster = 8;
 
@@ -52,19 +62,68 @@ struct Smem {
   static constexpr int kLines = D / 64;                 // 128-byte lines of a row
   static constexpr int kLineBytes = kRows * 128;        // one line of a tile's rows
   static constexpr int kTileBytes = kLines * kLineBytes;
-  static constexpr int kSlots = D == 128 ? 5 : 8;       // K and V tiles in flight
+  static constexpr int kSlots = D == 128 ? 4 : 8;       // K and V tiles in flight
   static constexpr int kRing = 2 * kTileBytes;          // after the two query tiles
   static constexpr int kRowState = 0;                   // the cluster's meeting, over the tiles: max and sum of 256 rows,
   static constexpr int kRowsAt = 2048;                  // then [256][D] floats
-  static constexpr int kBars = kRing + kSlots * kTileBytes;
-  // full[kSlots], ready[kSlots], empty[kSlots], q, s[2], p[2][2], o[2], drain; bad blocks of each slot, tensor
-  // memory, abort, unit
-  static constexpr int kBytes = kBars + 8 * (3 * kSlots + 10) + 4 * kSlots + 64;
-  static_assert(kRowsAt + 2 * kRows * D * 4 <= kBars, "the cluster's rows fit over the tiles");
+  static constexpr int kStage = kRing + kSlots * kTileBytes;  // 4 KB a warp: 32 rows of 128 bytes on their way out
+  static constexpr int kStolen = kStage + 8 * 4096;
+  static constexpr int kUnits = kStolen + 16;           // two units of work
+  static constexpr int kBars = kUnits + 64;
+  static constexpr int kBarCount = 3 * kSlots + 18;
+  static constexpr int kWords = kBars + 8 * kBarCount;  // what each slot holds, tensor memory, abort
+  static constexpr int kBytes = kWords + 4 * (kSlots + 2);
+  static_assert(kRowsAt + 2 * kRows * D * 4 <= kStage, "the cluster's rows fit over the tiles");
+  static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
+// A pair of tiles of one KV head.
 struct Unit {
-  int s, first, n;  // sequence, first new token of the pair of tiles, the sequence's new tokens; s < 0: none
+  int s, g;          // sequence (-1: no more units), KV head
+  int first, n;      // first new token of the pair, the sequence's new tokens
+  int row0, len;     // the sequence's first row, its length
+  int pad[2];
+};
+static_assert(sizeof(Unit) == 32, "two units in shared memory");
+
+// What the rows of a pair of tiles see.
+struct View {
+  int per_tile, tokens, ntiles;  // tokens a tile holds, of this pair, tiles with any
+  int p0, p1;                    // positions of the pair's first and last token
+  int window, sinks_all;
+  int low, sinks;                // some row sees [0, sinks) and [low, p1]
+  int head, skip, cnt;           // their tiles: [0, head), [head + skip, ..); this CTA's number of them
+  int C, rank;
+
+  __device__ __forceinline__ View(const Unit& u, const PrefillArgs& pa, int tile_tokens, int c, int r)
+      : per_tile(tile_tokens), window(pa.window), C(c), rank(r) {
+    tokens = min(2 * per_tile, u.n - u.first);
+    ntiles = tokens > per_tile ? 2 : 1;
+    p0 = u.len - u.n + u.first;
+    p1 = p0 + tokens - 1;
+    sinks_all = window > 0 ? pa.sinks : 0;
+    low = low_of(p0);
+    sinks = min(sinks_all, low);
+    head = (sinks + kKeys - 1) / kKeys;
+    skip = max(0, low / kKeys - head);
+    const int count = p1 >= 0 ? p1 / kKeys + 1 - skip : 0;
+    cnt = count > rank ? (count - rank + C - 1) / C : 0;
+  }
+  // The first token of the window at position p.
+  __device__ __forceinline__ int low_of(int p) const { return window > 0 ? max(0, p - window + 1) : 0; }
+  __device__ __forceinline__ int tile_of(int j) const {
+    const int i = j * C + rank;
+    return i < head ? i : i + skip;
+  }
+  __device__ __forceinline__ bool seen(int t) const { return t <= p1 && (t >= low || t < sinks); }
+  // The halves (bit h: keys 64 h .. + 63) of history tile j that some row of
+  // tile t (0, 1) sees.
+  __device__ __forceinline__ uint32_t halves_of(int t, int j) const {
+    const int first = p0 + t * per_tile, last = min(first + per_tile - 1, p1), lo = low_of(first);
+    const int t0 = tile_of(j) * kKeys, few = min(sinks_all, lo);
+    auto some = [&](int at) { return at <= last && (at + 64 > lo || at < few); };
+    return (some(t0) ? 1u : 0u) | (some(t0 + 64) ? 2u : 0u);
+  }
 };
 
 template <int D, bool BF16>
@@ -75,111 +134,54 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
   using SM = Smem<D>;
   constexpr int NS = SM::kSlots, NL = SM::kLines;
   extern __shared__ __align__(1024) uint8_t smem[];
-  griddep_wait();
-  griddep_launch_dependents();
   if (smem_misaligned(smem, a.dev_status)) return;  // the same for every CTA
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-  const uint32_t base = smem_u32(smem);
+  const uint32_t base = smem_u32(smem), stolen = base + SM::kStolen;
   const uint32_t full = base + SM::kBars, ready = full + 8 * NS, empty = ready + 8 * NS, q_bar = empty + 8 * NS,
-                 s_bar = q_bar + 8, p_bar = s_bar + 16, o_bar = p_bar + 32, drain_bar = o_bar + 16;
-  uint32_t* bad_blocks = reinterpret_cast<uint32_t*>(smem + SM::kBars + 8 * (3 * NS + 10));
-  volatile uint32_t* tmem_at = bad_blocks + NS;
+                 q_free = q_bar + 8, s_bar = q_free + 8, p_bar = s_bar + 16, o_bar = p_bar + 32, o_free = o_bar + 16,
+                 u_full = o_free + 16, u_empty = u_full + 16, steal_bar = u_empty + 16, drain_bar = steal_bar + 8;
+  volatile Unit* units = reinterpret_cast<volatile Unit*>(smem + SM::kUnits);
+  // Of each slot: bits 0 to 15 the tile's blocks outside the pool; K tiles: bits
+  // 16 + 2 t, 17 + 2 t the halves that tile t of the rows sees.
+  volatile uint32_t* holds = reinterpret_cast<volatile uint32_t*>(smem + SM::kWords);
+  volatile uint32_t* tmem_at = holds + NS;
   volatile uint32_t* abort_at = tmem_at + 1;
-  Unit* unit_at = reinterpret_cast<Unit*>(bad_blocks + NS + 2);
-  int* warp_sums = reinterpret_cast<int*>(smem);  // over the tiles, before any copy
+  const int G = a.group, per_tile = kRows / G;
 
-  // Which pair of tiles: units count ceil(n / pair) a sequence, the last ones
-  // (whose history is longest) first.
-  const int G = a.group, per_tile = kRows / G, per_pair = 2 * per_tile;
-  const int g = static_cast<int>((blockIdx.x / C) % a.num_kv_heads);
-  const int u = static_cast<int>((blockIdx.x / C) / a.num_kv_heads);
-  const int S = a.num_seqs;
-  auto range = [&](int s, int& lo) {  // new tokens of sequence s; its first row
-    lo = min(max(pa.query_start[s], 0), pa.num_tokens);
-    const int hi = min(max(pa.query_start[s + 1], lo), pa.num_tokens);
-    return hi - lo;
-  };
-  {
-    if (tid == 0) *unit_at = Unit{-1, 0, 0};
-    const int chunk = (S + kThreads - 1) / kThreads, b = min(S, tid * chunk), e = min(S, b + chunk);
-    int mine = 0, lo;
-    for (int s = b; s < e; ++s) mine += (range(s, lo) + per_pair - 1) / per_pair;
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += x;
+  if (tid == 0) {
+    *abort_at = 0;
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(ready + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
     }
-    if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
-    int before = incl - mine, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += warp_sums[w];
-      total += warp_sums[w];
+    mbar_init(q_bar, 1);
+    mbar_init(q_free, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(s_bar + 8 * t, 1);
+      mbar_init(p_bar + 16 * t, kRows);
+      mbar_init(p_bar + 16 * t + 8, kRows);
+      mbar_init(o_bar + 8 * t, 1);
+      mbar_init(o_free + 8 * t, kRows);
+      mbar_init(u_full + 8 * t, 1);
+      mbar_init(u_empty + 8 * t, 11);  // the eight warps of rows, the loading warps, the issuing thread
     }
-    const int want = total - 1 - u;
-    if (want >= before && want < before + mine) {
-      for (int s = b; s < e; ++s) {
-        const int n = range(s, lo), c = (n + per_pair - 1) / per_pair;
-        if (want < before + c) {
-          *unit_at = Unit{s, (want - before) * per_pair, n};
-          break;
-        }
-        before += c;
-      }
-    }
-    if (tid == 0) {
-      *abort_at = 0;
-      for (int i = 0; i < NS; ++i) {
-        mbar_init(full + 8 * i, 1);
-        mbar_init(ready + 8 * i, 1);
-        mbar_init(empty + 8 * i, 1);
-      }
-      mbar_init(q_bar, 1);
-      for (int t = 0; t < 2; ++t) {
-        mbar_init(s_bar + 8 * t, 1);
-        mbar_init(p_bar + 16 * t, kRows);
-        mbar_init(p_bar + 16 * t + 8, kRows);
-        mbar_init(o_bar + 8 * t, 1);
-      }
-      mbar_init(drain_bar, 1);
-      fence_barrier_init();
-      fence_proxy_async_smem();
-    }
-    __syncthreads();
+    mbar_init(steal_bar, 1);
+    mbar_init(drain_bar, 1);
+    fence_barrier_init();
+    fence_proxy_async_smem();
   }
-  const Unit unit = *unit_at;
-  if (unit.s < 0) return;  // the same for the whole cluster
   if (warp == 9) {
     tc::alloc(smem_u32(const_cast<uint32_t*>(tmem_at)), 512);
     tc::fence_before();
   }
-  const int s = unit.s;
-  const int32_t raw_len = a.context_lens[s];
-  const bool reporter = unit.first == 0 && g == 0 && rank == 0 && tid == 0;
-  const int L = clamp_len(a, raw_len, reporter);
-  int row0;
-  range(s, row0);
-  if (reporter && (L < unit.n || pa.query_start[s] != row0 || pa.query_start[s + 1] != row0 + unit.n))
-    flag(a.dev_status, 8u);  // PKV_DEV_ERR_LENGTH
-  const int tokens = min(per_pair, unit.n - unit.first);  // of this pair
-  const int ntiles = tokens > per_tile ? 2 : 1;
-  const int p0 = L - unit.n + unit.first, p1 = p0 + tokens - 1;  // positions of the pair's first and last token
-  // Tokens that some row sees: [0, sinks) and [low, p1].
-  const int low = pa.window > 0 ? max(0, p0 - pa.window + 1) : 0;
-  const int sinks = pa.window > 0 ? min(pa.sinks, low) : 0;
-  // Their tiles: [0, head), [head + skip, ..), `count` in all; this CTA's are rank, rank + C, ...
-  const int head = (sinks + kKeys - 1) / kKeys, skip = max(0, low / kKeys - head);
-  const int count = p1 >= 0 ? p1 / kKeys + 1 - skip : 0;
-  const int cnt = count > rank ? (count - rank + C - 1) / C : 0;
-  auto tile_of = [&](int j) {
-    const int i = j * C + rank;
-    return i < head ? i : i + skip;
-  };
-  __syncthreads();  // tensor memory's address
+  griddep_wait();  // what is above touches nothing that the last kernel writes
+  griddep_launch_dependents();
+  __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = *tmem_at;
+  constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
+  const bool odd_memory = *tmem_at != tmem;
 
   // Waits for the phase; gives up at the time limit, or when another thread has.
   auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -196,6 +198,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
       }
     }
   };
+  auto signal = [](uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory"); };
+  // Unit k of this CTA, from warp 11; false: none, or given up.
+  auto next_unit = [&](int k, Unit& u) {
+    if (odd_memory) return false;
+    if (!wait(u_full + 8 * (k & 1), (k >> 1) & 1)) return false;
+    const volatile Unit& v = units[k & 1];
+    u.s = v.s;
+    u.g = v.g;
+    u.first = v.first;
+    u.n = v.n;
+    u.row0 = v.row0;
+    u.len = v.len;
+    return u.s >= 0;
+  };
+  bool met = false;  // there was a unit
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -203,130 +220,276 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
       // -------------------------------------------------------------- loads
       // K tiles are 0, 2, 4, ... of the ring, V tiles 1, 3, 5, ...
       const bool is_v = warp == 10;
-      const int B = 1 << a.block_shift, nblk = kKeys >> a.block_shift;  // blocks of a tile: 2 to 16, one a lane
-      const int32_t* tbl = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
-      auto entry = [&](int j) {  // this lane's block of tile j: physical block, -1 where no row sees it, -2 outside the pool
-        if (j >= cnt || lane >= nblk) return -1;
-        const int t = tile_of(j) * kKeys + lane * B;
-        if (t > p1 || !(t + B > low || t < sinks)) return -1;
-        const int phys = __ldg(tbl + (t >> a.block_shift));
-        return static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks) ? phys : -2;
-      };
-      int phys = entry(0), j = 0;
-      fence_proxy_async_smem();  // the search's sums lay where the queries go
-      if (!is_v && cnt > 0 && tc::elect_one()) {
-        mbar_arrive_expect_tx(q_bar, ntiles * NL * per_tile * G * 128);
-        for (int t = 0; t < ntiles; ++t)
-          for (int l = 0; l < NL; ++l)
-            tma_load_4d(base + t * SM::kTileBytes + l * SM::kLineBytes, &tmap_q, 0, l, g * G,
-                        row0 + unit.first + t * per_tile, q_bar);
-      }
-      __syncwarp();
       const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
-      for (; j < cnt; ++j) {
-        const uint32_t bad = __ballot_sync(kFull, phys == -2), there = __ballot_sync(kFull, phys >= 0);
-        if (bad && lane == 0) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK; the block counts as zeros
-        const int i = 2 * j + is_v, slot = i % NS;
-        const uint32_t bar = full + 8 * slot, dst = base + SM::kRing + slot * SM::kTileBytes;
-        if (!__all_sync(kFull, wait(empty + 8 * slot, ((i / NS) & 1) ^ 1))) break;
-        if (lane == 0) {
-          bad_blocks[slot] = bad;
-          mbar_arrive_expect_tx(bar, __popc(there) * NL * B * 128);
-        }
+      const int B = 1 << a.block_shift, nblk = kKeys >> a.block_shift;  // blocks of a tile: 2 to 16, one a lane
+      Unit u;
+      int i = is_v, loaded = 0, k = 0;  // this warp's next tile of the ring; pairs of query tiles
+      bool ok = true;
+      for (; ok && __all_sync(kFull, next_unit(k, u)); ++k) {
         __syncwarp();
-        for (int k = 0; k < nblk; ++k) {
-          if (!((there >> k) & 1u)) continue;
-          const int block = __shfl_sync(kFull, phys, k);
+        if (lane == 0) signal(u_empty + 8 * (k & 1));
+        met = true;
+        const View v(u, pa, per_tile, C, rank);
+        const int32_t* tbl = a.block_tables + static_cast<int64_t>(u.s) * a.max_blocks_per_seq;
+        auto entry = [&](int j) {  // this lane's block of tile j: physical block, -1 where no row sees it, -2 outside the pool
+          if (j >= v.cnt || lane >= nblk) return -1;
+          const int t = v.tile_of(j) * kKeys + lane * B;
+          if (t > v.p1 || !(t + B > v.low || t < v.sinks)) return -1;
+          const int phys = __ldg(tbl + (t >> a.block_shift));
+          return static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks) ? phys : -2;
+        };
+        int phys = entry(0);
+        if (!is_v && v.cnt > 0) {
+          ok = __all_sync(kFull, wait(q_free, (loaded & 1) ^ 1));
+          if (!ok) break;
           if (tc::elect_one()) {
-#pragma unroll
-            for (int l = 0; l < NL; ++l)
-              tma_load_4d(dst + l * SM::kLineBytes + k * B * 128, map, 0, 0, g * NL + l, block, bar);
+            mbar_arrive_expect_tx(q_bar, v.ntiles * NL * per_tile * G * 128);
+            for (int t = 0; t < v.ntiles; ++t)
+              for (int l = 0; l < NL; ++l)
+                tma_load_4d(base + t * SM::kTileBytes + l * SM::kLineBytes, &tmap_q, 0, l, u.g * G,
+                            u.row0 + u.first + t * per_tile, q_bar);
           }
+          __syncwarp();
+          ++loaded;
         }
-        phys = entry(j + 1);
+        for (int j = 0; j < v.cnt; ++j, i += 2) {
+          const uint32_t bad = __ballot_sync(kFull, phys == -2), there = __ballot_sync(kFull, phys >= 0);
+          if (bad && lane == 0) flag(a.dev_status, 4u);  // PKV_DEV_ERR_BLOCK; the block counts as zeros
+          const int slot = i % NS;
+          const uint32_t bar = full + 8 * slot, dst = base + SM::kRing + slot * SM::kTileBytes;
+          ok = __all_sync(kFull, wait(empty + 8 * slot, ((i / NS) & 1) ^ 1));
+          if (!ok) break;
+          if (lane == 0) {
+            holds[slot] = bad | (is_v ? 0u : v.halves_of(0, j) << 16 | v.halves_of(1, j) << 18);
+            mbar_arrive_expect_tx(bar, __popc(there) * NL * B * 128);
+          }
+          __syncwarp();
+          for (int b = 0; b < nblk; ++b) {
+            if (!((there >> b) & 1u)) continue;
+            const int block = __shfl_sync(kFull, phys, b);
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int l = 0; l < NL; ++l)
+                tma_load_4d(dst + l * SM::kLineBytes + b * B * 128, map, 0, 0, u.g * NL + l, block, bar);
+            }
+          }
+          phys = entry(j + 1);
+        }
       }
-      if (j < cnt && lane == 0) {  // copies in flight land before the CTA leaves
-        if (!is_v) mbar_wait_bounded(q_bar, 0, a.timeout_ns);
-        for (int k = max(0, j - NS); k < j; ++k) {
-          const int i = 2 * k + is_v;
-          if (i + NS > 2 * j + is_v) mbar_wait_bounded(full + 8 * (i % NS), (i / NS) & 1, a.timeout_ns);
-        }
+      if (*abort_at && lane == 0) {  // copies in flight land before the CTA leaves
+        if (!is_v && loaded > 0) mbar_wait_bounded(q_bar, (loaded - 1) & 1, a.timeout_ns);
+        for (int b = i - 2; b >= 0 && b > i - 2 - NS; b -= 2)
+          mbar_wait_bounded(full + 8 * (b % NS), (b / NS) & 1, a.timeout_ns);
       }
     } else if (warp == 11) {
-      // --------------------------------------------------------- what is there
-      // Rows that no row of queries sees and blocks outside the pool become
-      // zeros: their weights are zero, but what the pool holds there may be
-      // anything, and zero times NaN is NaN.
-      for (int i = 0; i < 2 * cnt; ++i) {
-        const int slot = i % NS;
-        const bool is_v = i & 1;
-        if (!__all_sync(kFull, wait(full + 8 * slot, (i / NS) & 1))) break;
-        const uint32_t bad = bad_blocks[slot];
-        const int t0 = tile_of(i >> 1) * kKeys;
-        const bool edge = is_v && (t0 + kKeys - 1 > p1 || (t0 < low && t0 + kKeys > sinks));
-        if (bad || edge) {
-          const uint32_t at = base + SM::kRing + slot * SM::kTileBytes;
-          for (int r = lane; r < kKeys; r += 32) {
-            const int t = t0 + r;
-            const bool seen = t <= p1 && (t >= low || t < sinks);
-            if (!((bad >> (r >> a.block_shift)) & 1u) && (!is_v || seen)) continue;
-            for (int c = 0; c < NL * 8; ++c)  // rotated by the row: other banks for other lanes
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                               at + (c >> 3) * SM::kLineBytes + r * 128 + ((c + r) & 7) * 16),
-                           "r"(0)
-                           : "memory");
+      // ------------------------------------------------ units, and what is there
+      // Unit x in launch order: pairs of tiles from the last sequence's last
+      // (whose history is longest) to the first, the KV heads of each together.
+      auto find = [&](int x) {
+        Unit r{-1, 0, 0, 0, 0, 0, {0, 0}};
+        const int S = a.num_seqs, per_pair = 2 * per_tile;
+        r.g = x % a.num_kv_heads;
+        int before = x / a.num_kv_heads;  // pairs still to pass over
+        for (int top = S - 1; top >= 0; top -= 32) {
+          const int s = top - lane;
+          int lo = 0, n = 0, len = 0;
+          bool odd = false;
+          if (s >= 0) {
+            const int from = pa.query_start[s], to = pa.query_start[s + 1];
+            len = a.context_lens[s];
+            lo = min(max(from, 0), pa.num_tokens);
+            const int hi = min(max(to, lo), pa.num_tokens);
+            n = hi - lo;
+            odd = lo != from || hi != to;
           }
-          fence_proxy_async_smem();
+          const int mine = (n + per_pair - 1) / per_pair;
+          int incl = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += y;
+          }
+          const uint32_t at = __ballot_sync(kFull, incl > before);
+          if (at == 0) {
+            before -= __shfl_sync(kFull, incl, 31);
+            continue;
+          }
+          const int who = __ffs(at) - 1;
+          const int first = (mine - 1 - (before - (incl - mine))) * per_pair;
+          if (lane == who) {
+            const bool report = first == 0 && r.g == 0 && rank == 0;
+            len = clamp_len(a, len, report);
+            if (report && (len < n || odd)) flag(a.dev_status, 8u);  // PKV_DEV_ERR_LENGTH
+          }
+          r.s = __shfl_sync(kFull, s, who);
+          r.first = __shfl_sync(kFull, first, who);
+          r.n = __shfl_sync(kFull, n, who);
+          r.row0 = __shfl_sync(kFull, lo, who);
+          r.len = __shfl_sync(kFull, len, who);
+          break;
+        }
+        return r;
+      };
+      // Publishes unit k for the other warps; false: given up.
+      auto publish = [&](int k, const Unit& u) {
+        if (!__all_sync(kFull, wait(u_empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1))) return false;
+        if (lane == 0) {
+          volatile Unit& v = units[k & 1];
+          v.s = u.s;
+          v.g = u.g;
+          v.first = u.first;
+          v.n = u.n;
+          v.row0 = u.row0;
+          v.len = u.len;
+          signal(u_full + 8 * (k & 1));
         }
         __syncwarp();
-        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(ready + 8 * slot) : "memory");
+        return true;
+      };
+      int steals = 0;
+      bool more = C == 1;  // clusters do the unit they were launched for
+      auto steal = [&]() {
+        if (lane == 0) {
+          fence_proxy_async_smem();  // the last answer has been read
+          mbar_arrive_expect_tx(steal_bar, 16);
+          tc::steal_cta(stolen, steal_bar);
+        }
+        ++steals;
+        __syncwarp();
+      };
+      // The next unit that exists, from a CTA that has not started.
+      auto take = [&]() {
+        Unit u{-1, 0, 0, 0, 0, 0, {0, 0}};
+        while (more && u.s < 0) {
+          more = __all_sync(kFull, wait(steal_bar, (steals - 1) & 1));
+          if (!more) break;
+          const int x = tc::stolen_cta(stolen);
+          __syncwarp();
+          more = x >= 0;
+          if (more) {
+            steal();
+            u = find(x);
+          }
+        }
+        return u;
+      };
+      if (more) steal();
+      Unit u = find(blockIdx.x / C);
+      if (u.s < 0) u = take();
+      int i = 0;
+      bool ok = publish(0, u);
+      for (int k = 0; ok && u.s >= 0; ++k) {
+        met = true;
+        const Unit after = take();
+        if (!publish(k + 1, after)) break;
+        const View v(u, pa, per_tile, C, rank);
+        // Rows that no row of queries sees and blocks outside the pool become
+        // zeros: their weights are zero, but what the pool holds there may be
+        // anything, and zero times NaN is NaN.
+        for (int j = 0; j < 2 * v.cnt && ok; ++j, ++i) {
+          const int slot = i % NS;
+          const bool is_v = j & 1;
+          ok = __all_sync(kFull, wait(full + 8 * slot, (i / NS) & 1));
+          if (!ok) break;
+          const uint32_t bad = holds[slot] & 0xffffu;
+          const int t0 = v.tile_of(j >> 1) * kKeys;
+          const bool edge = is_v && (t0 + kKeys - 1 > v.p1 || (t0 < v.low && t0 + kKeys > v.sinks));
+          if (bad || edge) {
+            const uint32_t at = base + SM::kRing + slot * SM::kTileBytes;
+            for (int r = lane; r < kKeys; r += 32) {
+              if (!((bad >> (r >> a.block_shift)) & 1u) && (!is_v || v.seen(t0 + r))) continue;
+              for (int c = 0; c < NL * 8; ++c)  // rotated by the row: other banks for other lanes
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 at + (c >> 3) * SM::kLineBytes + r * 128 + ((c + r) & 7) * 16),
+                             "r"(0)
+                             : "memory");
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) signal(ready + 8 * slot);
+        }
+        u = after;
       }
+      // No answer is on its way into shared memory when the CTA leaves.
+      if (steals > 0 && lane == 0) mbar_wait_bounded(steal_bar, (steals - 1) & 1, a.timeout_ns);
     } else if (tc::elect_one()) {
       // ----------------------------------------------------------- products
-      const uint32_t qk = tc::instr_desc(BF16, kKeys, false, pa.negate != 0), pv = tc::instr_desc(BF16, D, true, false);
-      auto slot_addr = [&](int i) { return base + SM::kRing + (i % NS) * SM::kTileBytes; };
+      const uint32_t pv = tc::instr_desc(BF16, D, true, false);
+      const uint32_t qk = tc::instr_desc(BF16, kKeys, false, pa.negate != 0), qk_half = qk - (8u << 17);
+      const uint64_t q_desc = tc::smem_desc(base, 16, 1024), k_desc = tc::smem_desc(base + SM::kRing, 16, 1024);
+      const uint64_t v_desc = tc::smem_desc(base + SM::kRing, SM::kLineBytes, 1024);
+      constexpr uint32_t kSlotStep = SM::kTileBytes >> 4;  // of a descriptor
       auto arrive = [&](int i) { return wait(ready + 8 * (i % NS), (i / NS) & 1); };
-      auto scores = [&](int t, int i) {  // S_t = Q_t K^T
-        const uint64_t qd = tc::smem_desc(base + t * SM::kTileBytes, 16, 1024), kd = tc::smem_desc(slot_addr(i), 16, 1024);
+      auto scores = [&](int t, int slot, uint32_t halves) {  // S_t = Q_t K^T
+        const uint64_t qd = q_desc + t * kSlotStep, kd = k_desc + slot * kSlotStep + (halves == 2 ? 64 * 128 >> 4 : 0);
+        const uint32_t to = tmem + t * kKeys + (halves == 2 ? 64 : 0), idesc = halves == 3 ? qk : qk_half;
+        if (halves) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k / 4) * SM::kLineBytes + (k % 4) * 32) >> 4;
-          tc::mma_ss(tmem + t * kKeys, qd + off, kd + off, qk, k > 0);
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = ((s / 4) * SM::kLineBytes + (s % 4) * 32) >> 4;
+            tc::mma_ss(to, qd + off, kd + off, idesc, s > 0);
+          }
         }
+        tc::commit(s_bar + 8 * t);
       };
-      auto output = [&](int t, int i, int half, bool add) {  // O_t += P_t V, keys 64 half .. + 63
-        const uint64_t vd = tc::smem_desc(slot_addr(i), SM::kLineBytes, 1024);
-#pragma unroll
-        for (int k = 4 * half; k < 4 * half + 4; ++k)
-          tc::mma_ts(tmem + 256 + t * D, tmem + t * kKeys + 8 * k, vd + ((k * 2048) >> 4), pv, add || k > 0);
-      };
-      bool ok = cnt > 0 && wait(q_bar, 0) && arrive(0);
-      if (ok) {
+      int i = 0, pairs = 0, phase[2] = {0, 0}, outs[2] = {0, 0};
+      Unit u;
+      bool ok = true;
+      for (int k = 0; ok && next_unit(k, u); ++k) {
+        signal(u_empty + 8 * (k & 1));
+        const View v(u, pa, per_tile, C, rank);
+        const int cnt = v.cnt, ntiles = v.ntiles;
+        if (cnt == 0) continue;
+        ok = wait(q_bar, pairs & 1) && arrive(i);
+        if (!ok) break;
+        ++pairs;
         tc::fence_after();
-        for (int t = 0; t < ntiles; ++t) {
-          scores(t, 0);
-          tc::commit(s_bar + 8 * t);
-        }
-        tc::commit(empty);
-      }
-      for (int j = 0; j < cnt && ok; ++j) {
-        const int vi = 2 * j + 1, ki = 2 * j + 2;
-        ok = arrive(vi) && (j + 1 == cnt || arrive(ki));
-        for (int t = 0; t < ntiles && ok; ++t) {
-          ok = wait(p_bar + 16 * t, j & 1);
+        uint32_t now = holds[i % NS] >> 16;
+        for (int t = 0; t < ntiles; ++t) scores(t, i % NS, (now >> (2 * t)) & 3u);
+        tc::commit(empty + 8 * (i % NS));
+        if (cnt == 1) tc::commit(q_free);
+        for (int t = 0; t < ntiles && ok; ++t) ok = wait(o_free + 8 * t, (outs[t]++ & 1) ^ 1);
+        uint32_t begun = 0;  // bit t: O_t has been written
+        for (int j = 0; j < cnt && ok; ++j, i += 2) {
+          const bool last = j + 1 == cnt;
+          const int v_slot = (i + 1) % NS, k_slot = (i + 2) % NS;
+          const uint64_t vd = v_desc + v_slot * kSlotStep;
+          uint32_t next = 0;
+          ok = arrive(i + 1);
+          if (ok && !last) {
+            ok = arrive(i + 2);
+            next = holds[k_slot] >> 16;
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t >= ntiles || !ok) break;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // O_t += P_t V over keys 64 half .. + 63
+              if (!wait(p_bar + 16 * t + 8 * half, phase[t] & 1)) {
+                ok = false;
+                break;
+              }
+              if (!((now >> (2 * t + half)) & 1u)) continue;
+              tc::fence_after();
+#pragma unroll
+              for (int s = 4 * half; s < 4 * half + 4; ++s)
+                tc::mma_ts(tmem + 256 + t * D, tmem + t * kKeys + 8 * s, vd + ((s * 2048) >> 4), pv,
+                           s > 4 * half || ((begun >> t) & 1u));
+              begun |= 1u << t;
+            }
+            if (!ok) break;
+            ++phase[t];
+            if (last)
+              tc::commit(o_bar + 8 * t);
+            else
+              scores(t, k_slot, (next >> (2 * t)) & 3u);
+          }
           if (!ok) break;
-          tc::fence_after();
-          output(t, vi, 0, j > 0);
-          ok = wait(p_bar + 16 * t + 8, j & 1);
-          if (!ok) break;
-          tc::fence_after();
-          output(t, vi, 1, true);
-          if (j + 1 < cnt) scores(t, ki);
-          tc::commit(j + 1 < cnt ? s_bar + 8 * t : o_bar + 8 * t);
-        }
-        if (ok) {
-          tc::commit(empty + 8 * (vi % NS));
-          if (j + 1 < cnt) tc::commit(empty + 8 * (ki % NS));
+          tc::commit(empty + 8 * v_slot);
+          if (!last) tc::commit(empty + 8 * k_slot);
+          if (j + 2 == cnt) tc::commit(q_free);
+          now = next;
         }
       }
       // Every product has completed before tensor memory is freed.
@@ -344,50 +507,87 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
     // -------------------------------------------------------------- softmax
     const int t = warp >> 2, r = tid & (kRows - 1);  // tile and row
-    const int token = r / G, pos = p0 + t * per_tile + token;
-    const bool live = token < per_tile && t * per_tile + token < tokens;
+    const int token = r / G;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t s_at = tmem + t * kKeys + lanes, o_at = tmem + 256 + t * D + lanes;
+    const uint32_t my_s = s_bar + 8 * t, my_p = p_bar + 16 * t;
     constexpr float kGrow = 8.f;
     // f16 weights: times 2^7, so that small ones keep their bits (f16 ends at 2^-24).
     constexpr float kUp = BF16 ? 0.f : 7.f;
+    const float sl2 = a.scale_log2, grow = kGrow / sl2;
+    Unit u{-1, 0, 0, 0, 0, 0, {0, 0}};
     float m = kNegInf, l = 0.f;  // the row's reference, in scores; the sum of its weights
-    if (t < ntiles) {
-      const float sl2 = a.scale_log2, grow = kGrow / sl2;
-      const int my_low = pa.window > 0 ? max(0, pos - pa.window + 1) : 0, my_sinks = pa.window > 0 ? pa.sinks : 0;
+    int seen = 0, outs = 0, ntiles = 0;
+    auto row_at = [&](int tile, int row) {  // element index of a live row's first channel
+      const int tok = row / G;
+      return ((static_cast<int64_t>(u.row0) + u.first + tile * per_tile + tok) * a.num_q_heads + u.g * G + (row - tok * G)) *
+             D;
+    };
+    for (int k = 0; __all_sync(kFull, next_unit(k, u)); ++k) {
+      __syncwarp();
+      if (lane == 0) signal(u_empty + 8 * (k & 1));
+      met = true;
+      const View v(u, pa, per_tile, C, rank);
+      ntiles = v.ntiles;
+      m = kNegInf;
+      l = 0.f;
+      if (t >= ntiles) {
+        if (C > 1) break;  // keeps the unit
+        continue;
+      }
+      const int pos = v.p0 + t * per_tile + token, my_low = v.low_of(pos), my_sinks = v.sinks_all;
       // The tile's rows: positions first .. last, the widest and the narrowest view.
-      const int first = p0 + t * per_tile, last = first + per_tile - 1;
-      const int last_low = pa.window > 0 ? max(0, last - pa.window + 1) : 0;
+      const int first = v.p0 + t * per_tile, last_low = v.low_of(first + per_tile - 1);
       bool ok = true;
-      for (int j = 0; j < cnt; ++j) {
-        ok = __all_sync(kFull, wait(s_bar + 8 * t, j & 1));
+      for (int j = 0; j < v.cnt; ++j, ++seen) {
+        const uint32_t some = v.halves_of(t, j);
+        const int t0 = v.tile_of(j) * kKeys;
+        const bool whole = t0 + kKeys - 1 <= first && (t0 >= last_low || t0 + kKeys <= my_sinks);  // for every row
+        uint32_t x[kKeys];
+        float* y = reinterpret_cast<float*>(x);
+        float mx = kNegInf;
+        ok = __all_sync(kFull, wait(my_s, seen & 1));
         if (!ok) break;
         tc::fence_after();
-        uint32_t x[kKeys];
-#pragma unroll
-        for (int c = 0; c < kKeys; c += 32) tc::ld32(x + c, s_at + c);
-        tc::wait_ld();
-        float* v = reinterpret_cast<float*>(x);
-        const int t0 = tile_of(j) * kKeys;
-        if (!(t0 + kKeys - 1 <= first && (t0 >= last_low || t0 + kKeys <= my_sinks))) {
-          auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; };
-#pragma unroll
+        if (!whole) {  // 32 columns that some row does not see go back masked (a loop: this code runs rarely)
+#pragma unroll 1
           for (int c = 0; c < kKeys; c += 32) {
+            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; };
             const int at = t0 + c;
             const uint32_t see = below(pos + 1 - at) & (~below(my_low - at) | below(my_sinks - at));
+            if (!((some >> (c / 64)) & 1) || __all_sync(kFull, see == kFull)) continue;
+            uint32_t o[32];
+            tc::ld32(o, s_at + c);
+            tc::wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[c + i] = (see >> i) & 1u ? v[c + i] : kNegInf;
+            for (int i = 0; i < 32; ++i) o[i] = (see >> i) & 1u ? o[i] : __float_as_uint(kNegInf);
+            tc::st32(s_at + c, o);
           }
+          tc::wait_st();
         }
-        float top[4] = {v[0], v[1], v[2], v[3]};
+        // All of the columns, seen or not: loads under a condition would keep
+        // their registers from one pair of tiles to the next.
+        tc::ld32(x, s_at);
+        tc::ld32(x + 32, s_at + 32);
+        tc::wait_ld();
+        tc::ld32(x + 64, s_at + 64);  // on their way while the first half's maximum is taken
+        tc::ld32(x + 96, s_at + 96);
 #pragma unroll
-        for (int i = 4; i < kKeys - 4; i += 8) {
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1) tc::wait_ld();
+          if (!((some >> half) & 1)) continue;
+          const float* z = y + 64 * half;
+          float top[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], v[i + k]), v[i + 4 + k]);
+          for (int i = 4; i < 60; i += 8) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) top[q] = fmaxf(fmaxf(top[q], z[i + q]), z[i + 4 + q]);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) top[q] = fmaxf(top[q], z[60 + q]);
+          mx = fmaxf(mx, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], v[kKeys - 4 + k]);
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        // The reference moves to mx where that lies far above it.
         const bool raise = mx > m + grow;  // a first one counts: m is -infinity
         if (__any_sync(kFull, raise)) {
           const float mn = raise ? mx : m;
@@ -409,63 +609,123 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
         const float shift = m == kNegInf ? 0.f : kUp - m * sl2;
         const F2 scale2 = pair(sl2, sl2), shift2 = pair(shift, shift);
         F2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {  // the product with V begins on the first half
-#pragma unroll
-          for (int i = 64 * half; i < 64 * half + 64; i += 2) {
-            const float2 e = halves(fma2(pair(v[i], v[i + 1]), scale2, shift2));
-            const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
-            sum[(i / 2) & 1] = add2(sum[(i / 2) & 1], pair(p0, p1));
-            x[i / 2] = BF16 ? pack_bf16(p0, p1) : pack_f16(p0, p1);
-          }
-          tc::st32(s_at + 32 * half, x + 32 * half);
+        auto weigh = [&](int i) {  // columns i, i + 1
+          const float2 e = halves(fma2(pair(y[i], y[i + 1]), scale2, shift2));
+          const float w0 = ex2_approx(e.x), w1 = ex2_approx(e.y);
+          sum[(i / 2) & 1] = add2(sum[(i / 2) & 1], pair(w0, w1));
+          return BF16 ? pack_bf16(w0, w1) : pack_f16(w0, w1);
+        };
+        auto pass = [&](int half) {  // the weights of this half are in tensor memory
           tc::wait_st();
           tc::fence_before();
-          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_bar + 16 * t + 8 * half) : "memory");
+          signal(my_p + 8 * half);
+        };
+        if (some & 1) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] = weigh(2 * i);
+          tc::st32(s_at, w);
         }
+        if (some & 2) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = weigh(64 + 2 * i);
+          pass(0);  // a while after its stores
+#pragma unroll
+          for (int i = 16; i < 32; ++i) w[i] = weigh(64 + 2 * i);
+          tc::st32(s_at + 32, w);
+        } else {
+          pass(0);
+        }
+        pass(1);
         const float2 s0 = halves(sum[0]), s1 = halves(sum[1]);
         l += (s0.x + s0.y) + (s1.x + s1.y);
       }
-      if (cnt > 0 && ok) ok = __all_sync(kFull, wait(o_bar + 8 * t, 0));
-      tc::fence_after();
-    }
-
-    // ----------------------------------------------------------------- rows
-    auto store_row = [&](int64_t at, const float* o, float f) {  // 32 channels
-      if (a.out_dtype == 0) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
-        return;
+      if (!ok) break;
+      if (v.cnt > 0) {
+        if (!__all_sync(kFull, wait(o_bar + 8 * t, outs++ & 1))) break;
+        tc::fence_after();
       }
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at);
-      auto two = [&](int i) {
-        return a.out_dtype == 1 ? pack_f16(o[i] * f, o[i + 1] * f) : pack_bf16(o[i] * f, o[i + 1] * f);
+      if (C > 1) break;  // the rows meet below
+      // 128 bytes of the warp's 32 rows at a time go through shared memory, so
+      // that eight lanes store a row's side by side.  (Each thread storing its
+      // own row took 32 lines an instruction, 5 us a pair of tiles.)
+      const float f = l > 0.f ? 1.f / l : 0.f;
+      const bool none = __any_sync(kFull, l == 0.f);  // a row without a visible token: tensor memory may hold anything
+      const uint32_t stage = base + SM::kStage + warp * 4096;
+      const int eb = a.out_dtype == 0 ? 4 : 2, chunk = lane & 7;
+      const bool live = token < per_tile && t * per_tile + token < v.tokens;
+      const uint32_t lives = __ballot_sync(kFull, live);
+      uint8_t* mine = static_cast<uint8_t*>(a.out) +
+                      (((static_cast<int64_t>(u.row0) + u.first + t * per_tile + token) * a.num_q_heads + u.g * G +
+                        (r - token * G)) * D * eb);
+      uint8_t* to[8];  // rows 4 i + lane / 8
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        to[i] = reinterpret_cast<uint8_t*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(mine), 4 * i + (lane >> 3))) +
+                16 * chunk;
+      auto put = [&](int chunk, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4)),
+                     "r"(w0), "r"(w1), "r"(w2), "r"(w3)
+                     : "memory");
       };
+      auto flush = [&](int at) {  // 128 bytes of each row from byte `at`
+        __syncwarp();
+        uint4 w[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i] = make_uint4(two(8 * i), two(8 * i + 2), two(8 * i + 4), two(8 * i + 6));
-    };
-    auto row_at = [&](int tile, int row) {  // element index of a live row's first channel
-      const int tok = row / G;
-      return ((static_cast<int64_t>(row0) + unit.first + tile * per_tile + tok) * a.num_q_heads + g * G + (row - tok * G)) * D;
-    };
-    if (C == 1) {
-      if (t < ntiles) {
-        const float f = l > 0.f ? 1.f / l : 0.f;
-        const int64_t at = row_at(t, r);
+        for (int i = 0; i < 8; ++i) {
+          const int row = 4 * i + (lane >> 3);
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                       : "r"(stage + row * 128 + ((chunk ^ (row & 7)) << 4))
+                       : "memory");
+        }
 #pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if ((lives >> (4 * i + (lane >> 3))) & 1u) *reinterpret_cast<uint4*>(to[i] + at) = w[i];
+        __syncwarp();
+      };
+      auto free_rows = [&]() {  // the next pair's products may begin
+        if (v.cnt == 0) return;
+        tc::fence_before();
+        signal(o_free + 8 * t);
+      };
+      if (eb == 2) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 64) {
+          uint32_t o[64];
+          tc::ld32(o, o_at + c);
+          tc::ld32(o + 32, o_at + c + 32);
+          tc::wait_ld();
+          if (c + 64 == D) free_rows();
+          if (none) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) o[i] = l == 0.f ? 0u : o[i];
+          }
+          auto two = [&](int i) {
+            const float x = __uint_as_float(o[i]) * f, y = __uint_as_float(o[i + 1]) * f;
+            return a.out_dtype == 1 ? pack_f16(x, y) : pack_bf16(x, y);
+          };
+#pragma unroll
+          for (int i = 0; i < 8; ++i) put(i, two(8 * i), two(8 * i + 2), two(8 * i + 4), two(8 * i + 6));
+          flush(2 * c);
+        }
+      } else {
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           tc::ld32(o, o_at + c);
           tc::wait_ld();
-          if (l == 0.f) {  // no visible token: whatever tensor memory holds
+          if (c + 32 == D) free_rows();
+          auto val = [&](int i) { return l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * f); };
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0u;
-          }
-          if (live) store_row(at + c, reinterpret_cast<const float*>(o), f);
+          for (int i = 0; i < 8; ++i) put(i, val(4 * i), val(4 * i + 1), val(4 * i + 2), val(4 * i + 3));
+          flush(4 * c);
         }
       }
-    } else {
+    }
+
+    if (C > 1) {
       // The cluster's rows: each CTA scales its part to the rows' common maximum
       // and leaves it in its shared memory; CTA r adds up rows r, r + C, ...
       float2* state = reinterpret_cast<float2*>(smem + SM::kRowState);
@@ -474,22 +734,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
       state[tid] = make_float2(m, l);
       cluster_sync();
       auto remote = [&](uint32_t addr, int from) {
-        float2 v;
+        float2 x;
         asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                     : "=f"(v.x), "=f"(v.y)
+                     : "=f"(x.x), "=f"(x.y)
                      : "r"(cluster_map(addr, from))
                      : "memory");
-        return v;
+        return x;
       };
-      if (t < ntiles) {
+      if (met && t < ntiles) {
         float top = kNegInf, sum = 0.f;
         for (int k = 0; k < C; ++k) top = fmaxf(top, remote(smem_u32(state + tid), k).x);
         const float ref = top == kNegInf ? 0.f : top;
         for (int k = 0; k < C; ++k) {
-          const float2 v = remote(smem_u32(state + tid), k);
-          sum += v.y * ex2_approx((v.x - ref) * a.scale_log2);
+          const float2 x = remote(smem_u32(state + tid), k);
+          sum += x.y * ex2_approx((x.x - ref) * sl2);
         }
-        const float f = l > 0.f ? ex2_approx((m - ref) * a.scale_log2) / sum : 0.f;
+        const float f = l > 0.f ? ex2_approx((m - ref) * sl2) / sum : 0.f;
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -508,23 +768,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
       }
       cluster_sync();
       // 4 channels a thread, D / 4 threads a row.
-      const int rows_in = ntiles * kRows, width = D / 4;
-      for (int e = tid; e < rows_in / C * width; e += 2 * kRows) {
+      const int width = D / 4, tokens = met ? min(2 * per_tile, u.n - u.first) : 0;
+      for (int e = tid; e < ntiles * kRows / C * width; e += 2 * kRows) {
         const int row = (e / width) * C + rank, ch = 4 * (e % width);
         const int tile = row / kRows, in = row & (kRows - 1), tok = in / G;
         if (tok >= per_tile || tile * per_tile + tok >= tokens) continue;
         const uint32_t addr = smem_u32(rows + row * D + ((ch + 4 * in) & (D - 1)));
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < C; ++k) {
-          float4 v;
+          float4 x;
           asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
                        : "r"(cluster_map(addr, k))
                        : "memory");
-          sum.x += v.x;
-          sum.y += v.y;
-          sum.z += v.z;
-          sum.w += v.w;
+          sum.x += x.x;
+          sum.y += x.y;
+          sum.z += x.z;
+          sum.w += x.w;
         }
         const int64_t at = row_at(tile, in) + ch;
         store_out(a.out, at, sum.x, a.out_dtype);

@@ -17,6 +17,29 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Takes over a CTA of this grid that has not started yet (whose blockIdx.x the
+// 16 bytes at `at` then hold), or learns that there is none; completes on `bar`.
+// Not called again once there is none.
+__device__ __forceinline__ void steal_cta(uint32_t at, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(at),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ int stolen_cta(uint32_t at) {  // -1: none
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(at)
+      : "memory");
+  return got ? static_cast<int>(x) : -1;
+}
+
 // Tensor memory: 128 lanes of 512 32-bit columns a SM; an address is (lane
 // << 16) | column, and a warp reaches the 32 lanes of its rank modulo 4.
 __device__ __forceinline__ void alloc(uint32_t result, uint32_t columns) {  // one whole warp
@@ -86,6 +109,14 @@ __device__ __forceinline__ void st32(uint32_t at, const uint32_t* r) {
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
       "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::PKV_I8(r, 0),
       PKV_I8(r, 8), PKV_I8(r, 16), PKV_I8(r, 24), "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ void st16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15};" ::PKV_I8(r, 0),
+      PKV_I8(r, 8), "r"(at)
       : "memory");
 }
 
