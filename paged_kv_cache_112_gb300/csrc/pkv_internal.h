@@ -203,6 +203,7 @@ struct PrefillArgs {
   const int32_t* query_start;  // [num_seqs + 1]: rows of each sequence's new tokens
   int num_tokens;              // rows of q
   int window, sinks;           // window 0: none
+  int out_sectors;             // out is 32-byte aligned
   int negate;                  // the softmax scale is negative: scale_log2 is its magnitude's
 };
 

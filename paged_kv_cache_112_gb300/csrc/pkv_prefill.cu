@@ -25,8 +25,9 @@
 // P overwrites the first half of S.  (With S of the next keys issued in halves,
 // one of them beside the exponentials, the products take 48 instructions an
 // iteration in place of 32, and the issuing thread is what everybody waits for:
-// 690 us for 8192 tokens instead of 400.)  Halves of 64 keys that no row of a
-// tile sees are left out.
+// 690 us for 8192 tokens instead of 400.)  (Leaving out halves of a
+// tile that no row sees costs more, in branches and registers, than it saves:
+// 413 and 232 us for 384 and 218 at 8192 tokens and 16 windowed prompts.)
 //
 // The grid has a CTA for each pair of tiles; those on the SMs take over the
 // others' work one after another (clusterlaunchcontrol), so that the next
@@ -62,18 +63,17 @@ struct Smem {
   static constexpr int kLines = D / 64;                 // 128-byte lines of a row
   static constexpr int kLineBytes = kRows * 128;        // one line of a tile's rows
   static constexpr int kTileBytes = kLines * kLineBytes;
-  static constexpr int kSlots = D == 128 ? 4 : 8;       // K and V tiles in flight
+  static constexpr int kSlots = D == 128 ? 5 : 8;       // K and V tiles in flight
   static constexpr int kRing = 2 * kTileBytes;          // after the two query tiles
   static constexpr int kRowState = 0;                   // the cluster's meeting, over the tiles: max and sum of 256 rows,
   static constexpr int kRowsAt = 2048;                  // then [256][D] floats
-  static constexpr int kStage = kRing + kSlots * kTileBytes;  // 4 KB a warp: 32 rows of 128 bytes on their way out
-  static constexpr int kStolen = kStage + 8 * 4096;
+  static constexpr int kStolen = kRing + kSlots * kTileBytes;
   static constexpr int kUnits = kStolen + 16;           // two units of work
   static constexpr int kBars = kUnits + 64;
   static constexpr int kBarCount = 3 * kSlots + 18;
-  static constexpr int kWords = kBars + 8 * kBarCount;  // what each slot holds, tensor memory, abort
+  static constexpr int kWords = kBars + 8 * kBarCount;  // bad blocks of each slot, tensor memory, abort
   static constexpr int kBytes = kWords + 4 * (kSlots + 2);
-  static_assert(kRowsAt + 2 * kRows * D * 4 <= kStage, "the cluster's rows fit over the tiles");
+  static_assert(kRowsAt + 2 * kRows * D * 4 <= kStolen, "the cluster's rows fit over the tiles");
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -116,14 +116,6 @@ struct View {
     return i < head ? i : i + skip;
   }
   __device__ __forceinline__ bool seen(int t) const { return t <= p1 && (t >= low || t < sinks); }
-  // The halves (bit h: keys 64 h .. + 63) of history tile j that some row of
-  // tile t (0, 1) sees.
-  __device__ __forceinline__ uint32_t halves_of(int t, int j) const {
-    const int first = p0 + t * per_tile, last = min(first + per_tile - 1, p1), lo = low_of(first);
-    const int t0 = tile_of(j) * kKeys, few = min(sinks_all, lo);
-    auto some = [&](int at) { return at <= last && (at + 64 > lo || at < few); };
-    return (some(t0) ? 1u : 0u) | (some(t0 + 64) ? 2u : 0u);
-  }
 };
 
 template <int D, bool BF16>
@@ -142,10 +134,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
                  q_free = q_bar + 8, s_bar = q_free + 8, p_bar = s_bar + 16, o_bar = p_bar + 32, o_free = o_bar + 16,
                  u_full = o_free + 16, u_empty = u_full + 16, steal_bar = u_empty + 16, drain_bar = steal_bar + 8;
   volatile Unit* units = reinterpret_cast<volatile Unit*>(smem + SM::kUnits);
-  // Of each slot: bits 0 to 15 the tile's blocks outside the pool; K tiles: bits
-  // 16 + 2 t, 17 + 2 t the halves that tile t of the rows sees.
-  volatile uint32_t* holds = reinterpret_cast<volatile uint32_t*>(smem + SM::kWords);
-  volatile uint32_t* tmem_at = holds + NS;
+  volatile uint32_t* bad_blocks = reinterpret_cast<volatile uint32_t*>(smem + SM::kWords);
+  volatile uint32_t* tmem_at = bad_blocks + NS;
   volatile uint32_t* abort_at = tmem_at + 1;
   const int G = a.group, per_tile = kRows / G;
 
@@ -260,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
           ok = __all_sync(kFull, wait(empty + 8 * slot, ((i / NS) & 1) ^ 1));
           if (!ok) break;
           if (lane == 0) {
-            holds[slot] = bad | (is_v ? 0u : v.halves_of(0, j) << 16 | v.halves_of(1, j) << 18);
+            bad_blocks[slot] = bad;
             mbar_arrive_expect_tx(bar, __popc(there) * NL * B * 128);
           }
           __syncwarp();
@@ -391,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
           const bool is_v = j & 1;
           ok = __all_sync(kFull, wait(full + 8 * slot, (i / NS) & 1));
           if (!ok) break;
-          const uint32_t bad = holds[slot] & 0xffffu;
+          const uint32_t bad = bad_blocks[slot];
           const int t0 = v.tile_of(j >> 1) * kKeys;
           const bool edge = is_v && (t0 + kKeys - 1 > v.p1 || (t0 < v.low && t0 + kKeys > v.sinks));
           if (bad || edge) {
@@ -416,20 +406,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
     } else if (tc::elect_one()) {
       // ----------------------------------------------------------- products
       const uint32_t pv = tc::instr_desc(BF16, D, true, false);
-      const uint32_t qk = tc::instr_desc(BF16, kKeys, false, pa.negate != 0), qk_half = qk - (8u << 17);
+      const uint32_t qk = tc::instr_desc(BF16, kKeys, false, pa.negate != 0);
       const uint64_t q_desc = tc::smem_desc(base, 16, 1024), k_desc = tc::smem_desc(base + SM::kRing, 16, 1024);
       const uint64_t v_desc = tc::smem_desc(base + SM::kRing, SM::kLineBytes, 1024);
       constexpr uint32_t kSlotStep = SM::kTileBytes >> 4;  // of a descriptor
       auto arrive = [&](int i) { return wait(ready + 8 * (i % NS), (i / NS) & 1); };
-      auto scores = [&](int t, int slot, uint32_t halves) {  // S_t = Q_t K^T
-        const uint64_t qd = q_desc + t * kSlotStep, kd = k_desc + slot * kSlotStep + (halves == 2 ? 64 * 128 >> 4 : 0);
-        const uint32_t to = tmem + t * kKeys + (halves == 2 ? 64 : 0), idesc = halves == 3 ? qk : qk_half;
-        if (halves) {
+      auto scores = [&](int t, int slot) {  // S_t = Q_t K^T
+        const uint64_t qd = q_desc + t * kSlotStep, kd = k_desc + slot * kSlotStep;
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint32_t off = ((s / 4) * SM::kLineBytes + (s % 4) * 32) >> 4;
-            tc::mma_ss(to, qd + off, kd + off, idesc, s > 0);
-          }
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = ((s / 4) * SM::kLineBytes + (s % 4) * 32) >> 4;
+          tc::mma_ss(tmem + t * kKeys, qd + off, kd + off, qk, s > 0);
         }
         tc::commit(s_bar + 8 * t);
       };
@@ -445,22 +432,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
         if (!ok) break;
         ++pairs;
         tc::fence_after();
-        uint32_t now = holds[i % NS] >> 16;
-        for (int t = 0; t < ntiles; ++t) scores(t, i % NS, (now >> (2 * t)) & 3u);
+        for (int t = 0; t < ntiles; ++t) scores(t, i % NS);
         tc::commit(empty + 8 * (i % NS));
         if (cnt == 1) tc::commit(q_free);
         for (int t = 0; t < ntiles && ok; ++t) ok = wait(o_free + 8 * t, (outs[t]++ & 1) ^ 1);
-        uint32_t begun = 0;  // bit t: O_t has been written
         for (int j = 0; j < cnt && ok; ++j, i += 2) {
           const bool last = j + 1 == cnt;
           const int v_slot = (i + 1) % NS, k_slot = (i + 2) % NS;
           const uint64_t vd = v_desc + v_slot * kSlotStep;
-          uint32_t next = 0;
-          ok = arrive(i + 1);
-          if (ok && !last) {
-            ok = arrive(i + 2);
-            next = holds[k_slot] >> 16;
-          }
+          ok = arrive(i + 1) && (last || arrive(i + 2));
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (t >= ntiles || !ok) break;
@@ -470,26 +450,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
                 ok = false;
                 break;
               }
-              if (!((now >> (2 * t + half)) & 1u)) continue;
               tc::fence_after();
 #pragma unroll
               for (int s = 4 * half; s < 4 * half + 4; ++s)
                 tc::mma_ts(tmem + 256 + t * D, tmem + t * kKeys + 8 * s, vd + ((s * 2048) >> 4), pv,
-                           s > 4 * half || ((begun >> t) & 1u));
-              begun |= 1u << t;
+                           s > 0 || j > 0);
             }
             if (!ok) break;
             ++phase[t];
             if (last)
               tc::commit(o_bar + 8 * t);
             else
-              scores(t, k_slot, (next >> (2 * t)) & 3u);
+              scores(t, k_slot);
           }
           if (!ok) break;
           tc::commit(empty + 8 * v_slot);
           if (!last) tc::commit(empty + 8 * k_slot);
           if (j + 2 == cnt) tc::commit(q_free);
-          now = next;
         }
       }
       // Every product has completed before tensor memory is freed.
@@ -540,7 +517,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
       const int first = v.p0 + t * per_tile, last_low = v.low_of(first + per_tile - 1);
       bool ok = true;
       for (int j = 0; j < v.cnt; ++j, ++seen) {
-        const uint32_t some = v.halves_of(t, j);
         const int t0 = v.tile_of(j) * kKeys;
         const bool whole = t0 + kKeys - 1 <= first && (t0 >= last_low || t0 + kKeys <= my_sinks);  // for every row
         uint32_t x[kKeys];
@@ -555,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
             auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; };
             const int at = t0 + c;
             const uint32_t see = below(pos + 1 - at) & (~below(my_low - at) | below(my_sinks - at));
-            if (!((some >> (c / 64)) & 1) || __all_sync(kFull, see == kFull)) continue;
+            if (__all_sync(kFull, see == kFull)) continue;
             uint32_t o[32];
             tc::ld32(o, s_at + c);
             tc::wait_ld();
@@ -565,8 +541,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
           }
           tc::wait_st();
         }
-        // All of the columns, seen or not: loads under a condition would keep
-        // their registers from one pair of tiles to the next.
         tc::ld32(x, s_at);
         tc::ld32(x + 32, s_at + 32);
         tc::wait_ld();
@@ -575,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (half == 1) tc::wait_ld();
-          if (!((some >> half) & 1)) continue;
           const float* z = y + 64 * half;
           float top[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
@@ -620,23 +593,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
           tc::fence_before();
           signal(my_p + 8 * half);
         };
-        if (some & 1) {
-          uint32_t w[32];
+        uint32_t w[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] = weigh(2 * i);
-          tc::st32(s_at, w);
-        }
-        if (some & 2) {
-          uint32_t w[32];
+        for (int i = 0; i < 32; ++i) w[i] = weigh(2 * i);
+        tc::st32(s_at, w);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = weigh(64 + 2 * i);
-          pass(0);  // a while after its stores
+        for (int i = 0; i < 16; ++i) w[i] = weigh(64 + 2 * i);
+        pass(0);  // a while after its stores
 #pragma unroll
-          for (int i = 16; i < 32; ++i) w[i] = weigh(64 + 2 * i);
-          tc::st32(s_at + 32, w);
-        } else {
-          pass(0);
-        }
+        for (int i = 16; i < 32; ++i) w[i] = weigh(64 + 2 * i);
+        tc::st32(s_at + 32, w);
         pass(1);
         const float2 s0 = halves(sum[0]), s1 = halves(sum[1]);
         l += (s0.x + s0.y) + (s1.x + s1.y);
@@ -647,80 +613,58 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
         tc::fence_after();
       }
       if (C > 1) break;  // the rows meet below
-      // 128 bytes of the warp's 32 rows at a time go through shared memory, so
-      // that eight lanes store a row's side by side.  (Each thread storing its
-      // own row took 32 lines an instruction, 5 us a pair of tiles.)
+      // 32 bytes a store: whole sectors of the thread's own row.
       const float f = l > 0.f ? 1.f / l : 0.f;
       const bool none = __any_sync(kFull, l == 0.f);  // a row without a visible token: tensor memory may hold anything
-      const uint32_t stage = base + SM::kStage + warp * 4096;
-      const int eb = a.out_dtype == 0 ? 4 : 2, chunk = lane & 7;
+      const int eb = a.out_dtype == 0 ? 4 : 2;
       const bool live = token < per_tile && t * per_tile + token < v.tokens;
-      const uint32_t lives = __ballot_sync(kFull, live);
       uint8_t* mine = static_cast<uint8_t*>(a.out) +
                       (((static_cast<int64_t>(u.row0) + u.first + t * per_tile + token) * a.num_q_heads + u.g * G +
                         (r - token * G)) * D * eb);
-      uint8_t* to[8];  // rows 4 i + lane / 8
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        to[i] = reinterpret_cast<uint8_t*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(mine), 4 * i + (lane >> 3))) +
-                16 * chunk;
-      auto put = [&](int chunk, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4)),
-                     "r"(w0), "r"(w1), "r"(w2), "r"(w3)
-                     : "memory");
-      };
-      auto flush = [&](int at) {  // 128 bytes of each row from byte `at`
-        __syncwarp();
-        uint4 w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = 4 * i + (lane >> 3);
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                       : "r"(stage + row * 128 + ((chunk ^ (row & 7)) << 4))
+      auto store8 = [&](uint8_t* to, const uint32_t (&x)[8]) {
+        if (!live) return;
+        if (pa.out_sectors) {
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                       "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                        : "memory");
+        } else {
+          reinterpret_cast<uint4*>(to)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+          reinterpret_cast<uint4*>(to)[1] = make_uint4(x[4], x[5], x[6], x[7]);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if ((lives >> (4 * i + (lane >> 3))) & 1u) *reinterpret_cast<uint4*>(to[i] + at) = w[i];
-        __syncwarp();
       };
-      auto free_rows = [&]() {  // the next pair's products may begin
-        if (v.cnt == 0) return;
-        tc::fence_before();
-        signal(o_free + 8 * t);
-      };
-      if (eb == 2) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
-          uint32_t o[64];
-          tc::ld32(o, o_at + c);
-          tc::ld32(o + 32, o_at + c + 32);
-          tc::wait_ld();
-          if (c + 64 == D) free_rows();
-          if (none) {
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tc::ld32(o, o_at + c);
+        tc::wait_ld();
+        if (c + 32 == D && v.cnt > 0) {  // the next pair's products may begin
+          tc::fence_before();
+          signal(o_free + 8 * t);
+        }
+        if (none) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) o[i] = l == 0.f ? 0u : o[i];
+          for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0u : o[i];
+        }
+        auto val = [&](int i) { return __uint_as_float(o[i]) * f; };
+        if (eb == 2) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int e = 16 * h + 2 * i;
+              x[i] = a.out_dtype == 1 ? pack_f16(val(e), val(e + 1)) : pack_bf16(val(e), val(e + 1));
+            }
+            store8(mine + 2 * c + 32 * h, x);
           }
-          auto two = [&](int i) {
-            const float x = __uint_as_float(o[i]) * f, y = __uint_as_float(o[i + 1]) * f;
-            return a.out_dtype == 1 ? pack_f16(x, y) : pack_bf16(x, y);
-          };
+        } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) put(i, two(8 * i), two(8 * i + 2), two(8 * i + 4), two(8 * i + 6));
-          flush(2 * c);
-        }
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tc::ld32(o, o_at + c);
-          tc::wait_ld();
-          if (c + 32 == D) free_rows();
-          auto val = [&](int i) { return l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * f); };
+          for (int h = 0; h < 4; ++h) {
+            uint32_t x[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) put(i, val(4 * i), val(4 * i + 1), val(4 * i + 2), val(4 * i + 3));
-          flush(4 * c);
+            for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(val(8 * h + i));
+            store8(mine + 4 * c + 32 * h, x);
+          }
         }
       }
     }
