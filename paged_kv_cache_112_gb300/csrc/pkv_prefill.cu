@@ -86,16 +86,20 @@ struct Unit {
 };
 static_assert(sizeof(Unit) == 32, "two units in shared memory");
 
-// What the rows of a pair of tiles see.
+// What the rows of a pair of tiles see.  The history's tiles of 128 are cut from
+// an axis of the blocks that some row sees: those of the first tokens, then
+// those of the window, with no gap between (tokens 0 .. mid - 1, then mid + gap
+// and on).
 struct View {
   int per_tile, tokens, ntiles;  // tokens a tile holds, of this pair, tiles with any
   int p0, p1;                    // positions of the pair's first and last token
   int window, sinks_all;
   int low, sinks;                // some row sees [0, sinks) and [low, p1]
-  int head, skip, cnt;           // their tiles: [0, head), [head + skip, ..); this CTA's number of them
+  int mid, gap;
+  int end, cnt;                  // the axis' length, this CTA's number of tiles
   int C, rank;
 
-  __device__ __forceinline__ View(const Unit& u, const PrefillArgs& pa, int tile_tokens, int c, int r)
+  __device__ __forceinline__ View(const Unit& u, const PrefillArgs& pa, int tile_tokens, int block_shift, int c, int r)
       : per_tile(tile_tokens), window(pa.window), C(c), rank(r) {
     tokens = min(2 * per_tile, u.n - u.first);
     ntiles = tokens > per_tile ? 2 : 1;
@@ -104,18 +108,20 @@ struct View {
     sinks_all = window > 0 ? pa.sinks : 0;
     low = low_of(p0);
     sinks = min(sinks_all, low);
-    head = (sinks + kKeys - 1) / kKeys;
-    skip = max(0, low / kKeys - head);
-    const int count = p1 >= 0 ? p1 / kKeys + 1 - skip : 0;
+    const int first = (sinks + (1 << block_shift) - 1) >> block_shift, from = low >> block_shift;  // blocks
+    mid = from > first ? first << block_shift : 0;
+    gap = from > first ? (from - first) << block_shift : 0;
+    end = max(0, p1 + 1 - gap);
+    const int count = (end + kKeys - 1) / kKeys;
     cnt = count > rank ? (count - rank + C - 1) / C : 0;
   }
   // The first token of the window at position p.
   __device__ __forceinline__ int low_of(int p) const { return window > 0 ? max(0, p - window + 1) : 0; }
-  __device__ __forceinline__ int tile_of(int j) const {
-    const int i = j * C + rank;
-    return i < head ? i : i + skip;
-  }
-  __device__ __forceinline__ bool seen(int t) const { return t <= p1 && (t >= low || t < sinks); }
+  // Where tile j begins on the axis; the token at a place of the axis.
+  __device__ __forceinline__ int begin(int j) const { return (j * C + rank) * kKeys; }
+  __device__ __forceinline__ int token(int x) const { return x < mid ? x : x + gap; }
+  // Places from `low_place` on, and those before `sinks`, are seen by some row.
+  __device__ __forceinline__ bool seen(int x) const { return x < end && (x >= low - gap || x < sinks); }
 };
 
 template <int D, bool BF16>
@@ -219,13 +225,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
         __syncwarp();
         if (lane == 0) signal(u_empty + 8 * (k & 1));
         met = true;
-        const View v(u, pa, per_tile, C, rank);
+        const View v(u, pa, per_tile, a.block_shift, C, rank);
         const int32_t* tbl = a.block_tables + static_cast<int64_t>(u.s) * a.max_blocks_per_seq;
         auto entry = [&](int j) {  // this lane's block of tile j: physical block, -1 where no row sees it, -2 outside the pool
           if (j >= v.cnt || lane >= nblk) return -1;
-          const int t = v.tile_of(j) * kKeys + lane * B;
-          if (t > v.p1 || !(t + B > v.low || t < v.sinks)) return -1;
-          const int phys = __ldg(tbl + (t >> a.block_shift));
+          const int x = v.begin(j) + lane * B;
+          if (x >= v.end || !(x + B > v.low - v.gap || x < v.sinks)) return -1;
+          const int phys = __ldg(tbl + (v.token(x) >> a.block_shift));
           return static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks) ? phys : -2;
         };
         int phys = entry(0);
@@ -372,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
         met = true;
         const Unit after = take();
         if (!publish(k + 1, after)) break;
-        const View v(u, pa, per_tile, C, rank);
+        const View v(u, pa, per_tile, a.block_shift, C, rank);
         // Rows that no row of queries sees and blocks outside the pool become
         // zeros: their weights are zero, but what the pool holds there may be
         // anything, and zero times NaN is NaN.
@@ -382,12 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
           ok = __all_sync(kFull, wait(full + 8 * slot, (i / NS) & 1));
           if (!ok) break;
           const uint32_t bad = bad_blocks[slot];
-          const int t0 = v.tile_of(j >> 1) * kKeys;
-          const bool edge = is_v && (t0 + kKeys - 1 > v.p1 || (t0 < v.low && t0 + kKeys > v.sinks));
+          const int x0 = v.begin(j >> 1);
+          const bool edge = is_v && (x0 + kKeys > v.end || (x0 < v.low - v.gap && x0 + kKeys > v.sinks));
           if (bad || edge) {
             const uint32_t at = base + SM::kRing + slot * SM::kTileBytes;
             for (int r = lane; r < kKeys; r += 32) {
-              if (!((bad >> (r >> a.block_shift)) & 1u) && (!is_v || v.seen(t0 + r))) continue;
+              if (!((bad >> (r >> a.block_shift)) & 1u) && (!is_v || v.seen(x0 + r))) continue;
               for (int c = 0; c < NL * 8; ++c)  // rotated by the row: other banks for other lanes
                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
                                  at + (c >> 3) * SM::kLineBytes + r * 128 + ((c + r) & 7) * 16),
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
       bool ok = true;
       for (int k = 0; ok && next_unit(k, u); ++k) {
         signal(u_empty + 8 * (k & 1));
-        const View v(u, pa, per_tile, C, rank);
+        const View v(u, pa, per_tile, a.block_shift, C, rank);
         const int cnt = v.cnt, ntiles = v.ntiles;
         if (cnt == 0) continue;
         ok = wait(q_bar, pairs & 1) && arrive(i);
@@ -504,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
       __syncwarp();
       if (lane == 0) signal(u_empty + 8 * (k & 1));
       met = true;
-      const View v(u, pa, per_tile, C, rank);
+      const View v(u, pa, per_tile, a.block_shift, C, rank);
       ntiles = v.ntiles;
       m = kNegInf;
       l = 0.f;
@@ -517,8 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
       const int first = v.p0 + t * per_tile, last_low = v.low_of(first + per_tile - 1);
       bool ok = true;
       for (int j = 0; j < v.cnt; ++j, ++seen) {
-        const int t0 = v.tile_of(j) * kKeys;
-        const bool whole = t0 + kKeys - 1 <= first && (t0 >= last_low || t0 + kKeys <= my_sinks);  // for every row
+        const int x0 = v.begin(j), t0 = v.token(x0), t1 = v.token(x0 + kKeys - 1);
+        const bool whole = t1 - t0 == kKeys - 1 && t1 <= first && (t0 >= last_low || t1 < my_sinks);  // for every row
         uint32_t x[kKeys];
         float* y = reinterpret_cast<float*>(x);
         float mx = kNegInf;
@@ -529,8 +535,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
 #pragma unroll 1
           for (int c = 0; c < kKeys; c += 32) {
             auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; };
-            const int at = t0 + c;
-            const uint32_t see = below(pos + 1 - at) & (~below(my_low - at) | below(my_sinks - at));
+            auto from = [&](int at) {  // bit i: this row sees token at + i
+              return below(pos + 1 - at) & (~below(my_low - at) | below(my_sinks - at));
+            };
+            const uint32_t before = below(v.mid - (x0 + c));
+            const uint32_t see = (from(x0 + c) & before) | (from(x0 + c + v.gap) & ~before);
             if (__all_sync(kFull, see == kFull)) continue;
             uint32_t o[32];
             tc::ld32(o, s_at + c);
@@ -787,7 +796,10 @@ struct Launch {
     const int per_pair = 2 * (kRows / a.group);
     // Pairs of tiles: at most one more than whole ones a sequence.
     const int64_t pairs = pa.num_tokens / per_pair + std::min<int64_t>(a.num_seqs, pa.num_tokens);
-    const int64_t units = pairs * a.num_kv_heads, tiles = (static_cast<int64_t>(a.max_context_len) + kKeys - 1) / kKeys;
+    const int64_t units = pairs * a.num_kv_heads;
+    int64_t longest = a.max_context_len;  // tokens that a pair of tiles sees
+    if (pa.window > 0) longest = std::min(longest, static_cast<int64_t>(pa.window) + pa.sinks + per_pair + 128);
+    const int64_t tiles = (longest + kKeys - 1) / kKeys;
     int C = 1;
     while (C < kMaxCluster && units * C * 2 <= current_sm_count(152) && 2 * C <= tiles && units <= resident(2 * C)) C *= 2;
     return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(units * C)), dim3(kThreads), Smem<D>::kBytes, C, stream,
