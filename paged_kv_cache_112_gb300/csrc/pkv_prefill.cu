@@ -66,14 +66,14 @@ struct Smem {
   static constexpr int kSlots = D == 128 ? 5 : 8;       // K and V tiles in flight
   static constexpr int kRing = 2 * kTileBytes;          // after the two query tiles
   static constexpr int kRowState = 0;                   // the cluster's meeting, over the tiles: max and sum of 256 rows,
-  static constexpr int kRowsAt = 2048;                  // then [256][D] floats
+  static constexpr int kRowsAt = 2048;                  // then 256 x [D] floats, 4 KB a warp
   static constexpr int kStolen = kRing + kSlots * kTileBytes;
   static constexpr int kUnits = kStolen + 16;           // two units of work
   static constexpr int kBars = kUnits + 64;
   static constexpr int kBarCount = 3 * kSlots + 18;
   static constexpr int kWords = kBars + 8 * kBarCount;  // bad blocks of each slot, tensor memory, abort
   static constexpr int kBytes = kWords + 4 * (kSlots + 2);
-  static_assert(kRowsAt + 2 * kRows * D * 4 <= kStolen, "the cluster's rows fit over the tiles");
+  static_assert(kRowsAt + 2 * kRows * D * 4 + 8 * 4096 <= kStolen, "the cluster's rows fit over the tiles");
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -484,7 +484,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
       __syncthreads();
       cluster_sync();
       cluster_sync();
-      cluster_sync();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
@@ -680,72 +679,87 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
 
     if (C > 1) {
       // The cluster's rows: each CTA scales its part to the rows' common maximum
-      // and leaves it in its shared memory; CTA r adds up rows r, r + C, ...
+      // and sends rows 256 / C i .. to CTA i, which adds the parts up.  32
+      // channels of a warp's rows at a time are brought into order first, so that
+      // a store's lanes lie side by side (16 bytes of 32 rows a store took 6600
+      // cycles in place of 1600).
       float2* state = reinterpret_cast<float2*>(smem + SM::kRowState);
-      float* rows = reinterpret_cast<float*>(smem + SM::kRowsAt);
+      float* inbox = reinterpret_cast<float*>(smem + SM::kRowsAt);  // [from][256 / C rows][D]
+      const int tokens = met ? min(2 * per_tile, u.n - u.first) : 0, rows = 2 * kRows / C;
       __syncthreads();  // the tiles are no longer read
       state[tid] = make_float2(m, l);
       cluster_sync();
-      auto remote = [&](uint32_t addr, int from) {
-        float2 x;
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                     : "=f"(x.x), "=f"(x.y)
-                     : "r"(cluster_map(addr, from))
-                     : "memory");
-        return x;
-      };
-      if (met && t < ntiles) {
-        float top = kNegInf, sum = 0.f;
-        for (int k = 0; k < C; ++k) top = fmaxf(top, remote(smem_u32(state + tid), k).x);
-        const float ref = top == kNegInf ? 0.f : top;
-        for (int k = 0; k < C; ++k) {
-          const float2 x = remote(smem_u32(state + tid), k);
-          sum += x.y * ex2_approx((x.x - ref) * sl2);
-        }
-        const float f = l > 0.f ? ex2_approx((m - ref) * sl2) / sum : 0.f;
+      if (t < ntiles && token < per_tile && t * per_tile + token < tokens) {
+        float2 part[kMaxCluster];
 #pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+          if (k < C)
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                         : "=f"(part[k].x), "=f"(part[k].y)
+                         : "r"(cluster_map(smem_u32(state + tid), k))
+                         : "memory");
+        float top = kNegInf, sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+          if (k < C) top = fmaxf(top, part[k].x);
+        const float ref = top == kNegInf ? 0.f : top;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+          if (k < C) sum += part[k].y * ex2_approx((part[k].x - ref) * sl2);
+        part[0].x = l > 0.f ? ex2_approx((m - ref) * sl2) / sum : 0.f;
+        l = part[0].x;  // the factor of this part
+      }
+      const uint32_t stage = base + SM::kRowsAt + 2 * kRows * D * 4 + warp * 4096;  // 32 rows of 128 bytes
+      const int owner = warp * 32 / rows, first_row = warp * 32 - owner * rows;
+      const uint32_t to = cluster_map(smem_u32(inbox + (rank * rows + first_row) * D), owner);
+      if (__any_sync(kFull, t < ntiles && token < per_tile && t * per_tile + token < tokens)) {
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           tc::ld32(o, o_at + c);
           tc::wait_ld();
-          // Rotated by the row, so that a warp's stores meet different banks.
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (l > 0.f)
-              w = make_float4(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f, __uint_as_float(o[i + 2]) * f,
-                              __uint_as_float(o[i + 3]) * f);
-            *reinterpret_cast<float4*>(rows + tid * D + ((c + i + 4 * r) & (D - 1))) = w;
+          for (int i = 0; i < 8; ++i) {
+            auto val = [&](int e) { return l > 0.f ? __uint_as_float(o[4 * i + e]) * l : 0.f; };
+            *reinterpret_cast<float4*>(smem + (stage - base) + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                make_float4(val(0), val(1), val(2), val(3));
           }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + (lane >> 3);
+            cluster_store_float4(to + (row * D + c) * 4 + 16 * (lane & 7),
+                                 *reinterpret_cast<const float4*>(smem + (stage - base) + row * 128 +
+                                                                  (((lane & 7) ^ (row & 7)) << 4)));
+          }
+          __syncwarp();
         }
       }
       cluster_sync();
       // 4 channels a thread, D / 4 threads a row.
-      const int width = D / 4, tokens = met ? min(2 * per_tile, u.n - u.first) : 0;
-      for (int e = tid; e < ntiles * kRows / C * width; e += 2 * kRows) {
-        const int row = (e / width) * C + rank, ch = 4 * (e % width);
-        const int tile = row / kRows, in = row & (kRows - 1), tok = in / G;
-        if (tok >= per_tile || tile * per_tile + tok >= tokens) continue;
-        const uint32_t addr = smem_u32(rows + row * D + ((ch + 4 * in) & (D - 1)));
+      constexpr int kWidth = D / 4;
+      const int ch = 4 * (tid % kWidth);
+      for (int i = tid / kWidth; i < rows; i += 2 * kRows / kWidth) {
+        const int row = rank * rows + i, tile = row / kRows, in = row & (kRows - 1), tok = in / G;
+        if (tile >= ntiles || tok >= per_tile || tile * per_tile + tok >= tokens) continue;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < C; ++k) {
-          float4 x;
-          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                       : "r"(cluster_map(addr, k))
-                       : "memory");
-          sum.x += x.x;
-          sum.y += x.y;
-          sum.z += x.z;
-          sum.w += x.w;
-        }
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+          if (k < C) {
+            const float4 x = *reinterpret_cast<const float4*>(inbox + (k * rows + i) * D + ch);
+            sum.x += x.x;
+            sum.y += x.y;
+            sum.z += x.z;
+            sum.w += x.w;
+          }
         const int64_t at = row_at(tile, in) + ch;
-        store_out(a.out, at, sum.x, a.out_dtype);
-        store_out(a.out, at + 1, sum.y, a.out_dtype);
-        store_out(a.out, at + 2, sum.z, a.out_dtype);
-        store_out(a.out, at + 3, sum.w, a.out_dtype);
+        if (a.out_dtype == 0)
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = sum;
+        else
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+              a.out_dtype == 1 ? make_uint2(pack_f16(sum.x, sum.y), pack_f16(sum.z, sum.w))
+                               : make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
       }
-      cluster_sync();  // no CTA leaves while its rows are read
     }
   }
   tc::fence_before();
