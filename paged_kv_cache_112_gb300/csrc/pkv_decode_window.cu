@@ -405,17 +405,77 @@ struct Launch {
   }
 };
 
+// Microseconds that `units` units of up to `tiles` tiles take with NW warps a CTA
+// and C CTAs a unit, `held` clusters at a time: the sparse decode's estimate
+// (pkv_sparse_decode.cu has the reasoning), whose 16-bit constants hold here.
+// 4-bit pools: fitted to 18 shapes measured with each NW and C (8 to 2048 units
+// of 10 to 514 tiles): the form of the lowest cost is 2% slower than the best
+// one in the mean, 10% at the most.  A SM takes its tiles at the rate of the
+// conversions, 34 GB a second, not of the memory.  Microseconds, 4 bits:
+//   8 of 514 tiles: 9.1 with 8 warps in clusters of 8, 13.0 of 4, 37.5 alone;
+//   72 of 514: 22.0 with 8 warps of 4, 23.7 of 2, 32.6 with 4 of 2, 39.6 with 8 alone;
+//   512 of 258: 60.8 with 4 warps of 2, 65.2 with 8 alone, 89.6 with 2;
+//   2048 of 18: 28.9 with 2 warps alone, 45.3 with 8.  16 bits:
+//   8 of 514: 11.7 with 8 warps of 8, 17.1 of 4; 72 of 514: 47.9 with 8 of 2, 56.0 alone;
+//   512 of 66: 46.3 with 2 alone, 53.1 with 8.
+template <int D, int POOL>
+float form_cost(int64_t units, int64_t tiles, int group, int NW, int C, int held, int64_t sms) {
+  constexpr bool kFour = POOL == 4;
+  constexpr float kStartUs = kFour ? 2.5f : 3.5f, kTileUs = D == 64 ? 0.6f : 0.9f;
+  constexpr float kSmBytes = kFour ? 34e3f : D == 64 ? 60e3f : 75e3f;  // a microsecond
+  constexpr float kTileBytes = 2.f * (kFour ? fp4::Record<D>::kBytes : kTile * D * 2);
+  const float bytes_us = kFour ? 4.2e6f : 6.4e6f;
+  const int64_t full = (static_cast<int64_t>(held) * C + sms - 1) / sms;  // CTAs a SM holds
+  const int64_t per_sm = C == 1 ? std::min((units + sms - 1) / sms, full) : units * C <= sms ? 1 : full;
+  constexpr int NT = kTilesAStep<POOL>;
+  const int64_t n = NT * (((tiles + NT - 1) / NT + NW * C - 1) / (NW * C));  // tiles of a warp
+  const float tile = std::max(kTileUs, static_cast<float>(per_sm * NW) * (kTileBytes / kSmBytes));
+  const float start = kStartUs + (C > 1 ? 0.4f + 0.1f * static_cast<float>(group) : 0.f);
+  const float wave = start + tile * static_cast<float>(n), waves = static_cast<float>(units) / static_cast<float>(held);
+  const float exposed = units > held ? wave * (0.5f + 0.15f * (waves - 1.f)) / static_cast<float>(full) : 0.f;
+  const float bytes = static_cast<float>(units) * static_cast<float>(tiles) * kTileBytes;
+  return std::max(static_cast<float>((units + held - 1) / held) * wave, start + bytes / bytes_us + exposed) +
+         0.25f * wave;
+}
+
 template <int D, bool BF16, int POOL>
 cudaError_t launch_t(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t stream) {
+  using Two = Launch<D, BF16, POOL, 2>;
   using Four = Launch<D, BF16, POOL, 4>;
   using Eight = Launch<D, BF16, POOL, 8>;
-  if (a.max_parts > 1 || w.window == 0) return Four::launch(a, w, 1, tk, tv, stream);
-  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads, sms = current_sm_count(152);
-  int C = 1;
-  while (C < kMaxCluster && units * C * 2 <= sms) C *= 2;
-  while (C > 1 && units > Eight::resident(C)) C /= 2;
-  return Eight::launch(a, w, C, tk, tv, stream);
+  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * a.max_parts, sms = current_sm_count(152);
+  int64_t tokens = std::min<int64_t>(a.max_context_len, static_cast<int64_t>(a.max_blocks_per_seq) << a.block_shift);
+  tokens = std::min(tokens, static_cast<int64_t>(w.window) + w.sinks);
+  const int64_t tiles = std::max<int64_t>(1, (tokens + kTile - 1) / kTile);
+  int best_nw = 4, best_c = 1;
+  float best = 0.f;
+  auto consider = [&](int NW, int C, int held) {
+    const float cost = form_cost<D, POOL>(units, tiles, a.group, NW, C, held, sms);
+    if (best > 0.f && cost >= best) return;
+    best = cost;
+    best_nw = NW;
+    best_c = C;
+  };
+  if (w.window == 0) {
+    // Partitions: alike, and none but the last short.  Two warps a CTA where
+    // that leaves one wave and four do not (100001 tokens, 8 heads, partitions
+    // of 1024: 30.4 us against 32.8; with 8 warps 36.5).
+    best_nw = units > Four::resident(1) && units <= Two::resident(1) ? 2 : 4;
+  } else {
+    consider(4, 1, Four::resident(1));
+    consider(8, 1, Eight::resident(1));
+    consider(2, 1, Two::resident(1));
+    for (int C = 2; C <= kMaxCluster && units * C <= 8 * sms; C *= 2) {
+      consider(8, C, Eight::resident(C));
+      consider(4, C, Four::resident(C));
+    }
+  }
+  switch (best_nw) {
+    case 2: return Two::launch(a, w, 1, tk, tv, stream);
+    case 4: return Four::launch(a, w, best_c, tk, tv, stream);
+    default: return Eight::launch(a, w, best_c, tk, tv, stream);
+  }
 }
 
 template <int POOL>

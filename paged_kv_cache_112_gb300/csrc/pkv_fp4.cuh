@@ -22,16 +22,19 @@ struct Record {
   static constexpr int kBytes = 9 * D;
 };
 
-// Two values to codes: lo in the low half of the byte.  Nearest, ties to the
-// even code, magnitudes beyond 6 saturate.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+// Eight values to codes, element i in bits 4i ..: nearest, ties to the even
+// code, magnitudes beyond 6 saturate.
+__device__ __forceinline__ uint32_t e2m1x8(const float2 (&x)[4]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 t, z;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
-      "mov.b32 %0, {t, t, t, t};\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(lo), "f"(hi));
-  return r & 0xffu;
+      : "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y));
+  return r;
 }
 
 // Four bytes of codes to four pairs of f16 (the low half's value in the lower half).

@@ -20,6 +20,9 @@
 // kernel: 52% of the issue slots, 28% of DRAM, and loads that wait for one
 // another (position -> angles, sum -> weights, slot -> scale) as the largest
 // stall.  With few tokens that latency alone (1.7 us for one, 3.4 for 256).
+// 16384 tokens of 32 + 16 heads into 4-bit pools take 85.9 us, 1.6 times their
+// bytes' time: quantising a row is some 100 instructions of 32 lanes for four
+// heads, next to the norm's and the rotation's.
 //
 // Layout: D/16 lanes share a head, each holding two 16-byte chunks chosen so
 // that both members of every rotated pair (i, i + rot_dim/2) sit in one lane:
@@ -97,7 +100,7 @@ __device__ __forceinline__ uint2 codes8(const F2 (&x)[4], float scale) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// 4-bit rows.  The largest magnitude of a chunk; NaN where it holds one.
+// 4-bit rows.  The larger of two, of three magnitudes; NaN where one is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -108,32 +111,39 @@ __device__ __forceinline__ float top8(const F2 (&x)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = halves(x[i]);
-    m = max_nan(m, max_nan(fabsf(f.x), fabsf(f.y)));
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(f.x)), "f"(fabsf(f.y)));
   }
   return m;
 }
 
-// Eight e2m1 codes (element i in bits 4i ..) of x / s, s the value of an e4m3
-// scale, the quotient as IEEE float32 division gives it: with y = RN(1 / s)
-// and q = RN(x y), RN(q + (x - q s) y) is the rounded quotient (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990; x - q s is exact).  16-bit values often lie on a border
-// exactly, so an approximate quotient would not do.  Where a quotient is not
-// finite it saturates as it is; a scale of 0 (or NaN, when the values mean
-// nothing) gives zeros.
+// IEEE quotients without a divide: with y = RN(1 / b) and q = RN(a y),
+// RN(q + (a - q b) y) is the rounded quotient (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990; a - q b is
+// exact).  16-bit values often lie on a border of the codes exactly, so an
+// approximate quotient would not do.
+__device__ __forceinline__ float sixth(float a) {
+  constexpr float y = 1.f / 6.f;
+  const float q = a * y;
+  return a < 3e38f ? fmaf(fmaf(-q, 6.f, a), y, q) : q;  // infinite and NaN as they are
+}
+
+// Eight e2m1 codes of x / s, s the value of an e4m3 scale.  Where a quotient is not finite it saturates as it is; a scale of
+// 0 (or NaN, when the values mean nothing) gives zeros.
 __device__ __forceinline__ uint32_t codes8_e2m1(const F2 (&x)[4], float s, float top) {
   const bool usable = s > 0.f;
   const float inv = usable ? __frcp_rn(s) : 0.f, div = usable ? s : 0.f;
   const F2 y = pair(inv, inv), d = pair(-div, -div);
-  uint32_t r = 0;
+  float2 r[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    F2 q = mul2(x[i], y);
-    if (top < 3e38f) q = fma2(fma2(q, d, x[i]), y, q);
-    const float2 f = halves(q);
-    r |= fp4::e2m1x2(f.x, f.y) << (8 * i);
+  for (int i = 0; i < 4; ++i) r[i] = halves(mul2(x[i], y));
+  if (top < 3e38f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const F2 q = pair(r[i].x, r[i].y);
+      r[i] = halves(fma2(fma2(q, d, x[i]), y, q));
+    }
   }
-  return r;
+  return fp4::e2m1x8(r);
 }
 
 // One lane's work on a head: the norm, the rotation and the stores of its two
@@ -267,30 +277,22 @@ struct LaneWork {
     }
     [[maybe_unused]] float top0 = 0.f, top1 = 0.f;  // the largest magnitudes of the two chunks' groups
     if constexpr (POOL == 4) {
-      if (!is_q) {
+      if (__any_sync(kFull, !is_q)) {
         const float* hs = is_v ? a.v_scale : a.k_scale;
-        if (hs && h < heads) {
-          const float inv = __frcp_rn(__ldg(hs + g));
-          const F2 m = pair(inv, inv);
+        const float inv = hs && !is_q && h < heads ? __frcp_rn(__ldg(hs + g)) : 1.f;
+        const F2 m = pair(inv, inv);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            z0[j] = mul2(x0[j], m);
-            z1[j] = mul2(x1[j], m);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            z0[j] = x0[j];
-            z1[j] = x1[j];
-          }
+        for (int j = 0; j < 4; ++j) {
+          z0[j] = mul2(x0[j], m);
+          z1[j] = mul2(x1[j], m);
         }
         top0 = top8(z0);
         top1 = top8(z1);
+        const float a0 = __shfl_sync(kFull, top0, mate0), a1 = __shfl_sync(kFull, top1, mate0);
+        const float b0 = __shfl_sync(kFull, top0, mate1), b1 = __shfl_sync(kFull, top1, mate1);
+        top0 = max_nan(top0, second0 ? a1 : a0);
+        top1 = max_nan(top1, second1 ? b1 : b0);
       }
-      const float a0 = __shfl_sync(kFull, top0, mate0), a1 = __shfl_sync(kFull, top1, mate0);
-      const float b0 = __shfl_sync(kFull, top0, mate1), b1 = __shfl_sync(kFull, top1, mate1);
-      top0 = max_nan(top0, second0 ? a1 : a0);
-      top1 = max_nan(top1, second1 ? b1 : b0);
     }
     if (h >= heads) return;
     if (is_q || (a.k_out && !is_v) || (POOL == 16 && !is_v && writes)) {
@@ -317,7 +319,7 @@ struct LaneWork {
                      (static_cast<int64_t>(g) << (a.block_shift - 4)) * fp4::Record<D>::kBytes;
       uint8_t* codes = rec + row_in_tile * fp4::Record<D>::kRowBytes;
       uint8_t* scales = rec + fp4::Record<D>::kScalesAt + row_in_tile * fp4::Record<D>::kRowScales;
-      const uint32_t s01 = fp8::e4m3x2_satfinite(__fdiv_rn(top0, 6.f), __fdiv_rn(top1, 6.f));
+      const uint32_t s01 = fp8::e4m3x2_satfinite(sixth(top0), sixth(top1));
       const uint32_t sf = fp4::e4m3x2_to_f16(s01);
       const float2 sv = __half22float2(*reinterpret_cast<const __half2*>(&sf));
       *reinterpret_cast<uint32_t*>(codes + 4 * c0) = codes8_e2m1(z0, sv.x, top0);
@@ -479,9 +481,10 @@ __global__ void __launch_bounds__(kStreamWarps * 32) norm_rope_stream_kernel(con
 // kernel's shorter start counts for more.  Microseconds direct / streaming at
 // 81, 162, 323 and 647 groups a SM (32 + 16 heads, 16 bits): 5.8 / 7.1,
 // 13.0 / 13.1, 24.0 / 20.2, 45.3 / 34.8; FP8 pools (32 + 8 heads) at 135,
-// 270 and 539: 11.0 / 13.1, 20.2 / 21.1, 37.2 / 35.5.
+// 270 and 539: 11.0 / 13.1, 20.2 / 21.1, 37.2 / 35.5; 4-bit pools (32 + 16
+// heads) at 162, 323 and 647: 14.5 / 16.7, 26.1 / 26.4, 49.4 / 46.3.
 template <int POOL>
-constexpr int kManyTasks = POOL == 8 ? 320 : 160;
+constexpr int kManyTasks = POOL == 16 ? 160 : 320;
 
 template <int D, bool BF16, int POOL>  // POOL: bits of a pool's elements
 cudaError_t launch_t(const NormRopeArgs& a, cudaStream_t stream) {
