@@ -112,9 +112,14 @@ pkv_status prepare_summarize(SummarizeArgs* a, void* summary, float* summary_sca
 int64_t fp4_block_bytes(int num_layers, int block_size, int num_kv_heads, int head_dim) {
   return static_cast<int64_t>(num_layers) * (block_size / 16) * num_kv_heads * (9 * head_dim);
 }
-pkv_status check_fp4(int num_layers, int block_size, const float* k_scale, const float* v_scale) {
+pkv_status check_fp4(int num_layers, int block_size, int num_blocks, int num_kv_heads, const float* k_scale,
+                     const float* v_scale) {
   if (num_layers <= 0 || num_layers > kMaxLayers) return PKV_ERR_INVALID_ARG;
   if (block_shift_of(block_size) < 4) return PKV_ERR_UNSUPPORTED;
+  // Records are numbered in 32 bits.
+  if (num_blocks > 0 && num_kv_heads > 0 &&
+      (num_kv_heads > 0x7fffff || fp4_block_bytes(num_layers, block_size, num_kv_heads, 1) / 9 > 0x7fffffff / num_blocks))
+    return PKV_ERR_UNSUPPORTED;
   return aligned(k_scale, 4) && aligned(v_scale, 4) ? PKV_OK : PKV_ERR_INVALID_ARG;
 }
 
@@ -393,7 +398,7 @@ pkv_status pkv_write_cache_fp4(const void* k_new, const void* v_new, void* k_poo
                                const float* v_scale, const int32_t* slot_mapping, int num_tokens,
                                int64_t new_row_stride, int num_kv_heads, int head_dim, int block_size, int num_blocks,
                                int num_layers, pkv_dtype new_dtype, int32_t* dev_status, void* stream) {
-  pkv_status st = check_fp4(num_layers, block_size, k_scale, v_scale);
+  pkv_status st = check_fp4(num_layers, block_size, num_blocks, num_kv_heads, k_scale, v_scale);
   if (st != PKV_OK) return st;
   NormRopeArgs a{};
   st = prepare_norm_rope(&a, nullptr, 0, nullptr, 0, nullptr, 0, k_new, v_new, new_row_stride, nullptr, nullptr, 0.f,
@@ -415,7 +420,7 @@ pkv_status pkv_norm_rope_write_fp4(void* q_out, int64_t q_out_stride, void* k_ou
                                    const int32_t* slot_mapping, int num_tokens, int num_q_heads, int num_kv_heads,
                                    int head_dim, int block_size, int num_blocks, int num_layers, pkv_dtype new_dtype,
                                    int32_t* dev_status, void* stream) {
-  pkv_status st = check_fp4(num_layers, block_size, k_scale, v_scale);
+  pkv_status st = check_fp4(num_layers, block_size, num_blocks, num_kv_heads, k_scale, v_scale);
   if (st != PKV_OK) return st;
   NormRopeArgs a{};
   st = prepare_norm_rope(&a, q_out, q_out_stride, k_out, k_out_stride, q, q_stride, k, v, new_row_stride, q_weight,
@@ -434,7 +439,7 @@ pkv_status pkv_copy_blocks_fp4(void* k_pool, void* v_pool, const int32_t* pairs,
                                int num_kv_heads, int head_dim, int block_size, int num_blocks, int32_t* dev_status,
                                void* stream) {
   if (num_pairs < 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0) return PKV_ERR_INVALID_ARG;
-  const pkv_status st = check_fp4(num_layers, block_size, nullptr, nullptr);
+  const pkv_status st = check_fp4(num_layers, block_size, num_blocks, num_kv_heads, nullptr, nullptr);
   if (st != PKV_OK) return st;
   if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
   if (num_pairs == 0) return PKV_OK;
@@ -459,7 +464,7 @@ pkv_status pkv_decode_attention_fp4(void* out, const void* q, const void* k_pool
                                     float scale, int partition_size, int max_context_len, void* workspace,
                                     size_t workspace_bytes, pkv_dtype q_dtype, pkv_dtype out_dtype,
                                     int32_t* dev_status, void* stream) {
-  pkv_status st = check_fp4(num_layers, block_size, k_scale, v_scale);
+  pkv_status st = check_fp4(num_layers, block_size, num_blocks, num_kv_heads, k_scale, v_scale);
   if (st != PKV_OK) return st;
   if (partition_size == PKV_PARTITION_BALANCED) return PKV_ERR_UNSUPPORTED;
   if (partition_size < 0) return PKV_ERR_INVALID_ARG;
@@ -472,7 +477,7 @@ pkv_status pkv_decode_attention_fp4(void* out, const void* q, const void* k_pool
   const int64_t len = max_context_len > 0 ? max_context_len : 1;
   const int64_t whole = (len + kTile - 1) / kTile * kTile, size = partition_size > 0 ? partition_size : whole;
   const int64_t parts = (len + size - 1) / size;
-  if (parts * num_seqs * num_kv_heads > 0x7fffffff || size > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+  if (parts * num_seqs * num_kv_heads > 0x7fffffff || size > 1 << 30) return PKV_ERR_UNSUPPORTED;
   a.partition_size = static_cast<int>(size);
   a.max_parts = static_cast<int>(parts);
   if (parts > 1) {
@@ -523,7 +528,7 @@ pkv_status pkv_decode_window_fp4(void* out, const void* q, const void* k_pool, c
                                  float scale, int window, int sinks, int max_context_len, pkv_dtype q_dtype,
                                  pkv_dtype out_dtype, int32_t* dev_status, void* stream) {
   if (window <= 0 || sinks < 0) return PKV_ERR_INVALID_ARG;
-  pkv_status st = check_fp4(num_layers, block_size, k_scale, v_scale);
+  pkv_status st = check_fp4(num_layers, block_size, num_blocks, num_kv_heads, k_scale, v_scale);
   if (st != PKV_OK) return st;
   DecodeArgs a{};
   st = prepare_rows(&a, out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,

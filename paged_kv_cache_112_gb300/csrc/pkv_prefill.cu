@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
   tc::fence_after();
   constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
   const bool odd_memory = *tmem_at != tmem;
+  if (odd_memory && tid == 0) flag(a.dev_status, 32u);  // PKV_DEV_ERR_SMEM: nothing is done
 
   // Waits for the phase; gives up at the time limit, or when another thread has.
   auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -621,16 +622,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
         tc::fence_after();
       }
       if (C > 1) break;  // the rows meet below
-      // 32 bytes a store: whole sectors of the thread's own row.
-      const float f = l > 0.f ? 1.f / l : 0.f;
-      const bool none = __any_sync(kFull, l == 0.f);  // a row without a visible token: tensor memory may hold anything
+      const float f = l == 0.f ? 0.f : 1.f / l;  // a sum that is no number makes the row none
       const int eb = a.out_dtype == 0 ? 4 : 2;
       const bool live = token < per_tile && t * per_tile + token < v.tokens;
       uint8_t* mine = static_cast<uint8_t*>(a.out) +
                       (((static_cast<int64_t>(u.row0) + u.first + t * per_tile + token) * a.num_q_heads + u.g * G +
                         (r - token * G)) * D * eb);
       auto store8 = [&](uint8_t* to, const uint32_t (&x)[8]) {
-        if (!live) return;
         if (pa.out_sectors) {
           asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]),
                        "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
@@ -640,38 +638,69 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
           reinterpret_cast<uint4*>(to)[1] = make_uint4(x[4], x[5], x[6], x[7]);
         }
       };
+      auto free_rows = [&]() {  // the next pair's products may begin
+        if (v.cnt == 0) return;
+        tc::fence_before();
+        signal(o_free + 8 * t);
+      };
+      if (eb == 2) {
+        // A quad of lanes has 64 channels of a row, every fourth pair each; two
+        // exchanges give each lane 16 in a row, so that a store is eight lines of
+        // 128 bytes.  (Each lane storing its own row: 32 lines a store, 5500
+        // cycles a pair of tiles.)
+        const uint32_t lives = __ballot_sync(kFull, live), empty_rows = __ballot_sync(kFull, l == 0.f);
+        const bool up2 = lane & 2, up1 = lane & 1;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        tc::ld32(o, o_at + c);
-        tc::wait_ld();
-        if (c + 32 == D && v.cnt > 0) {  // the next pair's products may begin
-          tc::fence_before();
-          signal(o_free + 8 * t);
-        }
-        if (none) {
+        for (int part = 0; part < D / 32; ++part) {  // 16 rows, 64 channels
+          const int c = (part >> 1) * 64, half = part & 1;
+          uint32_t o[32];
+          tc::ld16x64(o, o_at + (static_cast<uint32_t>(half) << 20) + c);
+          tc::wait_ld();
+          if (part + 1 == D / 32) free_rows();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0u : o[i];
-        }
-        auto val = [&](int i) { return __uint_as_float(o[i]) * f; };
-        if (eb == 2) {
+          for (int e = 0; e < 2; ++e) {
+            const int row = 16 * half + 8 * e + (lane >> 2);  // of the warp's
+            const float fr = __shfl_sync(kFull, f, row);
+            uint8_t* to = reinterpret_cast<uint8_t*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(mine), row));
+            uint32_t w[8];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int e = 16 * h + 2 * i;
-              x[i] = a.out_dtype == 1 ? pack_f16(val(e), val(e + 1)) : pack_bf16(val(e), val(e + 1));
+            for (int k = 0; k < 8; ++k) {
+              const float x = __uint_as_float(o[4 * k + 2 * e]) * fr, y = __uint_as_float(o[4 * k + 2 * e + 1]) * fr;
+              w[k] = a.out_dtype == 1 ? pack_f16(x, y) : pack_bf16(x, y);
+              if ((empty_rows >> row) & 1u) w[k] = 0u;  // no visible token: whatever tensor memory holds
             }
-            store8(mine + 2 * c + 32 * h, x);
+            uint32_t h[8], z[8];  // after the exchange with the lane 2 further: [which of the two][k of four]
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t keep = up2 ? w[k + 4] : w[k], got = __shfl_xor_sync(kFull, up2 ? w[k] : w[k + 4], 2);
+              h[k] = up2 ? got : keep;
+              h[4 + k] = up2 ? keep : got;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {  // lanes (b, own) and (b, the other's) of the quad
+                const uint32_t keep = up1 ? h[4 * b + k + 2] : h[4 * b + k];
+                const uint32_t got = __shfl_xor_sync(kFull, up1 ? h[4 * b + k] : h[4 * b + k + 2], 1);
+                z[4 * k + 2 * b] = up1 ? got : keep;
+                z[4 * k + 2 * b + 1] = up1 ? keep : got;
+              }
+            if ((lives >> row) & 1u) store8(to + 2 * c + 32 * (lane & 3), z);
           }
-        } else {
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tc::ld32(o, o_at + c);
+          tc::wait_ld();
+          if (c + 32 == D) free_rows();
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             uint32_t x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(val(8 * h + i));
-            store8(mine + 4 * c + 32 * h, x);
+            for (int i = 0; i < 8; ++i) x[i] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[8 * h + i]) * f);
+            if (live) store8(mine + 4 * c + 32 * h, x);
           }
         }
       }
@@ -706,8 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
 #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k)
           if (k < C) sum += part[k].y * ex2_approx((part[k].x - ref) * sl2);
-        part[0].x = l > 0.f ? ex2_approx((m - ref) * sl2) / sum : 0.f;
-        l = part[0].x;  // the factor of this part
+        l = l == 0.f ? 0.f : ex2_approx((m - ref) * sl2) / sum;  // the factor of this part
       }
       const uint32_t stage = base + SM::kRowsAt + 2 * kRows * D * 4 + warp * 4096;  // 32 rows of 128 bytes
       const int owner = warp * 32 / rows, first_row = warp * 32 - owner * rows;
@@ -720,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
           tc::wait_ld();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            auto val = [&](int e) { return l > 0.f ? __uint_as_float(o[4 * i + e]) * l : 0.f; };
+            auto val = [&](int e) { return l == 0.f ? 0.f : __uint_as_float(o[4 * i + e]) * l; };
             *reinterpret_cast<float4*>(smem + (stage - base) + lane * 128 + ((i ^ (lane & 7)) << 4)) =
                 make_float4(val(0), val(1), val(2), val(3));
           }

@@ -104,6 +104,15 @@ __device__ __forceinline__ void ld32(uint32_t* r, uint32_t at) {
       : PKV_R8(r, 0), PKV_R8(r, 8), PKV_R8(r, 16), PKV_R8(r, 24)
       : "r"(at));
 }
+// 64 columns of 16 lanes (those from the address'): thread i has columns 8k + 2
+// (i % 4), + 1 of lanes i / 4 (r[4k], r[4k + 1]) and i / 4 + 8 (r[4k + 2], r[4k + 3]).
+__device__ __forceinline__ void ld16x64(uint32_t* r, uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : PKV_R8(r, 0), PKV_R8(r, 8), PKV_R8(r, 16), PKV_R8(r, 24)
+      : "r"(at));
+}
 __device__ __forceinline__ void st32(uint32_t at, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "

@@ -263,6 +263,44 @@ def test_decode_layers_view():
     d.check(100, 5)
 
 
+def test_pools_past_four_gigabytes():
+    """Records whose bytes lie past 2^32: written, read whole and through a window."""
+    H, D, B, n = 8, 128, 16, 100
+    NB = (1 << 32) // (B * H * D * 9 // 16) + 50
+    kp, vp = (torch.zeros(NB, H, 1, 9 * D, dtype=torch.uint8, device="cuda") for _ in range(2))
+    rng = np.random.default_rng(5)
+    k, v = rows(rng, n, H, D, "bf16", False), rows(rng, n, H, D, "bf16", False)
+    blocks = np.arange(NB - 1, NB - 1 - 7, -1).astype(np.int32)
+    slots = blocks[np.arange(n) // B] * B + np.arange(n) % B
+    st = status()
+    pkv.write_cache_fp4(k.cuda(), v.cuda(), kp, vp, None, None, torch.from_numpy(slots.astype(np.int32)).cuda(), status=st)
+    vals = []
+    for x in (k, v):
+        code, sc = R.quantise(x.float().numpy())
+        vals.append(R.E2M1[code] * R.E4M3[sc].repeat(16, -1))
+    q = torch.from_numpy(rng.normal(size=(1, 8, D))).bfloat16().cuda()
+    out, win = (torch.zeros(1, 8, D, device="cuda") for _ in range(2))
+    tables, lens = torch.from_numpy(blocks[None]).cuda(), torch.tensor([n], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(pkv.decode_workspace_bytes(1, 8, D, n, 32), dtype=torch.uint8, device="cuda")
+    pkv.decode_attention_fp4(out, q, kp, vp, None, None, tables, lens, 0.1, partition_size=32, max_context_len=n,
+                             workspace=ws, status=st)
+    pkv.decode_window_fp4(win, q, kp, vp, None, None, tables, lens, 0.1, window=30, sinks=1, max_context_len=n, status=st)
+    assert int(st.item()) == 0
+    for got, w, f in ((out, 0, 0), (win, 30, 1)):
+        want, extra = R.attend(q[0].double().cpu().numpy(), *vals, 0.1, R.visible(n - 1, n, w, f))
+        far = R.bound(want, extra, D, n, 2.0 ** -11, 2.0 ** -24, 2.0 ** -33)
+        assert np.all(np.abs(got[0].double().cpu().numpy() - want) <= far)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_units_and_repeated_calls(D):
+    """More partitions than the device holds at once, called again on the same workspace."""
+    d = Decode([3000 + 37 * (i % 7) for i in range(40)], 8, 4, D, out=torch.bfloat16, seed=8)
+    for _ in range(2):
+        d.attend(partition_size=128)
+    d.check()
+
+
 def test_bad_tables_and_lengths():
     d = Decode([200, 300, 50], 8, 2, seed=5)
     keep = d.tables.copy()

@@ -178,6 +178,86 @@ def test_graph_replay_with_other_lengths():
         p.check(rows=20)
 
 
+@pytest.mark.parametrize("past,Hkv", [(0, 20), (3000, 1)])
+@pytest.mark.parametrize("out", [None, torch.float32])
+def test_what_is_no_number_stays_so(past, Hkv, out):
+    """A NaN query, and a NaN or infinite key: the rows that meet them are no numbers, the others are as ever (on
+    whole grids and over clusters)."""
+    n, G = 200, 4
+    p = Prompt([n], [past], G * Hkv, Hkv, seed=41, out=out)
+    p.q[50, 1] = float("nan")
+    at = past + 120
+    blk, off = p.tables[0, at // p.B], at % p.B
+    p.dev[0][blk, off, 0] = float("nan")
+    p.call()
+    torch.cuda.synchronize()
+    assert int(p.st.item()) == 0
+    bad = torch.isnan(p.out[:n]).all(-1).cpu()
+    want = torch.zeros(n, G * Hkv, dtype=torch.bool)
+    want[50, 1] = True
+    want[120:, :G] = True
+    assert torch.equal(bad, want) and torch.equal(torch.isnan(p.out[:n]).any(-1).cpu(), want)
+    got, q = p.out.double().cpu().numpy(), p.q.double().cpu().numpy()
+    k, v = (x[p.tables[0]].reshape(-1, Hkv, p.D)[:n + past] for x in p.vals)
+    for r in (0, 49, 51, 119, n - 1):
+        ok = ~want[r].numpy()
+        ref, extra = R.attend(q[r], np.nan_to_num(k), v, p.scale, R.visible(past + r, n + past, 0, 0))
+        far = R.bound(ref, extra, p.D, n + past, STEP[p.dt], STEP[p.out.dtype], 2.0 ** -32)
+        assert np.all(np.abs(got[r] - ref)[ok] <= far[ok])
+
+
+def test_two_streams_and_graphs_of_whole_grids():
+    """Calls that fill the device, of both head sizes, side by side on two streams, eagerly and from two graphs, with
+    an output that is 16-byte aligned alone."""
+    a, b = Prompt([3000, 2500], [0, 400], 8, 2, seed=21), Prompt([4000, 700, 60], [5, 0, 300], 8, 2, 64, dt="f16", seed=22)
+    flat = torch.full((a.out.numel() + 8,), 77.0, dtype=a.dt, device="cuda")
+    a.out = flat[8:].view(a.out.shape)
+    assert a.out.data_ptr() % 32 == 16
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for p, st in zip((a, b), streams):
+            p.call(stream=st)
+    for p in (a, b):
+        p.check(rows=20)
+        p.out.fill_(77)
+    graphs = []
+    for p, st, w in zip((a, b), streams, (0, 600)):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for _ in range(2):
+                p.call(w, 3)
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    a.check(0, 0, rows=20)
+    b.check(600, 3, rows=20)
+
+
+def test_pools_past_four_gigabytes():
+    """Blocks whose bytes lie past 2^32, for prompts and windowed decode."""
+    H, D, B, n = 8, 128, 16, 300
+    NB = (1 << 32) // (B * H * D * 2) + 40
+    pools = [torch.zeros(NB, B, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    p = Prompt([n], Hq=8, Hkv=8, seed=31)
+    far = torch.arange(NB - 1, NB - 1 - p.tables.shape[1], -1, dtype=torch.int32)
+    for whole, small in zip(pools, p.dev):
+        whole[far.cuda().long()] = small[torch.from_numpy(p.tables[0]).cuda().long()]
+    p.dev, p.d_tables = pools, far[None].cuda()
+    p.call()
+    p.check(rows=20)
+    one = torch.zeros(1, 8, D, device="cuda")
+    pkv.decode_window(one, p.q[n - 1:n].contiguous(), *pools, p.d_tables, p.d_lens, p.scale, window=100, sinks=2,
+                      max_context_len=n, status=p.st)
+    k, v = (x[p.tables[0]].reshape(-1, H, D)[:n] for x in p.vals)
+    want, extra = R.attend(p.q[n - 1].double().cpu().numpy(), k, v, p.scale, R.visible(n - 1, n, 100, 2))
+    assert np.all(np.abs(one[0].double().cpu().numpy() - want) <= R.bound(want, extra, D, n, 2.0 ** -16, 2.0 ** -24))
+
+
 def test_flags():
     p = Prompt([40, 30], [0, 10], seed=2)
     p.d_tables[1, 1] = p.NB

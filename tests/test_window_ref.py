@@ -53,6 +53,7 @@ def test_fp4_refusals(lib):
     assert w(T=0) == pkv.PKV_OK
     assert w(D=96) == w(B=8) == w(B=128) == pkv.PKV_ERR_UNSUPPORTED
     assert w(L=0) == w(L=4097) == w(T=-1) == w(H=0) == w(k=None) == w(kp=FAKE + 8) == pkv.PKV_ERR_INVALID_ARG
+    assert w(H=2 ** 20, L=4096) == pkv.PKV_ERR_UNSUPPORTED  # more records than 32 bits number
     assert w(ks=FAKE + 2) == w(vs=FAKE + 1) == w(stride=100) == w(dt=pkv.PKV_F32) == pkv.PKV_ERR_INVALID_ARG
 
     n = lambda **kw: lib.pkv_norm_rope_write_fp4(
