@@ -475,7 +475,7 @@ pkv_status pkv_decode_attention_fp4(void* out, const void* q, const void* k_pool
                     dev_status);
   if (st != PKV_OK || num_seqs == 0) return st;
   const int64_t len = max_context_len > 0 ? max_context_len : 1;
-  const int64_t whole = (len + kTile - 1) / kTile * kTile, size = partition_size > 0 ? partition_size : whole;
+  const int64_t size = partition_size > 0 ? partition_size : (len + kTile - 1) / kTile * kTile;
   const int64_t parts = (len + size - 1) / size;
   if (parts * num_seqs * num_kv_heads > 0x7fffffff || size > 1 << 30) return PKV_ERR_UNSUPPORTED;
   a.partition_size = static_cast<int>(size);
@@ -489,11 +489,16 @@ pkv_status pkv_decode_attention_fp4(void* out, const void* q, const void* k_pool
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.block_stride = fp4_block_bytes(num_layers, block_size, num_kv_heads, head_dim);
-  const WindowArgs w{0, 0, static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool)};
+  WindowArgs w{0, 0, static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool)};
+  const bool whole = decode_whole_fp4(a, head_dim, q_dtype == PKV_BF16);
+  if (whole) {  // a window of everything
+    w.window = 0x7fffffff;
+    a.max_parts = 1;
+  }
   const CUtensorMap none{};
   st = cuda_status(
       launch_decode_window(a, w, none, none, head_dim, q_dtype == PKV_BF16, true, static_cast<cudaStream_t>(stream)));
-  if (st != PKV_OK || parts == 1) return st;
+  if (st != PKV_OK || whole) return st;
   return cuda_status(launch_decode_reduce(a, head_dim, static_cast<cudaStream_t>(stream)));
 }
 

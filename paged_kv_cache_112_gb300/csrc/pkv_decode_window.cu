@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(NW * 32) decode_window_kernel(const DecodeArgs
   };
   const int64_t head0 = static_cast<int64_t>(s) * a.num_q_heads + g * G;
   auto store4 = [&](int e, float4 o, float l) {
-    const float inv = l > 0.f ? post / l : 0.f;
+    const float inv = l == 0.f ? 0.f : post / l;  // a sum that is no number makes the row none
     store_out(a.out, head0 * D + e, o.x * inv, a.out_dtype);
     store_out(a.out, head0 * D + e + 1, o.y * inv, a.out_dtype);
     store_out(a.out, head0 * D + e + 2, o.z * inv, a.out_dtype);
@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(NW * 32) decode_window_kernel(const DecodeArgs
       } else {
         const int64_t rec = (head0 + h) * a.max_parts + part;
         *reinterpret_cast<float4*>(a.ws_acc + rec * D + d) = make_float4(o.x * post, o.y * post, o.z * post, o.w * post);
-        if (d == 0) a.ws_ml[rec] = make_float2(M, l);
+        // A sum that is no number: over the other parts, and above the zero that the join asks of a sum.
+        if (d == 0) a.ws_ml[rec] = l == l ? make_float2(M, l) : make_float2(3e38f, __int_as_float(0x7f800000));
       }
     }
     return;
@@ -438,44 +439,78 @@ float form_cost(int64_t units, int64_t tiles, int group, int NW, int C, int held
          0.25f * wave;
 }
 
+struct Form {
+  int nw = 8, c = 1;
+  float cost = 0.f;  // microseconds
+};
+
+// The form of the lowest cost; `clusters`: a unit may be shared by CTAs.
 template <int D, bool BF16, int POOL>
-cudaError_t launch_t(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tk, const CUtensorMap& tv,
-                     cudaStream_t stream) {
+Form best_form(int64_t units, int64_t tiles, int group, bool clusters) {
   using Two = Launch<D, BF16, POOL, 2>;
   using Four = Launch<D, BF16, POOL, 4>;
   using Eight = Launch<D, BF16, POOL, 8>;
-  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * a.max_parts, sms = current_sm_count(152);
-  int64_t tokens = std::min<int64_t>(a.max_context_len, static_cast<int64_t>(a.max_blocks_per_seq) << a.block_shift);
-  tokens = std::min(tokens, static_cast<int64_t>(w.window) + w.sinks);
-  const int64_t tiles = std::max<int64_t>(1, (tokens + kTile - 1) / kTile);
-  int best_nw = 4, best_c = 1;
-  float best = 0.f;
+  const int64_t sms = current_sm_count(152);
+  Form best;
   auto consider = [&](int NW, int C, int held) {
-    const float cost = form_cost<D, POOL>(units, tiles, a.group, NW, C, held, sms);
-    if (best > 0.f && cost >= best) return;
-    best = cost;
-    best_nw = NW;
-    best_c = C;
+    const float cost = form_cost<D, POOL>(units, tiles, group, NW, C, held, sms);
+    if (best.cost == 0.f || cost < best.cost) best = Form{NW, C, cost};
   };
-  if (w.window == 0) {
+  if (!clusters) {
     // Partitions: alike, and none but the last short.  Two warps a CTA where
     // that leaves one wave and four do not (100001 tokens, 8 heads, partitions
     // of 1024: 30.4 us against 32.8; with 8 warps 36.5).
-    best_nw = units > Four::resident(1) && units <= Two::resident(1) ? 2 : 4;
-  } else {
-    consider(4, 1, Four::resident(1));
-    consider(8, 1, Eight::resident(1));
-    consider(2, 1, Two::resident(1));
-    for (int C = 2; C <= kMaxCluster && units * C <= 8 * sms; C *= 2) {
-      consider(8, C, Eight::resident(C));
-      consider(4, C, Four::resident(C));
-    }
+    if (units > Four::resident(1) && units <= Two::resident(1))
+      consider(2, 1, Two::resident(1));
+    else
+      consider(4, 1, Four::resident(1));
+    return best;
   }
-  switch (best_nw) {
-    case 2: return Two::launch(a, w, 1, tk, tv, stream);
-    case 4: return Four::launch(a, w, best_c, tk, tv, stream);
-    default: return Eight::launch(a, w, best_c, tk, tv, stream);
+  consider(4, 1, Four::resident(1));
+  consider(8, 1, Eight::resident(1));
+  consider(2, 1, Two::resident(1));
+  for (int C = 2; C <= kMaxCluster && units * C <= 8 * sms; C *= 2) {
+    consider(8, C, Eight::resident(C));
+    consider(4, C, Four::resident(C));
   }
+  return best;
+}
+
+int64_t longest_of(const DecodeArgs& a) {
+  return std::min<int64_t>(a.max_context_len, static_cast<int64_t>(a.max_blocks_per_seq) << a.block_shift);
+}
+int64_t tiles_of(int64_t tokens) { return std::max<int64_t>(1, (tokens + kTile - 1) / kTile); }
+
+template <int D, bool BF16, int POOL>
+cudaError_t launch_t(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tk, const CUtensorMap& tv,
+                     cudaStream_t stream) {
+  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * a.max_parts;
+  const int64_t seen = w.window > 0 ? static_cast<int64_t>(w.window) + w.sinks : a.partition_size;
+  const Form f = best_form<D, BF16, POOL>(units, tiles_of(std::min(longest_of(a), seen)), a.group, w.window > 0);
+  switch (f.nw) {
+    case 2: return Launch<D, BF16, POOL, 2>::launch(a, w, 1, tk, tv, stream);
+    case 4: return Launch<D, BF16, POOL, 4>::launch(a, w, f.c, tk, tv, stream);
+    default: return Launch<D, BF16, POOL, 8>::launch(a, w, f.c, tk, tv, stream);
+  }
+}
+
+// A history in partitions takes a second kernel, which joins them, and leaves
+// SMs without work where there are few; over a cluster it takes one launch, but
+// not more than eight SMs.  Microseconds of histories of 8 KV heads, whole and
+// in partitions of 1024: 1 of 4000 tokens 6.3 and 11.0, 4 of 10000 16.1 and
+// 19.2, 1 of 40000 26.9 and 19.0, 16 of 8000 39.5 and 36.0, 64 of 2000 alike.
+// Lengths differ, and only the longest is known here: whole has to be the
+// faster one with every history that long and with one of them, by more than
+// the estimates' error where there are many (16 of 8000: 5% apart).
+template <int D, bool BF16>
+bool whole_t(const DecodeArgs& a) {
+  const int64_t longest = longest_of(a), in_part = std::min<int64_t>(longest, a.partition_size);
+  constexpr float kJoinUs = 2.f;
+  auto wins = [&](int64_t units) {
+    return 1.05f * best_form<D, BF16, 4>(units, tiles_of(longest), a.group, true).cost <
+           best_form<D, BF16, 4>(units * a.max_parts, tiles_of(in_part), a.group, false).cost + kJoinUs;
+  };
+  return wins(a.num_kv_heads) && wins(static_cast<int64_t>(a.num_seqs) * a.num_kv_heads);
 }
 
 template <int POOL>
@@ -489,6 +524,12 @@ cudaError_t launch_p(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap
 }
 
 }  // namespace
+
+bool decode_whole_fp4(const DecodeArgs& a, int head_dim, bool bf16) {
+  if (a.num_seqs == 0 || a.max_parts <= 1) return true;
+  if (head_dim == 64) return bf16 ? whole_t<64, true>(a) : whole_t<64, false>(a);
+  return bf16 ? whole_t<128, true>(a) : whole_t<128, false>(a);
+}
 
 cudaError_t launch_decode_window(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tmap_k,
                                  const CUtensorMap& tmap_v, int head_dim, bool bf16, bool fp4, cudaStream_t stream) {

@@ -301,6 +301,35 @@ def test_many_units_and_repeated_calls(D):
     d.check()
 
 
+@pytest.mark.parametrize("lens,Hkv,D,ps", [([40000, 1, 0, 333], 8, 128, 1024), ([50000, 49999], 4, 64, 1024),
+                                           ([4000, 900], 2, 128, 256), ([4000, 900], 2, 64, 256)])
+def test_a_visible_nan_stays_one(lens, Hkv, D, ps):
+    """In partitions (long histories of many heads) and whole: the heads that meet a NaN scale give no numbers, the
+    others are as ever."""
+    d = Decode(lens, 2 * Hkv, Hkv, D, seed=ps)
+    d.attend(partition_size=ps)
+    d.check()
+    assert bool((d.ws != 0xFF).any()) == (max(lens) > 10000)  # the workspace holds what the partitions gave
+    t = lens[0] // 2
+    d.dev[0][d.tables[0, t // 16], 1, 0, 8 * D + t % 16 * (D // 16)] = 0x7F
+    before = d.out.clone()
+    d.attend(partition_size=ps)
+    bad = torch.isnan(d.out)
+    assert bool(bad[0, 2:4].all()) and int(bad.sum()) == 2 * D
+    assert torch.equal(d.out[~bad], before[~bad])
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("window", [40, 3900])
+def test_a_nan_in_the_window_stays_one(bits, window):
+    d = Decode([4000, 900], 8, 4, bits=bits, seed=window)
+    d.window(window, 4)
+    before = d.out.clone()
+    d.poison(0, 3985)
+    d.window(window, 4)
+    assert bool(torch.isnan(d.out[0]).all()) and torch.equal(d.out[1], before[1])
+
+
 def test_bad_tables_and_lengths():
     d = Decode([200, 300, 50], 8, 2, seed=5)
     keep = d.tables.copy()
