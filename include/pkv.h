@@ -722,10 +722,12 @@ pkv_status pkv_decode_window_fp4(void* out, const void* q, const void* k_pool, c
  *   q            : [num_tokens][num_q_heads][head_dim] of kv_dtype, 16-byte aligned,
  *                  consecutive tokens q_stride elements apart (0 = dense, else a
  *                  multiple of 8 and at least a row).
- *   query_start  : int32[num_seqs + 1], ascending from 0 to at most num_tokens (device).
- *                  Rows at and behind query_start[num_seqs] are left as they are.
- *                  Entries that descend or lie outside are clamped and set
- *                  PKV_DEV_ERR_LENGTH, as does n > L (rows with p < 0 are zero).
+ *   query_start  : int32[num_seqs + 1], ascending, from 0 or more to at most num_tokens
+ *                  (device).  Rows before the first and from the last entry on are
+ *                  left as they are.  Entries that descend or lie outside are clamped
+ *                  and set PKV_DEV_ERR_LENGTH (a row that two sequences then claim
+ *                  holds what either gives, or is left), as does n > L (rows with
+ *                  p < 0 are zero).
  *   window, sinks: >= 0; window 0: all of the history (sinks then mean nothing).
  * Blocks without a token that some new one sees are not read.  A table entry
  * outside the pool, of a block that is seen, sets PKV_DEV_ERR_BLOCK; the block

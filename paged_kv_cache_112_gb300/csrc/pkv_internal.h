@@ -336,11 +336,11 @@ cudaError_t launch_select_blocks(const SelectArgs& a, int head_dim, bool bf16, c
 cudaError_t launch_decode_sparse(const DecodeArgs& a, const SparseArgs& sp, const CUtensorMap& tmap_k,
                                  const CUtensorMap& tmap_v, int head_dim, bool bf16, bool fp8, cudaStream_t stream);
 
+// Whether 4-bit histories are read whole, a cluster each, in less time than in
+// their partitions (a.partition_size, a.max_parts).
+bool decode_whole_fp4(const DecodeArgs& a, int head_dim, bool bf16);
 // The visible tiles of each sequence, over 16-bit pools (tensor maps as for
 // launch_decode_sparse) or 4-bit pools (maps unused).
-// decode_whole_fp4: whether 4-bit histories are read whole, a cluster each, in
-// less time than in their partitions (a.partition_size, a.max_parts).
-bool decode_whole_fp4(const DecodeArgs& a, int head_dim, bool bf16);
 cudaError_t launch_decode_window(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tmap_k,
                                  const CUtensorMap& tmap_v, int head_dim, bool bf16, bool fp4, cudaStream_t stream);
 

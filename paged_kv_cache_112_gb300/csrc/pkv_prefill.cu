@@ -290,14 +290,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
         for (int top = S - 1; top >= 0; top -= 32) {
           const int s = top - lane;
           int lo = 0, n = 0, len = 0;
-          bool odd = false;
           if (s >= 0) {
             const int from = pa.query_start[s], to = pa.query_start[s + 1];
             len = a.context_lens[s];
             lo = min(max(from, 0), pa.num_tokens);
             const int hi = min(max(to, lo), pa.num_tokens);
             n = hi - lo;
-            odd = lo != from || hi != to;
           }
           const int mine = (n + per_pair - 1) / per_pair;
           int incl = mine;
@@ -316,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
           if (lane == who) {
             const bool report = first == 0 && r.g == 0 && rank == 0;
             len = clamp_len(a, len, report);
-            if (report && (len < n || odd)) flag(a.dev_status, 8u);  // PKV_DEV_ERR_LENGTH
+            if (report && len < n) flag(a.dev_status, 8u);  // PKV_DEV_ERR_LENGTH
           }
           r.s = __shfl_sync(kFull, s, who);
           r.first = __shfl_sync(kFull, first, who);
@@ -375,6 +373,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
       if (u.s < 0) u = take();
       int i = 0;
       bool ok = publish(0, u);
+      if (blockIdx.x == 0) {  // while the first tiles are on their way; a sequence without rows has no unit to report it
+        for (int s = lane; s < a.num_seqs; s += 32) {
+          const int from = pa.query_start[s], to = pa.query_start[s + 1];
+          if (from < 0 || to < from || to > pa.num_tokens) flag(a.dev_status, 8u);  // PKV_DEV_ERR_LENGTH
+        }
+        __syncwarp();
+      }
       for (int k = 0; ok && u.s >= 0; ++k) {
         met = true;
         const Unit after = take();

@@ -283,6 +283,16 @@ def test_flags():
     p.call()
     p.lens[1] = 0
     p.check(want_status=pkv.DEV_ERR_LENGTH)
+    # a descent that leaves a sequence without rows: alone, behind many others, and of no rows at all
+    for start in ([0, 5, 3, 8], [0] * 40 + [4, 3] + [8] * 40, [8, 8, 2], [-3, 0, 8], [20, 20, 20]):
+        S = len(start) - 1
+        p = Prompt([4] * S, seed=2)
+        p.q, p.out = p.q[:8], p.out[:8]
+        p.d_start = torch.tensor(start, dtype=torch.int32, device="cuda")
+        p.d_lens[:] = 16
+        p.call(max_len=16)
+        torch.cuda.synchronize()
+        assert int(p.st.item()) == pkv.DEV_ERR_LENGTH, start
     # starts that descend or lie outside
     p = Prompt([40, 30], [0, 10], seed=2)
     p.d_start[2] = 1000
