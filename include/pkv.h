@@ -633,6 +633,7 @@ pkv_status pkv_decode_sparse_fp8(void* out, const void* q, const void* k_pool, c
  * ties to even, magnitudes beyond 448 and 6 saturating.  s = 0: codes of zero.
  * (The sign of a zero is not specified.)
  * A group with a NaN gets the scale NaN: its 16 values are.
+ * A slot given twice in a call holds some mix of both rows.
  * Other arguments and flags as pkv_write_cache_fp8.
  */
 pkv_status pkv_write_cache_fp4(const void* k_new, const void* v_new, void* k_pool, void* v_pool, const float* k_scale,

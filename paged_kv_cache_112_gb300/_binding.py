@@ -582,8 +582,8 @@ def copy_blocks_fp4(k_pool, v_pool, pairs, *, status=None, stream=None):
 
 def decode_attention_fp4(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale, *,
                          partition_size=0, max_context_len, workspace=None, status=None, stream=None):
-    """pkv_decode_attention_fp4: decode_attention over 4-bit pools (partition kernel + reduce kernel; workspace of
-    decode_workspace_bytes)."""
+    """pkv_decode_attention_fp4: decode_attention over 4-bit pools (partition kernel + reduce kernel, or one kernel where
+    whole histories take less time; workspace of decode_workspace_bytes)."""
     (_EXT or _ext()).decode_attention_fp4(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens, scale,
                                           partition_size, max_context_len, workspace, status, stream)
 

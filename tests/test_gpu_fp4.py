@@ -320,6 +320,20 @@ def test_a_visible_nan_stays_one(lens, Hkv, D, ps):
 
 
 @pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_other_scales(bits, scale):
+    """A scale of 0 (every visible token alike) and a negative one."""
+    d = Decode([0, 1, 100, 700], 8, 2, bits=bits, seed=3)
+    d.scale = scale
+    d.window(60, 5)
+    d.check(60, 5)
+    if bits == 4:
+        for ps in (0, 64):
+            d.attend(partition_size=ps)
+            d.check()
+
+
+@pytest.mark.parametrize("bits", [4, 16])
 @pytest.mark.parametrize("window", [40, 3900])
 def test_a_nan_in_the_window_stays_one(bits, window):
     d = Decode([4000, 900], 8, 4, bits=bits, seed=window)
