@@ -841,14 +841,37 @@ struct Launch {
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), Smem<D>::kBytes);
     if (e != cudaSuccess) return e;
     const int per_pair = 2 * (kRows / a.group);
-    // Pairs of tiles: at most one more than whole ones a sequence.
-    const int64_t pairs = pa.num_tokens / per_pair + std::min<int64_t>(a.num_seqs, pa.num_tokens);
+    // Pairs of tiles, at most: each sequence with one of a single token, all the others whole.
+    const int64_t some = std::min<int64_t>(a.num_seqs, pa.num_tokens);
+    const int64_t pairs = some + (pa.num_tokens - some) / per_pair;
     const int64_t units = pairs * a.num_kv_heads;
     int64_t longest = a.max_context_len;  // tokens that a pair of tiles sees
-    if (pa.window > 0) longest = std::min(longest, static_cast<int64_t>(pa.window) + pa.sinks + per_pair + 128);
+    if (pa.window > 0)  // its blocks' other tokens with them, at both ends
+      longest = std::min(longest, static_cast<int64_t>(pa.window) + pa.sinks + per_pair + (2 << a.block_shift));
     const int64_t tiles = (longest + kKeys - 1) / kKeys;
+    // Few pairs share their histories over clusters, unless the tiles saved take
+    // less time than the rows' meeting.  A pair takes start + step * its CTA's
+    // tiles (+ the meeting), microseconds, fitted at 1 to 16 sequences of 4 to 1024
+    // new tokens behind 0 to 20000 and 1 to 8 KV heads: of 45 shapes, the choice
+    // was within 2% of the fastest form in 44 and 9% off in one.  D = 128, 256
+    // tokens alone: 10.9 without clusters, 15.3 in twos; 64 behind 2000: 31.3,
+    // 26.3, 19.6 in fours, 18.2 in eights.  D = 64, 64 behind 500: 12.2, 12.8, 10.9.
+    constexpr float kStartUs = D == 64 ? 6.7f : 8.2f, kStepUs = D == 64 ? 1.1f : 1.43f;
+    constexpr float kMeetUs = D == 64 ? 2.3f : 5.f, kMeetCtaUs = D == 64 ? 0.f : 0.25f;
+    // The most pairs there can be come of odd lengths; as many as are likely
+    // have to be resident at once (8 sequences of 32 behind 4000: 37.5 in
+    // twos, 51.9 without; were there more pairs, some clusters would wait).
+    const int64_t likely =
+        std::min(pairs, std::max(some, (2 * pa.num_tokens + some * per_pair + 2 * per_pair - 1) / (2 * per_pair))) *
+        a.num_kv_heads;
     int C = 1;
-    while (C < kMaxCluster && units * C * 2 <= current_sm_count(152) && 2 * C <= tiles && units <= resident(2 * C)) C *= 2;
+    float best = kStartUs + kStepUs * static_cast<float>(tiles);
+    for (int c = 2; c <= kMaxCluster && c <= tiles && likely * c <= current_sm_count(152) && likely <= resident(c); c *= 2) {
+      const float cost = kStartUs + kStepUs * static_cast<float>((tiles + c - 1) / c) + kMeetUs + kMeetCtaUs * c;
+      if (cost >= best) continue;
+      best = cost;
+      C = c;
+    }
     return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(units * C)), dim3(kThreads), Smem<D>::kBytes, C, stream,
                               a, pa, tq, tk, tv);
   }
