@@ -115,6 +115,18 @@ def test_few_rows_over_clusters(n, past, window, sinks, dt):
         p.check(window, sinks, rows=20)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,past,Hkv", [([5, 1, 30, 0, 2], [3000, 0, 4, 9, 130], 2), ([65] * 6, [2000] * 6, 3),
+                                          ([33, 129, 1], [0, 0, 4000], 8)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2500, 70)])
+def test_uneven_sequences_over_clusters(D, new, past, Hkv, window, sinks):
+    """CTAs of a cluster without a tile of a short history, pairs of a single row, more of them than are resident."""
+    p = Prompt(new, past, 4 * Hkv, Hkv, D, 32, seed=sum(new))
+    p.poison(window, sinks)
+    p.call(window, sinks, max_len=4200)
+    p.check(window, sinks, rows=12)
+
+
 @pytest.mark.parametrize("window", [0, 1000])
 def test_long_prompt(window):
     p = Prompt([6000, 2100], [100, 0], 8, 2, seed=3)
