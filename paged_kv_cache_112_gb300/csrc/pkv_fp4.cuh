@@ -4,8 +4,8 @@
 // Layout.  A block holds, per KV head and per 16 tokens, one record
 //     [16 tokens][D / 2] bytes of codes (the even channel in the low half),
 //     [16 tokens][D / 16] bytes of scales,
-// 9 D bytes.  A tile (16 tokens of a head) is then one contiguous, 64-byte
-// aligned copy, codes and scales together; the records of a block's heads
+// 9 D bytes.  A tile (16 tokens of a head) is then one contiguous copy of
+// 16-byte pieces, codes and scales together; the records of a block's heads
 // follow one another, so the CTAs of neighbouring heads read one range.
 #pragma once
 
