@@ -665,7 +665,7 @@ pkv_status pkv_copy_blocks_fp4(void* k_pool, void* v_pool, const int32_t* pairs,
  * history is read whole instead, by a cluster, and the workspace is not used.
  * PKV_PARTITION_BALANCED returns PKV_ERR_UNSUPPORTED.  Rows of tokens >= L,
  * NaN scales included, are never used; a visible one makes its head's row NaN.
- * Softmax weights enter the product with V rounded to f16 (2^-11 of each).
+ * Softmax weights enter the product with V in two f16 parts (2^-22 of each).
  * 1 <= group <= 8.
  */
 pkv_status pkv_decode_attention_fp4(void* out, const void* q, const void* k_pool, const void* v_pool,

@@ -81,13 +81,19 @@ __device__ __forceinline__ void copies_wait() {  // all but the last N groups ha
 template <int POOL>
 constexpr int kTilesAStep = POOL == 4 ? 2 : 1;
 
-template <int D, bool BF16, int POOL, int NW, int NST>
-__global__ void __launch_bounds__(NW * 32) decode_window_kernel(const DecodeArgs a, const WindowArgs wa,
-                                                                const __grid_constant__ CUtensorMap tmap_k,
-                                                                const __grid_constant__ CUtensorMap tmap_v) {
+// Least CTAs a SM, for the compiler: 16 warps' registers (0: as many as it likes).  4-bit pools with 64 channels
+// and more than two warps a CTA do better with what it takes by itself (8 of 60000 tokens 73 us for 76).
+template <int D, int POOL, int NW>
+constexpr int kLeastCtas = POOL == 4 && (D == 128 || NW == 2) ? 16 / NW : 0;
+
+// NARROW: 4-bit pools with at most four heads a group (WarpAttentionFp4).
+template <int D, bool BF16, int POOL, bool NARROW, int NW, int NST>
+__global__ void __launch_bounds__(NW * 32, kLeastCtas<D, POOL, NW>)
+    decode_window_kernel(const DecodeArgs a, const WindowArgs wa, const __grid_constant__ CUtensorMap tmap_k,
+                         const __grid_constant__ CUtensorMap tmap_v) {
   constexpr int NT = kTilesAStep<POOL>;
   using R = Ring<D, POOL, NW, NST, NT>;
-  using Att = std::conditional_t<POOL == 4, WarpAttentionFp4<D>, WarpAttention<D, BF16, true>>;
+  using Att = std::conditional_t<POOL == 4, WarpAttentionFp4<D, NARROW>, WarpAttention<D, BF16, true>>;
   constexpr int kRow = D + 4;  // floats between a saved state's head rows
   extern __shared__ __align__(1024) uint8_t smem[];
   const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
@@ -362,11 +368,11 @@ __global__ void __launch_bounds__(NW * 32) decode_window_kernel(const DecodeArgs
 }
 
 // The kernel with NW warps a CTA, and what launching it in clusters of C takes.
-template <int D, bool BF16, int POOL, int NW>
+template <int D, bool BF16, int POOL, bool NARROW, int NW>
 struct Launch {
   static constexpr int NST = POOL == 4 ? 2 : D == 64 ? 3 : 2;
   using R = Ring<D, POOL, NW, NST, kTilesAStep<POOL>>;
-  static constexpr auto kernel = decode_window_kernel<D, BF16, POOL, NW, NST>;
+  static constexpr auto kernel = decode_window_kernel<D, BF16, POOL, NARROW, NW, NST>;
 
   // Clusters of C that the current device holds at a time (a cluster stays
   // within one of the GPU's groups of SMs, so fewer than SMs / C).
@@ -449,11 +455,11 @@ struct Form {
 };
 
 // The form of the lowest cost; `clusters`: a unit may be shared by CTAs.
-template <int D, bool BF16, int POOL>
+template <int D, bool BF16, int POOL, bool NARROW>
 Form best_form(int64_t units, int64_t tiles, int group, bool clusters) {
-  using Two = Launch<D, BF16, POOL, 2>;
-  using Four = Launch<D, BF16, POOL, 4>;
-  using Eight = Launch<D, BF16, POOL, 8>;
+  using Two = Launch<D, BF16, POOL, NARROW, 2>;
+  using Four = Launch<D, BF16, POOL, NARROW, 4>;
+  using Eight = Launch<D, BF16, POOL, NARROW, 8>;
   const int64_t sms = current_sm_count(152);
   Form best;
   auto consider = [&](int NW, int C, int held) {
@@ -485,16 +491,16 @@ int64_t longest_of(const DecodeArgs& a) {
 }
 int64_t tiles_of(int64_t tokens) { return std::max<int64_t>(1, (tokens + kTile - 1) / kTile); }
 
-template <int D, bool BF16, int POOL>
+template <int D, bool BF16, int POOL, bool NARROW>
 cudaError_t launch_t(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * a.max_parts;
   const int64_t seen = w.window > 0 ? static_cast<int64_t>(w.window) + w.sinks : a.partition_size;
-  const Form f = best_form<D, BF16, POOL>(units, tiles_of(std::min(longest_of(a), seen)), a.group, w.window > 0);
+  const Form f = best_form<D, BF16, POOL, NARROW>(units, tiles_of(std::min(longest_of(a), seen)), a.group, w.window > 0);
   switch (f.nw) {
-    case 2: return Launch<D, BF16, POOL, 2>::launch(a, w, 1, tk, tv, stream);
-    case 4: return Launch<D, BF16, POOL, 4>::launch(a, w, f.c, tk, tv, stream);
-    default: return Launch<D, BF16, POOL, 8>::launch(a, w, f.c, tk, tv, stream);
+    case 2: return Launch<D, BF16, POOL, NARROW, 2>::launch(a, w, 1, tk, tv, stream);
+    case 4: return Launch<D, BF16, POOL, NARROW, 4>::launch(a, w, f.c, tk, tv, stream);
+    default: return Launch<D, BF16, POOL, NARROW, 8>::launch(a, w, f.c, tk, tv, stream);
   }
 }
 
@@ -506,40 +512,50 @@ cudaError_t launch_t(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap
 // Lengths differ, and only the longest is known here: whole has to be the
 // faster one with every history that long and with one of them, by more than
 // the estimates' error where there are many (16 of 8000: 5% apart).
-template <int D, bool BF16>
+template <int D, bool BF16, bool NARROW>
 bool whole_t(const DecodeArgs& a) {
   const int64_t longest = longest_of(a), in_part = std::min<int64_t>(longest, a.partition_size);
   constexpr float kJoinUs = 2.f;
   auto wins = [&](int64_t units) {
-    return 1.05f * best_form<D, BF16, 4>(units, tiles_of(longest), a.group, true).cost <
-           best_form<D, BF16, 4>(units * a.max_parts, tiles_of(in_part), a.group, false).cost + kJoinUs;
+    return 1.05f * best_form<D, BF16, 4, NARROW>(units, tiles_of(longest), a.group, true).cost <
+           best_form<D, BF16, 4, NARROW>(units * a.max_parts, tiles_of(in_part), a.group, false).cost + kJoinUs;
   };
   return wins(a.num_kv_heads) && wins(static_cast<int64_t>(a.num_seqs) * a.num_kv_heads);
 }
 
-template <int POOL>
+template <int POOL, bool NARROW>
 cudaError_t launch_p(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tk, const CUtensorMap& tv,
                      int head_dim, bool bf16, cudaStream_t stream) {
   if (head_dim == 128)
-    return bf16 ? launch_t<128, true, POOL>(a, w, tk, tv, stream) : launch_t<128, false, POOL>(a, w, tk, tv, stream);
+    return bf16 ? launch_t<128, true, POOL, NARROW>(a, w, tk, tv, stream)
+                : launch_t<128, false, POOL, NARROW>(a, w, tk, tv, stream);
   if (head_dim == 64)
-    return bf16 ? launch_t<64, true, POOL>(a, w, tk, tv, stream) : launch_t<64, false, POOL>(a, w, tk, tv, stream);
+    return bf16 ? launch_t<64, true, POOL, NARROW>(a, w, tk, tv, stream)
+                : launch_t<64, false, POOL, NARROW>(a, w, tk, tv, stream);
   return cudaErrorInvalidValue;
 }
+
+template <bool NARROW>
+bool whole_p(const DecodeArgs& a, int head_dim, bool bf16) {
+  if (head_dim == 64) return bf16 ? whole_t<64, true, NARROW>(a) : whole_t<64, false, NARROW>(a);
+  return bf16 ? whole_t<128, true, NARROW>(a) : whole_t<128, false, NARROW>(a);
+}
+
+bool narrow(const DecodeArgs& a) { return a.group <= 4; }
 
 }  // namespace
 
 bool decode_whole_fp4(const DecodeArgs& a, int head_dim, bool bf16) {
   if (a.num_seqs == 0 || a.max_parts <= 1) return true;
-  if (head_dim == 64) return bf16 ? whole_t<64, true>(a) : whole_t<64, false>(a);
-  return bf16 ? whole_t<128, true>(a) : whole_t<128, false>(a);
+  return narrow(a) ? whole_p<true>(a, head_dim, bf16) : whole_p<false>(a, head_dim, bf16);
 }
 
 cudaError_t launch_decode_window(const DecodeArgs& a, const WindowArgs& w, const CUtensorMap& tmap_k,
                                  const CUtensorMap& tmap_v, int head_dim, bool bf16, bool fp4, cudaStream_t stream) {
   if (a.num_seqs == 0) return cudaSuccess;
-  return fp4 ? launch_p<4>(a, w, tmap_k, tmap_v, head_dim, bf16, stream)
-             : launch_p<16>(a, w, tmap_k, tmap_v, head_dim, bf16, stream);
+  if (!fp4) return launch_p<16, false>(a, w, tmap_k, tmap_v, head_dim, bf16, stream);
+  return narrow(a) ? launch_p<4, true>(a, w, tmap_k, tmap_v, head_dim, bf16, stream)
+                   : launch_p<4, false>(a, w, tmap_k, tmap_v, head_dim, bf16, stream);
 }
 
 }  // namespace pkv
