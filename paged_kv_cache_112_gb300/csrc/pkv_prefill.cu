@@ -126,7 +126,17 @@ struct View {
   __device__ __forceinline__ bool seen(int x) const { return x < end && (x >= low - gap || x < sinks); }
 };
 
-template <int D, bool BF16>
+// TWO: a softmax weight enters the product in two 16-bit parts, its rounding and
+// what that leaves (2^-17 of it in bf16, 2^-22 in f16), for outputs in 32 bits.  A
+// 16-bit output takes the first part alone, off by half a step of its own type
+// and, over many tokens, by less of the row than the row's rounding (errors
+// against 64 bits: 2.1e-3 for 1.6e-3 in bf16, 2.7e-4 for 2.1e-4 in f16): the second
+// part is half as much work again for the tensor cores.  Microseconds with one
+// and two: 8192 tokens 363 and 529, 16 windowed prompts 196 and 247, 37 behind
+// 2000 16.2 and 18.1 (32-bit outputs both).  Either way the sum is that of the weights
+// before their rounding: adding up the rounded ones, which would give a row of one
+// token that token's values to the bit, took 381 for 347 at 8192 tokens.
+template <int D, bool BF16, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a, const PrefillArgs pa,
                                                               const __grid_constant__ CUtensorMap tmap_q,
                                                               const __grid_constant__ CUtensorMap tmap_k,
@@ -466,9 +476,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
               }
               tc::fence_after();
 #pragma unroll
-              for (int s = 4 * half; s < 4 * half + 4; ++s)
+              for (int s = 4 * half; s < 4 * half + 4; ++s) {
                 tc::mma_ts(tmem + 256 + t * D, tmem + t * kKeys + 8 * s, vd + ((s * 2048) >> 4), pv,
                            s > 0 || j > 0);
+                if (TWO) tc::mma_ts(tmem + 256 + t * D, tmem + t * kKeys + 64 + 8 * s, vd + ((s * 2048) >> 4), pv, true);
+              }
             }
             if (!ok) break;
             ++phase[t];
@@ -598,28 +610,48 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
         const float shift = m == kNegInf ? 0.f : kUp - m * sl2;
         const F2 scale2 = pair(sl2, sl2), shift2 = pair(shift, shift);
         F2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-        auto weigh = [&](int i) {  // columns i, i + 1
+        [[maybe_unused]] uint32_t rest[16];
+        auto weigh = [&](int i) {  // columns i, i + 1; with TWO, what rounding left of them to `rest`
           const float2 e = halves(fma2(pair(y[i], y[i + 1]), scale2, shift2));
           const float w0 = ex2_approx(e.x), w1 = ex2_approx(e.y);
           sum[(i / 2) & 1] = add2(sum[(i / 2) & 1], pair(w0, w1));
-          return BF16 ? pack_bf16(w0, w1) : pack_f16(w0, w1);
+          const uint32_t p = BF16 ? pack_bf16(w0, w1) : pack_f16(w0, w1);
+          if constexpr (TWO) {
+            const float2 r = BF16 ? unpack_bf16(p) : __half22float2(*reinterpret_cast<const __half2*>(&p));
+            const float2 z = halves(fma2(pair(r.x, r.y), pair(-1.f, -1.f), pair(w0, w1)));
+            rest[(i / 2) & 15] = BF16 ? pack_bf16(z.x, z.y) : pack_f16(z.x, z.y);
+          }
+          return p;
         };
         auto pass = [&](int half) {  // the weights of this half are in tensor memory
           tc::wait_st();
           tc::fence_before();
           signal(my_p + 8 * half);
         };
-        uint32_t w[32];
+        if constexpr (TWO) {
+          uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = weigh(2 * i);
-        tc::st32(s_at, w);
+          for (int part = 0; part < 4; ++part) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = weigh(64 + 2 * i);
-        pass(0);  // a while after its stores
+            for (int i = 0; i < 16; ++i) w[i] = weigh(32 * part + 2 * i);
+            if (part == 2) pass(0);
+            tc::st16(s_at + 16 * part, w);
+            tc::st16(s_at + 64 + 16 * part, rest);
+          }
+          pass(1);
+        } else {
+          uint32_t w[32];
 #pragma unroll
-        for (int i = 16; i < 32; ++i) w[i] = weigh(64 + 2 * i);
-        tc::st32(s_at + 32, w);
-        pass(1);
+          for (int i = 0; i < 32; ++i) w[i] = weigh(2 * i);
+          tc::st32(s_at, w);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = weigh(64 + 2 * i);
+          pass(0);  // a while after its stores
+#pragma unroll
+          for (int i = 16; i < 32; ++i) w[i] = weigh(64 + 2 * i);
+          tc::st32(s_at + 32, w);
+          pass(1);
+        }
         const float2 s0 = halves(sum[0]), s1 = halves(sum[1]);
         l += (s0.x + s0.y) + (s1.x + s1.y);
       }
@@ -805,9 +837,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
   }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool TWO>
 struct Launch {
-  static constexpr auto kernel = prefill_kernel<D, BF16>;
+  static constexpr auto kernel = prefill_kernel<D, BF16, TWO>;
 
   static int resident(int C) {
     constexpr int kDevices = 64;
@@ -858,7 +890,7 @@ struct Launch {
     // was within 2% of the fastest form in 44 and 9% off in one.  D = 128, 256
     // tokens alone: 10.9 without clusters, 15.3 in twos; 64 behind 2000: 31.3,
     // 26.3, 19.6 in fours, 18.2 in eights.  D = 64, 64 behind 500: 12.2, 12.8, 10.9.
-    constexpr float kStartUs = D == 64 ? 6.7f : 8.2f, kStepUs = D == 64 ? 1.1f : 1.43f;
+    constexpr float kStartUs = D == 64 ? 6.7f : 8.2f, kStepUs = (D == 64 ? 1.1f : 1.43f) * (TWO ? 1.4f : 1.f);
     constexpr float kMeetUs = D == 64 ? 2.3f : 5.f, kMeetCtaUs = D == 64 ? 0.f : 0.25f;
     // The most pairs there can be come of odd lengths; as many as are likely
     // have to be resident at once (8 sequences of 32 behind 4000: 37.5 in
@@ -879,18 +911,25 @@ struct Launch {
   }
 };
 
+template <bool TWO>
+cudaError_t launch_p(const DecodeArgs& a, const PrefillArgs& pa, const CUtensorMap& tq, const CUtensorMap& tk,
+                     const CUtensorMap& tv, int head_dim, bool bf16, cudaStream_t stream) {
+  if (head_dim == 128)
+    return bf16 ? Launch<128, true, TWO>::launch(a, pa, tq, tk, tv, stream)
+                : Launch<128, false, TWO>::launch(a, pa, tq, tk, tv, stream);
+  if (head_dim == 64)
+    return bf16 ? Launch<64, true, TWO>::launch(a, pa, tq, tk, tv, stream)
+                : Launch<64, false, TWO>::launch(a, pa, tq, tk, tv, stream);
+  return cudaErrorInvalidValue;
+}
+
 }  // namespace
 
 cudaError_t launch_prefill(const DecodeArgs& a, const PrefillArgs& pa, const CUtensorMap& tmap_q,
                            const CUtensorMap& tmap_k, const CUtensorMap& tmap_v, int head_dim, bool bf16,
                            cudaStream_t stream) {
-  if (head_dim == 128)
-    return bf16 ? Launch<128, true>::launch(a, pa, tmap_q, tmap_k, tmap_v, stream)
-                : Launch<128, false>::launch(a, pa, tmap_q, tmap_k, tmap_v, stream);
-  if (head_dim == 64)
-    return bf16 ? Launch<64, true>::launch(a, pa, tmap_q, tmap_k, tmap_v, stream)
-                : Launch<64, false>::launch(a, pa, tmap_q, tmap_k, tmap_v, stream);
-  return cudaErrorInvalidValue;
+  return a.out_dtype == 0 ? launch_p<true>(a, pa, tmap_q, tmap_k, tmap_v, head_dim, bf16, stream)
+                          : launch_p<false>(a, pa, tmap_q, tmap_k, tmap_v, head_dim, bf16, stream);
 }
 
 }  // namespace pkv
