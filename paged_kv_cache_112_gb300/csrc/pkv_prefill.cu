@@ -117,8 +117,8 @@ struct View {
     const int count = (end + kKeys - 1) / kKeys;
     cnt = count > rank ? (count - rank + C - 1) / C : 0;
   }
-  // The first token of the window at position p.
-  __device__ __forceinline__ int low_of(int p) const { return window > 0 ? max(0, p - window + 1) : 0; }
+  // The first token of the window at position p (which may lie before the history: p - window need not fit).
+  __device__ __forceinline__ int low_of(int p) const { return window > 0 && p >= window ? p - window + 1 : 0; }
   // Where tile j begins on the axis; the token at a place of the axis.
   __device__ __forceinline__ int begin(int j) const { return (j * C + rank) * kKeys; }
   __device__ __forceinline__ int token(int x) const { return x < mid ? x : x + gap; }
