@@ -128,28 +128,24 @@ __device__ __forceinline__ float sixth(float a) {
 }
 
 // Eight e2m1 codes of x / s, s the value of an e4m3 scale; a scale of 0 (or NaN, when the values mean nothing) gives
-// zeros.  Infinite values, whose codes are the largest whatever they are divided by, become the largest finite ones
-// first, so that the corrections hold for all eight.
-__device__ __forceinline__ uint32_t codes8_e2m1(const F2 (&values)[4], float s, float top) {
+// zeros.  An infinite value's correction is no number: it stands for its quotient, and saturates.
+__device__ __forceinline__ uint32_t codes8_e2m1(const F2 (&x)[4], float s, float top) {
   const bool usable = s > 0.f;
   const float inv = usable ? __frcp_rn(s) : 0.f, div = usable ? s : 0.f;
   const F2 y = pair(inv, inv), d = pair(-div, -div);
-  F2 x[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = values[i];
-  if (!(top < INFINITY)) {
-    constexpr float kLast = 3.402823466e38f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = halves(x[i]);
-      x[i] = pair(fminf(fmaxf(f.x, -kLast), kLast), fminf(fmaxf(f.y, -kLast), kLast));
-    }
-  }
   float2 r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const F2 q = mul2(x[i], y);
     r[i] = halves(fma2(fma2(q, d, x[i]), y, q));
+  }
+  if (!(top < INFINITY)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = halves(x[i]);
+      if (!(fabsf(v.x) < INFINITY)) r[i].x = v.x;
+      if (!(fabsf(v.y) < INFINITY)) r[i].y = v.y;
+    }
   }
   return fp4::e2m1x8(r);
 }
