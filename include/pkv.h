@@ -732,12 +732,12 @@ pkv_status pkv_decode_window_fp4(void* out, const void* q, const void* k_pool, c
  *   window, sinks: >= 0; window 0: all of the history (sinks then mean nothing).
  * Blocks without a token that some new one sees are not read.  A table entry
  * outside the pool, of a block that is seen, sets PKV_DEV_ERR_BLOCK; the block
- * then counts as zero keys and values.  Tokens that no new token of the
- * sequence sees may hold anything; V of a token that some of them see has to be
- * finite, as it meets weights of zero in the others' rows.  Weights enter the
- * product with V rounded to kv_dtype (half a step of it each) where out is of 16
- * bits, in two parts of kv_dtype (2^-17 of each, f16 2^-22) where it is float32.
- * Block sizes 8 to 64, head_dim 64 or 128, 1 <= group <= 8.  One kernel, no workspace; other
+ * then counts as zero keys and values.  What a row does not see does not change
+ * it, whatever the pools hold there.  A channel that meets an infinite value in a
+ * visible token is infinite or NaN.  Weights enter the product with V rounded to
+ * kv_dtype (half a step of it each) where out is of 16 bits, in two parts of
+ * kv_dtype (2^-17 of each, f16 2^-22) where it is float32.  Block sizes 8 to 64,
+ * head_dim 64 or 128, 1 <= group <= 8.  One kernel, no workspace; other
  * arguments and flags as in pkv_decode_attention.
  */
 pkv_status pkv_prefill_attention(void* out, const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,

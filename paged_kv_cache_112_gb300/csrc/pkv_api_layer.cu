@@ -577,7 +577,8 @@ pkv_status pkv_prefill_attention(void* out, const void* q, int64_t q_stride, con
       !encode_block_map(&tk, k_pool, num_blocks, block_size, num_kv_heads, head_dim, a.block_stride) ||
       !encode_block_map(&tv, v_pool, num_blocks, block_size, num_kv_heads, head_dim, a.block_stride))
     return PKV_ERR_CUDA;
-  const PrefillArgs pa{query_start, num_tokens, window, sinks, aligned(out, 32), scale < 0.f};
+  const PrefillArgs pa{query_start, num_tokens, window, sinks, aligned(out, 32), scale < 0.f,
+                       static_cast<const uint16_t*>(v_pool)};
   return cuda_status(
       launch_prefill(a, pa, tq, tk, tv, head_dim, kv_dtype == PKV_BF16, static_cast<cudaStream_t>(stream)));
 }

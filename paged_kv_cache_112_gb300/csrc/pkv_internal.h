@@ -205,6 +205,7 @@ struct PrefillArgs {
   int window, sinks;           // window 0: none
   int out_sectors;             // out is 32-byte aligned
   int negate;                  // the softmax scale is negative: scale_log2 is its magnitude's
+  const uint16_t* v_pool;
 };
 
 // Split-K workspace layout (regions 256-byte aligned).  Fixed partitions:

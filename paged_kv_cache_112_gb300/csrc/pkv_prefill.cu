@@ -39,6 +39,13 @@
 // grown by more than 2^8 since: weights up to 2^8 do as well (a weight is
 // rounded relative to itself), and O is read and written rarely.
 //
+// A row's weight for a token that it does not see is 0, and 0 times an infinite or
+// NaN value would be NaN.  Where some rows of a pair see a token and others do not,
+// warp 11 looks for such values, makes them 0 and keeps a list of their tokens; the
+// rows that see one get it added once the products are done.  (Without all that
+// 8192 tokens took 351 us for 358, 16 windowed prompts 172 for 175, 200 prompts of
+// 20 tokens behind 50, where warp 11 is what the others wait for, 59 for 64.)
+//
 // With few query rows a cluster of up to eight CTAs shares a pair of tiles:
 // each takes every C-th tile of the history, and their rows meet in distributed
 // shared memory.
@@ -55,10 +62,16 @@ using namespace dev;
 constexpr int kRows = 128;     // query rows a tile
 constexpr int kKeys = 128;     // history tokens a tile
 constexpr int kThreads = 384;  // two tiles' threads, and four warps that load, pass on and multiply
-// Registers: 168 a thread at launch; the tiles' threads hold a row of scores.
-constexpr int kRowRegs = 216, kOtherRegs = 72;
+// Registers: 168 a thread at launch; the tiles' threads hold a row of scores.  (216
+// and 72: 16 windowed prompts 179 us for 175, 8192 tokens 365 for 358.)
+constexpr int kRowRegs = 200, kOtherRegs = 104;
 static_assert(256 * kRowRegs + 128 * kOtherRegs <= 384 * 168, "shares of the launch's registers");
 constexpr int kMaxCluster = 8;
+// Tokens of a pair whose values are not all finite: the number of history tiles
+// with some, then of each the place where it begins and a bit a token.  Only tiles
+// at the edges of the rows' views are listed: at most 255 tokens lie between the
+// first row's end and the last one's, as many between the window's two starts.
+constexpr int kListTiles = 6, kListWords = 1 + 5 * kListTiles;
 
 template <int D>
 struct Smem {
@@ -74,10 +87,36 @@ struct Smem {
   static constexpr int kBars = kUnits + 64;
   static constexpr int kBarCount = 3 * kSlots + 18;
   static constexpr int kWords = kBars + 8 * kBarCount;  // bad blocks of each slot, tensor memory, abort
-  static constexpr int kBytes = kWords + 4 * (kSlots + 2);
+  static constexpr int kLists = kWords + 4 * (kSlots + 2);
+  static constexpr int kBytes = kLists + 2 * 4 * kListWords;
   static_assert(kRowsAt + 2 * kRows * D * 4 + 8 * 4096 <= kStolen, "the cluster's rows fit over the tiles");
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
+
+__device__ __forceinline__ uint4 load16(uint32_t at) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+  return r;
+}
+__device__ __forceinline__ void store16(uint32_t at, uint4 x) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+
+// 0 for two finite 16-bit values, NaN in the half of one that is not; added to `sum`.
+template <bool BF16>
+__device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t sum) {
+  if constexpr (BF16)
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(x), "r"(0));
+  else
+    asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(x), "r"(0));
+  return sum;
+}
+// Two 16-bit values, those that are no finite numbers 0.
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite(uint32_t x) {
+  constexpr uint32_t kOdd = BF16 ? 0x7f80u : 0x7c00u;  // magnitudes from here on
+  return ((x & 0x7fffu) >= kOdd ? 0u : x & 0xffffu) | (((x >> 16) & 0x7fffu) >= kOdd ? 0u : x & 0xffff0000u);
+}
 
 // A pair of tiles of one KV head.
 struct Unit {
@@ -122,8 +161,12 @@ struct View {
   // Where tile j begins on the axis; the token at a place of the axis.
   __device__ __forceinline__ int begin(int j) const { return (j * C + rank) * kKeys; }
   __device__ __forceinline__ int token(int x) const { return x < mid ? x : x + gap; }
-  // Places from `low_place` on, and those before `sinks`, are seen by some row.
+  // Places from low - gap on, and those before `sinks`, are seen by some row.
   __device__ __forceinline__ bool seen(int x) const { return x < end && (x >= low - gap || x < sinks); }
+  // Places in [all_from(), all_to()), and those of them before sinks_all, are seen by every row.  (Where there is a
+  // gap, sinks_all ends before it.)
+  __device__ __forceinline__ int all_from() const { return low_of(p1) - gap; }
+  __device__ __forceinline__ int all_to() const { return p0 + 1 - gap; }
 };
 
 // TWO: a softmax weight enters the product in two 16-bit parts, its rounding and
@@ -155,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
   volatile uint32_t* bad_blocks = reinterpret_cast<volatile uint32_t*>(smem + SM::kWords);
   volatile uint32_t* tmem_at = bad_blocks + NS;
   volatile uint32_t* abort_at = tmem_at + 1;
+  volatile uint32_t* lists = reinterpret_cast<volatile uint32_t*>(smem + SM::kLists);  // of two units
   const int G = a.group, per_tile = kRows / G;
 
   if (tid == 0) {
@@ -399,7 +443,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
         const View v(u, pa, per_tile, a.block_shift, C, rank);
         // Rows that no row of queries sees and blocks outside the pool become
         // zeros: their weights are zero, but what the pool holds there may be
-        // anything, and zero times NaN is NaN.
+        // anything, and zero times NaN is NaN.  So do infinite and NaN values that
+        // some rows see and others do not: the former get them from the list.
+        volatile uint32_t* list = lists + (k & 1) * kListWords;
+        int listed = 0;
+        if (lane == 0) list[0] = 0;  // the unit before last, whose list this was, is done with
+        const int all_from = v.all_from(), all_to = v.all_to();
         for (int j = 0; j < 2 * v.cnt && ok; ++j, ++i) {
           const int slot = i % NS;
           const bool is_v = j & 1;
@@ -407,19 +456,57 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
           if (!ok) break;
           const uint32_t bad = bad_blocks[slot];
           const int x0 = v.begin(j >> 1);
+          const uint32_t at = base + SM::kRing + slot * SM::kTileBytes;
+          // A row's 16-byte pieces, rotated by the row: other banks for other lanes.
+          auto piece = [&](int r, int c) { return at + (c >> 3) * SM::kLineBytes + r * 128 + ((c + r) & 7) * 16; };
           const bool edge = is_v && (x0 + kKeys > v.end || (x0 < v.low - v.gap && x0 + kKeys > v.sinks));
-          if (bad || edge) {
-            const uint32_t at = base + SM::kRing + slot * SM::kTileBytes;
+          bool changed = bad || edge;
+          if (changed) {
             for (int r = lane; r < kKeys; r += 32) {
               if (!((bad >> (r >> a.block_shift)) & 1u) && (!is_v || v.seen(x0 + r))) continue;
-              for (int c = 0; c < NL * 8; ++c)  // rotated by the row: other banks for other lanes
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                 at + (c >> 3) * SM::kLineBytes + r * 128 + ((c + r) & 7) * 16),
-                             "r"(0)
-                             : "memory");
+              for (int c = 0; c < NL * 8; ++c) store16(piece(r, c), make_uint4(0, 0, 0, 0));
             }
-            fence_proxy_async_smem();
+            __syncwarp();
           }
+          if (is_v && (x0 < all_from || x0 + kKeys > all_to)) {
+            // All lanes side by side over the rows of one range of places, then the other's.
+            uint32_t nan = 0;
+            const uint32_t col = at + ((lane >> 3) & (NL - 1)) * SM::kLineBytes + (lane & 7) * 16;
+            int r = max(v.low - v.gap - x0, 0) + lane / (NL * 8), last = min(all_from - x0, kKeys);
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part) {
+#pragma unroll 4
+              for (; r < last; r += 32 / (NL * 8)) {
+                const uint4 w = load16(col + r * 128);
+                nan = times_zero<BF16>(w.x, times_zero<BF16>(w.y, times_zero<BF16>(w.z, times_zero<BF16>(w.w, nan))));
+              }
+              r = max(all_to - x0, 0) + lane / (NL * 8);
+              last = min(v.end - x0, kKeys);
+            }
+            if (__any_sync(kFull, nan != 0)) {
+              changed = true;
+              if (lane == 0 && listed < kListTiles) list[1 + 5 * listed] = x0;
+#pragma unroll 1
+              for (int r = lane; r < kKeys; r += 32) {
+                const int x = x0 + r;
+                bool odd = false;
+                if (v.seen(x) && (x >= all_to || (x < all_from && x >= v.sinks_all))) {
+#pragma unroll 1
+                  for (int c = 0; c < NL * 8; ++c) {
+                    const uint4 w = load16(piece(r, c));
+                    const uint4 z = make_uint4(finite<BF16>(w.x), finite<BF16>(w.y), finite<BF16>(w.z), finite<BF16>(w.w));
+                    odd |= w.x != z.x || w.y != z.y || w.z != z.z || w.w != z.w;
+                    store16(piece(r, c), z);
+                  }
+                }
+                const uint32_t m = __ballot_sync(kFull, odd);
+                if (lane == 0 && listed < kListTiles) list[2 + 5 * listed + (r >> 5)] = m;
+              }
+              listed = min(listed + 1, kListTiles);
+              if (lane == 0) list[0] = listed;
+            }
+          }
+          if (changed) fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) signal(ready + 8 * slot);
         }
@@ -659,6 +746,38 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const DecodeArgs a
       if (v.cnt > 0) {
         if (!__all_sync(kFull, wait(o_bar + 8 * t, outs++ & 1))) break;
         tc::fence_after();
+      }
+      // Values that the products left out (see warp 11): added for the rows that see their tokens.
+      const volatile uint32_t* list = lists + (k & 1) * kListWords;
+      if (__builtin_expect(v.cnt > 0 && list[0] != 0, 0)) {
+        const int32_t* tbl = a.block_tables + static_cast<int64_t>(u.s) * a.max_blocks_per_seq;
+#pragma unroll 1
+        for (int e = 0; e < 4 * min(static_cast<int>(list[0]), kListTiles); ++e) {
+          const int x = static_cast<int>(list[1 + 5 * (e >> 2)]) + 32 * (e & 3);
+#pragma unroll 1
+          for (uint32_t left = list[2 + 5 * (e >> 2) + (e & 3)]; left; left &= left - 1) {
+            const int tok = v.token(x + __ffs(left) - 1);
+            const bool sees = tok <= pos && (tok >= my_low || tok < my_sinks);
+            const uint32_t* row = reinterpret_cast<const uint32_t*>(
+                pa.v_pool + __ldg(tbl + (tok >> a.block_shift)) * a.block_stride +
+                (static_cast<int64_t>(tok & ((1 << a.block_shift) - 1)) * a.num_kv_heads + u.g) * D);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 8) {
+              uint32_t o[8];
+              tc::ld8(o, o_at + c);
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                const uint32_t w = __ldg(row + (c + i) / 2);
+                const float2 y = BF16 ? unpack_bf16(w) : __half22float2(*reinterpret_cast<const __half2*>(&w));
+                if (sees && !(fabsf(y.x) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + y.x);
+                if (sees && !(fabsf(y.y) < INFINITY)) o[i + 1] = __float_as_uint(__uint_as_float(o[i + 1]) + y.y);
+              }
+              tc::st8(o_at + c, o);
+              tc::wait_st();
+            }
+          }
+        }
       }
       if (C > 1) break;  // the rows meet below
       const float f = l == 0.f ? 0.f : 1.f / l;  // a sum that is no number makes the row none

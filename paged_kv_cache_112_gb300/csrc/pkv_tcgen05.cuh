@@ -104,6 +104,9 @@ __device__ __forceinline__ void ld32(uint32_t* r, uint32_t at) {
       : PKV_R8(r, 0), PKV_R8(r, 8), PKV_R8(r, 16), PKV_R8(r, 24)
       : "r"(at));
 }
+__device__ __forceinline__ void ld8(uint32_t* r, uint32_t at) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : PKV_R8(r, 0) : "r"(at));
+}
 // 64 columns of 16 lanes (those from the address'): thread i has columns 8k + 2
 // (i % 4), + 1 of lanes i / 4 (r[4k], r[4k + 1]) and i / 4 + 8 (r[4k + 2], r[4k + 3]).
 __device__ __forceinline__ void ld16x64(uint32_t* r, uint32_t at) {
@@ -127,6 +130,11 @@ __device__ __forceinline__ void st16(uint32_t at, const uint32_t* r) {
       "%14, %15};" ::PKV_I8(r, 0),
       PKV_I8(r, 8), "r"(at)
       : "memory");
+}
+
+__device__ __forceinline__ void st8(uint32_t at, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::PKV_I8(r, 0), "r"(at)
+               : "memory");
 }
 
 #undef PKV_R8
