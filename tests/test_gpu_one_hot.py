@@ -20,22 +20,39 @@ def _lib():
 
 
 class OneHot(Decode):
-    """A batch of such histories; `chain`: tokens that one accumulator takes up at the most."""
+    """A batch of such histories in scattered blocks; what lies behind them is NaN."""
 
     def __init__(self, lens, Hq=8, Hkv=2, D=128, B=16, dt="bf16", bits=4, seed=0, out=torch.float32):
-        super().__init__(lens, Hq, Hkv, D, B, dt, bits, seed=seed, out=out)
+        super().__init__([0] * len(lens), Hq, Hkv, D, B, dt, bits, seed=seed, out=out)
         rng = np.random.default_rng(seed + 1)
+        self.lens = np.asarray(lens)
+        n = -(-self.lens // B)
+        self.NB, self.width, self.max_len = int(n.sum()) + 3, int(n.max()) + 1, int(self.lens.max())
+        self.tables, perm, at = np.full((len(lens), self.width), -7, np.int32), rng.permutation(self.NB), 0
+        for i, m in enumerate(n):
+            self.tables[i, :m] = perm[at:at + m]
+            at += m
+        self.dt_tables = torch.from_numpy(self.tables).cuda()
+        self.dt_lens = torch.from_numpy(self.lens.astype(np.int32)).cuda()
         self.seen = {}  # sequences whose tokens are not all visible
-        for i, x in enumerate(H.histories(lens, self.tables, self.NB, B, Hkv, D, rng)):
+        for j, x in enumerate(H.histories(lens, self.tables, self.NB, B, Hkv, D, rng)):
             if bits == 4:
                 code, sc = R.quantise(x)
                 p = R.pack(code.transpose(0, 2, 1, 3), sc.transpose(0, 2, 1, 3))
-                self.vals[i], self.dev[i] = R.values(p, D), torch.from_numpy(p).cuda()
+                self.vals[j], self.dev[j] = R.values(p, D), torch.from_numpy(p).cuda()
             else:
                 x = torch.from_numpy(x).to(DT[dt])
-                self.vals[i], self.dev[i] = x.double().numpy(), x.cuda()
+                self.vals[j], self.dev[j] = x.double().numpy(), x.cuda()
+        for i, L in enumerate(lens):
+            if L % B:
+                self.poison(i, L)
         self.q = torch.from_numpy(H.queries(len(lens), Hq, D, rng)).to(DT[dt]).cuda()
         self.scale = 1.0
+
+    def in_partitions(self):
+        """Whether the last call went through the workspace."""
+        torch.cuda.synchronize()
+        return bool((self.ws != 0xFF).any())
 
     def rows(self, i, L):
         return [x[self.tables[i, :-(-L // self.B)]].reshape(-1, *x.shape[2:])[:L] for x in self.vals]
@@ -62,3 +79,59 @@ def test_weights_keep_their_bits(Hq, Hkv, D, B, dt):
     d.compare(1000)
     d.window(100, 20)
     d.compare(120, 100, 20)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,B,dt,ps", H.PARTITIONS)
+def test_partitions(lens, Hq, Hkv, D, B, dt, ps):
+    """Histories cut into partitions and joined, twice on the same workspace: every group size, block size and type,
+    partitions of an odd number of tiles, whose last step of two holds a tile of the next partition."""
+    d = OneHot(lens, Hq, Hkv, D, B, dt, seed=ps)
+    d.attend(partition_size=ps)
+    assert d.in_partitions()
+    d.compare(H.partition_chain(max(lens), ps))
+    first = d.out.clone()
+    d.out.fill_(0)
+    d.attend(partition_size=ps)
+    assert torch.equal(d.out, first)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16])
+def test_partitions_of_a_layer_with_bad_entries_and_lengths(out):
+    """One layer of an all-layer pool in partitions; entries outside the pool are left out, lengths beyond the table are
+    cut, negative ones are none."""
+    ps = 1008
+    d = OneHot([30000, 20000, 500, 100], 8, 2, 128, 32, "f16", seed=3, out=out)
+    whole = [torch.full((d.NB, 3, *p.shape[1:]), 0xFF, dtype=torch.uint8, device="cuda") for p in d.dev]
+    for w, p in zip(whole, d.dev):
+        w[:, 1] = p
+    d.dev = [w[:, 1] for w in whole]
+    d.attend(partition_size=ps)
+    assert d.in_partitions()
+    d.compare(H.partition_chain(30000, ps))
+    for i, blk in ((0, 0), (0, 31), (0, 32), (0, 937), (1, 300), (2, 15)):  # 31 and 32: where two partitions meet
+        d.dt_tables[i, blk] = d.NB if blk % 2 else -1
+        see = d.seen.setdefault(i, np.ones(int(d.lens[i]), bool))
+        see[blk * 32:blk * 32 + 32] = False
+    d.attend(partition_size=ps)
+    assert d.in_partitions()
+    d.compare(H.partition_chain(30000, ps), want_status=pkv.DEV_ERR_BLOCK)
+    d.st.zero_()
+    d.dt_lens[1], d.dt_lens[2], d.dt_lens[3] = 2 ** 31 - 1, -1, 0
+    d.seen = {0: d.seen[0]}
+    d.dt_tables[1] = d.dt_tables[0]  # as long as the table is, with the first one's entries
+    d.tables[1] = d.tables[0]
+    d.lens[1] = 30000
+    d.max_len = 30000
+    d.seen[1] = d.seen[0]
+    d.attend(partition_size=ps)
+    assert d.in_partitions()
+    d.compare(H.partition_chain(30000, ps), lens=[30000, 30000, 0, 0], want_status=pkv.DEV_ERR_BLOCK | pkv.DEV_ERR_LENGTH)
+
+
+@pytest.mark.parametrize("bits,S,L,window", H.WINDOWS)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_windows(bits, S, L, window, dt):
+    """From one sequence on clusters of eight to more units than the device holds."""
+    d = OneHot([L - 7 * (i % 5) for i in range(S)], 4, 1, bits=bits, dt=dt, seed=S)
+    d.window(window, 20)
+    d.compare(window + 20, window, 20)

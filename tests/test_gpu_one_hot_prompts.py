@@ -28,10 +28,9 @@ class OneHot(Prompt):
         rows = torch.from_numpy(H.queries(len(self.out), Hq, D, rng)).to(self.dt)
         self.q = rows.cuda()
         self.scale = 1.0
-        # Weights: in the pools' type, or in two parts of it; off by half of f16's smallest step, times 2^7, too.
-        f16 = self.dt == torch.float16
-        self.part = (2.0 ** -22 if f16 else 2.0 ** -17) if out == torch.float32 else STEP[self.dt]
-        self.floor = 2.0 ** -32 if f16 else 0.0
+        # Weights in f16 are off by half of its smallest step, times 2^7, too.
+        self.part = H.prompt_part(dt, "f32" if out == torch.float32 else None)
+        self.floor = 2.0 ** -32 if dt == "f16" else 0.0
 
     def compare(self, window=0, sinks=0, rows=None):
         torch.cuda.synchronize()
@@ -61,3 +60,12 @@ def test_float32_outputs_keep_the_weights_bits(Hq, Hkv, D, B, dt, window, sinks)
     p = OneHot([500], [900], 16 * Hq, 16 * Hkv, D, B, dt, seed=Hq, out=torch.float32)
     p.call(window, sinks)
     p.compare(window, sinks, rows=6)
+
+
+@pytest.mark.parametrize("new,past,Hq,Hkv,D", H.PROMPTS)
+@pytest.mark.parametrize("dt,out", H.PROMPT_TYPES)
+def test_long_histories(new, past, Hq, Hkv, D, dt, out):
+    """Over clusters of two to eight CTAs and on whole grids."""
+    p = OneHot(new, past, Hq, Hkv, D, dt=dt, seed=sum(new), out=torch.float32 if out else None)
+    p.call()
+    p.compare(rows=8)
