@@ -664,7 +664,8 @@ pkv_status pkv_copy_blocks_fp4(void* k_pool, void* v_pool, const int32_t* pairs,
  * pkv_decode_workspace_bytes); where the sizes say that it takes less time, a
  * history is read whole instead, by a cluster, and the workspace is not used.
  * PKV_PARTITION_BALANCED returns PKV_ERR_UNSUPPORTED.  Rows of tokens >= L,
- * NaN scales included, are never used; a visible one makes its head's row NaN.
+ * NaN scales included, are never used.  A visible NaN scale of K makes the rows of
+ * its KV head's query heads NaN, one of V its 16 channels of these rows.
  * Softmax weights enter the product with V in two f16 parts (2^-22 of each).
  * 1 <= group <= 8.
  */

@@ -135,3 +135,25 @@ def test_windows(bits, S, L, window, dt):
     d = OneHot([L - 7 * (i % 5) for i in range(S)], 4, 1, bits=bits, dt=dt, seed=S)
     d.window(window, 20)
     d.compare(window + 20, window, 20)
+
+
+@pytest.mark.parametrize("lens,ps", [([40000, 400], 1024), ([4000, 900], 256)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_nan_value_stays_in_its_channels(lens, ps, D):
+    """The scale of 16 channels of V alone is NaN: they are no numbers in the rows that see the token, all else is as
+    ever.  In partitions, whole and in a window."""
+    Hkv, G = 4, 2
+    d = OneHot(lens, G * Hkv, Hkv, D, seed=ps)
+    d.attend(partition_size=ps)
+    assert d.in_partitions() == (max(lens) > 10000)
+    plain = d.out.clone()
+    d.window(300, 4)
+    window = d.out.clone()
+    t, g, group = lens[0] - 50, 2, 1
+    d.dev[1][d.tables[0, t // 16], g, 0, 8 * D + t % 16 * (D // 16) + group] = 0x7F
+    want = torch.zeros_like(plain, dtype=torch.bool)
+    want[0, G * g:G * g + G, 16 * group:16 * group + 16] = True
+    for before, call in ((plain, lambda: d.attend(partition_size=ps)), (window, lambda: d.window(300, 4))):
+        call()
+        assert torch.equal(torch.isnan(d.out), want)
+        assert torch.equal(d.out[~want], before[~want])
