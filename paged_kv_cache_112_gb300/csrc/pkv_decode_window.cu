@@ -467,13 +467,23 @@ Form best_form(int64_t units, int64_t tiles, int group, bool clusters) {
     if (best.cost == 0.f || cost < best.cost) best = Form{NW, C, cost};
   };
   if (!clusters) {
-    // Partitions: alike, and none but the last short.  Two warps a CTA where
-    // that leaves one wave and four do not (100001 tokens, 8 heads, partitions
-    // of 1024: 30.4 us against 32.8; with 8 warps 36.5).
-    if (units > Four::resident(1) && units <= Two::resident(1))
+    // Partitions: alike, and none but the last short.  Once there are more than
+    // four-warp CTAs at a time, CTAs of two warps leave less of the last wave empty,
+    // and pay for it with twice the chain of a warp's steps: worth it for
+    // partitions of up to 512 tokens, and for longer ones while they stay within one
+    // wave and groups are small.  Microseconds of one sequence with four warps and
+    // two, D = 128, in units (KV heads x partitions) of tokens: G = 4, 784 of
+    // 1024 32.5, 30.6, 1000 of 1024 36.8, 37.5, 1400 of 1024 49.6, 52.6, 784 of 512
+    // 22.3, 19.5, 1400 of 512 32.7, 32.9, 2400 of 512 48.5, 43.5, 784 of 256 17.3, 14.2,
+    // 2400 of 256 34.9, 29.7, but 496 of 1024 23.3, 24.5; G = 8, 784 of 1024 34.7,
+    // 38.9, 784 of 512 23.9, 24.0, 1800 of 256 29.7, 27.8.  Of 78 shapes with more units
+    // than that, of both head sizes, 68 take two warps by this rule: 8% less time in
+    // the mean, 18% less at best, 6% more at worst.
+    const int resident = Four::resident(1);
+    if (units > resident && (tiles <= 32 || (group <= 4 && units <= Two::resident(1))))
       consider(2, 1, Two::resident(1));
     else
-      consider(4, 1, Four::resident(1));
+      consider(4, 1, resident);
     return best;
   }
   consider(4, 1, Four::resident(1));
