@@ -9,11 +9,13 @@
 //
 // Bound over 16-bit pools: HBM bytes of the visible K and V, each read once for
 // all query heads of the group (256 windows of 70B-class heads, f16: 290 us, the
-// rate of a plain copy).  Over 4-bit pools: instructions, 321 a warp and tile
-// of 2304 bytes (D = 128), some 144 of them conversions, scales, products and
-// fragment loads; 56% of the issue slots and 54% of DRAM are used at 2 contexts
-// of 65536 tokens.  8 of 32 to 128 thousand, 8 KV heads: 180 us, 76% of a
-// copy's rate.
+// rate of a plain copy).  Over 4-bit pools: the latency of a warp's chain of
+// steps (copy, conversion, product, maximum, exponential, product) at 16 warps a
+// SM; 304 instructions a warp and tile of 2304 bytes (D = 128), some 144 of them
+// conversions, scales, products and fragment loads.  57% of the issue slots and
+// 52% of DRAM are used at 2 contexts of 65536 tokens, and a warp's largest stall
+// is an instruction's fixed latency.  8 of 32 to 128 thousand, 8 KV heads: 182
+// us, 75% of a copy's rate.
 //
 // A cluster of C CTAs of NW warps serves one (s, g, partition).  The visible
 // 16-token tiles are dealt to its warps in turn; each streams its tiles

@@ -20,9 +20,11 @@
 // kernel: 52% of the issue slots, 28% of DRAM, and loads that wait for one
 // another (position -> angles, sum -> weights, slot -> scale) as the largest
 // stall.  With few tokens that latency alone (1.7 us for one, 3.4 for 256).
-// 16384 tokens of 32 + 16 heads into 4-bit pools take 85.9 us, 1.6 times their
-// bytes' time: quantising a row is some 100 instructions of 32 lanes for four
-// heads, next to the norm's and the rotation's.
+// 16384 tokens of 32 + 16 heads into 4-bit pools take 89.2 us, 1.67 times their
+// bytes' time, with 57% of the issue slots and 44% of DRAM: quantising a row is
+// some 100 instructions of 32 lanes for four heads, next to the norm's and the
+// rotation's, and each quotient's two corrections wait for one another (the
+// largest stall: an instruction's fixed latency, at 16 warps a SM).
 //
 // Layout: D/16 lanes share a head, each holding two 16-byte chunks chosen so
 // that both members of every rotated pair (i, i + rot_dim/2) sit in one lane:

@@ -8,8 +8,8 @@
 //
 // Bound: the two products, 4 D flops a visible (query, head, token) on the
 // tensor cores; and next to them 32 exponentials a SM and cycle.  8192 tokens of
-// 32 + 8 heads of 128: 373 us, 1.47 PFLOP/s; a step of 128 history tokens for two
-// tiles takes 2870 cycles, the products alone 2048.
+// 32 + 8 heads of 128: 376 us, 1.46 PFLOP/s; a step of 128 history tokens for two
+// tiles takes some 2900 cycles, the products alone 2048.
 //
 // A CTA works on two tiles of 128 query rows of one KV head: the group's G heads
 // of 128 / G tokens, rows ordered (token, head), so that K and V are read once
