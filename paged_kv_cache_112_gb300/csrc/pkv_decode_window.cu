@@ -424,7 +424,8 @@ struct Launch {
 // 4-bit pools: fitted to 18 shapes measured with each NW and C (8 to 2048 units
 // of 10 to 514 tiles): the form of the lowest cost is 2% slower than the best
 // one in the mean, 10% at the most.  A SM takes its tiles at the rate of the
-// conversions, 34 GB a second, not of the memory.  Microseconds, 4 bits:
+// conversions, 34 GB a second, not of the memory.  Microseconds, 4 bits (with
+// weights in one part, 1 to 5% less than now):
 //   8 of 514 tiles: 9.1 with 8 warps in clusters of 8, 13.0 of 4, 37.5 alone;
 //   72 of 514: 22.0 with 8 warps of 4, 23.7 of 2, 32.6 with 4 of 2, 39.6 with 8 alone;
 //   512 of 258: 60.8 with 4 warps of 2, 65.2 with 8 alone, 89.6 with 2;

@@ -1008,7 +1008,7 @@ struct Launch {
     // new tokens behind 0 to 20000 and 1 to 8 KV heads: of 45 shapes, the choice
     // was within 2% of the fastest form in 44 and 9% off in one.  D = 128, 256
     // tokens alone: 10.9 without clusters, 15.3 in twos; 64 behind 2000: 31.3,
-    // 26.3, 19.6 in fours, 18.2 in eights.  D = 64, 64 behind 500: 12.2, 12.8, 10.9.
+    // 26.3, 19.6 in fours, 18.2 in eights (18.7 now).  D = 64, 64 behind 500: 12.2, 12.8, 10.9.
     constexpr float kStartUs = D == 64 ? 6.7f : 8.2f, kStepUs = (D == 64 ? 1.1f : 1.43f) * (TWO ? 1.4f : 1.f);
     constexpr float kMeetUs = D == 64 ? 2.3f : 5.f, kMeetCtaUs = D == 64 ? 0.f : 0.25f;
     // The most pairs there can be come of odd lengths; as many as are likely
